@@ -200,10 +200,10 @@ def _delta(q, k, v, lg, beta, state):
     qe, ke, last = eg * q, torch.exp(g[..., -1:] - g)[..., None] * k, torch.exp(g[..., -1])[..., None, None]
     S = torch.zeros(B, H, d, d, device=q.device) if state is None else state.float()
     outs = []
-    for n in range(N):
-        u = tv[:, :, n] - tk[:, :, n] @ S
-        outs.append(qe[:, :, n] @ S + att[:, :, n] @ u)
-        S = last[:, :, n] * S + ke[:, :, n].transpose(-1, -2) @ u
+    for tvn, tkn, qen, attn, ken, lastn in zip(*(x.unbind(2) for x in (tv, tk, qe, att, ke, last))):
+        u = tvn - tkn @ S
+        outs.append(qen @ S + attn @ u)
+        S = lastn * S + ken.transpose(-1, -2) @ u
     return torch.stack(outs, 2).view(B, H, N * CHUNK, d)[:, :, :T], S
 
 
