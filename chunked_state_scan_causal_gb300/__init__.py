@@ -32,6 +32,7 @@ OP_FWD, OP_BWD, OP_CHUNK_STATES, OP_CHECKPOINT = 1, 2, 3, 4
 OP_FWD_GATED, OP_BWD_GATED, OP_CHECKPOINT_GATED = 5, 6, 7
 OP_SOFTMAX_SEGMENT, OP_SOFTMAX_SEGMENT_BWD = 8, 9
 OP_FWD_GATED_VEC, OP_BWD_GATED_VEC, OP_CHECKPOINT_GATED_VEC = 10, 11, 12
+OP_FWD_DELTA, OP_BWD_DELTA, OP_CHECKPOINT_DELTA, OP_PAGED_DECODE = 13, 14, 15, 16
 ABI_VERSION = 2
 
 
@@ -54,7 +55,7 @@ class Shape(ctypes.Structure):
 
 _lock = threading.Lock()
 _lib = None
-_vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _SIGS = {
     "linattn_abi_version": ([], _i32),
     "linattn_status_string": ([_i32], ctypes.c_char_p),
@@ -77,6 +78,15 @@ _SIGS = {
     "linattn_bwd_gated_vec_ckpt": ([ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp,
                                     _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "linattn_decode": ([ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp], _i32),
+    "linattn_fwd_delta": ([ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp, _sz,
+                           _vp], _i32),
+    "linattn_bwd_delta": ([ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _sz, _vp, _vp,
+                           _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
+    "linattn_decode_delta": ([ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp], _i32),
+    "linattn_paged_append": ([ctypes.POINTER(Shape), ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp,
+                              _vp, _vp, _vp], _i32),
+    "linattn_paged_decode": ([ctypes.POINTER(Shape), ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64,
+                              _vp, ctypes.c_float, _vp, _sz, _vp], _i32),
     "linattn_state_scan_workspace_size": ([_i32, _i32, _i32, _i32, ctypes.POINTER(_sz)], _i32),
     "linattn_state_scan": ([_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32),
     "linattn_device_status": ([_vp, _vp], _i32),
@@ -93,7 +103,7 @@ _SIGS = {
     "linattn_timing_collect": ([_i32, ctypes.POINTER(_i32), ctypes.POINTER(ctypes.c_float)], _i32),
     "linattn_kernel_name": ([_i32], ctypes.c_char_p),
 }
-KERNEL_KINDS = 20
+KERNEL_KINDS = 30
 
 
 def lib():
@@ -232,6 +242,35 @@ def linattn_softmax_segment_bwd(q_shape, kv_shape, q, k, v, o, dO, lse, dq, dk, 
                                 stream) -> int:
     return lib().linattn_softmax_segment_bwd(ctypes.byref(q_shape), ctypes.byref(kv_shape), q, k, v, o, dO, lse, dq,
                                              dk, dv, softmax_scale, ws, ws_bytes, stream)
+
+
+def linattn_fwd_delta(shape, q, k, v, log_gate, beta, gate_dtype, o, init_state, final_state, ckpt, ckpt_bytes, ws,
+                      ws_bytes, stream) -> int:
+    return lib().linattn_fwd_delta(ctypes.byref(shape), q, k, v, log_gate, beta, gate_dtype, o, init_state,
+                                   final_state, ckpt, ckpt_bytes, ws, ws_bytes, stream)
+
+
+def linattn_bwd_delta(shape, q, k, v, dO, log_gate, beta, gate_dtype, init_state, d_final, ckpt, ckpt_bytes, dq, dk,
+                      dv, d_log_gate, d_beta, d_init, ws, ws_bytes, stream) -> int:
+    return lib().linattn_bwd_delta(ctypes.byref(shape), q, k, v, dO, log_gate, beta, gate_dtype, init_state, d_final,
+                                   ckpt, ckpt_bytes, dq, dk, dv, d_log_gate, d_beta, d_init, ws, ws_bytes, stream)
+
+
+def linattn_decode_delta(shape, q, k, v, log_gate, beta, gate_dtype, o, state, stream) -> int:
+    return lib().linattn_decode_delta(ctypes.byref(shape), q, k, v, log_gate, beta, gate_dtype, o, state, stream)
+
+
+def linattn_paged_append(new_shape, cache_shape, k, v, k_cache, v_cache, block_table, max_blocks, table_stride, start,
+                         new_lens, device_status, stream) -> int:
+    return lib().linattn_paged_append(ctypes.byref(new_shape), ctypes.byref(cache_shape), k, v, k_cache, v_cache,
+                                      block_table, max_blocks, table_stride, start, new_lens, device_status, stream)
+
+
+def linattn_paged_decode(q_shape, cache_shape, q, k_cache, v_cache, o, lse, block_table, max_blocks, table_stride,
+                         seq_lens, softmax_scale, ws, ws_bytes, stream) -> int:
+    return lib().linattn_paged_decode(ctypes.byref(q_shape), ctypes.byref(cache_shape), q, k_cache, v_cache, o, lse,
+                                      block_table, max_blocks, table_stride, seq_lens, softmax_scale, ws, ws_bytes,
+                                      stream)
 
 
 def linattn_segment_decay(decay, B, H, seg_len, out, stream) -> int:
@@ -616,6 +655,146 @@ def softmax_segment_bwd(q, k, v, o, dO, lse, scale: float = 0.0, outs=None, ws=N
                                      _stream(q.device, stream))
     _check(st, "linattn_softmax_segment_bwd")
     return dq, dk, dv
+
+
+def checkpoint_delta(q):
+    """Checkpoint buffer of fwd_delta(..., ckpt=) for bwd_delta."""
+    import torch
+    st, n = linattn_workspace_size(shape_of(q), OP_CHECKPOINT_DELTA)
+    _check(st, "linattn_workspace_size")
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+
+
+def _delta_gates(log_gate, beta, q):
+    """The gate type of the C ABI, after checking both gates (log_gate may be None)."""
+    import torch
+    dt = {torch.float32: F32, torch.bfloat16: BF16}.get(beta.dtype)
+    for g in (beta,) if log_gate is None else (beta, log_gate):
+        if dt is None or g.dtype != beta.dtype or not g.is_contiguous() or g.shape != q.shape[:3] \
+                or g.device != q.device:
+            raise ValueError("log_gate and beta must be contiguous [B, H, T], both fp32 or both bf16, on q's device")
+    return dt
+
+
+def _states(q, *ts):
+    import torch
+    B, H, _, d = q.shape
+    for t in ts:
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (B, H, d, d)
+                              or t.device != q.device):
+            raise ValueError("states must be contiguous fp32 [B, H, d, d] on q's device")
+
+
+def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=None, ws=None, stream=None, ckpt=None):
+    """(o, final_state or None) of the gated delta rule: S_t = S' + beta_t k_t (v_t - S'^T k_t)^T with
+    S' = exp(log_gate_t) S_{t-1}, o_t = S_t^T q_t (log_gate None: no decay; log_gate and beta [B, H, T],
+    both fp32 or both bf16).  With ``ckpt`` (from checkpoint_delta) what bwd_delta needs is kept."""
+    import torch
+    _same_layout(q, k, v, out)
+    gdt = _delta_gates(log_gate, beta, q)
+    _states(q, init_state)
+    o = out if out is not None else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    B, H, T, d = q.shape
+    fin = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if want_final else None
+    if ws is None:
+        ws = workspace(q, OP_FWD_DELTA)
+    st = linattn_fwd_delta(shape_of(q), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
+                           _ptr(init_state), _ptr(fin), _ptr(ckpt), 0 if ckpt is None else ckpt.numel(), _ptr(ws),
+                           ws.numel(), _stream(q.device, stream))
+    _check(st, "linattn_fwd_delta")
+    return o, fin
+
+
+def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, want_dinit=False, outs=None, ws=None,
+              stream=None):
+    """(dq, dk, dv, d_log_gate or None, d_beta, d_init or None) of fwd_delta for the upstream gradient dO
+    (the gates' gradients in the gates' type)."""
+    import torch
+    _same_layout(q, k, v, dO)
+    gdt = _delta_gates(log_gate, beta, q)
+    _states(q, init_state, d_final)
+    B, H, T, d = q.shape
+    if outs is None:
+        outs = [torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device) for _ in range(3)]
+    dq, dk, dv = outs
+    _same_layout(q, dq, dk, dv)
+    dlg = None if log_gate is None else torch.empty_like(log_gate)
+    db = torch.empty_like(beta)
+    dinit = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if want_dinit else None
+    if ws is None:
+        ws = workspace(q, OP_BWD_DELTA)
+    st = linattn_bwd_delta(shape_of(q), _ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(log_gate), _ptr(beta), gdt,
+                           _ptr(init_state), _ptr(d_final), _ptr(ckpt), ckpt.numel(), _ptr(dq), _ptr(dk), _ptr(dv),
+                           _ptr(dlg), _ptr(db), _ptr(dinit), _ptr(ws), ws.numel(), _stream(q.device, stream))
+    _check(st, "linattn_bwd_delta")
+    return dq, dk, dv, dlg, db, dinit
+
+
+def decode_delta(q, k, v, log_gate, beta, state, out=None, stream=None):
+    """o of the gated delta rule for T new tokens [B, H, T, d]; `state` [B, H, d, d] fp32 is updated in place."""
+    import torch
+    _same_layout(q, k, v, out)
+    gdt = _delta_gates(log_gate, beta, q)
+    _states(q, state)
+    o = out if out is not None else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    st = linattn_decode_delta(shape_of(q), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
+                              _ptr(state), _stream(q.device, stream))
+    _check(st, "linattn_decode_delta")
+    return o
+
+
+def _int_rows(q, B, *ts):
+    import torch
+    for t in ts:
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous()
+                              or t.device != q.device):
+            raise ValueError("lengths and positions must be contiguous int32 [B] on the cache's device")
+
+
+def _table(q, block_table):
+    import torch
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != q.shape[0] \
+            or block_table.stride(1) != 1 or block_table.device != q.device:
+        raise ValueError("block_table must be int32 [B, max_blocks] with contiguous rows on the cache's device")
+    n = block_table.shape[1]
+    return _ptr(block_table), n, max(n, block_table.stride(0)) if block_table.shape[0] > 1 else n
+
+
+def paged_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, device_status=None, stream=None):
+    """Writes new tokens k, v [B, Hkv, T, d] into a paged cache [pages, Hkv, page, d] (any strides): token t of
+    sequence b at position start[b] + t, in page block_table[b, position // page].  new_lens [B]: only the first
+    new_lens[b] tokens of a padded batch.  device_status: int32 tensor for LINATTN_ERR_INVALID (bad pages)."""
+    _same_layout(k, v)
+    _same_layout(k_cache, v_cache)
+    if k_cache.device != k.device:
+        raise ValueError("the new tokens and the cache must be on one device")
+    _int_rows(k, k.shape[0], start, new_lens)
+    tab, n, stride = _table(k, block_table)
+    st = linattn_paged_append(shape_of(k), shape_of(k_cache), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), tab, n,
+                              stride, _ptr(start), _ptr(new_lens), _ptr(device_status), _stream(k.device, stream))
+    _check(st, "linattn_paged_append")
+
+
+def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0, want_lse: bool = False, out=None,
+                 ws=None, stream=None):
+    """(o, lse or None): softmax attention of one new token per sequence, q [B, Hq, 1, d], over the first
+    seq_lens[b] tokens of its pages (scale 0 means 1/sqrt(d); lse [B, Hq, 1] fp32)."""
+    import torch
+    _same_layout(q, out)
+    _same_layout(k_cache, v_cache)
+    if k_cache.device != q.device:
+        raise ValueError("q and the cache must be on one device")
+    _int_rows(q, q.shape[0], seq_lens)
+    tab, n, stride = _table(q, block_table)
+    o = out if out is not None else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if want_lse else None
+    if ws is None:
+        ws = workspace(q, OP_PAGED_DECODE)
+    st = linattn_paged_decode(shape_of(q), shape_of(k_cache), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
+                              _ptr(lse), tab, n, stride, _ptr(seq_lens), scale, _ptr(ws), ws.numel(),
+                              _stream(q.device, stream))
+    _check(st, "linattn_paged_decode")
+    return o, lse
 
 
 def device_status(ws, stream=None) -> int:

@@ -47,12 +47,13 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool make_tmap_bf16(void *map, const void *base, const uint64_t dims[4], const uint64_t strides[3]) {
+bool make_tmap_bf16(void *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
+                    uint32_t box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t gd[4] = {dims[0], dims[1], dims[2], dims[3]};
   cuuint64_t gs[3] = {strides[0], strides[1], strides[2]};
-  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t box[4] = {64, box_rows, 1, 1};
   cuuint32_t es[4] = {1, 1, 1, 1};
   CUresult r = fn(reinterpret_cast<CUtensorMap *>(map), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                   const_cast<void *>(base), gd, gs, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -264,6 +265,10 @@ static cudaError_t plan_scan(const Problem &p, const GroupPlan &gp, bool reverse
                     init, out, total, ws, status, s, group_log2, gp.kb, gp.Ls);
 }
 
+static size_t delta_ckpt_bytes(const Problem &p) { return delta_walk_ckpt_bytes(p); }
+static size_t delta_fwd_ws_bytes(const Problem &) { return kHeader; }
+static size_t delta_bwd_ws_bytes(const Problem &p) { return kHeader + delta_walk_bwd_ws_bytes(p); }
+
 static int check_ws(void *ws, size_t bytes, size_t need) {
   if (!ws) return LINATTN_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LINATTN_ERR_WORKSPACE;
@@ -322,6 +327,14 @@ int32_t linattn_workspace_size(const linattn_shape *shape, int32_t op, int32_t s
     *bytes = gated_vec_ckpt_bytes(p);
   } else if (op == LINATTN_OP_SOFTMAX_SEGMENT_BWD) {
     *bytes = kHeader + softmax_bwd_stats_bytes(p.B, p.H, p.T);
+  } else if (op == LINATTN_OP_FWD_DELTA) {
+    *bytes = delta_fwd_ws_bytes(p);
+  } else if (op == LINATTN_OP_BWD_DELTA) {
+    *bytes = delta_bwd_ws_bytes(p);
+  } else if (op == LINATTN_OP_CHECKPOINT_DELTA) {
+    *bytes = delta_ckpt_bytes(p);
+  } else if (op == LINATTN_OP_PAGED_DECODE) {
+    *bytes = kHeader + paged_decode_ws_bytes(p.d, p.num_sms);
   } else {
     return LINATTN_ERR_INVALID;
   }
@@ -752,6 +765,157 @@ int32_t linattn_decode(const linattn_shape *shape, const void *q, const void *k,
   return cuda_status(decode(p, q, k, v, o, state, static_cast<cudaStream_t>(stream)));
 }
 
+// ------------------------------------------------------------------ gated delta rule
+static int delta_checks(const linattn_shape *shape, Problem *p, int32_t gate_dtype) {
+  int st = validate(shape, p);
+  if (st) return st;
+  if (p->decay) return LINATTN_ERR_INVALID;  // the gates replace the per-head decay
+  if (gate_dtype != LINATTN_BF16 && gate_dtype != LINATTN_F32) return LINATTN_ERR_INVALID;
+  return LINATTN_OK;
+}
+
+int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void *k, const void *v,
+                          const void *log_gate, const void *beta, int32_t gate_dtype, void *o,
+                          const float *init_state, float *final_state, void *checkpoint, size_t checkpoint_bytes,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+  Problem p;
+  int st = delta_checks(shape, &p, gate_dtype);
+  if (st) return st;
+  if ((st = check_ptrs({}, {init_state, final_state}))) return st;
+  if ((st = check_ws(workspace, workspace_bytes, delta_fwd_ws_bytes(p)))) return st;
+  if (checkpoint && ((reinterpret_cast<uintptr_t>(checkpoint) & 255u) || checkpoint_bytes < delta_ckpt_bytes(p)))
+    return LINATTN_ERR_INVALID;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.T == 0) {
+    if ((st = device_ok())) return st;
+    if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
+    if (!final_state) return LINATTN_OK;
+    const size_t bytes = (size_t)p.B * p.H * p.d * p.d * sizeof(float);
+    return cuda_status(init_state ? cudaMemcpyAsync(final_state, init_state, bytes, cudaMemcpyDeviceToDevice, s)
+                                  : cudaMemsetAsync(final_state, 0, bytes, s));
+  }
+  if ((st = check_ptrs({q, k, v, beta, o}, {log_gate}))) return st;
+  if ((st = device_ok())) return st;
+  if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
+  const DeltaGates g{log_gate, beta, gate_dtype == LINATTN_F32};
+  return cuda_status(delta_walk_fwd(p, g, q, k, v, o, init_state, final_state, checkpoint, s));
+}
+
+int32_t linattn_bwd_delta(const linattn_shape *shape, const void *q, const void *k, const void *v, const void *dO,
+                          const void *log_gate, const void *beta, int32_t gate_dtype, const float *init_state,
+                          const float *d_final_state, const void *checkpoint, size_t checkpoint_bytes, void *dq,
+                          void *dk, void *dv, void *d_log_gate, void *d_beta, float *d_init_state, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+  Problem p;
+  int st = delta_checks(shape, &p, gate_dtype);
+  if (st) return st;
+  if ((st = check_ptrs({}, {init_state, d_final_state, d_init_state}))) return st;
+  if ((st = check_ws(workspace, workspace_bytes, delta_bwd_ws_bytes(p)))) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.T == 0) {
+    if ((st = device_ok())) return st;
+    if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
+    if (!d_init_state) return LINATTN_OK;
+    const size_t bytes = (size_t)p.B * p.H * p.d * p.d * sizeof(float);
+    return cuda_status(d_final_state
+                           ? cudaMemcpyAsync(d_init_state, d_final_state, bytes, cudaMemcpyDeviceToDevice, s)
+                           : cudaMemsetAsync(d_init_state, 0, bytes, s));
+  }
+  if ((st = check_ptrs({q, k, v, dO, beta, dq, dk, dv, d_beta}, {log_gate, d_log_gate}))) return st;
+  if (!log_gate != !d_log_gate) return LINATTN_ERR_INVALID;
+  if (!checkpoint || (reinterpret_cast<uintptr_t>(checkpoint) & 255u) || checkpoint_bytes < delta_ckpt_bytes(p))
+    return LINATTN_ERR_INVALID;
+  if ((st = device_ok())) return st;
+  if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
+  const DeltaGates g{log_gate, beta, gate_dtype == LINATTN_F32};
+  return cuda_status(delta_walk_bwd(p, g, q, k, dO, init_state, d_final_state, checkpoint, dq, dk, dv, d_log_gate,
+                                    d_beta, d_init_state, static_cast<char *>(workspace) + kHeader, s));
+}
+
+int32_t linattn_decode_delta(const linattn_shape *shape, const void *q, const void *k, const void *v,
+                             const void *log_gate, const void *beta, int32_t gate_dtype, void *o, float *state,
+                             void *stream) {
+  Problem p;
+  int st = delta_checks(shape, &p, gate_dtype);
+  if (st) return st;
+  if (p.T == 0) return LINATTN_OK;
+  if ((st = check_ptrs({q, k, v, beta, o, state}, {log_gate}))) return st;
+  if ((st = device_ok())) return st;
+  const DeltaGates g{log_gate, beta, gate_dtype == LINATTN_F32};
+  return cuda_status(delta_decode(p, g, q, k, v, o, state, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------------------------ paged key-value cache
+static int paged_checks(const linattn_shape *x_shape, const linattn_shape *cache_shape, const int32_t *block_table,
+                        int32_t max_blocks, int64_t table_stride, Problem *x, PagedProblem *p) {
+  Problem c;
+  int st = validate(x_shape, x);
+  if (st) return st;
+  if ((st = validate(cache_shape, &c))) return st;
+  if (x->decay || c.decay || x->dtype != c.dtype || x->d != c.d || c.T < 1) return LINATTN_ERR_INVALID;
+  if (!block_table || max_blocks < 1 || table_stride < max_blocks) return LINATTN_ERR_INVALID;
+  if ((int64_t)max_blocks * c.T > 0x7fffff00) return LINATTN_ERR_UNSUPPORTED;  // positions are 32-bit
+  p->B = x->B;
+  p->Hkv = c.H;
+  p->d = x->d;
+  p->esz = x->dtype == 0 ? 2 : 4;
+  p->pages = c.B;
+  p->page = c.T;
+  p->max_blocks = max_blocks;
+  p->num_sms = c.num_sms;
+  p->csb = c.sb;
+  p->csh = c.sh;
+  p->cst = c.st;
+  p->tstride = table_stride;
+  p->table = block_table;
+  return LINATTN_OK;
+}
+
+int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape *cache_shape, const void *k,
+                             const void *v, void *k_cache, void *v_cache, const int32_t *block_table,
+                             int32_t max_blocks, int64_t table_stride, const int32_t *start,
+                             const int32_t *new_lens, int32_t *device_status, void *stream) {
+  Problem x;
+  PagedProblem p{};
+  int st = paged_checks(new_shape, cache_shape, block_table, max_blocks, table_stride, &x, &p);
+  if (st) return st;
+  if (x.H != p.Hkv) return LINATTN_ERR_INVALID;
+  if (x.T == 0) return LINATTN_OK;
+  if ((st = check_ptrs({k, v, k_cache, v_cache}, {}))) return st;
+  if (!start) return LINATTN_ERR_INVALID;
+  if ((int64_t)x.B * x.H * x.T > ((int64_t)1 << 36)) return LINATTN_ERR_UNSUPPORTED;  // the launch's block count
+  if ((st = device_ok())) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (device_status && clear_header(device_status, 4, s) != cudaSuccess) return LINATTN_ERR_CUDA;
+  return cuda_status(paged_append(p, k, v, k_cache, v_cache, x.T, x.sb, x.sh, x.st, start, new_lens, device_status, s));
+}
+
+int32_t linattn_paged_decode(const linattn_shape *q_shape, const linattn_shape *cache_shape, const void *q,
+                             const void *k_cache, const void *v_cache, void *o, float *lse,
+                             const int32_t *block_table, int32_t max_blocks, int64_t table_stride,
+                             const int32_t *seq_lens, float softmax_scale, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+  Problem x;
+  PagedProblem p{};
+  int st = paged_checks(q_shape, cache_shape, block_table, max_blocks, table_stride, &x, &p);
+  if (st) return st;
+  if (x.T != 1 || x.H % p.Hkv) return LINATTN_ERR_UNSUPPORTED;
+  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale)) return LINATTN_ERR_INVALID;
+  if ((st = check_ptrs({q, k_cache, v_cache, o}, {}))) return st;
+  if (!seq_lens) return LINATTN_ERR_INVALID;
+  if ((st = check_ws(workspace, workspace_bytes, kHeader + paged_decode_ws_bytes(x.d, x.num_sms)))) return st;
+  if ((st = device_ok())) return st;
+  p.Hq = x.H;
+  p.qsb = x.sb;
+  p.qsh = x.sh;
+  p.seq_lens = seq_lens;
+  p.scale = softmax_scale > 0.f ? softmax_scale : 1.f / std::sqrt((float)x.d);
+  p.status = static_cast<int *>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
+  return cuda_status(paged_decode(p, q, k_cache, v_cache, o, lse, static_cast<char *>(workspace) + kHeader, s));
+}
+
 static int32_t chunk_states_impl(const linattn_shape *shape, int32_t seg_len, const void *x, const void *y,
                                  bool reverse, float *out, void *workspace, size_t workspace_bytes, void *stream) {
   Problem p;
@@ -940,7 +1104,9 @@ const char *linattn_kernel_name(int32_t kind) {
                                        "diag_mma", "decode", "tc_dual_rev", "tc_chunked_fwd_agg",
                                        "gate_prep_and_grad", "tc_chunk_states", "softmax_segment",
                                        "gated_vec_fwd", "gated_vec_bwd", "pad_d64", "softmax_bwd_prep",
-                                       "softmax_bwd_dkdv", "softmax_bwd_dq", "clear_status"};
+                                       "softmax_bwd_dkdv", "softmax_bwd_dq", "clear_status",
+                                       "delta_walk", "delta_gate_sums", "delta_decode", "delta_prep", "delta_chain",
+                                       "delta_reverse", "delta_grad", "paged_append", "paged_decode", "paged_join"};
   return (kind >= 0 && kind < K_KINDS) ? names[kind] : "?";
 }
 

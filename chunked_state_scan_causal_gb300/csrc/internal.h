@@ -82,7 +82,9 @@ int device_ok();
 enum KernelKind {
   K_SIMT_FWD = 0, K_SIMT_BWD, K_SIMT_SEGMENT, K_SCAN, K_TC_AGG, K_TC_MAIN_FWD, K_DIAG,
   K_DECODE, K_TC_DUAL_REV, K_TC_MAIN_AGG, K_GATE, K_TC_CHUNK_STATES, K_SOFTMAX_SEGMENT, K_GATED_VEC_FWD,
-  K_GATED_VEC_BWD, K_PAD_D64, K_SOFTMAX_BWD_PREP, K_SOFTMAX_BWD_KV, K_SOFTMAX_BWD_Q, K_CLEAR_STATUS, K_KINDS
+  K_GATED_VEC_BWD, K_PAD_D64, K_SOFTMAX_BWD_PREP, K_SOFTMAX_BWD_KV, K_SOFTMAX_BWD_Q, K_CLEAR_STATUS,
+  K_DELTA_WALK, K_DELTA_GATE, K_DELTA_DECODE, K_DELTA_PREP, K_DELTA_CHAIN, K_DELTA_REVERSE, K_DELTA_GRAD,
+  K_PAGED_APPEND, K_PAGED_DECODE, K_PAGED_JOIN, K_KINDS
 };
 // Records timing events around one launch on `s` while timing is enabled.
 struct TimedLaunch {
@@ -244,13 +246,63 @@ cudaError_t softmax_segment_bwd(const SoftmaxProblem &p, const void *q, const vo
 
 // ---------------------------------------------------------------- TMA descriptors (api.cu)
 // 4-D bf16 tiled tensor map, dims innermost first, strides in bytes for dims 1..3,
-// box {64, 128, 1, 1} with the 128-byte swizzle (the SW128 tile half).
-bool make_tmap_bf16(void *map, const void *base, const uint64_t dims[4], const uint64_t strides[3]);
+// box {64, box_rows, 1, 1} with the 128-byte swizzle (128 rows: the SW128 tile half).
+bool make_tmap_bf16(void *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
+                    uint32_t box_rows = 128);
 
 // ---------------------------------------------------------------- recurrent decode (decode.cu)
 // For t = 0..T-1: S <- lambda S + k_t v_t^T, o_t = S^T q_t; state [BH][d][d] in/out.
 cudaError_t decode(const Problem &p, const void *q, const void *k, const void *v, void *o, float *state,
                    cudaStream_t s);
+
+// ---------------------------------------------------------------- gated delta rule (delta.cu)
+// log_gate (or null: no decay) and beta, [B*H][T], fp32 when f32 is set, else bf16.
+struct DeltaGates {
+  const void *lg, *beta;
+  int f32;
+};
+// The CUDA-core walks (fp32): one CTA per (batch, head).  ckpt (or null) keeps y and the chunk
+// states for the backward.
+size_t delta_walk_ckpt_bytes(const Problem &p);
+size_t delta_walk_bwd_ws_bytes(const Problem &p);
+cudaError_t delta_walk_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v,
+                           void *o, const float *init, float *fin, void *ckpt, cudaStream_t s);
+cudaError_t delta_walk_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
+                           const float *init, const float *d_final, const void *ckpt, void *dq, void *dk, void *dv,
+                           void *dlg, void *dbeta, float *dinit, void *ws, cudaStream_t s);
+// d_log_gate from the tokens' cumulative log-gate gradients gx [BH][T] and the anchors [BH][ceil(T/64)]
+// (each the sum of `parts` values).
+cudaError_t delta_gate_sums(const Problem &p, const float *gx, const float *anchor, int parts, void *dlg, int f32,
+                            cudaStream_t s);
+// The tensor-core path (bf16; delta_tc.cu).  ckpt: NULL, or what the backward reads.
+bool delta_tc_supported(const Problem &p);
+size_t delta_tc_fwd_ws_bytes(const Problem &p);
+size_t delta_tc_ckpt_bytes(const Problem &p);
+size_t delta_tc_bwd_ws_bytes(const Problem &p);
+cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
+                         const float *init, float *fin, void *ckpt, void *ws, int *status, cudaStream_t s);
+cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
+                         const float *d_final, const void *ckpt, void *dq, void *dk, void *dv, void *dlg, void *dbeta,
+                         float *dinit, void *ws, int *status, cudaStream_t s);
+// For t = 0..T-1 the recurrence itself; state [BH][d][d] in/out.
+cudaError_t delta_decode(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
+                         float *state, cudaStream_t s);
+
+// ---------------------------------------------------------------- paged key-value cache (paged.cu)
+// k and v caches: [pages][Hkv][page][d], element strides csb, csh, cst (contiguous d); table [B] rows of
+// max_blocks page ids, tstride apart; q and o [B][Hq][1][d], element strides qsb, qsh.
+struct PagedProblem {
+  int B, Hq, Hkv, d, esz, pages, page, max_blocks, num_sms;
+  int64_t csb, csh, cst, tstride, qsb, qsh;
+  const int *table, *seq_lens;
+  float scale;
+  int *status;
+};
+cudaError_t paged_append(const PagedProblem &p, const void *k, const void *v, void *kc, void *vc, int T, int64_t sb,
+                         int64_t sh, int64_t st, const int *start, const int *new_lens, int *status, cudaStream_t s);
+size_t paged_decode_ws_bytes(int d, int num_sms);
+cudaError_t paged_decode(const PagedProblem &p, const void *q, const void *kc, const void *vc, void *o, float *lse,
+                         void *ws, cudaStream_t s);
 
 // ---------------------------------------------------------------- diagnostics (diag.cu)
 cudaError_t diag_mma(int mode, const void *A, const void *B, float *D, cudaStream_t s);

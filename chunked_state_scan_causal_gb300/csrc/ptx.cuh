@@ -191,6 +191,18 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void 
       "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
       : "memory");
 }
+// Untiled bulk copies (both addresses 16-byte aligned, bytes a multiple of 16).
+__device__ __forceinline__ void bulk_load(uint64_t *bar, void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
+               "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_all() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -360,6 +372,15 @@ __device__ __forceinline__ uint64_t desc_kmajor(uint32_t tile, uint32_t kstep) {
 // [0, 8) covers tile rows [16k, 16k+16).
 __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t tile, uint32_t kstep) {
   return sdesc_sw128(tile + kstep * 2048u, kTileHalfBytes, 1024u);
+}
+
+// The same views of a tile whose 64-column blocks are `half` bytes apart (any number of rows: one
+// block of 64 rows is 8 KiB).
+__device__ __forceinline__ uint64_t desc_kmajor_h(uint32_t tile, uint32_t kstep, uint32_t half) {
+  return sdesc_sw128(tile + (kstep >> 2) * half + (kstep & 3) * 32u, 16u, 1024u);
+}
+__device__ __forceinline__ uint64_t desc_mnmajor_h(uint32_t tile, uint32_t kstep, uint32_t half) {
+  return sdesc_sw128(tile + kstep * 2048u, half, 1024u);
 }
 
 // Byte offset of (row, 16-byte chunk c in [0,16)) inside an SW128 tile.

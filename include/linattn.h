@@ -79,7 +79,8 @@ enum { LINATTN_BF16 = 0, LINATTN_F32 = 1 };
 enum { LINATTN_OP_FWD = 1, LINATTN_OP_BWD = 2, LINATTN_OP_CHUNK_STATES = 3, LINATTN_OP_CHECKPOINT = 4,
        LINATTN_OP_FWD_GATED = 5, LINATTN_OP_BWD_GATED = 6, LINATTN_OP_CHECKPOINT_GATED = 7,
        LINATTN_OP_SOFTMAX_SEGMENT = 8, LINATTN_OP_SOFTMAX_SEGMENT_BWD = 9, LINATTN_OP_FWD_GATED_VEC = 10,
-       LINATTN_OP_BWD_GATED_VEC = 11, LINATTN_OP_CHECKPOINT_GATED_VEC = 12 };
+       LINATTN_OP_BWD_GATED_VEC = 11, LINATTN_OP_CHECKPOINT_GATED_VEC = 12, LINATTN_OP_FWD_DELTA = 13,
+       LINATTN_OP_BWD_DELTA = 14, LINATTN_OP_CHECKPOINT_DELTA = 15, LINATTN_OP_PAGED_DECODE = 16 };
 
 typedef struct {
   int32_t abi_version;  /* must be LINATTN_ABI_VERSION                              */
@@ -257,6 +258,85 @@ int32_t linattn_bwd_gated_vec_ckpt(const linattn_shape *shape, const void *q, co
 int32_t linattn_decode(const linattn_shape *shape, const void *q, const void *k, const void *v, void *o,
                        float *state, void *stream);
 
+/* Gated delta rule: the linear-attention state with an overwriting write.  Before
+ * k_t v_t^T is added, what the decayed state already holds at k_t is taken away:
+ *   S'_t = exp(log_gate_t) S_{t-1},   y_t = v_t - S'_t^T k_t,
+ *   S_t  = S'_t + beta_t k_t y_t^T,   o_t = S_t^T q_t.
+ * log_gate [B,H,T] (values <= 0; NULL: no decay) and beta [B,H,T] (write strengths,
+ * usually in [0, 1]) are contiguous, 16-byte aligned and both of type gate_dtype
+ * (LINATTN_F32 or LINATTN_BF16, with either type of shape).  The recurrence is
+ * stable for beta_t |k_t|^2 in [0, 2]; callers normalise k.  q is used as given
+ * (no scale).  The shape's decay must be NULL.
+ *   init_state  [B,H,dk,dv] fp32 or NULL (zeros); final_state the same or NULL
+ *   checkpoint  LINATTN_OP_CHECKPOINT_DELTA bytes, 256-byte aligned, filled for
+ *               linattn_bwd_delta; or NULL (inference)
+ *   workspace   LINATTN_OP_FWD_DELTA bytes
+ * T == 0: final_state is init_state (or zeros).  Returns a status
+ * (LINATTN_ERR_INVALID for a misaligned or short checkpoint). */
+int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void *k, const void *v,
+                          const void *log_gate, const void *beta, int32_t gate_dtype, void *o,
+                          const float *init_state, float *final_state, void *checkpoint, size_t checkpoint_bytes,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward of linattn_fwd_delta (same shape, q, k, v, gates, init_state and its
+ * checkpoint), for an upstream gradient dO and the gradient d_final_state arriving at
+ * the final state (or NULL).  With R_t the gradient at S_t (R_{T-1} starts from
+ * d_final_state), u_t = beta_t y_t and dy_t = beta_t R_t^T k_t:
+ *   dq_t = S_t dO_t,   dv_t = dy_t,   dk_t = R_t u_t - S'_t dy_t,
+ *   d_beta_t = (R_t^T k_t) . y_t,   d_log_gate_t = <R_t - k_t dy_t^T, S'_t>,
+ *   R_{t-1} = exp(log_gate_t) (R_t - k_t dy_t^T) + q_{t-1} dO_{t-1}^T,
+ * d_init_state ([B,H,dk,dv] fp32, or NULL) the gradient at the initial state.
+ * d_log_gate (NULL exactly when log_gate is) and d_beta [B,H,T] have gate_dtype.
+ * Workspace: LINATTN_OP_BWD_DELTA bytes.  Returns a status. */
+int32_t linattn_bwd_delta(const linattn_shape *shape, const void *q, const void *k, const void *v, const void *dO,
+                          const void *log_gate, const void *beta, int32_t gate_dtype, const float *init_state,
+                          const float *d_final_state, const void *checkpoint, size_t checkpoint_bytes, void *dq,
+                          void *dk, void *dv, void *d_log_gate, void *d_beta, float *d_init_state, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Recurrent decode of the gated delta rule: T new tokens per sequence (meant for a
+ * few, as linattn_decode), `state` ([B,H,dk,dv] fp32) read and updated in place.
+ * Gates as in linattn_fwd_delta.  No workspace.  Returns a status. */
+int32_t linattn_decode_delta(const linattn_shape *shape, const void *q, const void *k, const void *v,
+                             const void *log_gate, const void *beta, int32_t gate_dtype, void *o, float *state,
+                             void *stream);
+
+/* Paged key-value cache of the hybrid's softmax layers while serving.  A cache is a
+ * set of pages: cache_shape has B = pages, H = key heads, T = tokens of a page and the
+ * element strides of k_cache and v_cache (so [pages, H, page, d] and [pages, page, H,
+ * d] orders both fit).  Token n of sequence b sits in page block_table[b][n / page],
+ * slot n % page; block_table is int32 device memory, rows table_stride >= max_blocks
+ * apart.  max_blocks * page must stay below 2^31 - 256.
+ *
+ * linattn_paged_append copies new tokens k, v ([B, H, T, d] of new_shape, the cache's
+ * type) to positions start[b] .. start[b] + new_lens[b] - 1 (int32 device; new_lens NULL:
+ * all T; larger values are taken as T, negative ones as 0).  Positions outside the table
+ * and page ids outside the cache are not written; device_status (int32 device, 16-byte
+ * aligned, or NULL) is zeroed and then receives LINATTN_ERR_INVALID if there were any.
+ * Two tokens of one call with the same slot leave one of them.  Returns a status. */
+int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape *cache_shape, const void *k,
+                             const void *v, void *k_cache, void *v_cache, const int32_t *block_table,
+                             int32_t max_blocks, int64_t table_stride, const int32_t *start,
+                             const int32_t *new_lens, int32_t *device_status, void *stream);
+
+/* Attention of one new token per sequence over its pages:
+ *   o[b,h]   = sum_{n < seq_lens[b]} softmax_n(scale q[b,h] . k_n) v_n,
+ *   lse[b,h] = log sum_n exp(scale q[b,h] . k_n)
+ * with query head h reading key head h / (Hq / Hkv) (q_shape: B, H = Hq a multiple of
+ * the cache's heads, T = 1, the strides of q and o).  Slots past seq_lens[b] are never
+ * used, whatever they hold.  An empty sequence gives o = 0, lse = -inf.  The length is
+ * split over the whole GPU and the pieces are joined.  Bad page ids count as absent
+ * tokens and set the workspace's status word to LINATTN_ERR_INVALID; lengths are
+ * clamped to [0, max_blocks * page].
+ *   lse [B,Hq] fp32 or NULL; seq_lens [B] int32 device; softmax_scale > 0, or 0 for
+ *   1/sqrt(d); workspace: LINATTN_OP_PAGED_DECODE bytes for q_shape
+ * Returns a status. */
+int32_t linattn_paged_decode(const linattn_shape *q_shape, const linattn_shape *cache_shape, const void *q,
+                             const void *k_cache, const void *v_cache, void *o, float *lse,
+                             const int32_t *block_table, int32_t max_blocks, int64_t table_stride,
+                             const int32_t *seq_lens, float softmax_scale, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
 /* Segment-local states (what each sequence-parallel rank computes from its
  * own contiguous segment before the exchange; LASP-2 page, abstract):
  *   local_states[g,b,h] = sum_{s in segment g} lambda^{end_g - s} k_s v_s^T
@@ -394,7 +474,7 @@ int32_t linattn_device_status(const void *workspace, void *stream);
  * for every kernel kind k < max_kinds its launch count and summed device time
  * (ms), clears the record and returns the number of kinds
  * (LINATTN_KERNEL_KINDS), or a negative status. */
-#define LINATTN_KERNEL_KINDS 20
+#define LINATTN_KERNEL_KINDS 30
 int32_t linattn_timing_enable(int32_t on);
 int32_t linattn_timing_collect(int32_t max_kinds, int32_t *launches, float *total_ms);
 /* Name of kernel kind k (static string; "?" when out of range). */
