@@ -265,9 +265,15 @@ static cudaError_t plan_scan(const Problem &p, const GroupPlan &gp, bool reverse
                     init, out, total, ws, status, s, group_log2, gp.kb, gp.Ls);
 }
 
-static size_t delta_ckpt_bytes(const Problem &p) { return delta_walk_ckpt_bytes(p); }
-static size_t delta_fwd_ws_bytes(const Problem &) { return kHeader; }
-static size_t delta_bwd_ws_bytes(const Problem &p) { return kHeader + delta_walk_bwd_ws_bytes(p); }
+static size_t delta_ckpt_bytes(const Problem &p) {
+  return delta_tc_supported(p) ? delta_tc_ckpt_bytes(p) : delta_walk_ckpt_bytes(p);
+}
+static size_t delta_fwd_ws_bytes(const Problem &p) {
+  return kHeader + (delta_tc_supported(p) ? delta_tc_fwd_ws_bytes(p) : 0);
+}
+static size_t delta_bwd_ws_bytes(const Problem &p) {
+  return kHeader + (delta_tc_supported(p) ? delta_tc_bwd_ws_bytes(p) : delta_walk_bwd_ws_bytes(p));
+}
 
 static int check_ws(void *ws, size_t bytes, size_t need) {
   if (!ws) return LINATTN_ERR_WORKSPACE;
@@ -798,6 +804,9 @@ int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void 
   if ((st = device_ok())) return st;
   if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
   const DeltaGates g{log_gate, beta, gate_dtype == LINATTN_F32};
+  if (delta_tc_supported(p))
+    return cuda_status(delta_tc_fwd(p, g, q, k, v, o, init_state, final_state, checkpoint,
+                                    static_cast<char *>(workspace) + kHeader, static_cast<int *>(workspace), s));
   return cuda_status(delta_walk_fwd(p, g, q, k, v, o, init_state, final_state, checkpoint, s));
 }
 
@@ -828,6 +837,10 @@ int32_t linattn_bwd_delta(const linattn_shape *shape, const void *q, const void 
   if ((st = device_ok())) return st;
   if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
   const DeltaGates g{log_gate, beta, gate_dtype == LINATTN_F32};
+  if (delta_tc_supported(p))
+    return cuda_status(delta_tc_bwd(p, g, q, k, dO, d_final_state, checkpoint, dq, dk, dv, d_log_gate, d_beta,
+                                    d_init_state, static_cast<char *>(workspace) + kHeader,
+                                    static_cast<int *>(workspace), s));
   return cuda_status(delta_walk_bwd(p, g, q, k, dO, init_state, d_final_state, checkpoint, dq, dk, dv, d_log_gate,
                                     d_beta, d_init_state, static_cast<char *>(workspace) + kHeader, s));
 }

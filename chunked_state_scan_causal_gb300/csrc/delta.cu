@@ -445,22 +445,25 @@ size_t delta_walk_bwd_ws_bytes(const Problem &p) {
   return p.T == 0 ? 0 : align256(4 * (BH * p.T * (2 * p.d + 1) + BH * N));
 }
 
-#define LINATTN_DELTA_DISPATCH(fn, ...)                                                 \
-  (p.d == 64 ? (p.dtype == 1 ? fn<64, float>(__VA_ARGS__) : fn<64, __nv_bfloat16>(__VA_ARGS__)) \
-             : (p.dtype == 1 ? fn<128, float>(__VA_ARGS__) : fn<128, __nv_bfloat16>(__VA_ARGS__)))
-
 cudaError_t delta_walk_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v,
                            void *o, const float *init, float *fin, void *ckpt, cudaStream_t s) {
-  return LINATTN_DELTA_DISPATCH(fwd_launch, p, g, q, k, v, o, init, fin, ckpt, s);
+  return p.d == 64 ? fwd_launch<64, float>(p, g, q, k, v, o, init, fin, ckpt, s)
+                   : fwd_launch<128, float>(p, g, q, k, v, o, init, fin, ckpt, s);
 }
 cudaError_t delta_walk_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
                            const float *init, const float *d_final, const void *ckpt, void *dq, void *dk, void *dv,
                            void *dlg, void *dbeta, float *dinit, void *ws, cudaStream_t s) {
-  return LINATTN_DELTA_DISPATCH(bwd_launch, p, g, q, k, dO, init, d_final, ckpt, dq, dk, dv, dlg, dbeta, dinit, ws, s);
+  return p.d == 64
+             ? bwd_launch<64, float>(p, g, q, k, dO, init, d_final, ckpt, dq, dk, dv, dlg, dbeta, dinit, ws, s)
+             : bwd_launch<128, float>(p, g, q, k, dO, init, d_final, ckpt, dq, dk, dv, dlg, dbeta, dinit, ws, s);
 }
 cudaError_t delta_decode(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
                          float *state, cudaStream_t s) {
-  return LINATTN_DELTA_DISPATCH(decode_launch, p, g, q, k, v, o, state, s);
+  if (p.d == 64)
+    return p.dtype == 1 ? decode_launch<64, float>(p, g, q, k, v, o, state, s)
+                        : decode_launch<64, __nv_bfloat16>(p, g, q, k, v, o, state, s);
+  return p.dtype == 1 ? decode_launch<128, float>(p, g, q, k, v, o, state, s)
+                      : decode_launch<128, __nv_bfloat16>(p, g, q, k, v, o, state, s);
 }
 
 }  // namespace linattn

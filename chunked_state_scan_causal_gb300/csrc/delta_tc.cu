@@ -1,0 +1,1361 @@
+// Gated delta rule on the tensor cores (bf16, d = 128; d = 64 as the zero-padded problem), by chunks
+// of 64 tokens.  For one chunk, with g the cumulative log-gates inside it, Gam_ij = exp(g_i - g_j)
+// (j <= i), b the write strengths, phi_j = exp(g_last - g_j) and S the state entering it:
+//
+//     Y  = T (V - diag(e^g) K S),   T = (I + tril(Gam * K K^T, -1) diag(b))^-1        (what each write
+//     O  = diag(e^g) Q S + P diag(b) Y,   P = tril(Gam * Q K^T)                        corrects, y_t)
+//     S' = e^(g_last) S + K^T diag(phi b) Y.
+//
+// T, W = -T diag(e^g) K and P do not involve the state, so one kernel forms them for all chunks at
+// once (delta_prep); only Y = T V + W S and the update of S are a chain over the chunks, one CTA per
+// (batch, head) (delta_chain).  The chain keeps everything transposed: lane = value dimension, columns =
+// key dimension or token, so S^T, Y^T and O^T live in tensor memory, each is re-read by the thread that
+// owns its lane, and every product takes S^T or Y^T as the A operand from tensor memory and an
+// untransposed tile from shared memory as B.  The backward runs the same chain in reverse time on R,
+// the gradient at the state (delta_reverse), and then all gradients chunk by chunk (delta_grad):
+//
+//     dU  = P^T dO + diag(phi) K R,    Z = T^T diag(b) dU  (= dV),
+//     R'  = e^(g_last) R + Q^T diag(e^g) dO + W^T diag(b) dU,
+//     dQ  = diag(e^g) dO S^T + A K,      A_ij = b_j Gam_ij dO_i . y_j   (j <= i)
+//     dK  = [ -diag(e^g) Z S^T + D K ] + [ diag(phi b) Y R^T + A^T Q + D^T K ],
+//                                        D_ij = -b_j Gam_ij z_i . y_j   (j < i)
+//     db_j = dU_j . y_j - sum_{i > j} Gam_ij (k_i . k_j) (z_i . y_j),
+//     d(cumulative log-gate)_i = q_i . dq_i + k_i . [read part] - k_i . [write part].
+//
+// Precision: the state and every accumulator are fp32.  Operands of the chain that are not bf16 inputs
+// (S, Y, W, T, P, R, dU) enter its products as two bf16 parts, hi + lo (16 significant bits), three
+// products for two such operands: what the chain carries from chunk to chunk stays within about 2^-16
+// per step instead of 2^-8, so a final state is good for a decode that goes on for long.  The
+// gradient kernel's operands are single bf16 (its results are rounded to bf16 anyway).
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace linattn {
+namespace {
+
+constexpr int kC = 64;                    // tokens of a chunk
+constexpr uint32_t kSlot = 16384;         // a 64 x 128 (or 128 x 64) bf16 tile
+// A chunk's record: W hi, W lo (64 x 128), T hi, lo (64 x 64), P hi, lo (64 x 64), all as swizzled tiles
+// ready for a plain bulk copy; then five fp32 rows of 64: e^g, phi, b, g and its low part (log2 units).
+constexpr uint32_t kRecW = 0, kRecT = 32768, kRecP = 49152, kRecG = 65536, kGateBytes = 5 * 64 * 4;
+constexpr size_t kRecBytes = 67584;
+constexpr size_t kStateImg = 32768, kRowImg = 16384;
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
+  return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// a and b as packed bf16 and what is left of them as packed bf16
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = pack_bf16(a, b);
+  lo = pack_bf16(a - bf16lo(hi), b - bf16hi(hi));
+}
+// offset of 16-byte piece c (0..7) of row r in a swizzled 64-column block
+__device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
+// offset of element (row r, column x) of a [64 x 128] tile with blocks `half` apart
+__device__ __forceinline__ uint32_t sw_el(uint32_t r, uint32_t x, uint32_t half) {
+  return (x >> 6) * half + sw(r, (x & 63u) >> 3) + (x & 7u) * 2u;
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, float x) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))) : "memory");
+}
+__device__ __forceinline__ float ld_shared_bf16(uint32_t addr) {
+  unsigned short u;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(addr) : "memory");
+  return __uint_as_float((uint32_t)u << 16);
+}
+__device__ __forceinline__ float2 ld_shared_f2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+
+// Column sums over a warp: on return lane l holds the sum over all lanes of x[l].
+__device__ __forceinline__ float warp_col_sum(float (&x)[32], int lane) {
+#pragma unroll
+  for (int n = 16; n >= 1; n /= 2) {
+    const bool up = lane & n;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, n);
+    }
+  }
+  return x[0];
+}
+
+struct DeltaTcParams {
+  int H, T, N, d;          // N chunks; d = 64 or 128 (state rows and columns; the tiles are 128 wide)
+  int f32;                 // type of the gates
+  const void *lg, *beta;
+  uint8_t *rec;            // [BH][N] records
+  uint8_t *simg, *yimg;    // [BH][N + 1] images of S^T, [BH][N] images of Y^T (or null: not kept)
+  uint8_t *rimg, *uimg;    // backward: [BH][N] images of R^T and of dU^T
+  const float *in;         // initial state, or the final state's gradient (or null)
+  float *out;              // final state, or the initial state's gradient (or null)
+  float *anchor;           // backward: [BH][N][8] parts of <R, S> at the chunks' ends
+  float *gx;               // backward: [BH][T]
+  void *dbeta;
+  int *status;
+};
+
+__device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
+  return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+
+// ================================================================== prep
+// One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
+// cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks by forward
+// substitution, one column per thread, then the off-diagonal block as two 32^3 products), and
+// W^T = K^T (T diag(e^g))^T on the tensor cores.  128 threads; three CTAs fit an SM and hide each
+// other's latencies.
+constexpr int kPrepThreads = 128;
+constexpr int kLd = 68;  // row stride of the fp32 64 x 64 matrices: 16-byte rows, spread over the banks
+constexpr uint32_t kPrepA = 32768, kPrepT = kPrepA + 17408, kPrepEnd = kPrepT + 17408;
+constexpr size_t kPrepSmem = kPrepEnd + 1024;
+static_assert(kPrepT % 1024 == 0 && kLd * 64 * 4 == 17408, "tiles stay 1 KiB aligned");
+
+__global__ void __launch_bounds__(kPrepThreads)
+    delta_prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, DeltaTcParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  __shared__ uint64_t bar[3];
+  __shared__ uint32_t tslot;
+  __shared__ int abort_flag;
+  __shared__ float s_hi[kC], s_lo[kC], s_b[kC], s_eg[kC];
+  float *A = reinterpret_cast<float *>(smem + kPrepA), *Ti = reinterpret_cast<float *>(smem + kPrepT);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int c = blockIdx.x, bh = blockIdx.y, b = bh / P.H, h = bh % P.H;
+  uint8_t *rec = P.rec + ((int64_t)bh * P.N + c) * kRecBytes;
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < 3; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tslot, 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tslot;
+  griddep_wait();
+  if (tid == 0) {
+    mbar_arrive_expect_tx(&bar[0], 32768);
+    for (int x = 0; x < 2; ++x) {
+      tma_load_4d(&mk, &bar[0], smem + x * 16384, 64 * x, kC * c, h, b, kPolicyEvictNormal);
+      tma_load_4d(&mq, &bar[0], smem + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
+    }
+  }
+  if (warp == 2) {
+    // cumulative log2-gates in 64 bits (differences of far sums must keep their low bits); a gate below
+    // 2^-1000 is zero either way
+    const int t0 = kC * c + 2 * lane;
+    const int64_t gi = (int64_t)bh * P.T + t0;
+    double l[2];
+    float be[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const bool in = t0 + x < P.T;
+      double v = in && P.lg ? (double)load_gate(P.lg, gi + x, P.f32) * 1.4426950408889634 : 0.0;
+      l[x] = v < -1000.0 ? -1000.0 : v;
+      be[x] = in ? load_gate(P.beta, gi + x, P.f32) : 0.f;
+    }
+    double s = l[0] + l[1];
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const double y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    const double last = __shfl_sync(0xffffffffu, s, 31);
+    float *g = reinterpret_cast<float *>(rec + kRecG);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const double gx = x ? s : s - l[1];
+      const int j = 2 * lane + x;
+      const float hi = (float)gx, lo = (float)(gx - (double)hi), eg = ex2(hi) * ex2(lo), phi = ex2((float)(last - gx));
+      s_hi[j] = hi;
+      s_lo[j] = lo;
+      s_b[j] = be[x];
+      s_eg[j] = eg;
+      g[j] = eg;
+      g[64 + j] = phi;
+      g[128 + j] = be[x];
+      g[192 + j] = hi;
+      g[256 + j] = lo;
+    }
+  }
+  bool ok = true;
+  if (warp == 0) {
+    ok = mbar_wait_w(&bar[0], 0, &abort_flag, P.status);
+    if (ok) {
+#pragma unroll
+      for (uint32_t ks = 0; ks < 8; ++ks)
+        mma_ss_warp(tmem, desc_kmajor(base, ks), desc_kmajor(base, ks), idesc_bf16(128, 64, false, false), ks > 0);
+      mma_commit_warp(&bar[1]);
+    }
+  }
+  __syncthreads();
+  ok = ok && mbar_wait(&bar[1], 0, &abort_flag, P.status);
+  if (__syncthreads_and(ok)) {
+    tc_fence_after();
+    const int i = tid & 63;
+    const float hi = s_hi[i], lo = s_lo[i];
+    const uint32_t lb = (uint32_t)(warp * 32) << 16;
+    if (warp < 2) {
+      // A_ij = Gam_ij (k_i . k_j) b_j, j < i
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t r[32];
+        tmem_ld32(tmem + lb + 32 * x, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          float a[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int j = 32 * x + 4 * y + z;
+            const float e = ex2((hi - s_hi[j]) + (lo - s_lo[j]));
+            a[z] = j < i ? e * __uint_as_float(r[4 * y + z]) * s_b[j] : 0.f;
+          }
+          *reinterpret_cast<float4 *>(A + i * kLd + 32 * x + 4 * y) = make_float4(a[0], a[1], a[2], a[3]);
+        }
+      }
+      named_bar_sync(1, 64);
+      // the diagonal block of this warp: column `lane` of its inverse
+      const float *Ab = A + (warp * 32) * kLd + warp * 32;
+      float x[32];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int m = 0; m < r; m += 4) {
+          const float4 a = *reinterpret_cast<const float4 *>(Ab + r * kLd + m);
+          s0 = fmaf(a.x, x[m], s0);
+          if (m + 1 < r) s1 = fmaf(a.y, x[m + 1], s1);
+          if (m + 2 < r) s2 = fmaf(a.z, x[m + 2], s2);
+          if (m + 3 < r) s3 = fmaf(a.w, x[m + 3], s3);
+        }
+        x[r] = (r == lane ? 1.f : 0.f) - ((s0 + s1) + (s2 + s3));
+        Ti[(warp * 32 + r) * kLd + warp * 32 + lane] = x[r];
+      }
+    } else {
+      // P_ij = Gam_ij (q_i . k_j), j <= i, straight to the record
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t r[32];
+        tmem_ld32(tmem + lb + 32 * x, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          uint32_t ph[4], pl[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int j = 32 * x + 8 * y + 2 * z;
+            float p0 = ex2((hi - s_hi[j]) + (lo - s_lo[j])) * __uint_as_float(r[8 * y + 2 * z]);
+            float p1 = ex2((hi - s_hi[j + 1]) + (lo - s_lo[j + 1])) * __uint_as_float(r[8 * y + 2 * z + 1]);
+            split2(j <= i ? p0 : 0.f, j + 1 <= i ? p1 : 0.f, ph[z], pl[z]);
+          }
+          const uint32_t at = sw(i, 4 * x + y);
+          *reinterpret_cast<uint4 *>(rec + kRecP + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+          *reinterpret_cast<uint4 *>(rec + kRecP + 8192 + at) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+        }
+      }
+    }
+    __syncthreads();
+    {
+      // the off-diagonal block -T22 (A21 T11): X = A21 T11 parked in the (zero) upper right block
+      const int r = tid / 4, c0 = (tid % 4) * 8;
+      float acc[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll 8
+      for (int m = 0; m < 32; ++m) {
+        const float a = A[(32 + r) * kLd + m];
+        const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0);
+        const float4 v = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0 + 4);
+        acc[0] = fmaf(a, u.x, acc[0]); acc[1] = fmaf(a, u.y, acc[1]);
+        acc[2] = fmaf(a, u.z, acc[2]); acc[3] = fmaf(a, u.w, acc[3]);
+        acc[4] = fmaf(a, v.x, acc[4]); acc[5] = fmaf(a, v.y, acc[5]);
+        acc[6] = fmaf(a, v.z, acc[6]); acc[7] = fmaf(a, v.w, acc[7]);
+      }
+      float4 *X = reinterpret_cast<float4 *>(Ti + r * kLd + 32 + c0);
+      X[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      X[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll 8
+      for (int m = 0; m < 32; ++m) {
+        const float a = Ti[(32 + r) * kLd + 32 + m];
+        const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + 32 + c0);
+        const float4 v = *reinterpret_cast<const float4 *>(Ti + m * kLd + 32 + c0 + 4);
+        acc[0] = fmaf(-a, u.x, acc[0]); acc[1] = fmaf(-a, u.y, acc[1]);
+        acc[2] = fmaf(-a, u.z, acc[2]); acc[3] = fmaf(-a, u.w, acc[3]);
+        acc[4] = fmaf(-a, v.x, acc[4]); acc[5] = fmaf(-a, v.y, acc[5]);
+        acc[6] = fmaf(-a, v.z, acc[6]); acc[7] = fmaf(-a, v.w, acc[7]);
+      }
+      __syncthreads();
+      float4 *Y = reinterpret_cast<float4 *>(Ti + (32 + r) * kLd + c0);
+      Y[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      Y[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      X[0] = X[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      __syncthreads();
+    }
+    {
+      // T to the record; T diag(e^g), the operand of W, over A
+      const int half = tid / 64;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t th[4], tl[4], eh[4], el[4];
+        const float4 u = *reinterpret_cast<const float4 *>(Ti + i * kLd + 32 * half + 8 * y);
+        const float4 v = *reinterpret_cast<const float4 *>(Ti + i * kLd + 32 * half + 8 * y + 4);
+        const float *e = s_eg + 32 * half + 8 * y;
+        split2(u.x, u.y, th[0], tl[0]);
+        split2(u.z, u.w, th[1], tl[1]);
+        split2(v.x, v.y, th[2], tl[2]);
+        split2(v.z, v.w, th[3], tl[3]);
+        split2(u.x * e[0], u.y * e[1], eh[0], el[0]);
+        split2(u.z * e[2], u.w * e[3], eh[1], el[1]);
+        split2(v.x * e[4], v.y * e[5], eh[2], el[2]);
+        split2(v.z * e[6], v.w * e[7], eh[3], el[3]);
+        const uint32_t at = sw(i, 4 * half + y);
+        *reinterpret_cast<uint4 *>(rec + kRecT + at) = make_uint4(th[0], th[1], th[2], th[3]);
+        *reinterpret_cast<uint4 *>(rec + kRecT + 8192 + at) = make_uint4(tl[0], tl[1], tl[2], tl[3]);
+        st_shared_v4(base + kPrepA + at, eh[0], eh[1], eh[2], eh[3]);
+        st_shared_v4(base + kPrepA + 8192 + at, el[0], el[1], el[2], el[3]);
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ss_warp(tmem + 64, desc_mnmajor(base, ks), desc_kmajor(base + kPrepA + p * 8192, ks),
+                      idesc_bf16(128, 64, true, false), p + ks > 0);
+      mma_commit_warp(&bar[2]);
+    }
+    ok = mbar_wait(&bar[2], 0, &abort_flag, P.status);
+    if (__syncthreads_and(ok)) {
+      tc_fence_after();
+      // W^T: lane = key dimension, column = token; negated, over the K and Q tiles
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t r[32];
+        tmem_ld32(tmem + lb + 64 + 32 * x, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int t = 0; t < 32; ++t) {
+          const float w = -__uint_as_float(r[t]), wh = __bfloat162float(__float2bfloat16_rn(w));
+          const uint32_t at = base + sw_el(32 * x + t, tid, 8192);
+          st_shared_u16(at, w);
+          st_shared_u16(at + 16384, w - wh);
+        }
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (tid == 0) {
+        bulk_store(rec + kRecW, smem, 32768);
+        bulk_commit();
+        bulk_wait_all();
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 128);
+}
+
+// ================================================================== chains
+// Shared by both directions.  Warps: 0 loads, 1 issues the products, 4..11 carry the chain (thread =
+// lane of S^T, half of its columns), 12..15 the output (forward) or the scaled dO (backward).
+constexpr int kChainThreads = 512;
+constexpr int kSlots = 12;                      // ring of 16 KiB tiles, in order of use
+constexpr int kGateRing = 4;
+constexpr uint32_t kChStage = kSlots * kSlot;   // output tile (forward)
+constexpr uint32_t kChGate = kChStage + kSlot;
+constexpr uint32_t kChBar = kChGate + kGateRing * 2048;
+constexpr size_t kChainSmem = kChBar + 512 + 1024;
+static_assert(kChainSmem <= 231000, "one CTA per SM");
+
+enum { C_FULL = 0, C_EMPTY = C_FULL + kSlots, C_GFULL = C_EMPTY + kSlots, C_GEMPTY = C_GFULL + kGateRing,
+       C_OP = C_GEMPTY + kGateRing,   // S^T (R^T) operand parts ready
+       C_SCALED,                      // its accumulator scaled by the chunk's decay
+       C_ACC,                         // its accumulator complete (next chunk)
+       C_YFULL, C_YOP,                // Y^T (dU^T) accumulator complete; its operand for the update ready
+       C_UOP,                         // forward: the operand of the output product ready
+       C_QS, C_OSC, C_OFULL, C_OFREE, // forward: Q S done, scaled; output complete, read
+       C_COUNT };
+static_assert(C_COUNT * 8 + 8 <= 512, "barriers fit");
+
+struct ChainCtx {
+  uint8_t *smem;
+  uint64_t *bar;
+  volatile int *abort_flag;
+  int *status;
+  uint32_t base;
+  __device__ bool wait(int idx, int parity) const { return mbar_wait(&bar[idx], parity & 1, abort_flag, status); }
+  __device__ bool wait_w(int idx, int parity) const { return __all_sync(0xffffffffu, wait(idx, parity)); }
+  __device__ uint32_t slot(int n) const { return base + (uint32_t)(n % kSlots) * kSlot; }
+  __device__ bool full(int n) const { return wait_w(C_FULL + n % kSlots, n / kSlots); }
+  __device__ void release(int n) const { mma_commit_warp(&bar[C_EMPTY + n % kSlots]); }
+  __device__ const float *gates(int x) const {
+    return reinterpret_cast<const float *>(smem + kChGate + (x % kGateRing) * 2048);
+  }
+  // one arrival per warp, after the warp's tensor-memory accesses
+  __device__ void arrive(int idx, int lane) const {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[idx]);
+  }
+};
+
+__device__ __forceinline__ void chain_setup(const ChainCtx &k, uint32_t *tslot, int *abort_flag, int warp, int uop) {
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int i = 0; i < C_COUNT; ++i) {
+      int n = 1;
+      if (i >= C_GEMPTY && i < C_GEMPTY + kGateRing) n = 12;
+      if (i == C_OP || i == C_SCALED || i == C_YOP) n = 8;
+      if (i == C_UOP) n = uop;  // the warps that make that operand
+      if (i == C_OSC || i == C_OFREE) n = 4;
+      mbar_init(&k.bar[i], n);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+}
+
+// The loader's waits for what it has in flight, after the last load or an abort.
+__device__ __forceinline__ void chain_drain(const ChainCtx &k, int n, int ng) {
+  volatile int no_abort = 0;
+  for (int s = 0; s < kSlots; ++s) {
+    const int uses = n > s ? (n - 1 - s) / kSlots + 1 : 0;
+    if (uses) mbar_wait(&k.bar[C_FULL + s], (uses - 1) & 1, &no_abort, k.status);
+  }
+  for (int s = 0; s < kGateRing; ++s) {
+    const int uses = ng > s ? (ng - 1 - s) / kGateRing + 1 : 0;
+    if (uses) mbar_wait(&k.bar[C_GFULL + s], (uses - 1) & 1, &no_abort, k.status);
+  }
+}
+
+// 32 fp32 values (as bits) to 16 + 16 words of hi and lo parts in tensor memory
+__device__ __forceinline__ void store_split(const float (&x)[32], uint32_t hi_addr, uint32_t lo_addr, uint32_t (&hi)[16]) {
+  uint32_t lo[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
+  tmem_st16(hi_addr, hi);
+  tmem_st16(lo_addr, lo);
+}
+// 16 packed words of row r, pieces c0 .. c0 + 3 of a swizzled block in global memory
+__device__ __forceinline__ void store_row(uint8_t *block, uint32_t r, uint32_t c0, const uint32_t (&w)[16]) {
+#pragma unroll
+  for (uint32_t c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4 *>(block + sw(r, c0 + c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+}
+
+// Tensor memory of the forward chain (columns): S^T accumulator, its hi and lo parts, Y^T, the two
+// operands made from it (hi, lo each), O^T.
+constexpr uint32_t kTS = 0, kTSop = 128, kTY = 256, kTU = 320, kTUt = 384, kTO = 448;
+
+__global__ void __launch_bounds__(kChainThreads, 1)
+    delta_chain_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, DeltaTcParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int abort_flag;
+  uint8_t *smem = align1024(smem_raw);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChBar);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + C_COUNT);
+  const ChainCtx k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int bh = blockIdx.x, b = bh / P.H, h = bh % P.H;
+  chain_setup(k, tslot, &abort_flag, warp, 8);
+  const uint32_t tmem = *tslot;
+  griddep_wait();
+  const uint8_t *rec0 = P.rec + (int64_t)bh * P.N * kRecBytes;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int n = 0, ng = 0, c = 0;
+      bool ok = true;
+      auto slot = [&](uint8_t *&dst, uint64_t *&full) {
+        const int s = n % kSlots;
+        if (n >= kSlots && !(ok = k.wait(C_EMPTY + s, n / kSlots - 1))) return false;
+        dst = smem + s * kSlot;
+        full = &bar[C_FULL + s];
+        mbar_arrive_expect_tx(full, kSlot);
+        ++n;
+        return true;
+      };
+      uint8_t *dst;
+      uint64_t *full;
+      auto seq = [&](const CUtensorMap *m) {
+        if (!slot(dst, full)) return;
+        tma_load_4d(m, full, dst, 0, kC * c, h, b, kPolicyEvictFirst);
+        tma_load_4d(m, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictFirst);
+      };
+      auto img = [&](const uint8_t *src) {
+        if (slot(dst, full)) bulk_load(full, dst, src, kSlot);
+      };
+      for (; c < P.N && ok; ++c) {
+        const uint8_t *rec = rec0 + c * kRecBytes;
+        if (c >= kGateRing && !(ok = k.wait(C_GEMPTY + c % kGateRing, c / kGateRing - 1))) break;
+        mbar_arrive_expect_tx(&bar[C_GFULL + c % kGateRing], kGateBytes);
+        bulk_load(&bar[C_GFULL + c % kGateRing], smem + kChGate + (c % kGateRing) * 2048, rec + kRecG, kGateBytes);
+        ++ng;
+        if (ok) seq(&mv);
+        if (ok) img(rec + kRecT);
+        if (ok) img(rec + kRecW);
+        if (ok) img(rec + kRecW + kSlot);
+        if (ok) seq(&mq);
+        if (ok) seq(&mk);
+        if (ok) img(rec + kRecP);
+      }
+      chain_drain(k, n, ng);
+    }
+  } else if (warp == 1) {
+    const uint32_t id_vt = idesc_bf16(128, 64, true, false), id_64 = idesc_bf16(128, 64, false, false),
+                   id_k = idesc_bf16(128, 128, false, true);
+    auto vt = [&](int c) {  // Y^T = V^T T^T
+      const int n = 7 * c;
+      if (!k.full(n) || !k.full(n + 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ss_warp(tmem + kTY, desc_mnmajor_h(k.slot(n), ks, 8192), desc_kmajor(k.slot(n + 1) + p * 8192, ks), id_vt,
+                      p + ks > 0);
+      k.release(n);
+      k.release(n + 1);
+      return true;
+    };
+    bool ok = vt(0);
+    for (int c = 0; c < P.N && ok; ++c) {
+      const int n = 7 * c;
+      // Y^T += S^T W^T: hi hi, hi lo, lo hi
+      if (!(ok = k.wait_w(C_OP, c) && k.full(n + 2) && k.full(n + 3))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 3; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks)
+          mma_ts_warp(tmem + kTY, tmem + kTSop + (p == 2 ? 64u : 0u) + ks * 8,
+                      desc_kmajor_h(k.slot(n + 2 + (p == 1)), ks, 8192), id_64, 1);
+      mma_commit_warp(&bar[C_YFULL]);
+      k.release(n + 2);
+      k.release(n + 3);
+      // O^T = S^T Q^T
+      if (!(ok = (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.full(n + 4))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks)
+          mma_ts_warp(tmem + kTO, tmem + kTSop + p * 64 + ks * 8, desc_kmajor_h(k.slot(n + 4), ks, 8192), id_64,
+                      p + ks > 0);
+      mma_commit_warp(&bar[C_QS]);
+      k.release(n + 4);
+      // S^T += Y^T diag(phi b) K
+      if (!(ok = k.wait_w(C_YOP, c) && k.wait_w(C_SCALED, c) && k.full(n + 5))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ts_warp(tmem + kTS, tmem + kTUt + p * 32 + ks * 8, desc_mnmajor_h(k.slot(n + 5), ks, 8192), id_k, 1);
+      mma_commit_warp(&bar[C_ACC]);
+      k.release(n + 5);
+      if (c + 1 < P.N && !(ok = vt(c + 1))) break;
+      // O^T (scaled) += Y^T diag(b) P^T
+      if (!(ok = k.wait_w(C_UOP, c) && k.wait_w(C_OSC, c) && k.full(n + 6))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 3; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ts_warp(tmem + kTO, tmem + kTU + (p == 2 ? 32u : 0u) + ks * 8,
+                      desc_kmajor(k.slot(n + 6) + (p == 1 ? 8192u : 0u), ks), id_64, 1);
+      mma_commit_warp(&bar[C_OFULL]);
+      k.release(n + 6);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    const uint32_t quad = warp & 3, hf = (warp - 4) >> 2, row = quad * 32 + lane, lb = (quad * 32) << 16;
+    const uint32_t t = tmem + lb;
+    bool ok = true;
+    for (int c = 0; c <= P.N && ok; ++c) {
+      float s[2][32];
+      if (c == 0) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int dk = 64 * hf + 32 * x + j;
+            s[x][j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
+          }
+      } else {
+        if (!(ok = k.wait_w(C_ACC, c - 1))) break;
+        tc_fence_after();
+        tmem_ld32(t + kTS + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+        tmem_ld32(t + kTS + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[1]));
+        tmem_ld_wait();
+      }
+      uint8_t *img = P.simg ? P.simg + ((int64_t)bh * (P.N + 1) + c) * kStateImg + hf * 16384 : nullptr;
+      if (c == P.N) {
+        if (P.out && (int)row < P.d)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int dk = 64 * hf + 32 * x + j;
+              if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[x][j];
+            }
+        if (img)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t hi[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(s[x][2 * j], s[x][2 * j + 1]);
+            store_row(img, row, 4 * x, hi);
+          }
+        break;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t hi[16];
+        store_split(s[x], t + kTSop + 32 * hf + 16 * x, t + kTSop + 64 + 32 * hf + 16 * x, hi);
+        if (img) store_row(img, row, 4 * x, hi);
+      }
+      tmem_st_wait();
+      k.arrive(C_OP, lane);
+      if (!(ok = k.wait_w(C_GFULL + c % kGateRing, c / kGateRing))) break;
+      const float *g = k.gates(c);
+      const float f = g[63];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s[x][j] *= f;
+        tmem_st32(t + kTS + 64 * hf + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
+      }
+      tmem_st_wait();
+      k.arrive(C_SCALED, lane);
+      // Y^T: tokens 32 hf .. + 31 of this lane
+      if (!(ok = k.wait_w(C_YFULL, c))) break;
+      tc_fence_after();
+      float y[32], u[32];
+      uint32_t hi[16];
+      tmem_ld32(t + kTY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&y));
+      tmem_ld_wait();
+      const float *phi = g + 64 + 32 * hf, *be = g + 128 + 32 * hf;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) u[j] = be[j] * y[j];
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = phi[j] * u[j];
+      store_split(v, t + kTUt + 16 * hf, t + kTUt + 32 + 16 * hf, hi);
+      tmem_st_wait();
+      k.arrive(C_YOP, lane);
+      store_split(u, t + kTU + 16 * hf, t + kTU + 32 + 16 * hf, hi);
+      tmem_st_wait();
+      k.arrive(C_UOP, lane);
+      if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
+      if (P.yimg) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+        store_row(P.yimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, hi);
+      }
+    }
+  } else if (warp >= 12) {
+    const uint32_t quad = warp & 3, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16);
+    const uint32_t stage = k.base + kChStage;
+    bool ok = true;
+    for (int c = 0; c < P.N && ok; ++c) {
+      float o[2][32];
+      // one verdict for the four warps, at the barrier below: none is left alone in it
+      ok = k.wait_w(C_GFULL + c % kGateRing, c / kGateRing) && k.wait_w(C_QS, c);
+      if (ok) {
+        tc_fence_after();
+        const float *g = k.gates(c);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[x][j] *= g[32 * x + j];
+          tmem_st32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
+        }
+        tmem_st_wait();
+        k.arrive(C_OSC, lane);
+        if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
+        ok = k.wait_w(C_OFULL, c);
+      }
+      if (threadIdx.x == 384) bulk_wait_read_all();  // the previous tile has left the staging buffer
+      if (!(ok = group_all(ok, 2, 128))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
+      tmem_ld_wait();
+      k.arrive(C_OFREE, lane);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) st_shared_u16(stage + sw_el(32 * x + j, row, 8192), o[x][j]);
+      fence_proxy_async_smem();
+      named_bar_sync(2, 128);
+      if (threadIdx.x == 384) {
+        tma_store_4d(&mo, smem + kChStage, 0, kC * c, h, b);
+        if (P.d == 128) tma_store_4d(&mo, smem + kChStage + 8192, 64, kC * c, h, b);
+        bulk_commit();
+      }
+    }
+    if (threadIdx.x == 384) bulk_wait_all();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Tensor memory of the reverse chain: R^T accumulator, its parts, P^T dO and K R (transposed), the
+// operand diag(b) dU (hi, lo), the operand diag(e^g) dO (hi, lo).
+constexpr uint32_t kTR = 0, kTRop = 128, kTD1 = 256, kTD2 = 320, kTD = 384, kTdO = 448;
+
+__global__ void __launch_bounds__(kChainThreads, 1)
+    delta_reverse_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                         const __grid_constant__ CUtensorMap mdo, DeltaTcParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int abort_flag;
+  uint8_t *smem = align1024(smem_raw);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChBar);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + C_COUNT);
+  const ChainCtx k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int bh = blockIdx.x, b = bh / P.H, h = bh % P.H;
+  chain_setup(k, tslot, &abort_flag, warp, 4);
+  const uint32_t tmem = *tslot;
+  griddep_wait();
+  const uint8_t *rec0 = P.rec + (int64_t)bh * P.N * kRecBytes;
+
+  // step x of the walk is chunk N - 1 - x
+  if (warp == 0) {
+    if (lane == 0) {
+      int n = 0, ng = 0, x = 0, c = P.N - 1;
+      bool ok = true;
+      auto slot = [&](uint8_t *&dst, uint64_t *&full) {
+        const int s = n % kSlots;
+        if (n >= kSlots && !(ok = k.wait(C_EMPTY + s, n / kSlots - 1))) return false;
+        dst = smem + s * kSlot;
+        full = &bar[C_FULL + s];
+        mbar_arrive_expect_tx(full, kSlot);
+        ++n;
+        return true;
+      };
+      uint8_t *dst;
+      uint64_t *full;
+      auto seq = [&](const CUtensorMap *m) {
+        if (!slot(dst, full)) return;
+        tma_load_4d(m, full, dst, 0, kC * c, h, b, kPolicyEvictNormal);
+        tma_load_4d(m, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictNormal);
+      };
+      auto img = [&](const uint8_t *src) {
+        if (slot(dst, full)) bulk_load(full, dst, src, kSlot);
+      };
+      for (; x < P.N && ok; ++x) {
+        c = P.N - 1 - x;
+        const uint8_t *rec = rec0 + c * kRecBytes;
+        if (x >= kGateRing && !(ok = k.wait(C_GEMPTY + x % kGateRing, x / kGateRing - 1))) break;
+        mbar_arrive_expect_tx(&bar[C_GFULL + x % kGateRing], kGateBytes);
+        bulk_load(&bar[C_GFULL + x % kGateRing], smem + kChGate + (x % kGateRing) * 2048, rec + kRecG, kGateBytes);
+        ++ng;
+        if (ok) seq(&mdo);
+        if (ok) img(rec + kRecP);
+        if (ok) seq(&mk);
+        if (ok) seq(&mq);
+        if (ok) img(rec + kRecW);
+        if (ok) img(rec + kRecW + kSlot);
+      }
+      chain_drain(k, n, ng);
+    }
+  } else if (warp == 1) {
+    const uint32_t id_mm = idesc_bf16(128, 64, true, true), id_64 = idesc_bf16(128, 64, false, false),
+                   id_k = idesc_bf16(128, 128, false, true);
+    auto pd = [&](int x) {  // (P^T dO)^T = dO^T P
+      const int n = 6 * x;
+      if (!k.full(n) || !k.full(n + 1)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ss_warp(tmem + kTD1, desc_mnmajor_h(k.slot(n), ks, 8192),
+                      desc_mnmajor_h(k.slot(n + 1) + p * 8192, ks, 8192), id_mm, p + ks > 0);
+      k.release(n + 1);
+      return true;
+    };
+    bool ok = pd(0);
+    for (int x = 0; x < P.N && ok; ++x) {
+      const int n = 6 * x;
+      if (!(ok = k.wait_w(C_OP, x) && k.full(n + 2))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks)
+          mma_ts_warp(tmem + kTD2, tmem + kTRop + p * 64 + ks * 8, desc_kmajor_h(k.slot(n + 2), ks, 8192), id_64,
+                      p + ks > 0);
+      mma_commit_warp(&bar[C_YFULL]);
+      k.release(n + 2);
+      // R^T += dO^T diag(e^g) Q
+      if (!(ok = k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x) && k.full(n + 3))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ts_warp(tmem + kTR, tmem + kTdO + p * 32 + ks * 8, desc_mnmajor_h(k.slot(n + 3), ks, 8192), id_k, 1);
+      k.release(n + 3);
+      k.release(n);  // the scaled dO is ready: every reader of this tile is done
+      // R^T += dU^T diag(b) W
+      if (!(ok = k.wait_w(C_YOP, x) && k.full(n + 4) && k.full(n + 5))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 3; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ts_warp(tmem + kTR, tmem + kTD + (p == 2 ? 32u : 0u) + ks * 8,
+                      desc_mnmajor_h(k.slot(n + 4 + (p == 1)), ks, 8192), id_k, 1);
+      mma_commit_warp(&bar[C_ACC]);
+      k.release(n + 4);
+      k.release(n + 5);
+      if (x + 1 < P.N && !(ok = pd(x + 1))) break;
+    }
+  } else if (warp >= 4 && warp < 12) {
+    const uint32_t quad = warp & 3, hf = (warp - 4) >> 2, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16);
+    bool ok = true;
+    for (int x = 0; x <= P.N && ok; ++x) {
+      const int c = P.N - 1 - x;
+      float s[2][32];
+      if (x == 0) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int dk = 64 * hf + 32 * y + j;
+            s[y][j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
+          }
+      } else {
+        if (!(ok = k.wait_w(C_ACC, x - 1))) break;
+        tc_fence_after();
+        tmem_ld32(t + kTR + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+        tmem_ld32(t + kTR + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[1]));
+        tmem_ld_wait();
+      }
+      if (x == P.N) {
+        if (P.out && (int)row < P.d)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int dk = 64 * hf + 32 * y + j;
+              if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[y][j];
+            }
+        break;
+      }
+      uint8_t *img = P.rimg + ((int64_t)bh * P.N + c) * kStateImg + hf * 16384;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t hi[16];
+        store_split(s[y], t + kTRop + 32 * hf + 16 * y, t + kTRop + 64 + 32 * hf + 16 * y, hi);
+        store_row(img, row, 4 * y, hi);
+      }
+      tmem_st_wait();
+      k.arrive(C_OP, lane);
+      if (!(ok = k.wait_w(C_GFULL + x % kGateRing, x / kGateRing))) break;
+      const float *g = k.gates(x);
+      const float f = g[63];
+      // <R, S> at the chunk's end: the anchor of the log-gates' gradient
+      float dot = 0.f;
+      const uint8_t *simg = P.simg + ((int64_t)bh * (P.N + 1) + c + 1) * kStateImg + hf * 16384;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float w[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] = s[y][j] * f;
+        tmem_st32(t + kTR + 64 * hf + 32 * y, *reinterpret_cast<uint32_t(*)[32]>(&w));
+      }
+      tmem_st_wait();
+      k.arrive(C_SCALED, lane);
+      if (x > 0 || P.in)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(simg + sw(row, 4 * y + q));
+            dot = fmaf(s[y][8 * q + 0], bf16lo(v.x), dot);
+            dot = fmaf(s[y][8 * q + 1], bf16hi(v.x), dot);
+            dot = fmaf(s[y][8 * q + 2], bf16lo(v.y), dot);
+            dot = fmaf(s[y][8 * q + 3], bf16hi(v.y), dot);
+            dot = fmaf(s[y][8 * q + 4], bf16lo(v.z), dot);
+            dot = fmaf(s[y][8 * q + 5], bf16hi(v.z), dot);
+            dot = fmaf(s[y][8 * q + 6], bf16lo(v.w), dot);
+            dot = fmaf(s[y][8 * q + 7], bf16hi(v.w), dot);
+          }
+#pragma unroll
+      for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) P.anchor[((int64_t)bh * P.N + c) * 8 + warp - 4] = dot;
+      // dU^T: tokens 32 hf .. + 31 of this lane
+      if (!(ok = k.wait_w(C_YFULL, x))) break;
+      tc_fence_after();
+      float u[32], v[32];
+      uint32_t hi[16];
+      tmem_ld32(t + kTD1 + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&u));
+      tmem_ld32(t + kTD2 + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&v));
+      tmem_ld_wait();
+      const float *phi = g + 64 + 32 * hf, *be = g + 128 + 32 * hf;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        u[j] = fmaf(phi[j], v[j], u[j]);
+        v[j] = be[j] * u[j];
+      }
+      store_split(v, t + kTD + 16 * hf, t + kTD + 32 + 16 * hf, hi);
+      tmem_st_wait();
+      k.arrive(C_YOP, lane);
+      if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
+      store_row(P.uimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, hi);
+    }
+  } else if (warp >= 12) {
+    // diag(e^g) dO, transposed into tensor memory
+    const uint32_t quad = warp & 3, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16);
+    bool ok = true;
+    for (int x = 0; x < P.N && ok; ++x) {
+      const int n = 6 * x;
+      if (!(ok = k.wait_w(C_GFULL + x % kGateRing, x / kGateRing) && k.full(n) && (x == 0 || k.wait_w(C_ACC, x - 1))))
+        break;
+      tc_fence_after();
+      const float *g = k.gates(x);
+      const uint32_t tile = k.slot(n);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float v[32];
+        uint32_t hi[16];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = g[32 * y + j] * ld_shared_bf16(tile + sw_el(32 * y + j, row, 8192));
+        store_split(v, t + kTdO + 16 * y, t + kTdO + 32 + 16 * y, hi);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&bar[C_UOP]);
+        mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ================================================================== gradients of a chunk
+// One CTA per chunk, 256 threads.  Products of the form [dimension x token] keep lane = dimension, as in
+// the chains; the 64 x 64 ones come from 128-row operands whose other rows are unused: [K; dO] stacked
+// gives K K^T in lanes 0..63 and dO Y^T in lanes 64..127.
+constexpr int kGradThreads = 256;
+constexpr uint32_t kGrKD = 0, kGrQ = 32768, kGrS = 49152, kGrR = 81920, kGrY = 114688, kGrU = 131072, kGrT = 147456,
+                   kGrZ = 163840, kGrD = 180224, kGrA = 188416, kGrV = 196608, kGrG = 212992, kGrEnd = 215040;
+constexpr size_t kGradSmem = kGrEnd + 1024;
+constexpr uint32_t kGZ = 0, kGOp = 64, kGKK = 128, kGdP = 192, kGGY = 256, kGdq = 320, kGdr = 384, kGdw = 448;
+
+__global__ void __launch_bounds__(kGradThreads, 1)
+    delta_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mdo, const __grid_constant__ CUtensorMap mdq,
+                      const __grid_constant__ CUtensorMap mdk, const __grid_constant__ CUtensorMap mdv,
+                      DeltaTcParams P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  __shared__ uint64_t bar[6];
+  __shared__ uint32_t tslot;
+  __shared__ int abort_flag;
+  __shared__ float s_dot[4][kC], s_col[2][kC], s_x[4][kC];
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t quad = warp & 3, hf = warp >> 2, row = quad * 32 + lane;
+  const int c = blockIdx.x, bh = blockIdx.y, b = bh / P.H, h = bh % P.H;
+  const int64_t ci = (int64_t)bh * P.N + c;
+  const float *g = reinterpret_cast<const float *>(smem + kGrG);
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < 6; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&tslot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tslot, t = tmem + ((quad * 32) << 16);
+  griddep_wait();
+  if (tid == 0) {
+    const uint8_t *rec = P.rec + ci * kRecBytes;
+    mbar_arrive_expect_tx(&bar[0], 3 * 16384 + 16384 + kGateBytes + 16384);
+    bulk_load(&bar[0], smem + kGrU, P.uimg + ci * kRowImg, 16384);
+    bulk_load(&bar[0], smem + kGrG, rec + kRecG, kGateBytes);
+    bulk_load(&bar[0], smem + kGrT, rec + kRecT, 16384);
+    bulk_load(&bar[0], smem + kGrY, P.yimg + ci * kRowImg, 16384);
+    for (int x = 0; x < 2; ++x) {
+      tma_load_4d(&mk, &bar[0], smem + kGrKD + x * 16384, 64 * x, kC * c, h, b, kPolicyEvictNormal);
+      tma_load_4d(&mdo, &bar[0], smem + kGrKD + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
+    }
+    mbar_arrive_expect_tx(&bar[1], 32768 + 32768 + 16384);
+    bulk_load(&bar[1], smem + kGrS, P.simg + ((int64_t)bh * (P.N + 1) + c) * kStateImg, 32768);
+    bulk_load(&bar[1], smem + kGrR, P.rimg + ci * kStateImg, 32768);
+    for (int x = 0; x < 2; ++x)
+      tma_load_4d(&mq, &bar[1], smem + kGrQ + x * 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
+  }
+  const uint32_t KD = base + kGrKD, dO = KD + 8192, Y = base + kGrY, Z = base + kGrZ, S = base + kGrS, R = base + kGrR;
+  const uint32_t id_mm = idesc_bf16(128, 64, true, true), id_mk = idesc_bf16(128, 64, true, false),
+                 id_km = idesc_bf16(128, 64, false, true), id_kk = idesc_bf16(128, 64, false, false);
+  bool ok = mbar_wait(&bar[0], 0, &abort_flag, P.status);
+  if (__syncthreads_and(ok)) {
+    // diag(b) dU as an operand, and the parts of dU . y over this warp's 32 value dimensions
+    {
+      float dot[32];
+      uint32_t op[16];
+      const float *be = g + 128 + 32 * hf;
+#pragma unroll
+      for (uint32_t p = 0; p < 4; ++p) {
+        uint32_t u[4], y[4];
+        ld_shared_v4(base + kGrU + sw(row, 4 * hf + p), u[0], u[1], u[2], u[3]);
+        ld_shared_v4(Y + sw(row, 4 * hf + p), y[0], y[1], y[2], y[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 8 * p + 2 * e;
+          op[4 * p + e] = pack_bf16(be[j] * bf16lo(u[e]), be[j + 1] * bf16hi(u[e]));
+          dot[j] = bf16lo(u[e]) * bf16lo(y[e]);
+          dot[j + 1] = bf16hi(u[e]) * bf16hi(y[e]);
+        }
+      }
+      tmem_st16(t + kGOp + 16 * hf, op);
+      tmem_st_wait();
+      s_dot[quad][32 * hf + lane] = warp_col_sum(dot, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+      tc_fence_after();
+      // Z^T = (diag(b) dU)^T T
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_ts_warp(tmem + kGZ, tmem + kGOp + ks * 8, desc_mnmajor_h(base + kGrT + p * 8192, ks, 8192), id_km,
+                      p + ks > 0);
+      mma_commit_warp(&bar[2]);
+#pragma unroll
+      for (uint32_t ks = 0; ks < 8; ++ks)
+        mma_ss_warp(tmem + kGKK, desc_kmajor(KD, ks), desc_kmajor(KD, ks), id_kk, ks > 0);
+#pragma unroll
+      for (uint32_t ks = 0; ks < 8; ++ks)
+        mma_ss_warp(tmem + kGdP, desc_kmajor(KD, ks), desc_mnmajor_h(Y, ks, 8192), id_km, ks > 0);
+      ok = mbar_wait_w(&bar[1], 0, &abort_flag, P.status);
+      if (ok) {
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks)  // (dO S^T)^T
+          mma_ss_warp(tmem + kGdq, desc_mnmajor(S, ks), desc_kmajor(dO, ks), id_mk, ks > 0);
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks)  // (Y R^T)^T
+          mma_ss_warp(tmem + kGdw, desc_mnmajor(R, ks), desc_mnmajor_h(Y, ks, 8192), id_mm, ks > 0);
+      }
+    }
+    ok = ok && mbar_wait(&bar[2], 0, &abort_flag, P.status);
+  }
+  if (__syncthreads_and(ok)) {
+    tc_fence_after();
+    {
+      // Z: an operand tile (row = value dimension) and dv
+      float z[32];
+      tmem_ld32(t + kGZ + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&z));
+      tmem_ld_wait();
+#pragma unroll
+      for (uint32_t p = 0; p < 4; ++p)
+        st_shared_v4(Z + sw(row, 4 * hf + p), pack_bf16(z[8 * p], z[8 * p + 1]), pack_bf16(z[8 * p + 2], z[8 * p + 3]),
+                     pack_bf16(z[8 * p + 4], z[8 * p + 5]), pack_bf16(z[8 * p + 6], z[8 * p + 7]));
+#pragma unroll
+      for (int j = 0; j < 32; ++j) st_shared_u16(base + kGrV + sw_el(32 * hf + j, row, 8192), z[j]);
+    }
+    tc_fence_before();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      tma_store_4d(&mdv, smem + kGrV, 0, kC * c, h, b);
+      if (P.d == 128) tma_store_4d(&mdv, smem + kGrV + 8192, 64, kC * c, h, b);
+      bulk_commit();
+    }
+    if (warp == 0) {
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t ks = 0; ks < 8; ++ks)  // Z Y^T (lanes 0..63)
+        mma_ss_warp(tmem + kGGY, desc_mnmajor_h(Z, ks, 16384), desc_mnmajor_h(Y, ks, 8192), id_mm, ks > 0);
+      mma_commit_warp(&bar[3]);
+#pragma unroll
+      for (uint32_t ks = 0; ks < 8; ++ks)  // (Z S^T)^T
+        mma_ss_warp(tmem + kGdr, desc_mnmajor(S, ks), desc_mnmajor_h(Z, ks, 8192), id_mm, ks > 0);
+    }
+    ok = mbar_wait(&bar[3], 0, &abort_flag, P.status);
+  }
+  if (__syncthreads_and(ok)) {
+    tc_fence_after();
+    const int i = row & 63;
+    const float hi = g[192 + i], lo = g[256 + i];
+    const float *be = g + 128 + 32 * hf, *ghi = g + 192 + 32 * hf, *glo = g + 256 + 32 * hf;
+    if (quad < 2) {
+      // D_ij = -b_j Gam_ij z_i . y_j, and the parts of sum_i Gam_ij (k_i . k_j) (z_i . y_j)
+      float kk[32], zy[32];
+      tmem_ld32(t + kGKK + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&kk));
+      tmem_ld32(t + kGGY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&zy));
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float e = ex2((hi - ghi[j]) + (lo - glo[j])) * zy[j];
+        const bool in = 32 * (int)hf + j < i;
+        kk[j] = in ? e * kk[j] : 0.f;
+        zy[j] = in ? -be[j] * e : 0.f;
+      }
+#pragma unroll
+      for (uint32_t p = 0; p < 4; ++p)
+        st_shared_v4(base + kGrD + sw(i, 4 * hf + p), pack_bf16(zy[8 * p], zy[8 * p + 1]),
+                     pack_bf16(zy[8 * p + 2], zy[8 * p + 3]), pack_bf16(zy[8 * p + 4], zy[8 * p + 5]),
+                     pack_bf16(zy[8 * p + 6], zy[8 * p + 7]));
+      s_col[quad][32 * hf + lane] = warp_col_sum(kk, lane);
+    } else {
+      // A_ij = b_j Gam_ij dO_i . y_j
+      float a[32];
+      tmem_ld32(t + kGdP + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&a));
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        a[j] = 32 * (int)hf + j <= i ? ex2((hi - ghi[j]) + (lo - glo[j])) * be[j] * a[j] : 0.f;
+#pragma unroll
+      for (uint32_t p = 0; p < 4; ++p)
+        st_shared_v4(base + kGrA + sw(i, 4 * hf + p), pack_bf16(a[8 * p], a[8 * p + 1]),
+                     pack_bf16(a[8 * p + 2], a[8 * p + 3]), pack_bf16(a[8 * p + 4], a[8 * p + 5]),
+                     pack_bf16(a[8 * p + 6], a[8 * p + 7]));
+    }
+    tc_fence_before();
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (warp == 0) {
+      tc_fence_after();
+      const uint32_t D = base + kGrD, A = base + kGrA, Q = base + kGrQ;
+#pragma unroll
+      for (uint32_t ks = 0; ks < 4; ++ks)  // (A K)^T
+        mma_ss_warp(tmem + kGKK, desc_mnmajor(KD, ks), desc_kmajor(A, ks), id_mk, ks > 0);
+#pragma unroll
+      for (uint32_t ks = 0; ks < 4; ++ks)  // (D K)^T
+        mma_ss_warp(tmem + kGdP, desc_mnmajor(KD, ks), desc_kmajor(D, ks), id_mk, ks > 0);
+#pragma unroll
+      for (uint32_t ks = 0; ks < 4; ++ks)  // (A^T Q + D^T K)^T
+        mma_ss_warp(tmem + kGGY, desc_mnmajor_h(Q, ks, 8192), desc_mnmajor_h(A, ks, 8192), id_mm, ks > 0);
+#pragma unroll
+      for (uint32_t ks = 0; ks < 4; ++ks)
+        mma_ss_warp(tmem + kGGY, desc_mnmajor(KD, ks), desc_mnmajor_h(D, ks, 8192), id_mm, 1);
+      mma_commit_warp(&bar[4]);
+    }
+    ok = mbar_wait(&bar[4], 0, &abort_flag, P.status);
+  }
+  if (__syncthreads_and(ok)) {
+    tc_fence_after();
+    // lane = key dimension, tokens 32 hf .. + 31; x gathers q . dq + k . (read - write part)
+    const float *eg = g + 32 * hf, *phi = g + 64 + 32 * hf, *be = g + 128 + 32 * hf;
+    float x[32];
+    {
+      float a[32], w[32];
+      tmem_ld32(t + kGdq + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&a));
+      tmem_ld32(t + kGKK + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&w));
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float v = fmaf(eg[j], a[j], w[j]);
+        x[j] = v * ld_shared_bf16(base + kGrQ + sw_el(32 * hf + j, row, 8192));
+        st_shared_u16(S + sw_el(32 * hf + j, row, 8192), v);
+      }
+    }
+    {
+      float a[32], w[32];
+      tmem_ld32(t + kGdr + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&a));
+      tmem_ld32(t + kGdP + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&w));
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) a[j] = fmaf(-eg[j], a[j], w[j]);  // the read part
+      float f[32];
+      tmem_ld32(t + kGdw + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&f));
+      tmem_ld32(t + kGGY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&w));
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float v = fmaf(phi[j] * be[j], f[j], w[j]);  // the write part
+        x[j] = fmaf(a[j] - v, ld_shared_bf16(KD + sw_el(32 * hf + j, row, 16384)), x[j]);
+        st_shared_u16(R + sw_el(32 * hf + j, row, 8192), a[j] + v);
+      }
+    }
+    s_x[quad][32 * hf + lane] = warp_col_sum(x, lane);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      for (int y = 0; y < (P.d == 128 ? 2 : 1); ++y) {
+        tma_store_4d(&mdq, smem + kGrS + y * 8192, 64 * y, kC * c, h, b);
+        tma_store_4d(&mdk, smem + kGrR + y * 8192, 64 * y, kC * c, h, b);
+      }
+      bulk_commit();
+    } else if (tid >= 64 && tid < 64 + kC) {
+      const int j = tid - 64;
+      const int64_t at = (int64_t)bh * P.T + kC * c + j;
+      if (kC * c + j < P.T) {
+        P.gx[at] = (s_x[0][j] + s_x[1][j]) + (s_x[2][j] + s_x[3][j]);
+        const float db = ((s_dot[0][j] + s_dot[1][j]) + (s_dot[2][j] + s_dot[3][j])) - (s_col[0][j] + s_col[1][j]);
+        if (P.f32)
+          static_cast<float *>(P.dbeta)[at] = db;
+        else
+          static_cast<__nv_bfloat16 *>(P.dbeta)[at] = __float2bfloat16_rn(db);
+      }
+    }
+  }
+  if (tid == 0) {
+    bulk_wait_all();
+    // after an abort the loads may still be in flight (a wait with a limit; done at once otherwise)
+    volatile int no_abort = 0;
+    mbar_wait(&bar[0], 0, &no_abort, P.status);
+    mbar_wait(&bar[1], 0, &no_abort, P.status);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+bool seq64_tmap(const Problem &p, const void *x, CUtensorMap *m) {
+  // d = 64: the box of columns 64..127 lies past the rows' end; loads fill zeros there
+  const uint64_t dims[4] = {(uint64_t)p.d, (uint64_t)p.T, (uint64_t)p.H, (uint64_t)p.B};
+  const uint64_t strides[3] = {(uint64_t)p.st * 2, (uint64_t)p.sh * 2, (uint64_t)p.sb * 2};
+  return make_tmap_bf16(m, x, dims, strides, 64);
+}
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+int chunks(const Problem &p) { return (p.T + kC - 1) / kC; }
+size_t bhs(const Problem &p) { return (size_t)p.B * p.H; }
+size_t rec_bytes(const Problem &p) { return bhs(p) * chunks(p) * kRecBytes; }
+
+DeltaTcParams params(const Problem &p, const DeltaGates &g, int *status) {
+  DeltaTcParams P{};
+  P.H = p.H;
+  P.T = p.T;
+  P.N = chunks(p);
+  P.d = p.d;
+  P.f32 = g.f32;
+  P.lg = g.lg;
+  P.beta = g.beta;
+  P.status = status;
+  return P;
+}
+
+}  // namespace
+
+bool delta_tc_supported(const Problem &p) { return p.dtype == 0; }
+size_t delta_tc_fwd_ws_bytes(const Problem &p) { return align256(rec_bytes(p)); }
+size_t delta_tc_ckpt_bytes(const Problem &p) {
+  if (p.T == 0) return 0;
+  return align256(rec_bytes(p) + bhs(p) * ((size_t)(chunks(p) + 1) * kStateImg + (size_t)chunks(p) * kRowImg));
+}
+size_t delta_tc_bwd_ws_bytes(const Problem &p) {
+  const size_t n = bhs(p) * chunks(p);
+  return align256(n * (kStateImg + kRowImg + 8 * sizeof(float)) + bhs(p) * p.T * sizeof(float));
+}
+
+cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
+                         const float *init, float *fin, void *ckpt, void *ws, int *status, cudaStream_t s) {
+  CUtensorMap mq, mk, mv, mo;
+  if (!seq64_tmap(p, q, &mq) || !seq64_tmap(p, k, &mk) || !seq64_tmap(p, v, &mv) || !seq64_tmap(p, o, &mo))
+    return cudaErrorInvalidValue;
+  DeltaTcParams P = params(p, g, status);
+  P.rec = static_cast<uint8_t *>(ckpt ? ckpt : ws);
+  if (ckpt) {
+    P.simg = P.rec + rec_bytes(p);
+    P.yimg = P.simg + bhs(p) * (size_t)(P.N + 1) * kStateImg;
+  }
+  P.in = init;
+  P.out = fin;
+  cudaError_t e = allow_smem(delta_prep_kernel, kPrepSmem);
+  if (e == cudaSuccess) e = allow_smem(delta_chain_kernel, kChainSmem);
+  if (e != cudaSuccess) return e;
+  {
+    TimedLaunch t(K_DELTA_PREP, s);
+    e = launch_overlapped(delta_prep_kernel, dim3(P.N, (unsigned)bhs(p)), dim3(kPrepThreads), kPrepSmem, s, mq, mk, P);
+    if (e != cudaSuccess) return e;
+  }
+  TimedLaunch t(K_DELTA_CHAIN, s);
+  return launch_overlapped(delta_chain_kernel, dim3((unsigned)bhs(p)), dim3(kChainThreads), kChainSmem, s, mq, mk, mv,
+                           mo, P);
+}
+
+cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
+                         const float *d_final, const void *ckpt, void *dq, void *dk, void *dv, void *dlg, void *dbeta,
+                         float *dinit, void *ws, int *status, cudaStream_t s) {
+  CUtensorMap mq, mk, mdo, mdq, mdk, mdv;
+  if (!seq64_tmap(p, q, &mq) || !seq64_tmap(p, k, &mk) || !seq64_tmap(p, dO, &mdo) || !seq64_tmap(p, dq, &mdq) ||
+      !seq64_tmap(p, dk, &mdk) || !seq64_tmap(p, dv, &mdv))
+    return cudaErrorInvalidValue;
+  DeltaTcParams P = params(p, g, status);
+  const size_t n = bhs(p) * P.N;
+  P.rec = const_cast<uint8_t *>(static_cast<const uint8_t *>(ckpt));
+  P.simg = P.rec + rec_bytes(p);
+  P.yimg = P.simg + bhs(p) * (size_t)(P.N + 1) * kStateImg;
+  P.rimg = static_cast<uint8_t *>(ws);
+  P.uimg = P.rimg + n * kStateImg;
+  P.anchor = reinterpret_cast<float *>(P.uimg + n * kRowImg);
+  P.gx = P.anchor + n * 8;
+  P.dbeta = dbeta;
+  P.in = d_final;
+  P.out = dinit;
+  cudaError_t e = allow_smem(delta_reverse_kernel, kChainSmem);
+  if (e == cudaSuccess) e = allow_smem(delta_grad_kernel, kGradSmem);
+  if (e != cudaSuccess) return e;
+  {
+    TimedLaunch t(K_DELTA_REVERSE, s);
+    e = launch_overlapped(delta_reverse_kernel, dim3((unsigned)bhs(p)), dim3(kChainThreads), kChainSmem, s, mq, mk, mdo,
+                          P);
+    if (e != cudaSuccess) return e;
+  }
+  {
+    TimedLaunch t(K_DELTA_GRAD, s);
+    e = launch_overlapped(delta_grad_kernel, dim3(P.N, (unsigned)bhs(p)), dim3(kGradThreads), kGradSmem, s, mq, mk, mdo,
+                          mdq, mdk, mdv, P);
+    if (e != cudaSuccess) return e;
+  }
+  return dlg ? delta_gate_sums(p, P.gx, P.anchor, 8, dlg, g.f32, s) : cudaSuccess;
+}
+
+}  // namespace linattn
