@@ -278,8 +278,7 @@ __global__ void __launch_bounds__(kWalkThreads)
 
 // d_log_gate: the sums of G from every token to its chunk's end, plus the chunk's anchor.
 // One warp per chunk of 64 tokens.
-__global__ void delta_gate_grad(int64_t BH, int T, int N, const float *gx, const float *anchor, int parts,
-                                void *dlg, int f32) {
+__global__ void delta_gate_grad(int64_t BH, int T, int N, const float *gx, const float *anchor, void *dlg, int f32) {
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
   const int lane = threadIdx.x % 32;
   if (w >= BH * N) return;
@@ -292,7 +291,7 @@ __global__ void delta_gate_grad(int64_t BH, int T, int N, const float *gx, const
     const float y = __shfl_down_sync(0xffffffffu, s, o);
     if (lane + o < 32) s += y;
   }
-  for (int i = 0; i < parts; ++i) s += anchor[w * parts + i];
+  s += anchor[w];
   if (t0 < T) st_gate(dlg, bh * T + t0, f32, s);
   if (t0 + 1 < T) st_gate(dlg, bh * T + t0 + 1, f32, s - x0);
 }
@@ -420,19 +419,19 @@ cudaError_t bwd_launch(const Problem &p, const DeltaGates &g, const void *q, con
   if (dlg) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return delta_gate_sums(p, gx, anchor, 1, dlg, g.f32, s);
+    return delta_gate_sums(p, gx, anchor, dlg, g.f32, s);
   }
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t delta_gate_sums(const Problem &p, const float *gx, const float *anchor, int parts, void *dlg, int f32,
+cudaError_t delta_gate_sums(const Problem &p, const float *gx, const float *anchor, void *dlg, int f32,
                             cudaStream_t s) {
   TimedLaunch t(K_DELTA_GATE, s);
   const int64_t BH = (int64_t)p.B * p.H;
   const int N = (p.T + 63) / 64;
-  delta_gate_grad<<<(unsigned)((BH * N + 7) / 8), 256, 0, s>>>(BH, p.T, N, gx, anchor, parts, dlg, f32);
+  delta_gate_grad<<<(unsigned)((BH * N + 7) / 8), 256, 0, s>>>(BH, p.T, N, gx, anchor, dlg, f32);
   return cudaGetLastError();
 }
 

@@ -91,11 +91,11 @@ struct DeltaTcParams {
   int f32;                 // type of the gates
   const void *lg, *beta;
   uint8_t *rec;            // [BH][N] records
-  uint8_t *simg, *yimg;    // [BH][N + 1] images of S^T, [BH][N] images of Y^T (or null: not kept)
+  uint8_t *simg, *yimg;    // [BH][N] images of S^T entering the chunks, of Y^T (or null: not kept)
   uint8_t *rimg, *uimg;    // backward: [BH][N] images of R^T and of dU^T
   const float *in;         // initial state, or the final state's gradient (or null)
   float *out;              // final state, or the initial state's gradient (or null)
-  float *anchor;           // backward: [BH][N][8] parts of <R, S> at the chunks' ends
+  float *anchor;           // backward: [BH][N] <R, S> at the chunks' ends
   float *gx;               // backward: [BH][T]
   void *dbeta;
   int *status;
@@ -455,18 +455,34 @@ __device__ __forceinline__ void chain_drain(const ChainCtx &k, int n, int ng) {
 }
 
 // 32 fp32 values (as bits) to 16 + 16 words of hi and lo parts in tensor memory
-__device__ __forceinline__ void store_split(const float (&x)[32], uint32_t hi_addr, uint32_t lo_addr, uint32_t (&hi)[16]) {
-  uint32_t lo[16];
+__device__ __forceinline__ void store_split(const float (&x)[32], uint32_t hi_addr, uint32_t lo_addr) {
+  uint32_t hi[16], lo[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
   tmem_st16(hi_addr, hi);
   tmem_st16(lo_addr, lo);
 }
-// 16 packed words of row r, pieces c0 .. c0 + 3 of a swizzled block in global memory
+// 16 packed words of row r, pieces c0 .. c0 + 3 (c0 a multiple of 4) of a swizzled block in global
+// memory, as two 32-byte stores: the swizzle moves pairs of pieces and, in odd rows, swaps a pair.
 __device__ __forceinline__ void store_row(uint8_t *block, uint32_t r, uint32_t c0, const uint32_t (&w)[16]) {
+  const bool odd = r & 1u;
 #pragma unroll
-  for (uint32_t c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4 *>(block + sw(r, c0 + c)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  for (uint32_t m = 0; m < 2; ++m) {
+    uint8_t *dst = block + r * 128u + ((((c0 >> 1) + m) ^ ((r & 7u) >> 1)) << 5);
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = odd ? w[8 * m + 4 + e] : w[8 * m + e];
+      v[4 + e] = odd ? w[8 * m + e] : w[8 * m + 4 + e];
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  }
+}
+__device__ __forceinline__ void pack16(const float (&x)[32], uint32_t (&w)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
 }
 
 // Tensor memory of the forward chain (columns): S^T accumulator, its hi and lo parts, Y^T, the two
@@ -529,6 +545,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       chain_drain(k, n, ng);
     }
   } else if (warp == 1) {
+    // the chain's own products, in the order of its dependences
     const uint32_t id_vt = idesc_bf16(128, 64, true, false), id_64 = idesc_bf16(128, 64, false, false),
                    id_k = idesc_bf16(128, 128, false, true);
     auto vt = [&](int c) {  // Y^T = V^T T^T
@@ -549,7 +566,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     for (int c = 0; c < P.N && ok; ++c) {
       const int n = 7 * c;
       // Y^T += S^T W^T: hi hi, hi lo, lo hi
-      if (!(ok = k.wait_w(C_OP, c) && k.full(n + 2) && k.full(n + 3))) break;
+      if (!(ok = k.full(n + 2) && k.full(n + 3) && k.wait_w(C_OP, c))) break;
       tc_fence_after();
 #pragma unroll
       for (uint32_t p = 0; p < 3; ++p)
@@ -560,19 +577,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       mma_commit_warp(&bar[C_YFULL]);
       k.release(n + 2);
       k.release(n + 3);
-      // O^T = S^T Q^T
-      if (!(ok = (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.full(n + 4))) break;
-      tc_fence_after();
-#pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks)
-          mma_ts_warp(tmem + kTO, tmem + kTSop + p * 64 + ks * 8, desc_kmajor_h(k.slot(n + 4), ks, 8192), id_64,
-                      p + ks > 0);
-      mma_commit_warp(&bar[C_QS]);
-      k.release(n + 4);
       // S^T += Y^T diag(phi b) K
-      if (!(ok = k.wait_w(C_YOP, c) && k.wait_w(C_SCALED, c) && k.full(n + 5))) break;
+      if (!(ok = k.full(n + 5) && k.wait_w(C_SCALED, c) && k.wait_w(C_YOP, c))) break;
       tc_fence_after();
 #pragma unroll
       for (uint32_t p = 0; p < 2; ++p)
@@ -582,8 +588,27 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       mma_commit_warp(&bar[C_ACC]);
       k.release(n + 5);
       if (c + 1 < P.N && !(ok = vt(c + 1))) break;
+    }
+  } else if (warp == 2) {
+    // the output's products, put into the gaps that the chain leaves the tensor cores: Q S while the
+    // threads turn Y into operands, the other while they turn S into operands
+    const uint32_t id_64 = idesc_bf16(128, 64, false, false);
+    bool ok = true;
+    for (int c = 0; c < P.N && ok; ++c) {
+      const int n = 7 * c;
+      // O^T = S^T Q^T
+      if (!(ok = k.full(n + 4) && (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.wait_w(C_YFULL, c))) break;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t p = 0; p < 2; ++p)
+#pragma unroll
+        for (uint32_t ks = 0; ks < 8; ++ks)
+          mma_ts_warp(tmem + kTO, tmem + kTSop + p * 64 + ks * 8, desc_kmajor_h(k.slot(n + 4), ks, 8192), id_64,
+                      p + ks > 0);
+      mma_commit_warp(&bar[C_QS]);
+      k.release(n + 4);
       // O^T (scaled) += Y^T diag(b) P^T
-      if (!(ok = k.wait_w(C_UOP, c) && k.wait_w(C_OSC, c) && k.full(n + 6))) break;
+      if (!(ok = k.full(n + 6) && k.wait_w(C_UOP, c) && k.wait_w(C_OSC, c) && k.wait_w(C_ACC, c))) break;
       tc_fence_after();
 #pragma unroll
       for (uint32_t p = 0; p < 3; ++p)
@@ -615,7 +640,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         tmem_ld32(t + kTS + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[1]));
         tmem_ld_wait();
       }
-      uint8_t *img = P.simg ? P.simg + ((int64_t)bh * (P.N + 1) + c) * kStateImg + hf * 16384 : nullptr;
+      uint8_t *img = P.simg && c < P.N ? P.simg + ((int64_t)bh * P.N + c) * kStateImg + hf * 16384 : nullptr;
       if (c == P.N) {
         if (P.out && (int)row < P.d)
 #pragma unroll
@@ -625,22 +650,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
               const int dk = 64 * hf + 32 * x + j;
               if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[x][j];
             }
-        if (img)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            uint32_t hi[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(s[x][2 * j], s[x][2 * j + 1]);
-            store_row(img, row, 4 * x, hi);
-          }
         break;
       }
+      if (c > 0 && !(ok = k.wait_w(C_QS, c - 1))) break;  // Q S of the last chunk has read the operand
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t hi[16];
-        store_split(s[x], t + kTSop + 32 * hf + 16 * x, t + kTSop + 64 + 32 * hf + 16 * x, hi);
-        if (img) store_row(img, row, 4 * x, hi);
-      }
+      for (int x = 0; x < 2; ++x)
+        store_split(s[x], t + kTSop + 32 * hf + 16 * x, t + kTSop + 64 + 32 * hf + 16 * x);
       tmem_st_wait();
       k.arrive(C_OP, lane);
       if (!(ok = k.wait_w(C_GFULL + c % kGateRing, c / kGateRing))) break;
@@ -648,17 +663,24 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const float f = g[63];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
+        float w[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[x][j] *= f;
-        tmem_st32(t + kTS + 64 * hf + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&s[x]));
+        for (int j = 0; j < 32; ++j) w[j] = s[x][j] * f;
+        tmem_st32(t + kTS + 64 * hf + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&w));
       }
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
+      if (img)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t w[16];
+          pack16(s[x], w);
+          store_row(img, row, 4 * x, w);
+        }
       // Y^T: tokens 32 hf .. + 31 of this lane
       if (!(ok = k.wait_w(C_YFULL, c))) break;
       tc_fence_after();
       float y[32], u[32];
-      uint32_t hi[16];
       tmem_ld32(t + kTY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&y));
       tmem_ld_wait();
       const float *phi = g + 64 + 32 * hf, *be = g + 128 + 32 * hf;
@@ -667,17 +689,20 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       float v[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = phi[j] * u[j];
-      store_split(v, t + kTUt + 16 * hf, t + kTUt + 32 + 16 * hf, hi);
+      // the last chunk's output product is done: it has read the other operand, and its issuer has seen
+      // that chunk's C_ACC, which the arrival below may lead to complete again
+      if (c > 0 && !(ok = k.wait_w(C_OFULL, c - 1))) break;
+      store_split(v, t + kTUt + 16 * hf, t + kTUt + 32 + 16 * hf);
       tmem_st_wait();
       k.arrive(C_YOP, lane);
-      store_split(u, t + kTU + 16 * hf, t + kTU + 32 + 16 * hf, hi);
+      store_split(u, t + kTU + 16 * hf, t + kTU + 32 + 16 * hf);
       tmem_st_wait();
       k.arrive(C_UOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
       if (P.yimg) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
-        store_row(P.yimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, hi);
+        uint32_t w[16];
+        pack16(y, w);
+        store_row(P.yimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, w);
       }
     }
   } else if (warp >= 12) {
@@ -878,19 +903,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       uint8_t *img = P.rimg + ((int64_t)bh * P.N + c) * kStateImg + hf * 16384;
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t hi[16];
-        store_split(s[y], t + kTRop + 32 * hf + 16 * y, t + kTRop + 64 + 32 * hf + 16 * y, hi);
-        store_row(img, row, 4 * y, hi);
-      }
+      for (int y = 0; y < 2; ++y)
+        store_split(s[y], t + kTRop + 32 * hf + 16 * y, t + kTRop + 64 + 32 * hf + 16 * y);
       tmem_st_wait();
       k.arrive(C_OP, lane);
       if (!(ok = k.wait_w(C_GFULL + x % kGateRing, x / kGateRing))) break;
       const float *g = k.gates(x);
       const float f = g[63];
-      // <R, S> at the chunk's end: the anchor of the log-gates' gradient
-      float dot = 0.f;
-      const uint8_t *simg = P.simg + ((int64_t)bh * (P.N + 1) + c + 1) * kStateImg + hf * 16384;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         float w[32];
@@ -900,29 +919,16 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
-      if (x > 0 || P.in)
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(simg + sw(row, 4 * y + q));
-            dot = fmaf(s[y][8 * q + 0], bf16lo(v.x), dot);
-            dot = fmaf(s[y][8 * q + 1], bf16hi(v.x), dot);
-            dot = fmaf(s[y][8 * q + 2], bf16lo(v.y), dot);
-            dot = fmaf(s[y][8 * q + 3], bf16hi(v.y), dot);
-            dot = fmaf(s[y][8 * q + 4], bf16lo(v.z), dot);
-            dot = fmaf(s[y][8 * q + 5], bf16hi(v.z), dot);
-            dot = fmaf(s[y][8 * q + 6], bf16lo(v.w), dot);
-            dot = fmaf(s[y][8 * q + 7], bf16hi(v.w), dot);
-          }
-#pragma unroll
-      for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) P.anchor[((int64_t)bh * P.N + c) * 8 + warp - 4] = dot;
+      for (int y = 0; y < 2; ++y) {
+        uint32_t w[16];
+        pack16(s[y], w);
+        store_row(img, row, 4 * y, w);
+      }
       // dU^T: tokens 32 hf .. + 31 of this lane
       if (!(ok = k.wait_w(C_YFULL, x))) break;
       tc_fence_after();
       float u[32], v[32];
-      uint32_t hi[16];
       tmem_ld32(t + kTD1 + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&u));
       tmem_ld32(t + kTD2 + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&v));
       tmem_ld_wait();
@@ -932,13 +938,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         u[j] = fmaf(phi[j], v[j], u[j]);
         v[j] = be[j] * u[j];
       }
-      store_split(v, t + kTD + 16 * hf, t + kTD + 32 + 16 * hf, hi);
+      store_split(v, t + kTD + 16 * hf, t + kTD + 32 + 16 * hf);
       tmem_st_wait();
       k.arrive(C_YOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) hi[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
-      store_row(P.uimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, hi);
+      uint32_t w[16];
+      pack16(u, w);
+      store_row(P.uimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, w);
     }
   } else if (warp >= 12) {
     // diag(e^g) dO, transposed into tensor memory
@@ -954,10 +960,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         float v[32];
-        uint32_t hi[16];
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = g[32 * y + j] * ld_shared_bf16(tile + sw_el(32 * y + j, row, 8192));
-        store_split(v, t + kTdO + 16 * y, t + kTdO + 32 + 16 * y, hi);
+        store_split(v, t + kTdO + 16 * y, t + kTdO + 32 + 16 * y);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -993,7 +998,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   __shared__ uint64_t bar[6];
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
-  __shared__ float s_dot[4][kC], s_col[2][kC], s_x[4][kC];
+  __shared__ float s_dot[4][kC], s_col[2][kC], s_x[4][kC], s_rs[8], s_kw[8];
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t quad = warp & 3, hf = warp >> 2, row = quad * 32 + lane;
@@ -1027,7 +1032,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       tma_load_4d(&mdo, &bar[0], smem + kGrKD + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
     }
     mbar_arrive_expect_tx(&bar[1], 32768 + 32768 + 16384);
-    bulk_load(&bar[1], smem + kGrS, P.simg + ((int64_t)bh * (P.N + 1) + c) * kStateImg, 32768);
+    bulk_load(&bar[1], smem + kGrS, P.simg + ((int64_t)bh * P.N + c) * kStateImg, 32768);
     bulk_load(&bar[1], smem + kGrR, P.rimg + ci * kStateImg, 32768);
     for (int x = 0; x < 2; ++x)
       tma_load_4d(&mq, &bar[1], smem + kGrQ + x * 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
@@ -1126,6 +1131,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   }
   if (__syncthreads_and(ok)) {
     tc_fence_after();
+    // <R, S> of the chunk's two states (its end's needs the tokens' writes added: below)
+    {
+      float dot = 0.f;
+#pragma unroll 4
+      for (uint32_t p = 0; p < 8; ++p) {
+        uint32_t u[4], v[4];
+        const uint32_t at = hf * 16384 + sw(row, p);
+        ld_shared_v4(S + at, u[0], u[1], u[2], u[3]);
+        ld_shared_v4(R + at, v[0], v[1], v[2], v[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = fmaf(bf16lo(u[e]), bf16lo(v[e]), fmaf(bf16hi(u[e]), bf16hi(v[e]), dot));
+      }
+#pragma unroll
+      for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) s_rs[warp] = dot;
+    }
     const int i = row & 63;
     const float hi = g[192 + i], lo = g[256 + i];
     const float *be = g + 128 + 32 * hf, *ghi = g + 192 + 32 * hf, *glo = g + 256 + 32 * hf;
@@ -1212,12 +1233,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       tmem_ld32(t + kGdw + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&f));
       tmem_ld32(t + kGGY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&w));
       tmem_ld_wait();
+      float kw = 0.f;  // sum of phi b k^T R y: what the tokens' writes add to <R, S>
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
-        const float v = fmaf(phi[j] * be[j], f[j], w[j]);  // the write part
-        x[j] = fmaf(a[j] - v, ld_shared_bf16(KD + sw_el(32 * hf + j, row, 16384)), x[j]);
+        const float kv = ld_shared_bf16(KD + sw_el(32 * hf + j, row, 16384)), r = phi[j] * be[j] * f[j];
+        const float v = r + w[j];  // the write part
+        kw = fmaf(kv, r, kw);
+        x[j] = fmaf(a[j] - v, kv, x[j]);
         st_shared_u16(R + sw_el(32 * hf + j, row, 8192), a[j] + v);
       }
+#pragma unroll
+      for (int o = 16; o; o /= 2) kw += __shfl_xor_sync(0xffffffffu, kw, o);
+      if (lane == 0) s_kw[warp] = kw;
     }
     s_x[quad][32 * hf + lane] = warp_col_sum(x, lane);
     fence_proxy_async_smem();
@@ -1228,6 +1255,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         tma_store_4d(&mdk, smem + kGrR + y * 8192, 64 * y, kC * c, h, b);
       }
       bulk_commit();
+    } else if (tid == 32) {
+      float rs = 0.f, kw = 0.f;
+      for (int w = 0; w < 8; ++w) {
+        rs += s_rs[w];
+        kw += s_kw[w];
+      }
+      P.anchor[ci] = fmaf(g[63], rs, kw);
     } else if (tid >= 64 && tid < 64 + kC) {
       const int j = tid - 64;
       const int64_t at = (int64_t)bh * P.T + kC * c + j;
@@ -1288,11 +1322,11 @@ bool delta_tc_supported(const Problem &p) { return p.dtype == 0; }
 size_t delta_tc_fwd_ws_bytes(const Problem &p) { return align256(rec_bytes(p)); }
 size_t delta_tc_ckpt_bytes(const Problem &p) {
   if (p.T == 0) return 0;
-  return align256(rec_bytes(p) + bhs(p) * ((size_t)(chunks(p) + 1) * kStateImg + (size_t)chunks(p) * kRowImg));
+  return align256(rec_bytes(p) + bhs(p) * chunks(p) * (kStateImg + kRowImg));
 }
 size_t delta_tc_bwd_ws_bytes(const Problem &p) {
   const size_t n = bhs(p) * chunks(p);
-  return align256(n * (kStateImg + kRowImg + 8 * sizeof(float)) + bhs(p) * p.T * sizeof(float));
+  return align256(n * (kStateImg + kRowImg + sizeof(float)) + bhs(p) * p.T * sizeof(float));
 }
 
 cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
@@ -1304,7 +1338,7 @@ cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, c
   P.rec = static_cast<uint8_t *>(ckpt ? ckpt : ws);
   if (ckpt) {
     P.simg = P.rec + rec_bytes(p);
-    P.yimg = P.simg + bhs(p) * (size_t)(P.N + 1) * kStateImg;
+    P.yimg = P.simg + bhs(p) * (size_t)P.N * kStateImg;
   }
   P.in = init;
   P.out = fin;
@@ -1332,11 +1366,11 @@ cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, c
   const size_t n = bhs(p) * P.N;
   P.rec = const_cast<uint8_t *>(static_cast<const uint8_t *>(ckpt));
   P.simg = P.rec + rec_bytes(p);
-  P.yimg = P.simg + bhs(p) * (size_t)(P.N + 1) * kStateImg;
+  P.yimg = P.simg + bhs(p) * (size_t)P.N * kStateImg;
   P.rimg = static_cast<uint8_t *>(ws);
   P.uimg = P.rimg + n * kStateImg;
   P.anchor = reinterpret_cast<float *>(P.uimg + n * kRowImg);
-  P.gx = P.anchor + n * 8;
+  P.gx = P.anchor + n;
   P.dbeta = dbeta;
   P.in = d_final;
   P.out = dinit;
@@ -1355,7 +1389,7 @@ cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, c
                           mdq, mdk, mdv, P);
     if (e != cudaSuccess) return e;
   }
-  return dlg ? delta_gate_sums(p, P.gx, P.anchor, 8, dlg, g.f32, s) : cudaSuccess;
+  return dlg ? delta_gate_sums(p, P.gx, P.anchor, dlg, g.f32, s) : cudaSuccess;
 }
 
 }  // namespace linattn

@@ -270,9 +270,8 @@ cudaError_t delta_walk_fwd(const Problem &p, const DeltaGates &g, const void *q,
 cudaError_t delta_walk_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
                            const float *init, const float *d_final, const void *ckpt, void *dq, void *dk, void *dv,
                            void *dlg, void *dbeta, float *dinit, void *ws, cudaStream_t s);
-// d_log_gate from the tokens' cumulative log-gate gradients gx [BH][T] and the anchors [BH][ceil(T/64)]
-// (each the sum of `parts` values).
-cudaError_t delta_gate_sums(const Problem &p, const float *gx, const float *anchor, int parts, void *dlg, int f32,
+// d_log_gate from the tokens' cumulative log-gate gradients gx [BH][T] and the anchors [BH][ceil(T/64)].
+cudaError_t delta_gate_sums(const Problem &p, const float *gx, const float *anchor, void *dlg, int f32,
                             cudaStream_t s);
 // The tensor-core path (bf16; delta_tc.cu).  ckpt: NULL, or what the backward reads.
 bool delta_tc_supported(const Problem &p);
