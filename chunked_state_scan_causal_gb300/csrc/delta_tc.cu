@@ -51,10 +51,17 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// a and b as packed bf16 and what is left of them as packed bf16
+// a and b as packed bf16 and what is left of them as packed bf16 (the difference of a pair in one
+// packed instruction)
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
   hi = pack_bf16(a, b);
-  lo = pack_bf16(a - bf16lo(hi), b - bf16hi(hi));
+  float x, y;
+  asm("{\n\t.reg .b64 u, v, m;\n\t"
+      "mov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\tmov.b64 m, {%6, %6};\n\t"
+      "fma.rn.f32x2 u, v, m, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(bf16lo(hi)), "f"(bf16hi(hi)), "f"(-1.f));
+  lo = pack_bf16(x, y);
 }
 // offset of 16-byte piece c (0..7) of row r in a swizzled 64-column block
 __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
@@ -376,9 +383,11 @@ __global__ void __launch_bounds__(kPrepThreads)
 }
 
 // ================================================================== chains
-// Shared by both directions.  Warps: 0 loads, 1 issues the products, 4..11 carry the chain (thread =
-// lane of S^T, half of its columns), 12..15 the output (forward) or the scaled dO (backward).
-constexpr int kChainThreads = 512;
+// Shared by both directions.  Warps: 0 loads, 1 (and 2) issue the products, 4..19 carry the chain
+// (thread = lane of S^T, a quarter of its columns: the threads' own work is on the path from one
+// product to the next, so it is spread thin), 20..23 the output (forward) or the scaled dO (backward).
+constexpr int kChainThreads = 768;
+constexpr int kChainWarps = 16, kSideWarps = 4;
 constexpr int kSlots = 12;                      // ring of 16 KiB tiles, in order of use
 constexpr int kGateRing = 4;
 constexpr uint32_t kChStage = kSlots * kSlot;   // output tile (forward)
@@ -424,10 +433,10 @@ __device__ __forceinline__ void chain_setup(const ChainCtx &k, uint32_t *tslot, 
     *abort_flag = 0;
     for (int i = 0; i < C_COUNT; ++i) {
       int n = 1;
-      if (i >= C_GEMPTY && i < C_GEMPTY + kGateRing) n = 12;
-      if (i == C_OP || i == C_SCALED || i == C_YOP) n = 8;
+      if (i >= C_GEMPTY && i < C_GEMPTY + kGateRing) n = kChainWarps + kSideWarps;
+      if (i == C_OP || i == C_SCALED || i == C_YOP) n = kChainWarps;
       if (i == C_UOP) n = uop;  // the warps that make that operand
-      if (i == C_OSC || i == C_OFREE) n = 4;
+      if (i == C_OSC || i == C_OFREE) n = kSideWarps;
       mbar_init(&k.bar[i], n);
     }
     fence_mbar_init();
@@ -454,35 +463,35 @@ __device__ __forceinline__ void chain_drain(const ChainCtx &k, int n, int ng) {
   }
 }
 
-// 32 fp32 values (as bits) to 16 + 16 words of hi and lo parts in tensor memory
-__device__ __forceinline__ void store_split(const float (&x)[32], uint32_t hi_addr, uint32_t lo_addr) {
-  uint32_t hi[16], lo[16];
+// 32 (16) fp32 values to words of hi and lo parts in tensor memory; hi returns the former
+__device__ __forceinline__ void store_split(const float (&x)[32], uint32_t hi_addr, uint32_t lo_addr, uint32_t (&hi)[16]) {
+  uint32_t lo[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
   tmem_st16(hi_addr, hi);
   tmem_st16(lo_addr, lo);
 }
-// 16 packed words of row r, pieces c0 .. c0 + 3 (c0 a multiple of 4) of a swizzled block in global
-// memory, as two 32-byte stores: the swizzle moves pairs of pieces and, in odd rows, swaps a pair.
-__device__ __forceinline__ void store_row(uint8_t *block, uint32_t r, uint32_t c0, const uint32_t (&w)[16]) {
-  const bool odd = r & 1u;
+__device__ __forceinline__ void store_split(const float (&x)[16], uint32_t hi_addr, uint32_t lo_addr) {
+  uint32_t hi[8], lo[8];
 #pragma unroll
-  for (uint32_t m = 0; m < 2; ++m) {
-    uint8_t *dst = block + r * 128u + ((((c0 >> 1) + m) ^ ((r & 7u) >> 1)) << 5);
-    uint32_t v[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = odd ? w[8 * m + 4 + e] : w[8 * m + e];
-      v[4 + e] = odd ? w[8 * m + e] : w[8 * m + 4 + e];
-    }
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  }
+  for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
+  tmem_st8(hi_addr, hi);
+  tmem_st8(lo_addr, lo);
 }
-__device__ __forceinline__ void pack16(const float (&x)[32], uint32_t (&w)[16]) {
+// 8 packed words of row r, pieces 2 m and 2 m + 1 of a swizzled block in global memory, as one 32-byte
+// store: the swizzle moves pairs of pieces and, in odd rows, swaps a pair.
+__device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t m, const uint32_t *w) {
+  const bool odd = r & 1u;
+  uint8_t *dst = block + r * 128u + ((m ^ ((r & 7u) >> 1)) << 5);
+  uint32_t v[8];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+  for (int e = 0; e < 4; ++e) {
+    v[e] = odd ? w[4 + e] : w[e];
+    v[4 + e] = odd ? w[e] : w[4 + e];
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Tensor memory of the forward chain (columns): S^T accumulator, its hi and lo parts, Y^T, the two
@@ -500,7 +509,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const ChainCtx k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int bh = blockIdx.x, b = bh / P.H, h = bh % P.H;
-  chain_setup(k, tslot, &abort_flag, warp, 8);
+  chain_setup(k, tslot, &abort_flag, warp, kChainWarps);
   const uint32_t tmem = *tslot;
   griddep_wait();
   const uint8_t *rec0 = P.rec + (int64_t)bh * P.N * kRecBytes;
@@ -619,137 +628,132 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       mma_commit_warp(&bar[C_OFULL]);
       k.release(n + 6);
     }
-  } else if (warp >= 4 && warp < 12) {
-    const uint32_t quad = warp & 3, hf = (warp - 4) >> 2, row = quad * 32 + lane, lb = (quad * 32) << 16;
-    const uint32_t t = tmem + lb;
+  } else if (warp >= 4 && warp < 4 + kChainWarps) {
+    // lane `row` of S^T, its columns (key dimensions) 32 q4 .. + 31; of Y^T, tokens 16 q4 .. + 15
+    const uint32_t q4 = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
     bool ok = true;
     for (int c = 0; c <= P.N && ok; ++c) {
-      float s[2][32];
+      float s[32];
       if (c == 0) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int dk = 64 * hf + 32 * x + j;
-            s[x][j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
-          }
+        for (int j = 0; j < 32; ++j) {
+          const int dk = 32 * q4 + j;
+          s[j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
+        }
       } else {
-        if (!(ok = k.wait_w(C_ACC, c - 1))) break;
+        // (Q S of the last chunk has read the operand that is rewritten here)
+        if (!(ok = k.wait_w(C_QS, c - 1) && k.wait_w(C_ACC, c - 1))) break;
         tc_fence_after();
-        tmem_ld32(t + kTS + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-        tmem_ld32(t + kTS + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[1]));
+        tmem_ld32(t + kTS + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
         tmem_ld_wait();
       }
-      uint8_t *img = P.simg && c < P.N ? P.simg + ((int64_t)bh * P.N + c) * kStateImg + hf * 16384 : nullptr;
       if (c == P.N) {
         if (P.out && (int)row < P.d)
 #pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int dk = 64 * hf + 32 * x + j;
-              if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[x][j];
-            }
+          for (int j = 0; j < 32; ++j) {
+            const int dk = 32 * q4 + j;
+            if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[j];
+          }
         break;
       }
-      if (c > 0 && !(ok = k.wait_w(C_QS, c - 1))) break;  // Q S of the last chunk has read the operand
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        store_split(s[x], t + kTSop + 32 * hf + 16 * x, t + kTSop + 64 + 32 * hf + 16 * x);
+      uint32_t hi[16];
+      store_split(s, t + kTSop + 16 * q4, t + kTSop + 64 + 16 * q4, hi);
       tmem_st_wait();
       k.arrive(C_OP, lane);
       if (!(ok = k.wait_w(C_GFULL + c % kGateRing, c / kGateRing))) break;
       const float *g = k.gates(c);
       const float f = g[63];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float w[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = s[x][j] * f;
-        tmem_st32(t + kTS + 64 * hf + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&w));
-      }
+      for (int j = 0; j < 32; ++j) s[j] *= f;
+      tmem_st32(t + kTS + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
-      if (img)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t w[16];
-          pack16(s[x], w);
-          store_row(img, row, 4 * x, w);
-        }
-      // Y^T: tokens 32 hf .. + 31 of this lane
-      if (!(ok = k.wait_w(C_YFULL, c))) break;
+      if (P.simg) {
+        uint8_t *img = P.simg + ((int64_t)bh * P.N + c) * kStateImg + (q4 >> 1) * 16384;
+        store_row8(img, row, 2 * (q4 & 1), hi);
+        store_row8(img, row, 2 * (q4 & 1) + 1, hi + 8);
+      }
+      // The last chunk's output product is done: it has read the operand that is rewritten below, and its
+      // issuer has seen that chunk's C_ACC, which the arrival at C_YOP may lead to complete again.
+      if (!(ok = (c == 0 || k.wait_w(C_OFULL, c - 1)) && k.wait_w(C_YFULL, c))) break;
       tc_fence_after();
-      float y[32], u[32];
-      tmem_ld32(t + kTY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&y));
+      float y[16], u[16], v[16];
+      tmem_ld16(t + kTY + 16 * q4, *reinterpret_cast<uint32_t(*)[16]>(&y));
       tmem_ld_wait();
-      const float *phi = g + 64 + 32 * hf, *be = g + 128 + 32 * hf;
+      const float4 *phi = reinterpret_cast<const float4 *>(g + 64 + 16 * q4),
+                   *be = reinterpret_cast<const float4 *>(g + 128 + 16 * q4);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) u[j] = be[j] * y[j];
-      float v[32];
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = phi[j] * u[j];
-      // the last chunk's output product is done: it has read the other operand, and its issuer has seen
-      // that chunk's C_ACC, which the arrival below may lead to complete again
-      if (c > 0 && !(ok = k.wait_w(C_OFULL, c - 1))) break;
-      store_split(v, t + kTUt + 16 * hf, t + kTUt + 32 + 16 * hf);
+      for (int j = 0; j < 4; ++j) {
+        const float4 p = phi[j], b4 = be[j];
+        u[4 * j] = b4.x * y[4 * j];
+        u[4 * j + 1] = b4.y * y[4 * j + 1];
+        u[4 * j + 2] = b4.z * y[4 * j + 2];
+        u[4 * j + 3] = b4.w * y[4 * j + 3];
+        v[4 * j] = p.x * u[4 * j];
+        v[4 * j + 1] = p.y * u[4 * j + 1];
+        v[4 * j + 2] = p.z * u[4 * j + 2];
+        v[4 * j + 3] = p.w * u[4 * j + 3];
+      }
+      store_split(v, t + kTUt + 8 * q4, t + kTUt + 32 + 8 * q4);
       tmem_st_wait();
       k.arrive(C_YOP, lane);
-      store_split(u, t + kTU + 16 * hf, t + kTU + 32 + 16 * hf);
+      store_split(u, t + kTU + 8 * q4, t + kTU + 32 + 8 * q4);
       tmem_st_wait();
       k.arrive(C_UOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
       if (P.yimg) {
-        uint32_t w[16];
-        pack16(y, w);
-        store_row(P.yimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, w);
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+        store_row8(P.yimg + ((int64_t)bh * P.N + c) * kRowImg, row, q4, w);
       }
     }
-  } else if (warp >= 12) {
-    const uint32_t quad = warp & 3, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16);
+  } else if (warp >= 4 + kChainWarps) {
+    const uint32_t row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
     const uint32_t stage = k.base + kChStage;
+    const bool first = threadIdx.x == 32 * (4 + kChainWarps);
     bool ok = true;
     for (int c = 0; c < P.N && ok; ++c) {
-      float o[2][32];
       // one verdict for the four warps, at the barrier below: none is left alone in it
       ok = k.wait_w(C_GFULL + c % kGateRing, c / kGateRing) && k.wait_w(C_QS, c);
       if (ok) {
         tc_fence_after();
         const float *g = k.gates(c);
 #pragma unroll
-        for (int x = 0; x < 2; ++x) tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
-        tmem_ld_wait();
-#pragma unroll
         for (int x = 0; x < 2; ++x) {
+          float o[32];
+          tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o));
+          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[x][j] *= g[32 * x + j];
-          tmem_st32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
+          for (int j = 0; j < 32; ++j) o[j] *= g[32 * x + j];
+          tmem_st32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o));
         }
         tmem_st_wait();
         k.arrive(C_OSC, lane);
         if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
         ok = k.wait_w(C_OFULL, c);
       }
-      if (threadIdx.x == 384) bulk_wait_read_all();  // the previous tile has left the staging buffer
-      if (!(ok = group_all(ok, 2, 128))) break;
+      if (first) bulk_wait_read_all();  // the previous tile has left the staging buffer
+      if (!(ok = group_all(ok, 2, 32 * kSideWarps))) break;
       tc_fence_after();
 #pragma unroll
-      for (int x = 0; x < 2; ++x) tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o[x]));
-      tmem_ld_wait();
-      k.arrive(C_OFREE, lane);
+      for (int x = 0; x < 2; ++x) {
+        float o[32];
+        tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o));
+        tmem_ld_wait();
+        if (x == 1) k.arrive(C_OFREE, lane);
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) st_shared_u16(stage + sw_el(32 * x + j, row, 8192), o[x][j]);
+        for (int j = 0; j < 32; ++j) st_shared_u16(stage + sw_el(32 * x + j, row, 8192), o[j]);
+      }
       fence_proxy_async_smem();
-      named_bar_sync(2, 128);
-      if (threadIdx.x == 384) {
+      named_bar_sync(2, 32 * kSideWarps);
+      if (first) {
         tma_store_4d(&mo, smem + kChStage, 0, kC * c, h, b);
         if (P.d == 128) tma_store_4d(&mo, smem + kChStage + 8192, 64, kC * c, h, b);
         bulk_commit();
       }
     }
-    if (threadIdx.x == 384) bulk_wait_all();
+    if (first) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -771,7 +775,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const ChainCtx k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int bh = blockIdx.x, b = bh / P.H, h = bh % P.H;
-  chain_setup(k, tslot, &abort_flag, warp, 4);
+  chain_setup(k, tslot, &abort_flag, warp, kSideWarps);
   const uint32_t tmem = *tslot;
   griddep_wait();
   const uint8_t *rec0 = P.rec + (int64_t)bh * P.N * kRecBytes;
@@ -869,86 +873,81 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       k.release(n + 5);
       if (x + 1 < P.N && !(ok = pd(x + 1))) break;
     }
-  } else if (warp >= 4 && warp < 12) {
-    const uint32_t quad = warp & 3, hf = (warp - 4) >> 2, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16);
+  } else if (warp >= 4 && warp < 4 + kChainWarps) {
+    const uint32_t q4 = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
     bool ok = true;
     for (int x = 0; x <= P.N && ok; ++x) {
       const int c = P.N - 1 - x;
-      float s[2][32];
+      float s[32];
       if (x == 0) {
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int dk = 64 * hf + 32 * y + j;
-            s[y][j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
-          }
+        for (int j = 0; j < 32; ++j) {
+          const int dk = 32 * q4 + j;
+          s[j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
+        }
       } else {
         if (!(ok = k.wait_w(C_ACC, x - 1))) break;
         tc_fence_after();
-        tmem_ld32(t + kTR + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&s[0]));
-        tmem_ld32(t + kTR + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&s[1]));
+        tmem_ld32(t + kTR + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
         tmem_ld_wait();
       }
       if (x == P.N) {
         if (P.out && (int)row < P.d)
 #pragma unroll
-          for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int dk = 64 * hf + 32 * y + j;
-              if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[y][j];
-            }
+          for (int j = 0; j < 32; ++j) {
+            const int dk = 32 * q4 + j;
+            if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[j];
+          }
         break;
       }
-      uint8_t *img = P.rimg + ((int64_t)bh * P.N + c) * kStateImg + hf * 16384;
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        store_split(s[y], t + kTRop + 32 * hf + 16 * y, t + kTRop + 64 + 32 * hf + 16 * y);
+      uint32_t hi[16];
+      store_split(s, t + kTRop + 16 * q4, t + kTRop + 64 + 16 * q4, hi);
       tmem_st_wait();
       k.arrive(C_OP, lane);
       if (!(ok = k.wait_w(C_GFULL + x % kGateRing, x / kGateRing))) break;
       const float *g = k.gates(x);
       const float f = g[63];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float w[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = s[y][j] * f;
-        tmem_st32(t + kTR + 64 * hf + 32 * y, *reinterpret_cast<uint32_t(*)[32]>(&w));
-      }
+      for (int j = 0; j < 32; ++j) s[j] *= f;
+      tmem_st32(t + kTR + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t w[16];
-        pack16(s[y], w);
-        store_row(img, row, 4 * y, w);
-      }
-      // dU^T: tokens 32 hf .. + 31 of this lane
+      uint8_t *img = P.rimg + ((int64_t)bh * P.N + c) * kStateImg + (q4 >> 1) * 16384;
+      store_row8(img, row, 2 * (q4 & 1), hi);
+      store_row8(img, row, 2 * (q4 & 1) + 1, hi + 8);
+      // dU^T: tokens 16 q4 .. + 15 of this lane
       if (!(ok = k.wait_w(C_YFULL, x))) break;
       tc_fence_after();
-      float u[32], v[32];
-      tmem_ld32(t + kTD1 + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&u));
-      tmem_ld32(t + kTD2 + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&v));
+      float u[16], v[16];
+      tmem_ld16(t + kTD1 + 16 * q4, *reinterpret_cast<uint32_t(*)[16]>(&u));
+      tmem_ld16(t + kTD2 + 16 * q4, *reinterpret_cast<uint32_t(*)[16]>(&v));
       tmem_ld_wait();
-      const float *phi = g + 64 + 32 * hf, *be = g + 128 + 32 * hf;
+      const float4 *phi = reinterpret_cast<const float4 *>(g + 64 + 16 * q4),
+                   *be = reinterpret_cast<const float4 *>(g + 128 + 16 * q4);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        u[j] = fmaf(phi[j], v[j], u[j]);
-        v[j] = be[j] * u[j];
+      for (int j = 0; j < 4; ++j) {
+        const float4 p = phi[j], b4 = be[j];
+        u[4 * j] = fmaf(p.x, v[4 * j], u[4 * j]);
+        u[4 * j + 1] = fmaf(p.y, v[4 * j + 1], u[4 * j + 1]);
+        u[4 * j + 2] = fmaf(p.z, v[4 * j + 2], u[4 * j + 2]);
+        u[4 * j + 3] = fmaf(p.w, v[4 * j + 3], u[4 * j + 3]);
+        v[4 * j] = b4.x * u[4 * j];
+        v[4 * j + 1] = b4.y * u[4 * j + 1];
+        v[4 * j + 2] = b4.z * u[4 * j + 2];
+        v[4 * j + 3] = b4.w * u[4 * j + 3];
       }
-      store_split(v, t + kTD + 16 * hf, t + kTD + 32 + 16 * hf);
+      store_split(v, t + kTD + 8 * q4, t + kTD + 32 + 8 * q4);
       tmem_st_wait();
       k.arrive(C_YOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
-      uint32_t w[16];
-      pack16(u, w);
-      store_row(P.uimg + ((int64_t)bh * P.N + c) * kRowImg, row, 4 * hf, w);
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
+      store_row8(P.uimg + ((int64_t)bh * P.N + c) * kRowImg, row, q4, w);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + kChainWarps) {
     // diag(e^g) dO, transposed into tensor memory
-    const uint32_t quad = warp & 3, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16);
+    const uint32_t row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
     bool ok = true;
     for (int x = 0; x < P.N && ok; ++x) {
       const int n = 6 * x;
@@ -958,19 +957,15 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const float *g = k.gates(x);
       const uint32_t tile = k.slot(n);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        float v[32];
+      for (int y = 0; y < 4; ++y) {
+        float v[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = g[32 * y + j] * ld_shared_bf16(tile + sw_el(32 * y + j, row, 8192));
-        store_split(v, t + kTdO + 16 * y, t + kTdO + 32 + 16 * y);
+        for (int j = 0; j < 16; ++j) v[j] = g[16 * y + j] * ld_shared_bf16(tile + sw_el(16 * y + j, row, 8192));
+        store_split(v, t + kTdO + 8 * y, t + kTdO + 32 + 8 * y);
       }
       tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bar[C_UOP]);
-        mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
-      }
+      k.arrive(C_UOP, lane);
+      if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
     }
   }
   tc_fence_before();
