@@ -118,6 +118,384 @@ __device__ __forceinline__ PagedItem item_of(const PagedProblem &p, int slices, 
   return it;
 }
 
+// The pieces of a CTA's range, in order: next() gives the item and its tiles [t0, t1).
+struct PagedWalk {
+  int64_t x, end, first;
+  int b, slices, items;
+  PagedItem it;
+  int t0, t1, nt, len;
+  __device__ bool next(const PagedProblem &p) {
+    if (x >= end) return false;
+    while (true) {
+      nt = seq_tiles(p, b);
+      if (nt > 0 && x < first + (int64_t)nt * items) break;
+      first += (int64_t)nt * items;
+      ++b;
+    }
+    len = seq_len(p, b);
+    it = item_of(p, slices, b, (int)((x - first) / nt));
+    t0 = (int)((x - first) % nt);
+    t1 = (int)min((int64_t)nt, t0 + end - x);
+    x += t1 - t0;
+    return true;
+  }
+};
+
+// This CTA's walk; false when there is nothing for it.  Called by every thread of the block.
+template <int NT>
+__device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
+  w.slices = (p.Hq / p.Hkv + kHeads - 1) / kHeads;
+  w.items = p.Hkv * w.slices;
+  const int64_t total = locate<NT>(p, w.items, -1, buf, w.b, w.first);
+  const int G = (int)min((int64_t)gridDim.x, total);  // no empty range between two pieces of an item
+  if ((int)blockIdx.x >= G) return false;
+  w.x = range_lo(total, G, blockIdx.x);
+  w.end = range_lo(total, G, blockIdx.x + 1);
+  locate<NT>(p, w.items, w.x, buf, w.b, w.first);
+  return true;
+}
+
+// ------------------------------------------------------------------ bf16 decode (tensor cores)
+// Per tile of 128 tokens, with lane = token and column = query head,
+//     S = K Q^T,   p = 2^(c S - m),   O^T += V^T p^T   (lane = value dimension, column = query head):
+// K and V are the 128-row A operands straight from shared memory, and the (at most 16) query heads the
+// narrow side, so a tile costs 24 small products whatever the number of heads, and the kernel is bound by
+// reading the cache once.  p enters as two bf16 parts, so the weights keep 16 bits.  The reference maximum m
+// moves only when a tile exceeds it by more than 8 (in log2): p stays below 2^8 and O is rescaled rarely.
+// Warps: 0..3 softmax and output, 4 issues the products, 5..12 load: 16-byte asynchronous copies, since a
+// page may have any number of rows and they can fill absent rows with zeros (a slot past the length may
+// hold NaN, and 0 x NaN is NaN).  A ring of six 32 KiB tiles keeps about 130 KB in flight per SM.
+constexpr int kTcThreads = 416, kLoadWarps = 8, kRing = 6, kLag = 4;
+template <int D>
+struct TcLayout {
+  static constexpr uint32_t tile = 128 * D * 2, q = kRing * tile, p = q + kHeads * D * 2,  // P: two buffers of hi, lo
+      end = p + 2 * 2 * 4096;
+  static constexpr size_t smem = end + 1024;
+};
+// Barriers; S, P and O have one per buffer (even and odd tiles), since a role may run a tile ahead of another.
+enum { T_FULL = 0, T_EMPTY = kRing, T_Q = 2 * kRing, T_OFREE, T_S, T_P = T_S + 2, T_O = T_P + 2, T_COUNT = T_O + 2 };
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void st_shared_h(uint32_t addr, float x) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))) : "memory");
+}
+__device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
+
+// HN: query heads handled by the softmax threads (4, 8 or 16; the products are always 16 wide)
+template <int D, int HN>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    paged_decode_tc(PagedProblem p, const __nv_bfloat16 *q, const __nv_bfloat16 *kc, const __nv_bfloat16 *vc,
+                    __nv_bfloat16 *o, float *lse, float *part, float *ml) {
+  using L = TcLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int64_t buf[34];
+  __shared__ uint64_t bar[T_COUNT];
+  __shared__ uint32_t tslot;
+  __shared__ int abort_flag;
+  __shared__ __align__(16) float s_red[HN][4];
+  // by tile, four deep: the loads of tile j follow the value product of tile j - 4
+  __shared__ uint8_t s_valid[4][kTile];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t base = smem_u32(smem);
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar[T_FULL + i], kLoadWarps * 32);
+      mbar_init(&bar[T_EMPTY + i], 1);
+    }
+    mbar_init(&bar[T_Q], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar[T_S + i], 1);
+      mbar_init(&bar[T_P + i], 4);
+      mbar_init(&bar[T_O + i], 1);
+    }
+    mbar_init(&bar[T_OFREE], 4);
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    tmem_alloc(&tslot, 64);
+    tmem_relinquish();
+  }
+  // the P rows of heads that no thread writes
+  for (int i = tid; i < 4 * 4096 / 16; i += kTcThreads) st_shared_v4(base + L::p + 16 * i, 0, 0, 0, 0);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tslot;  // S of the even and odd tiles: columns 0, 16; O^T: 32
+  griddep_wait();
+  griddep_launch_dependents();
+  PagedWalk w;
+  const bool any = walk_start<kTcThreads>(p, buf, w);
+  auto wait = [&](int i, int parity) {
+    return __all_sync(0xffffffffu, mbar_wait(&bar[i], parity & 1, &abort_flag, p.status));
+  };
+  auto wait2 = [&](int which, int tile) { return wait(which + (tile & 1), tile >> 1); };
+  if (!any) {
+  } else if (warp >= 5) {
+    // ------------------------------------------------------------ loads
+    const int lt = tid - 160, c = lt % (D / 8), r0 = lt / (D / 8);
+    constexpr int kRows = kLoadWarps * 32 / (D / 8), kIter = kTile / kRows;
+    const bool pow2 = (p.page & (p.page - 1)) == 0;
+    const int shift = 31 - __clz(p.page);
+    int n = 0, done = 0;
+    bool ok = true;
+    auto arrive = [&](int i) {
+      fence_proxy_async_smem();
+      mbar_arrive(&bar[T_FULL + i % kRing]);
+    };
+    while (ok && w.next(p)) {
+      const int *row = p.table + (int64_t)w.b * p.tstride;
+      const int64_t head = w.it.hk * p.csh + 8 * c;
+      for (int t = w.t0; t < w.t1 && ok; ++t) {
+        int64_t off[kIter];
+        uint32_t in = 0;
+#pragma unroll
+        for (int j = 0; j < kIter; ++j) {
+          const int tok = t * kTile + r0 + j * kRows;
+          const int block = pow2 ? tok >> shift : tok / p.page;
+          int id = -1;
+          if (tok < w.len) {
+            id = row[block];
+            if (id < 0 || id >= p.pages) {
+              report_error(p.status, -1);
+              id = -1;
+            }
+          }
+          in |= (id >= 0 ? 1u : 0u) << j;
+          off[j] = id >= 0 ? id * p.csb + (tok - block * p.page) * p.cst + head : 0;
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int s = n % kRing;
+          if (n >= kRing && !(ok = wait(T_EMPTY + s, n / kRing - 1))) break;
+          const uint32_t dst = base + s * L::tile + (c >> 3) * 16384;
+          const __nv_bfloat16 *src = kv ? vc : kc;
+#pragma unroll
+          for (int j = 0; j < kIter; ++j)
+            cp_async16(dst + swz(r0 + j * kRows, c & 7), src + off[j], in >> j & 1);
+          if (kv == 0 && c == 0)
+#pragma unroll
+            for (int j = 0; j < kIter; ++j) s_valid[n / 2 % 4][r0 + j * kRows] = in >> j & 1;
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (n >= kLag) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
+            arrive(done++);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    while (done < n) arrive(done++);
+  } else if (warp == 4) {
+    // ------------------------------------------------------------ products
+    const uint32_t id_qk = idesc_bf16(128, 16, false, false), id_pv = idesc_bf16(128, 16, true, false);
+    int i = 0, seg = 0;  // tiles whose S is issued; pieces
+    bool ok = true;
+    auto qk = [&](int t) {
+      const int s = (2 * t) % kRing;
+      if (!wait(T_FULL + s, 2 * t / kRing)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (uint32_t ks = 0; ks < D / 16; ++ks)
+        mma_ss_warp(tmem + (t & 1) * 16, desc_kmajor(base + s * L::tile, ks), desc_kmajor_h(base + L::q, ks, 2048), id_qk,
+                    ks > 0);
+      mma_commit_warp(&bar[T_S + (t & 1)]);
+      mma_commit_warp(&bar[T_EMPTY + s]);
+      return true;
+    };
+    for (; ok && w.next(p); ++seg) {
+      if (!(ok = wait(T_Q, seg))) break;  // Q of this piece is in place (and S of the last one read)
+      tc_fence_after();
+      const int n = w.t1 - w.t0;
+      if (!(ok = qk(i))) break;
+      for (int t = 0; t < n && ok; ++t, ++i) {
+        if (t + 1 < n && !(ok = qk(i + 1))) break;
+        const int s = (2 * i + 1) % kRing;
+        if (!(ok = wait(T_FULL + s, (2 * i + 1) / kRing) && wait2(T_P, i) && (t > 0 || seg == 0 || wait(T_OFREE, seg - 1))))
+          break;
+        tc_fence_after();
+        const uint32_t P = base + L::p + (i & 1) * 8192;
+#pragma unroll
+        for (uint32_t x = 0; x < 2; ++x)
+#pragma unroll
+          for (uint32_t ks = 0; ks < 8; ++ks)
+            mma_ss_warp(tmem + 32, desc_mnmajor(base + s * L::tile, ks), desc_kmajor_h(P + x * 4096, ks, 2048), id_pv,
+                        t > 0 || x + ks > 0);
+        mma_commit_warp(&bar[T_O + (i & 1)]);
+        mma_commit_warp(&bar[T_EMPTY + s]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax and output: lane = token, then
+    // lane = value dimension
+    const uint32_t lt = tid, t4 = tmem + ((uint32_t)(warp * 32) << 16);
+    const float c = p.scale * 1.4426950408889634f;
+    int i = 0, slot = 0;
+    bool ok = true;
+    while (ok && w.next(p)) {
+      for (int e = lt; e < kHeads * D / 8; e += 128) {
+        const int h = e / (D / 8), x = e % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (h < w.it.nh) v = *reinterpret_cast<const uint4 *>(q + w.b * p.qsb + (w.it.h0 + h) * p.qsh + 8 * x);
+        st_shared_v4(base + L::q + (x >> 3) * 2048 + swz(h, x & 7), v.x, v.y, v.z, v.w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[T_Q]);
+      float m[HN], l[HN];
+#pragma unroll
+      for (int h = 0; h < HN; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.f;
+      }
+      const int n = w.t1 - w.t0;
+      for (int t = 0; t < n; ++t, ++i) {
+        ok = wait2(T_S, i);
+        // one verdict for the four warps: they share the barriers below
+        if (!(ok = group_all(ok, 1, 128))) break;
+        tc_fence_after();
+        uint32_t r[16];
+        tmem_ld16(t4 + (i & 1) * 16, r);
+        tmem_ld_wait();
+        tc_fence_before();
+        const bool valid = s_valid[i % 4][lt];
+        float x[HN];
+#pragma unroll
+        for (int h = 0; h < HN; ++h) x[h] = valid ? __uint_as_float(r[h]) * c : -INFINITY;
+        {
+          // the warp's maximum of every head: the heads are halved over the lanes
+          float y[HN];
+#pragma unroll
+          for (int h = 0; h < HN; ++h) y[h] = x[h];
+          int h0 = 0, off = 16;
+#pragma unroll
+          for (int z = HN / 2; z >= 1; z /= 2, off /= 2) {
+            const bool up = lane & off;
+#pragma unroll
+            for (int h = 0; h < z; ++h) {
+              const float send = up ? y[h] : y[h + z], keep = up ? y[h + z] : y[h];
+              y[h] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, off));
+            }
+            h0 += up ? z : 0;
+          }
+          for (; off >= 1; off /= 2) y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], off));
+          if (lane % (32 / HN) == 0) s_red[h0][warp] = y[0];
+        }
+        named_bar_sync(1, 128);
+        bool move = false;
+        float f[HN];
+#pragma unroll
+        for (int h = 0; h < HN; ++h) {
+          const float4 v = *reinterpret_cast<const float4 *>(s_red[h]);
+          const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+          f[h] = 1.f;
+          if (mx > m[h] + 8.f) {  // (also the first finite score: m is -inf)
+            f[h] = ex2(m[h] - mx);
+            m[h] = mx;
+            move = true;
+          }
+        }
+        if (move) {
+          // O (lane = value dimension) to the new references; the products into it must be done
+          if (t > 0) {
+            ok = wait2(T_O, i - 1);
+            if (ok) {
+              tc_fence_after();
+              uint32_t a[16];
+              tmem_ld16(t4 + 32, a);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < HN; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * f[h]);
+              tmem_st16(t4 + 32, a);
+              tmem_st_wait();
+              tc_fence_before();
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < HN; ++h) l[h] *= f[h];
+        }
+        // P of two tiles ago has been read
+        if (i >= 2) ok = wait2(T_O, i - 2) && ok;
+        const uint32_t P = base + L::p + (i & 1) * 8192 + (lt >> 6) * 2048 + (lt & 7) * 2;
+#pragma unroll
+        for (int h = 0; h < HN; ++h) {
+          const float e = m[h] == -INFINITY ? 0.f : ex2(x[h] - m[h]);
+          l[h] += e;
+          const uint32_t at = P + swz(h, (lt & 63) >> 3);
+          st_shared_h(at, e);
+          st_shared_h(at + 4096, e - __bfloat162float(__float2bfloat16_rn(e)));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[T_P + (i & 1)]);
+      }
+      if (!ok) break;
+      ok = wait2(T_O, i - 1);
+      if (!(ok = group_all(ok, 1, 128))) break;
+      tc_fence_after();
+      uint32_t a[16];
+      tmem_ld16(t4 + 32, a);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[T_OFREE]);
+      // the sums over all tokens of the piece
+      {
+        float y[HN];
+#pragma unroll
+        for (int h = 0; h < HN; ++h) y[h] = l[h];
+        int h0 = 0, off = 16;
+#pragma unroll
+        for (int z = HN / 2; z >= 1; z /= 2, off /= 2) {
+          const bool up = lane & off;
+#pragma unroll
+          for (int h = 0; h < z; ++h) {
+            const float send = up ? y[h] : y[h + z], keep = up ? y[h + z] : y[h];
+            y[h] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+          }
+          h0 += up ? z : 0;
+        }
+        for (; off >= 1; off /= 2) y[0] += __shfl_xor_sync(0xffffffffu, y[0], off);
+        if (lane % (32 / HN) == 0) s_red[h0][warp] = y[0];
+      }
+      named_bar_sync(1, 128);
+      const bool whole = w.t0 == 0 && w.t1 == w.nt;
+      const int64_t at = (int64_t)(2 * blockIdx.x + slot) * kHeads;
+#pragma unroll
+      for (int h = 0; h < HN; ++h) {
+        if (h >= w.it.nh) break;
+        const float4 v = *reinterpret_cast<const float4 *>(s_red[h]);
+        const float sum = (v.x + v.y) + (v.z + v.w), acc = __uint_as_float(a[h]);
+        if (whole) {
+          if ((int)lt < D)
+            o[w.b * p.qsb + (w.it.h0 + h) * p.qsh + lt] = __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+          if (lse && lt == 0) lse[(int64_t)w.b * p.Hq + w.it.h0 + h] = (m[h] + log2f(sum)) * 0.6931471805599453f;
+        } else {
+          if ((int)lt < D) part[(at + h) * D + lt] = acc;
+          if (lt == 0) {
+            ml[(at + h) * 2] = m[h];
+            ml[(at + h) * 2 + 1] = sum;
+          }
+        }
+      }
+      slot = 1;
+      named_bar_sync(1, 128);  // s_red is rewritten by the next piece
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) tmem_dealloc(tmem, 64);
+}
+
 // ------------------------------------------------------------------ fp32 decode (CUDA cores)
 constexpr int kSub = 64;       // tokens staged at a time
 constexpr int kPagedThreads = 128;
@@ -127,9 +505,10 @@ constexpr size_t paged_simt_smem() {
   return (size_t)(2 * kSub * (D + 4) + kHeads * kSub + kHeads * D + 3 * kHeads) * 4;
 }
 
-template <int D, typename T>
+template <int D>
 __global__ void __launch_bounds__(kPagedThreads)
-    paged_decode_simt(PagedProblem p, const T *q, const T *kc, const T *vc, T *o, float *lse, float *part, float *ml) {
+    paged_decode_simt(PagedProblem p, const float *q, const float *kc, const float *vc, float *o, float *lse, float *part,
+                      float *ml) {
   constexpr int LD = D + 4;
   constexpr int HT = kHeads * D / kPagedThreads;  // heads per thread in the value product
   extern __shared__ float4 smem4[];
@@ -139,31 +518,17 @@ __global__ void __launch_bounds__(kPagedThreads)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = blockIdx.x;
   griddep_wait();
   griddep_launch_dependents();
-  const int slices = (p.Hq / p.Hkv + kHeads - 1) / kHeads, items = p.Hkv * slices;
-  int b;
-  int64_t first;
-  const int64_t total = locate<kPagedThreads>(p, items, -1, buf, b, first);
-  const int G = (int)min((int64_t)gridDim.x, total);  // no empty range between two pieces of an item
-  if (g >= G) return;
-  int64_t x = range_lo(total, G, g);
-  const int64_t end = range_lo(total, G, g + 1);
-  locate<kPagedThreads>(p, items, x, buf, b, first);
+  PagedWalk w;
+  if (!walk_start<kPagedThreads>(p, buf, w)) return;
   const float c = p.scale * 1.4426950408889634f;
   const int dim = tid % D, hbase = (tid / D) * HT;
   int slot = 0;
-  while (x < end) {
-    const int nt = seq_tiles(p, b), len = seq_len(p, b);
-    if (nt == 0 || x >= first + (int64_t)nt * items) {
-      first += (int64_t)nt * items;
-      ++b;
-      continue;
-    }
-    const int i = (int)((x - first) / nt);
-    const PagedItem it = item_of(p, slices, b, i);
-    const int t0 = (int)((x - first) % nt), t1 = (int)min((int64_t)nt, t0 + end - x);
+  while (w.next(p)) {
+    const PagedItem it = w.it;
+    const int b = w.b, t0 = w.t0, t1 = w.t1, len = w.len;
     for (int e = tid; e < kHeads * D; e += kPagedThreads) {
       const int h = e / D;
-      sq[e] = h < it.nh ? (float)q[b * p.qsb + (it.h0 + h) * p.qsh + e % D] * c : 0.f;
+      sq[e] = h < it.nh ? q[b * p.qsb + (it.h0 + h) * p.qsh + e % D] * c : 0.f;
     }
     if (tid < kHeads) {
       sm[tid] = -INFINITY;
@@ -186,8 +551,8 @@ __global__ void __launch_bounds__(kPagedThreads)
         }
         const int64_t off = id * p.csb + it.hk * p.csh + (n % p.page) * p.cst;
         for (int e = lane; e < D; e += 32) {
-          sk[r * LD + e] = id >= 0 ? (float)kc[off + e] : 0.f;
-          sv[r * LD + e] = id >= 0 ? (float)vc[off + e] : 0.f;
+          sk[r * LD + e] = id >= 0 ? kc[off + e] : 0.f;
+          sv[r * LD + e] = id >= 0 ? vc[off + e] : 0.f;
         }
         if (lane < kHeads) sp[lane * kSub + r] = id >= 0 ? 0.f : -INFINITY;
       }
@@ -242,13 +607,13 @@ __global__ void __launch_bounds__(kPagedThreads)
         }
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == nt;
+    const bool whole = t0 == 0 && t1 == w.nt;
 #pragma unroll
     for (int h = 0; h < HT; ++h)
       if (hbase + h < it.nh) {
         const int hh = hbase + h;
         if (whole)
-          o[b * p.qsb + (it.h0 + hh) * p.qsh + dim] = (T)(sl[hh] > 0.f ? acc[h] / sl[hh] : 0.f);
+          o[b * p.qsb + (it.h0 + hh) * p.qsh + dim] = sl[hh] > 0.f ? acc[h] / sl[hh] : 0.f;
         else
           part[((int64_t)(2 * g + slot) * kHeads + hh) * D + dim] = acc[h];
       }
@@ -261,7 +626,6 @@ __global__ void __launch_bounds__(kPagedThreads)
       }
     }
     slot = 1;
-    x += t1 - t0;
     __syncthreads();
   }
 }
@@ -330,30 +694,41 @@ __global__ void __launch_bounds__(D) paged_join_kernel(PagedProblem p, int grid,
   if (lse && tid == 0) lse[(int64_t)b * p.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-int paged_grid(const PagedProblem &p) {
+// CTAs: `per` on each SM, fewer when even the longest possible sequences have fewer tiles.
+int paged_grid(const PagedProblem &p, int per) {
   const int64_t slices = (p.Hq / p.Hkv + kHeads - 1) / kHeads;
   const int64_t tiles = ((int64_t)p.max_blocks * p.page + kTile - 1) / kTile;
-  const int64_t most = tiles * p.B * p.Hkv * slices, want = (int64_t)p.num_sms * 2;
+  const int64_t most = tiles * p.B * p.Hkv * slices, want = (int64_t)p.num_sms * per;
   return (int)(most < want ? most : want);
 }
 
-template <int D, typename T>
-cudaError_t run_simt(const PagedProblem &p, const void *q, const void *kc, const void *vc, void *o, float *lse,
-                     void *ws, cudaStream_t s) {
-  const int G = paged_grid(p);
+template <int D, typename T, typename K>
+cudaError_t run_decode(K kernel, int threads, size_t smem, int per, const PagedProblem &p, const void *q, const void *kc,
+                       const void *vc, void *o, float *lse, void *ws, cudaStream_t s) {
+  const int G = paged_grid(p, per);
   float *part = static_cast<float *>(ws), *ml = part + (size_t)2 * (2 * p.num_sms) * kHeads * D;
-  constexpr size_t smem = paged_simt_smem<D>();
-  cudaError_t e = cudaFuncSetAttribute(paged_decode_simt<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   {
     TimedLaunch t(K_PAGED_DECODE, s);
-    e = launch_overlapped(paged_decode_simt<D, T>, dim3(G), dim3(kPagedThreads), smem, s, p, (const T *)q,
-                          (const T *)kc, (const T *)vc, (T *)o, lse, part, ml);
+    e = launch_overlapped(kernel, dim3(G), dim3(threads), smem, s, p, (const T *)q, (const T *)kc, (const T *)vc,
+                          (T *)o, lse, part, ml);
     if (e != cudaSuccess) return e;
   }
   TimedLaunch t(K_PAGED_JOIN, s);
   return launch_overlapped(paged_join_kernel<D, T>, dim3(p.B * p.Hq), dim3(D), 0, s, p, G, (T *)o, lse,
                            (const float *)part, (const float *)ml);
+}
+
+template <int D>
+cudaError_t run_dim(const PagedProblem &p, const void *q, const void *kc, const void *vc, void *o, float *lse, void *ws,
+                    cudaStream_t s) {
+  if (p.esz == 4)
+    return run_decode<D, float>(paged_decode_simt<D>, kPagedThreads, paged_simt_smem<D>(), 2, p, q, kc, vc, o, lse, ws,
+                                s);
+  const int group = p.Hq / p.Hkv;
+  auto kernel = group <= 4 ? paged_decode_tc<D, 4> : group <= 8 ? paged_decode_tc<D, 8> : paged_decode_tc<D, 16>;
+  return run_decode<D, __nv_bfloat16>(kernel, kTcThreads, TcLayout<D>::smem, 1, p, q, kc, vc, o, lse, ws, s);
 }
 
 }  // namespace
@@ -375,10 +750,7 @@ cudaError_t paged_append(const PagedProblem &p, const void *k, const void *v, vo
 
 cudaError_t paged_decode(const PagedProblem &p, const void *q, const void *kc, const void *vc, void *o, float *lse,
                          void *ws, cudaStream_t s) {
-  if (p.esz == 4)
-    return p.d == 64 ? run_simt<64, float>(p, q, kc, vc, o, lse, ws, s) : run_simt<128, float>(p, q, kc, vc, o, lse, ws, s);
-  return p.d == 64 ? run_simt<64, __nv_bfloat16>(p, q, kc, vc, o, lse, ws, s)
-                   : run_simt<128, __nv_bfloat16>(p, q, kc, vc, o, lse, ws, s);
+  return p.d == 64 ? run_dim<64>(p, q, kc, vc, o, lse, ws, s) : run_dim<128>(p, q, kc, vc, o, lse, ws, s);
 }
 
 }  // namespace linattn
