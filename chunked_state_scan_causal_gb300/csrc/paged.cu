@@ -64,46 +64,32 @@ __device__ __forceinline__ int seq_tiles(const PagedProblem &p, int b) { return 
 __device__ __forceinline__ int64_t range_lo(int64_t total, int G, int g) { return total * g / G; }
 __device__ __forceinline__ int range_of(int64_t total, int G, int64_t x) { return (int)(((x + 1) * G - 1) / total); }
 
-// Sum over b < B of tiles, and the sequence holding tile x with its first tile (b = B when x is
-// past the end; x = -1 only sums, the sequence index then limits the sum: tiles before sequence
-// `upto`).  Called by every thread of the block; `buf` holds 34 values.
+// Block-wide scan of the sequences' tiles: returns their sum, and `lo` is the first tile of this thread's
+// sequence b0 + tid (`mine` tiles).  `buf` holds a value per warp.
 template <int NT>
-__device__ int64_t locate(const PagedProblem &p, int items, int64_t x, int64_t *buf, int &b_out, int64_t &first) {
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  int64_t base = 0;
-  if (tid == 0) buf[32] = p.B;
-  __syncthreads();
-  for (int b0 = 0; b0 < p.B; b0 += NT) {
-    const int b = b0 + tid;
-    const int64_t mine = b < p.B ? (int64_t)seq_tiles(p, b) * items : 0;
-    int64_t s = mine;
+__device__ int64_t scan_tiles(const PagedProblem &p, int items, int b0, int64_t *buf, int64_t &lo, int64_t &mine) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, b = b0 + tid;
+  mine = b < p.B ? (int64_t)seq_tiles(p, b) * items : 0;
+  int64_t s = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    if (lane == 31) buf[warp] = s;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-      if (w < warp) before += buf[w];
-      all += buf[w];
-    }
-    const int64_t lo = base + before + s - mine;
-    if (mine > 0 && x >= lo && x < lo + mine) {
-      buf[32] = b;
-      buf[33] = lo;
-    }
-    base += all;
-    __syncthreads();
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
   }
-  b_out = (int)buf[32];
-  first = buf[33];
+  __syncthreads();  // the last scan's values have been read
+  if (lane == 31) buf[warp] = s;
   __syncthreads();
-  return base;
+  int64_t before = 0, all = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += buf[w];
+    all += buf[w];
+  }
+  lo = before + s - mine;
+  return all;
 }
 
-constexpr int kHeads = 16;  // query heads of an item
+constexpr int kHeads = 16;    // query heads of an item
+constexpr int kMaxGrid = 512;  // CTAs of a decode at most
 
 struct PagedItem {
   int b, hk, h0, nh;  // sequence, key head, first query head, query heads
@@ -141,17 +127,30 @@ struct PagedWalk {
   }
 };
 
-// This CTA's walk; false when there is nothing for it.  Called by every thread of the block.
+// This CTA's walk; false when there is nothing for it.  Called by every thread of the block; `buf` holds
+// 34 values.  Up to NT sequences take one scan; more are summed first and scanned again to the range's start.
 template <int NT>
 __device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
   w.slices = (p.Hq / p.Hkv + kHeads - 1) / kHeads;
   w.items = p.Hkv * w.slices;
-  const int64_t total = locate<NT>(p, w.items, -1, buf, w.b, w.first);
+  int64_t lo, mine, total = 0, base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += NT) total += scan_tiles<NT>(p, w.items, b0, buf, lo, mine);
   const int G = (int)min((int64_t)gridDim.x, total);  // no empty range between two pieces of an item
   if ((int)blockIdx.x >= G) return false;
   w.x = range_lo(total, G, blockIdx.x);
   w.end = range_lo(total, G, blockIdx.x + 1);
-  locate<NT>(p, w.items, w.x, buf, w.b, w.first);
+  for (int b0 = 0; b0 < p.B; b0 += NT) {
+    const int64_t all = p.B > NT ? scan_tiles<NT>(p, w.items, b0, buf, lo, mine) : total;
+    if (mine > 0 && w.x >= base + lo && w.x < base + lo + mine) {
+      buf[32] = b0 + threadIdx.x;
+      buf[33] = base + lo;
+    }
+    base += all;
+    if (w.x < base) break;
+  }
+  __syncthreads();
+  w.b = (int)buf[32];
+  w.first = buf[33];
   return true;
 }
 
@@ -162,17 +161,18 @@ __device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
 // narrow side, so a tile costs 24 small products whatever the number of heads, and the kernel is bound by
 // reading the cache once.  p enters as two bf16 parts, so the weights keep 16 bits.  The reference maximum m
 // moves only when a tile exceeds it by more than 8 (in log2): p stays below 2^8 and O is rescaled rarely.
-// Warps: 0..3 softmax and output, 4 issues the products, 5..12 load: 16-byte asynchronous copies, since a
-// page may have any number of rows and they can fill absent rows with zeros (a slot past the length may
-// hold NaN, and 0 x NaN is NaN).  A tile's barrier counts the copies themselves as they land, so all six
-// 32 KiB tiles of the ring can be in flight; the issuing warp then makes them visible to the products.
-// (Waiting for the copies in the loading threads, to signal after that, couples the loads to the products:
-// 0.80 ms at 64 sequences of 16K when signalling four tiles later, 0.54 two tiles later.)
-constexpr int kTcThreads = 416, kLoadWarps = 8, kRing = 6;
+// Even and odd tiles are two streams with an m, a sum and an O of their own, joined at the piece's end, so
+// the softmax of one tile overlaps the products of the next.
+// Warps: 0..3 and 4..7 softmax and output of the even and odd tiles, 8 issues the products, 9..12 load.
+// Pages of a multiple of 8 tokens are loaded by tensor-map copies of up to 128 rows (one lane per copy);
+// other pages by 16-byte asynchronous copies of all four warps, which are slower (a warp moves 512 bytes an
+// instruction: 1.07 ms instead of XXX at 64 sequences of 16K).  Either way the softmax threads clear the
+// value rows of absent tokens: a slot past the length may hold NaN, and 0 x NaN is NaN.
+constexpr int kTcThreads = 416, kLoadWarps = 4, kRing = 6;
 template <int D>
 struct TcLayout {
   static constexpr uint32_t tile = 128 * D * 2, q = kRing * tile, p = q + kHeads * D * 2,  // P: two buffers of hi, lo
-      end = p + 2 * 2 * 4096;
+      x = p + 2 * 2 * 4096, end = x + kHeads * D * 4;  // X: the odd stream's O on its way to the even one's threads
   static constexpr size_t smem = end + 1024;
 };
 // Barriers; S, P and O have one per buffer (even and odd tiles), since a role may run a tile ahead of another.
@@ -183,18 +183,20 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void st_shared_h(uint32_t addr, float x) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))) : "memory");
 }
 __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
 
+// box: rows of a tensor-map copy (0: none, the pages have another size).
 // HN: query heads handled by the softmax threads (4, 8 or 16; the products are always 16 wide)
 template <int D, int HN>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    paged_decode_tc(PagedProblem p, const __nv_bfloat16 *q, const __nv_bfloat16 *kc, const __nv_bfloat16 *vc,
+    paged_decode_tc(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, int box,
+                    PagedProblem p, const __nv_bfloat16 *q, const __nv_bfloat16 *kc, const __nv_bfloat16 *vc,
                     __nv_bfloat16 *o, float *lse, float *part, float *ml) {
   using L = TcLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -203,25 +205,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ uint64_t bar[T_COUNT];
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
-  __shared__ __align__(16) float s_red[HN][4];
+  __shared__ __align__(16) float s_red[2][HN][4];
+  __shared__ float s_m[HN], s_l[HN];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t base = smem_u32(smem);
   if (tid == 0) {
     abort_flag = 0;
     for (int i = 0; i < kRing; ++i) {
-      mbar_init(&bar[T_FULL + i], kLoadWarps * 32);
+      mbar_init(&bar[T_FULL + i], box ? 1 : kLoadWarps * 32);
       mbar_init(&bar[T_EMPTY + i], 1);
     }
-    mbar_init(&bar[T_Q], 4);
+    mbar_init(&bar[T_Q], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar[T_S + i], 1);
       mbar_init(&bar[T_P + i], 4);
       mbar_init(&bar[T_O + i], 1);
     }
-    mbar_init(&bar[T_OFREE], 4);
+    mbar_init(&bar[T_OFREE], 8);
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(&tslot, 64);
     tmem_relinquish();
   }
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tslot;  // S of the even and odd tiles: columns 0, 16; O^T: 32
+  const uint32_t tmem = tslot;  // S of the even and odd tiles: columns 0, 16; their O^T: 32, 48
   griddep_wait();
   griddep_launch_dependents();
   PagedWalk w;
@@ -240,56 +243,90 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(&bar[i], parity & 1, &abort_flag, p.status));
   };
   auto wait2 = [&](int which, int tile) { return wait(which + (tile & 1), tile >> 1); };
-  const bool pow2 = (p.page & (p.page - 1)) == 0;
-  const int shift = 31 - __clz(p.page);
   if (!any) {
-  } else if (warp >= 5) {
+  } else if (warp >= 9) {
     // ------------------------------------------------------------ loads
-    const int lt = tid - 160, c = lt % (D / 8), r0 = lt / (D / 8);
-    constexpr int kRows = kLoadWarps * 32 / (D / 8), kIter = kTile / kRows;
     int n = 0;
     bool ok = true;
-    while (ok && w.next(p)) {
-      const int *row = p.table + (int64_t)w.b * p.tstride;
-      const int64_t head = w.it.hk * p.csh + 8 * c;
-      auto block_of = [&](int tok) { return pow2 ? tok >> shift : tok / p.page; };
-      // the page ids of this thread's rows of a tile, fetched a tile ahead (-1: past the length)
-      int ids[kIter];
-      auto fetch = [&](int t) {
+    if (box && warp == 9) {
+      // lane x < 128 / box: rows x box .. of every tile
+      const int boxes = kTile / box;
+      while (ok && w.next(p)) {
+        const int *row = p.table + (int64_t)w.b * p.tstride;
+        auto fetch = [&](int t) {
+          const int tok = t * kTile + lane * box;
+          return lane < boxes && tok < w.len ? row[tok / p.page] : -1;
+        };
+        int next = fetch(w.t0);
+        for (int t = w.t0; t < w.t1 && ok; ++t) {
+          const int id = next, tok = t * kTile + lane * box;
+          const bool in = id >= 0 && id < p.pages;
+          if (!in && lane < boxes && tok < w.len) report_error(p.status, -1);
+          next = t + 1 < w.t1 ? fetch(t + 1) : -1;
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, in)) * box * D * 2;
 #pragma unroll
-        for (int j = 0; j < kIter; ++j) {
-          const int tok = t * kTile + r0 + j * kRows;
-          ids[j] = tok < w.len ? row[block_of(tok)] : -1;
-        }
-      };
-      fetch(w.t0);
-      for (int t = w.t0; t < w.t1 && ok; ++t) {
-        int64_t off[kIter];
-        uint32_t in = 0;
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int s = n % kRing;
+            if (n >= kRing && !(ok = wait(T_EMPTY + s, n / kRing - 1))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bar[T_FULL + s], bytes);
+            __syncwarp();
+            if (in)
 #pragma unroll
-        for (int j = 0; j < kIter; ++j) {
-          const int tok = t * kTile + r0 + j * kRows, id = ids[j];
-          const bool good = id >= 0 && id < p.pages;
-          if (!good && tok < w.len) report_error(p.status, -1);
-          in |= (good ? 1u : 0u) << j;
-          off[j] = good ? id * p.csb + (tok - block_of(tok) * p.page) * p.cst + head : 0;
-        }
-        if (t + 1 < w.t1) fetch(t + 1);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int s = n % kRing;
-          if (n >= kRing && !(ok = wait(T_EMPTY + s, n / kRing - 1))) break;
-          const uint32_t dst = base + s * L::tile + (c >> 3) * 16384;
-          const __nv_bfloat16 *src = kv ? vc : kc;
-#pragma unroll
-          for (int j = 0; j < kIter; ++j)
-            cp_async16(dst + swz(r0 + j * kRows, c & 7), src + off[j], in >> j & 1);
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&bar[T_FULL + s])) : "memory");
+              for (int x = 0; x < D / 64; ++x)
+                tma_load_4d(kv ? &mv : &mk, &bar[T_FULL + s], smem + s * L::tile + x * 16384 + lane * box * 128, 64 * x,
+                            tok % p.page, w.it.hk, id, kPolicyEvictFirst);
+          }
         }
       }
+      // what is in flight lands before the block ends (a wait with a limit, also after an abort)
+      volatile int no_abort = 0;
+      for (int s = 0; s < kRing; ++s) {
+        const int uses = n > s ? (n - 1 - s) / kRing + 1 : 0;
+        if (uses && lane == 0) mbar_wait(&bar[T_FULL + s], (uses - 1) & 1, &no_abort, p.status);
+      }
+      __syncwarp();
+    } else if (!box) {
+      const int lt = tid - 288, c = lt % (D / 8), r0 = lt / (D / 8);
+      constexpr int kRows = kLoadWarps * 32 / (D / 8), kIter = kTile / kRows;
+      while (ok && w.next(p)) {
+        const int *row = p.table + (int64_t)w.b * p.tstride;
+        const int64_t head = w.it.hk * p.csh + 8 * c;
+        // the page ids of this thread's rows of a tile, fetched a tile ahead (-1: past the length)
+        int ids[kIter];
+        auto fetch = [&](int t) {
+#pragma unroll
+          for (int j = 0; j < kIter; ++j) {
+            const int tok = t * kTile + r0 + j * kRows;
+            ids[j] = tok < w.len ? row[tok / p.page] : -1;
+          }
+        };
+        fetch(w.t0);
+        for (int t = w.t0; t < w.t1 && ok; ++t) {
+          int64_t off[kIter];
+#pragma unroll
+          for (int j = 0; j < kIter; ++j) {
+            const int tok = t * kTile + r0 + j * kRows, id = ids[j];
+            const bool good = id >= 0 && id < p.pages;
+            if (!good && tok < w.len) report_error(p.status, -1);
+            off[j] = good ? id * p.csb + (tok % p.page) * p.cst + head : -1;
+          }
+          if (t + 1 < w.t1) fetch(t + 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int s = n % kRing;
+            if (n >= kRing && !(ok = wait(T_EMPTY + s, n / kRing - 1))) break;
+            const uint32_t dst = base + s * L::tile + (c >> 3) * 16384;
+            const __nv_bfloat16 *src = kv ? vc : kc;
+#pragma unroll
+            for (int j = 0; j < kIter; ++j)
+              if (off[j] >= 0) cp_async16(dst + swz(r0 + j * kRows, c & 7), src + off[j]);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&bar[T_FULL + s])) : "memory");
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ------------------------------------------------------------ products
     const uint32_t id_qk = idesc_bf16(128, 16, false, false), id_pv = idesc_bf16(128, 16, true, false);
     int i = 0, seg = 0;  // tiles whose S is issued; pieces
@@ -297,7 +334,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto qk = [&](int t) {
       const int s = (2 * t) % kRing;
       if (!wait(T_FULL + s, 2 * t / kRing)) return false;
-      fence_proxy_async_smem();  // the tile came by ordinary (asynchronous) copies
+      if (!box) fence_proxy_async_smem();  // the tile came by ordinary (asynchronous) copies
       tc_fence_after();
 #pragma unroll
       for (uint32_t ks = 0; ks < D / 16; ++ks)
@@ -315,17 +352,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int t = 0; t < n && ok; ++t, ++i) {
         if (t + 1 < n && !(ok = qk(i + 1))) break;
         const int s = (2 * i + 1) % kRing;
-        if (!(ok = wait(T_FULL + s, (2 * i + 1) / kRing) && wait2(T_P, i) && (t > 0 || seg == 0 || wait(T_OFREE, seg - 1))))
+        if (!(ok = wait(T_FULL + s, (2 * i + 1) / kRing) && wait2(T_P, i) && (t > 1 || seg == 0 || wait(T_OFREE, seg - 1))))
           break;
-        fence_proxy_async_smem();
+        if (!box) fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t P = base + L::p + (i & 1) * 8192;
 #pragma unroll
         for (uint32_t x = 0; x < 2; ++x)
 #pragma unroll
           for (uint32_t ks = 0; ks < 8; ++ks)
-            mma_ss_warp(tmem + 32, desc_mnmajor(base + s * L::tile, ks), desc_kmajor_h(P + x * 4096, ks, 2048), id_pv,
-                        t > 0 || x + ks > 0);
+            mma_ss_warp(tmem + 32 + (i & 1) * 16, desc_mnmajor(base + s * L::tile, ks),
+                        desc_kmajor_h(P + x * 4096, ks, 2048), id_pv, t > 1 || x + ks > 0);
         mma_commit_warp(&bar[T_O + (i & 1)]);
         mma_commit_warp(&bar[T_EMPTY + s]);
       }
@@ -333,12 +370,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else {
     // ------------------------------------------------------------ softmax and output: lane = token, then
     // lane = value dimension
-    const uint32_t lt = tid, t4 = tmem + ((uint32_t)(warp * 32) << 16);
+    const int gr = warp >> 2;  // stream: tiles i with i % 2 == gr
+    const uint32_t lt = tid & 127, t4 = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = p.scale * 1.4426950408889634f;
-    int i = 0, slot = 0;
+    int i0 = 0, slot = 0;  // tiles of the pieces before
     bool ok = true;
+    // the warp's reductions of HN values over its lanes: the heads are halved over the lanes, so a lane ends
+    // with one head's value; then the four warps' values meet in s_red
+    auto reduce = [&](float (&y)[HN], auto op) {
+      int h0 = 0, off = 16;
+#pragma unroll
+      for (int z = HN / 2; z >= 1; z /= 2, off /= 2) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int h = 0; h < z; ++h) {
+          const float send = up ? y[h] : y[h + z], keep = up ? y[h + z] : y[h];
+          y[h] = op(keep, __shfl_xor_sync(0xffffffffu, send, off));
+        }
+        h0 += up ? z : 0;
+      }
+      for (; off >= 1; off /= 2) y[0] = op(y[0], __shfl_xor_sync(0xffffffffu, y[0], off));
+      if (lane % (32 / HN) == 0) s_red[gr][h0][warp & 3] = y[0];
+    };
     while (ok && w.next(p)) {
-      for (int e = lt; e < kHeads * D / 8; e += 128) {
+      for (int e = tid; e < kHeads * D / 8; e += 256) {
         const int h = e / (D / 8), x = e % (D / 8);
         uint4 v = make_uint4(0, 0, 0, 0);
         if (h < w.it.nh) v = *reinterpret_cast<const uint4 *>(q + w.b * p.qsb + (w.it.h0 + h) * p.qsh + 8 * x);
@@ -355,51 +410,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       const int n = w.t1 - w.t0;
       const int *row = p.table + (int64_t)w.b * p.tstride;
-      // this lane's token of a tile: its page id, fetched a tile ahead (-1: past the length)
+      // this lane's token of a tile: its page id, fetched a tile of the stream ahead (-1: past the length)
       auto fetch = [&](int t) {
         const int tok = (w.t0 + t) * kTile + lt;
-        return t < n && tok < w.len ? row[pow2 ? tok >> shift : tok / p.page] : -1;
+        return t < n && tok < w.len ? row[tok / p.page] : -1;
       };
-      int id = fetch(0);
-      for (int t = 0; t < n; ++t, ++i) {
+      const int tf = (gr ^ i0) & 1;  // the stream's first tile of the piece
+      int id = fetch(tf), last = -1;
+      for (int t = tf; t < n; t += 2) {
+        const int i = i0 + t;
         const bool valid = id >= 0 && id < p.pages;
-        id = fetch(t + 1);
+        id = fetch(t + 2);
+        last = i;
         ok = wait2(T_S, i);
+        // P of the stream's tile before has been read; its product into O is done
+        if (i >= 2) ok = wait2(T_O, i - 2) && ok;
         // one verdict for the four warps: they share the barriers below
-        if (!(ok = group_all(ok, 1, 128))) break;
+        if (!(ok = group_all(ok, 1 + gr, 128))) break;
         tc_fence_after();
         uint32_t r[16];
-        tmem_ld16(t4 + (i & 1) * 16, r);
+        tmem_ld16(t4 + gr * 16, r);
         tmem_ld_wait();
         tc_fence_before();
-        float x[HN];
+        float x[HN], y[HN];
 #pragma unroll
-        for (int h = 0; h < HN; ++h) x[h] = valid ? __uint_as_float(r[h]) * c : -INFINITY;
-        {
-          // the warp's maximum of every head: the heads are halved over the lanes
-          float y[HN];
-#pragma unroll
-          for (int h = 0; h < HN; ++h) y[h] = x[h];
-          int h0 = 0, off = 16;
-#pragma unroll
-          for (int z = HN / 2; z >= 1; z /= 2, off /= 2) {
-            const bool up = lane & off;
-#pragma unroll
-            for (int h = 0; h < z; ++h) {
-              const float send = up ? y[h] : y[h + z], keep = up ? y[h + z] : y[h];
-              y[h] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, off));
-            }
-            h0 += up ? z : 0;
-          }
-          for (; off >= 1; off /= 2) y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], off));
-          if (lane % (32 / HN) == 0) s_red[h0][warp] = y[0];
-        }
-        named_bar_sync(1, 128);
+        for (int h = 0; h < HN; ++h) y[h] = x[h] = valid ? __uint_as_float(r[h]) * c : -INFINITY;
+        reduce(y, [](float u, float v) { return fmaxf(u, v); });
+        named_bar_sync(1 + gr, 128);
         bool move = false;
         float f[HN];
 #pragma unroll
         for (int h = 0; h < HN; ++h) {
-          const float4 v = *reinterpret_cast<const float4 *>(s_red[h]);
+          const float4 v = *reinterpret_cast<const float4 *>(s_red[gr][h]);
           const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
           f[h] = 1.f;
           if (mx > m[h] + 8.f) {  // (also the first finite score: m is -inf)
@@ -409,27 +451,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
         if (move) {
-          // O (lane = value dimension) to the new references; the products into it must be done
-          if (t > 0) {
-            ok = wait2(T_O, i - 1);
-            if (ok) {
-              tc_fence_after();
-              uint32_t a[16];
-              tmem_ld16(t4 + 32, a);
-              tmem_ld_wait();
+          if (t > tf) {  // O (lane = value dimension) to the new references
+            tc_fence_after();
+            uint32_t a[16];
+            tmem_ld16(t4 + 32 + gr * 16, a);
+            tmem_ld_wait();
 #pragma unroll
-              for (int h = 0; h < HN; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * f[h]);
-              tmem_st16(t4 + 32, a);
-              tmem_st_wait();
-              tc_fence_before();
-            }
+            for (int h = 0; h < HN; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * f[h]);
+            tmem_st16(t4 + 32 + gr * 16, a);
+            tmem_st_wait();
+            tc_fence_before();
           }
 #pragma unroll
           for (int h = 0; h < HN; ++h) l[h] *= f[h];
         }
-        // P of two tiles ago has been read
-        if (i >= 2) ok = wait2(T_O, i - 2) && ok;
-        const uint32_t P = base + L::p + (i & 1) * 8192 + (lt >> 6) * 2048 + (lt & 7) * 2;
+        const uint32_t P = base + L::p + gr * 8192 + (lt >> 6) * 2048 + (lt & 7) * 2;
 #pragma unroll
         for (int h = 0; h < HN; ++h) {
           const float e = m[h] == -INFINITY ? 0.f : ex2(x[h] - m[h]);
@@ -438,66 +474,76 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           st_shared_h(at, e);
           st_shared_h(at + 4096, e - __bfloat162float(__float2bfloat16_rn(e)));
         }
+        if (!__all_sync(0xffffffffu, valid)) {
+          const int s = (2 * i + 1) % kRing;
+          ok = wait(T_FULL + s, (2 * i + 1) / kRing) && ok;
+          if (!valid)
+#pragma unroll
+            for (uint32_t x = 0; x < D / 8; ++x)
+              st_shared_v4(base + s * L::tile + (x >> 3) * 16384 + lt * 128 + (x & 7) * 16, 0, 0, 0, 0);
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[T_P + (i & 1)]);
+        if (lane == 0) mbar_arrive(&bar[T_P + gr]);
       }
-      if (!ok) break;
-      ok = wait2(T_O, i - 1);
-      if (!(ok = group_all(ok, 1, 128))) break;
-      tc_fence_after();
+      i0 += n;
+      if (ok && last >= 0) ok = wait2(T_O, last);
+      if (!(ok = group_all(ok, 3, 256))) break;
       uint32_t a[16];
-      tmem_ld16(t4 + 32, a);
-      tmem_ld_wait();
-      tc_fence_before();
+      if (last >= 0) {
+        tc_fence_after();
+        tmem_ld16(t4 + 32 + gr * 16, a);
+        tmem_ld_wait();
+        tc_fence_before();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[T_OFREE]);
-      // the sums over all tokens of the piece
-      {
-        float y[HN];
-#pragma unroll
-        for (int h = 0; h < HN; ++h) y[h] = l[h];
-        int h0 = 0, off = 16;
-#pragma unroll
-        for (int z = HN / 2; z >= 1; z /= 2, off /= 2) {
-          const bool up = lane & off;
-#pragma unroll
-          for (int h = 0; h < z; ++h) {
-            const float send = up ? y[h] : y[h + z], keep = up ? y[h + z] : y[h];
-            y[h] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-          }
-          h0 += up ? z : 0;
-        }
-        for (; off >= 1; off /= 2) y[0] += __shfl_xor_sync(0xffffffffu, y[0], off);
-        if (lane % (32 / HN) == 0) s_red[h0][warp] = y[0];
-      }
-      named_bar_sync(1, 128);
-      const bool whole = w.t0 == 0 && w.t1 == w.nt;
-      const int64_t at = (int64_t)(2 * blockIdx.x + slot) * kHeads;
+      // the stream's sums over all tokens of the piece; then the odd stream goes to the even one's threads
+      reduce(l, [](float u, float v) { return u + v; });
+      named_bar_sync(1 + gr, 128);
+      float *X = reinterpret_cast<float *>(smem + L::x);
 #pragma unroll
       for (int h = 0; h < HN; ++h) {
-        if (h >= w.it.nh) break;
-        const float4 v = *reinterpret_cast<const float4 *>(s_red[h]);
-        const float sum = (v.x + v.y) + (v.z + v.w), acc = __uint_as_float(a[h]);
-        if (whole) {
-          if ((int)lt < D)
-            o[w.b * p.qsb + (w.it.h0 + h) * p.qsh + lt] = __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
-          if (lse && lt == 0) lse[(int64_t)w.b * p.Hq + w.it.h0 + h] = (m[h] + log2f(sum)) * 0.6931471805599453f;
-        } else {
-          if ((int)lt < D) part[(at + h) * D + lt] = acc;
+        const float4 v = *reinterpret_cast<const float4 *>(s_red[gr][h]);
+        l[h] = (v.x + v.y) + (v.z + v.w);
+        if (gr == 1) {
+          if ((int)lt < D) X[h * D + lt] = last >= 0 ? __uint_as_float(a[h]) : 0.f;
           if (lt == 0) {
-            ml[(at + h) * 2] = m[h];
-            ml[(at + h) * 2 + 1] = sum;
+            s_m[h] = m[h];
+            s_l[h] = l[h];
+          }
+        }
+      }
+      named_bar_sync(3, 256);
+      if (gr == 0) {
+        const bool whole = w.t0 == 0 && w.t1 == w.nt;
+        const int64_t at = (int64_t)(2 * blockIdx.x + slot) * kHeads;
+#pragma unroll
+        for (int h = 0; h < HN; ++h) {
+          if (h >= w.it.nh) break;
+          const float mx = fmaxf(m[h], s_m[h]), use = mx == -INFINITY ? 0.f : mx;
+          const float f0 = ex2(m[h] - use), f1 = ex2(s_m[h] - use), sum = f0 * l[h] + f1 * s_l[h];
+          const float acc = (last >= 0 ? f0 * __uint_as_float(a[h]) : 0.f) + ((int)lt < D ? f1 * X[h * D + lt] : 0.f);
+          if (whole) {
+            if ((int)lt < D)
+              o[w.b * p.qsb + (w.it.h0 + h) * p.qsh + lt] = __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+            if (lse && lt == 0) lse[(int64_t)w.b * p.Hq + w.it.h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
+          } else {
+            if ((int)lt < D) part[(at + h) * D + lt] = acc;
+            if (lt == 0) {
+              ml[(at + h) * 2] = mx;
+              ml[(at + h) * 2 + 1] = sum;
+            }
           }
         }
       }
       slot = 1;
-      named_bar_sync(1, 128);  // s_red is rewritten by the next piece
+      named_bar_sync(3, 256);  // s_red, X and the odd stream's values are rewritten by the next piece
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) tmem_dealloc(tmem, 64);
+  if (warp == 8) tmem_dealloc(tmem, 64);
 }
 
 // ------------------------------------------------------------------ fp32 decode (CUDA cores)
@@ -679,20 +725,29 @@ __global__ void __launch_bounds__(D) paged_join_kernel(PagedProblem p, int grid,
   const int64_t lo = before + (int64_t)((h / group) * slices + s) * nt, hi = lo + nt;
   const int g0 = range_of(all, G, lo), g1 = range_of(all, G, hi - 1);
   if (g0 == g1) return;  // one CTA held the whole item and has written it
+  // the first piece may be the last of its CTA's range (slot 1); the others begin theirs (slot 0)
+  const int first = range_lo(all, G, g0) < lo;
+  auto at = [&](int g) { return (int64_t)(2 * g + (g == g0 ? first : 0)) * kHeads + hh; };
+  __shared__ float s_f[2 * kMaxGrid], s_w[D / 32];
   float m = -INFINITY;
-  for (int g = g0; g <= g1; ++g) {
-    const int slot = range_lo(all, G, g) < lo;
-    m = fmaxf(m, ml[((int64_t)(2 * g + slot) * kHeads + hh) * 2]);
+  for (int g = g0 + tid; g <= g1; g += D) {
+    const float2 v = *reinterpret_cast<const float2 *>(ml + at(g) * 2);
+    s_f[2 * (g - g0)] = v.x;
+    s_f[2 * (g - g0) + 1] = v.y;
+    m = fmaxf(m, v.x);
   }
+#pragma unroll
+  for (int w = 16; w; w /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  if (tid % 32 == 0) s_w[tid / 32] = m;
+  __syncthreads();
+  for (int w = 0; w < D / 32; ++w) m = fmaxf(m, s_w[w]);
   const float use = m == -INFINITY ? 0.f : m;
   float a = 0.f, l = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int g = g0; g <= g1; ++g) {
-    const int slot = range_lo(all, G, g) < lo;
-    const int64_t at = (int64_t)(2 * g + slot) * kHeads + hh;
-    const float f = exp2f(ml[at * 2] - use);
-    a = fmaf(f, part[at * D + tid], a);
-    l = fmaf(f, ml[at * 2 + 1], l);
+    const float f = exp2f(s_f[2 * (g - g0)] - use);
+    a = fmaf(f, part[at(g) * D + tid], a);
+    l = fmaf(f, s_f[2 * (g - g0) + 1], l);
   }
   o[orow] = (T)(l > 0.f ? a / l : 0.f);
   if (lse && tid == 0) lse[(int64_t)b * p.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
@@ -702,21 +757,17 @@ __global__ void __launch_bounds__(D) paged_join_kernel(PagedProblem p, int grid,
 int paged_grid(const PagedProblem &p, int per) {
   const int64_t slices = (p.Hq / p.Hkv + kHeads - 1) / kHeads;
   const int64_t tiles = ((int64_t)p.max_blocks * p.page + kTile - 1) / kTile;
-  const int64_t most = tiles * p.B * p.Hkv * slices, want = (int64_t)p.num_sms * per;
+  const int64_t most = tiles * p.B * p.Hkv * slices, want = (int64_t)(p.num_sms * per < kMaxGrid ? p.num_sms * per : kMaxGrid);
   return (int)(most < want ? most : want);
 }
 
-template <int D, typename T, typename K>
-cudaError_t run_decode(K kernel, int threads, size_t smem, int per, const PagedProblem &p, const void *q, const void *kc,
-                       const void *vc, void *o, float *lse, void *ws, cudaStream_t s) {
+template <int D, typename T, typename Launch>
+cudaError_t run_decode(Launch launch, int per, const PagedProblem &p, void *o, float *lse, void *ws, cudaStream_t s) {
   const int G = paged_grid(p, per);
   float *part = static_cast<float *>(ws), *ml = part + (size_t)2 * (2 * p.num_sms) * kHeads * D;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   {
     TimedLaunch t(K_PAGED_DECODE, s);
-    e = launch_overlapped(kernel, dim3(G), dim3(threads), smem, s, p, (const T *)q, (const T *)kc, (const T *)vc,
-                          (T *)o, lse, part, ml);
+    cudaError_t e = launch(G, part, ml);
     if (e != cudaSuccess) return e;
   }
   TimedLaunch t(K_PAGED_JOIN, s);
@@ -727,12 +778,40 @@ cudaError_t run_decode(K kernel, int threads, size_t smem, int per, const PagedP
 template <int D>
 cudaError_t run_dim(const PagedProblem &p, const void *q, const void *kc, const void *vc, void *o, float *lse, void *ws,
                     cudaStream_t s) {
-  if (p.esz == 4)
-    return run_decode<D, float>(paged_decode_simt<D>, kPagedThreads, paged_simt_smem<D>(), 2, p, q, kc, vc, o, lse, ws,
-                                s);
+  if (p.esz == 4) {
+    constexpr size_t smem = paged_simt_smem<D>();
+    cudaError_t e = cudaFuncSetAttribute(paged_decode_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return run_decode<D, float>(
+        [&](int G, float *part, float *ml) {
+          return launch_overlapped(paged_decode_simt<D>, dim3(G), dim3(kPagedThreads), smem, s, p, (const float *)q,
+                                   (const float *)kc, (const float *)vc, (float *)o, lse, part, ml);
+        },
+        2, p, o, lse, ws, s);
+  }
+  using bf16 = __nv_bfloat16;
+  // the rows of one copy: the largest power of two up to 128 that divides a page (a copy stays inside a page
+  // and starts on the 8-row pattern of the tile)
+  int box = p.page & -p.page;
+  box = box > kTile ? kTile : box < 8 ? 0 : box;
+  CUtensorMap mk{}, mv{};
+  if (box) {
+    const uint64_t dims[4] = {(uint64_t)D, (uint64_t)p.page, (uint64_t)p.Hkv, (uint64_t)p.pages};
+    const uint64_t strides[3] = {(uint64_t)p.cst * 2, (uint64_t)p.csh * 2, (uint64_t)p.csb * 2};
+    if (!make_tmap_bf16(&mk, kc, dims, strides, box) || !make_tmap_bf16(&mv, vc, dims, strides, box))
+      return cudaErrorInvalidValue;
+  }
   const int group = p.Hq / p.Hkv;
   auto kernel = group <= 4 ? paged_decode_tc<D, 4> : group <= 8 ? paged_decode_tc<D, 8> : paged_decode_tc<D, 16>;
-  return run_decode<D, __nv_bfloat16>(kernel, kTcThreads, TcLayout<D>::smem, 1, p, q, kc, vc, o, lse, ws, s);
+  constexpr size_t smem = TcLayout<D>::smem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return run_decode<D, bf16>(
+      [&](int G, float *part, float *ml) {
+        return launch_overlapped(kernel, dim3(G), dim3(kTcThreads), smem, s, mk, mv, box, p, (const bf16 *)q,
+                                 (const bf16 *)kc, (const bf16 *)vc, (bf16 *)o, lse, part, ml);
+      },
+      1, p, o, lse, ws, s);
 }
 
 }  // namespace
