@@ -158,8 +158,9 @@ __device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
 // Per tile of 128 tokens, with lane = token and column = query head,
 //     S = K Q^T,   p = 2^(c S - m),   O^T += V^T p^T   (lane = value dimension, column = query head):
 // K and V are the 128-row A operands straight from shared memory, and the (at most 16) query heads the
-// narrow side, so a tile costs 24 small products whatever the number of heads, and the kernel is bound by
-// reading the cache once.  p enters as two bf16 parts, so the weights keep 16 bits.  The reference maximum m
+// narrow side, so a tile costs 16 small products whatever the number of heads (each bound by reading its
+// 128-row operand), and the kernel is bound by reading the cache once.  p enters as two bf16 parts side by
+// side (columns 0..15 and 16..31 of O), so the weights keep 16 bits at no extra product.  The reference maximum m
 // moves only when a tile exceeds it by more than 8 (in log2): p stays below 2^8 and O is rescaled rarely.
 // Even and odd tiles are two streams with an m, a sum and an O of their own, joined at the piece's end, so
 // the softmax of one tile overlaps the products of the next.
@@ -171,7 +172,7 @@ __device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
 constexpr int kTcThreads = 416, kLoadWarps = 4, kRing = 6;
 template <int D>
 struct TcLayout {
-  static constexpr uint32_t tile = 128 * D * 2, q = kRing * tile, p = q + kHeads * D * 2,  // P: two buffers of hi, lo
+  static constexpr uint32_t tile = 128 * D * 2, q = kRing * tile, p = q + kHeads * D * 2,  // P: two buffers of 32 rows (hi, lo)
       x = p + 2 * 2 * 4096, end = x + kHeads * D * 4;  // X: the odd stream's O on its way to the even one's threads
   static constexpr size_t smem = end + 1024;
 };
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     fence_mbar_init();
   }
   if (warp == 8) {
-    tmem_alloc(&tslot, 64);
+    tmem_alloc(&tslot, 128);
     tmem_relinquish();
   }
   // the P rows of heads that no thread writes
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tslot;  // S of the even and odd tiles: columns 0, 16; their O^T: 32, 48
+  const uint32_t tmem = tslot;  // S of the even and odd tiles: columns 0, 16; their O^T: 32, 64
   griddep_wait();
   griddep_launch_dependents();
   PagedWalk w;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ products
-    const uint32_t id_qk = idesc_bf16(128, 16, false, false), id_pv = idesc_bf16(128, 16, true, false);
+    const uint32_t id_qk = idesc_bf16(128, 16, false, false), id_pv = idesc_bf16(128, 32, true, false);
     int i = 0, seg = 0;  // tiles whose S is issued; pieces
     bool ok = true;
     auto qk = [&](int t) {
@@ -358,11 +359,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         const uint32_t P = base + L::p + (i & 1) * 8192;
 #pragma unroll
-        for (uint32_t x = 0; x < 2; ++x)
-#pragma unroll
-          for (uint32_t ks = 0; ks < 8; ++ks)
-            mma_ss_warp(tmem + 32 + (i & 1) * 16, desc_mnmajor(base + s * L::tile, ks),
-                        desc_kmajor_h(P + x * 4096, ks, 2048), id_pv, t > 1 || x + ks > 0);
+        for (uint32_t ks = 0; ks < 8; ++ks)
+          mma_ss_warp(tmem + 32 + (i & 1) * 32, desc_mnmajor(base + s * L::tile, ks), desc_kmajor_h(P, ks, 4096), id_pv,
+                      t > 1 || ks > 0);
         mma_commit_warp(&bar[T_O + (i & 1)]);
         mma_commit_warp(&bar[T_EMPTY + s]);
       }
@@ -453,26 +452,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (move) {
           if (t > tf) {  // O (lane = value dimension) to the new references
             tc_fence_after();
-            uint32_t a[16];
-            tmem_ld16(t4 + 32 + gr * 16, a);
-            tmem_ld_wait();
 #pragma unroll
-            for (int h = 0; h < HN; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * f[h]);
-            tmem_st16(t4 + 32 + gr * 16, a);
+            for (int y = 0; y < 2; ++y) {
+              uint32_t a[16];
+              tmem_ld16(t4 + 32 + gr * 32 + 16 * y, a);
+              tmem_ld_wait();
+#pragma unroll
+              for (int h = 0; h < HN; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * f[h]);
+              tmem_st16(t4 + 32 + gr * 32 + 16 * y, a);
+            }
             tmem_st_wait();
             tc_fence_before();
           }
 #pragma unroll
           for (int h = 0; h < HN; ++h) l[h] *= f[h];
         }
-        const uint32_t P = base + L::p + gr * 8192 + (lt >> 6) * 2048 + (lt & 7) * 2;
+        const uint32_t P = base + L::p + gr * 8192 + (lt >> 6) * 4096 + (lt & 7) * 2;
 #pragma unroll
         for (int h = 0; h < HN; ++h) {
           const float e = m[h] == -INFINITY ? 0.f : ex2(x[h] - m[h]);
           l[h] += e;
           const uint32_t at = P + swz(h, (lt & 63) >> 3);
           st_shared_h(at, e);
-          st_shared_h(at + 4096, e - __bfloat162float(__float2bfloat16_rn(e)));
+          st_shared_h(at + 2048, e - __bfloat162float(__float2bfloat16_rn(e)));
         }
         if (!__all_sync(0xffffffffu, valid)) {
           const int s = (2 * i + 1) % kRing;
@@ -491,10 +493,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!(ok = group_all(ok, 3, 256))) break;
       uint32_t a[16];
       if (last >= 0) {
+        uint32_t a1[16];
         tc_fence_after();
-        tmem_ld16(t4 + 32 + gr * 16, a);
+        tmem_ld16(t4 + 32 + gr * 32, a);
+        tmem_ld16(t4 + 48 + gr * 32, a1);
         tmem_ld_wait();
         tc_fence_before();
+#pragma unroll
+        for (int h = 0; h < HN; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) + __uint_as_float(a1[h]));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar[T_OFREE]);
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 64);
+  if (warp == 8) tmem_dealloc(tmem, 128);
 }
 
 // ------------------------------------------------------------------ fp32 decode (CUDA cores)
