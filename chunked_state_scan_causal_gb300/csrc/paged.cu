@@ -167,17 +167,19 @@ __device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
 // Warps: 0..3 and 4..7 softmax and output of the even and odd tiles, 8 issues the products, 9..12 load.
 // Pages of a multiple of 8 tokens are loaded by tensor-map copies of up to 128 rows (one lane per copy);
 // other pages by 16-byte asynchronous copies of all four warps, which are slower (a warp moves 512 bytes an
-// instruction: 1.07 ms instead of XXX at 64 sequences of 16K).  Either way the softmax threads clear the
+// instruction: 1.07 ms instead of 0.36 at 64 sequences of 16K).  Either way the softmax threads clear the
 // value rows of absent tokens: a slot past the length may hold NaN, and 0 x NaN is NaN.
-constexpr int kTcThreads = 416, kLoadWarps = 4, kRing = 6;
+constexpr int kTcThreads = 416, kLoadWarps = 4;
 template <int D>
 struct TcLayout {
-  static constexpr uint32_t tile = 128 * D * 2, q = kRing * tile, p = q + kHeads * D * 2,  // P: two buffers of 32 rows (hi, lo)
+  static constexpr int ring = D == 128 ? 6 : 12;
+  static constexpr uint32_t tile = 128 * D * 2, q = ring * tile, p = q + kHeads * D * 2,  // P: two buffers of 32 rows (hi, lo)
       x = p + 2 * 2 * 4096, end = x + kHeads * D * 4;  // X: the odd stream's O on its way to the even one's threads
   static constexpr size_t smem = end + 1024;
 };
 // Barriers; S, P and O have one per buffer (even and odd tiles), since a role may run a tile ahead of another.
-enum { T_FULL = 0, T_EMPTY = kRing, T_Q = 2 * kRing, T_OFREE, T_S, T_P = T_S + 2, T_O = T_P + 2, T_COUNT = T_O + 2 };
+// The ring's full and empty barriers follow.
+enum { T_Q = 0, T_OFREE, T_S, T_P = T_S + 2, T_O = T_P + 2, T_FULL = T_O + 2 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -203,7 +205,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int64_t buf[34];
-  __shared__ uint64_t bar[T_COUNT];
+  constexpr int kRing = L::ring, T_EMPTY = T_FULL + kRing;
+  __shared__ uint64_t bar[T_EMPTY + kRing];
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
   __shared__ __align__(16) float s_red[2][HN][4];
