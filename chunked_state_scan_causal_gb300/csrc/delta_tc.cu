@@ -8,10 +8,7 @@
 //
 // T, W = -T diag(e^g) K and P do not involve the state, so one kernel forms them for all chunks at
 // once (delta_prep); only Y = T V + W S and the update of S are a chain over the chunks, one CTA per
-// (batch, head) (delta_chain).  The chain keeps everything transposed: lane = value dimension, columns =
-// key dimension or token, so S^T, Y^T and O^T live in tensor memory, each is re-read by the thread that
-// owns its lane, and every product takes S^T or Y^T as the A operand from tensor memory and an
-// untransposed tile from shared memory as B.  The backward runs the same chain in reverse time on R,
+// (batch, head) and slice of value dimensions (delta_chain).  The backward runs the same chain in reverse time on R,
 // the gradient at the state (delta_reverse), and then all gradients chunk by chunk (delta_grad):
 //
 //     dU  = P^T dO + diag(phi) K R,    Z = T^T diag(b) dU  (= dV),
@@ -98,8 +95,8 @@ struct DeltaTcParams {
   int f32;                 // type of the gates
   const void *lg, *beta;
   uint8_t *rec;            // [BH][N] records
-  uint8_t *simg, *yimg;    // [BH][N] images of S^T entering the chunks, of Y^T (or null: not kept)
-  uint8_t *rimg, *uimg;    // backward: [BH][N] images of R^T and of dU^T
+  uint8_t *simg, *yimg;    // [BH][N] images of S entering the chunks, of Y (or null: not kept)
+  uint8_t *rimg, *uimg;    // backward: [BH][N] images of R and of dU
   const float *in;         // initial state, or the final state's gradient (or null)
   float *out;              // final state, or the initial state's gradient (or null)
   float *anchor;           // backward: [BH][N] <R, S> at the chunks' ends
@@ -135,7 +132,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   float *A = reinterpret_cast<float *>(smem + kPrepA), *Ti = reinterpret_cast<float *>(smem + kPrepT);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int c = blockIdx.x, bh = blockIdx.y, b = bh / P.H, h = bh % P.H;
+  const int c = blockIdx.x % P.N, bh = blockIdx.x / P.N, b = bh / P.H, h = bh % P.H;
   uint8_t *rec = P.rec + ((int64_t)bh * P.N + c) * kRecBytes;
 
   if (tid == 0) {
@@ -383,30 +380,43 @@ __global__ void __launch_bounds__(kPrepThreads)
 }
 
 // ================================================================== chains
-// Shared by both directions.  Warps: 0 loads, 1 (and 2) issue the products, 4..19 carry the chain
-// (thread = lane of S^T, a quarter of its columns: the threads' own work is on the path from one
-// product to the next, so it is spread thin), 20..23 the output (forward) or the scaled dO (backward).
-constexpr int kChainThreads = 768;
-constexpr int kChainWarps = 16, kSideWarps = 4;
-constexpr int kSlots = 12;                      // ring of 16 KiB tiles, in order of use
-constexpr int kGateRing = 4;
-constexpr uint32_t kChStage = kSlots * kSlot;   // output tile (forward)
-constexpr uint32_t kChGate = kChStage + kSlot;
-constexpr uint32_t kChBar = kChGate + kGateRing * 2048;
-constexpr size_t kChainSmem = kChBar + 512 + 1024;
-static_assert(kChainSmem <= 231000, "one CTA per SM");
+// One CTA per (batch, head, slice of VS value dimensions): the columns of S are independent given W, K and
+// T, so slices spread a chain over several SMs.  Lanes are key dimensions (S: 128 rows) or tokens (Y, O, dU:
+// 64 rows, lanes 16 q .. 16 q + 15 of every quarter), columns the slice.  What the threads make for the next
+// product (S, Y, R, dU in two bf16 parts, side by side) goes to shared memory as its B operand; both parts
+// of S (R) meet the same A tile in one product of 2 VS columns.
+//
+// A chunk's path is S -> (W S) -> Y -> (K^T Y) -> S: two products and two passes of the threads, each
+// bounded by its latency (reading 64 or 128 operand rows per 16 of the contraction takes 33 to 51 cycles a
+// product whatever the width).  Warps: 0 loads, 1 issues the chain's products, 2 the output's, then
+// 4 VS/16 that carry the chain (16 columns each: the threads' work is on the path, so it is spread thin) and
+// 4 for the output (forward) or the scaled dO (backward).
+constexpr int kGateRing = 4, kSideWarps = 4;
+template <int VS>
+struct Chain {
+  static constexpr int warps = VS / 4, threads = 32 * (4 + warps + kSideWarps), side = 4 + warps;  // first side warp
+  static constexpr int slots = VS == 32 ? 11 : 9;          // ring of 16 KiB tiles, in order of use
+  // operand tiles: rows of hi and lo parts side by side (VS = 32: one 128-byte row; 64: two blocks)
+  static constexpr uint32_t state_lo = VS == 32 ? 64 : 16384, row_lo = VS == 32 ? 64 : 8192;
+  static constexpr uint32_t op = slots * kSlot, u0 = op + 128 * VS * 4, u1 = u0 + 64 * VS * 4,
+                            gate = u1 + 64 * VS * 4, bar = gate + kGateRing * 2048;
+  static constexpr size_t smem = bar + 512 + 1024;
+};
+static_assert(Chain<32>::smem <= 231000 && Chain<64>::smem <= 231000, "one CTA per SM");
 
-enum { C_FULL = 0, C_EMPTY = C_FULL + kSlots, C_GFULL = C_EMPTY + kSlots, C_GEMPTY = C_GFULL + kGateRing,
-       C_OP = C_GEMPTY + kGateRing,   // S^T (R^T) operand parts ready
-       C_SCALED,                      // its accumulator scaled by the chunk's decay
-       C_ACC,                         // its accumulator complete (next chunk)
-       C_YFULL, C_YOP,                // Y^T (dU^T) accumulator complete; its operand for the update ready
-       C_UOP,                         // forward: the operand of the output product ready
-       C_QS, C_OSC, C_OFULL, C_OFREE, // forward: Q S done, scaled; output complete, read
-       C_COUNT };
-static_assert(C_COUNT * 8 + 8 <= 512, "barriers fit");
+enum { C_OP = 0,    // S (R) operand parts ready
+       C_SCALED,    // its accumulator scaled by the chunk's decay
+       C_ACC,       // its accumulator complete (next chunk)
+       C_YFULL,     // Y (K R) accumulator complete
+       C_YOP,       // the operand made from it for the update ready
+       C_UOP,       // forward: its operand for the output ready; backward: the scaled dO
+       C_QS, C_OFULL, C_OFREE,   // forward: Q S done; output complete, read
+       C_GFULL, C_GEMPTY = C_GFULL + kGateRing, C_FULL = C_GEMPTY + kGateRing };
 
+template <int VS>
 struct ChainCtx {
+  using L = Chain<VS>;
+  static constexpr int empty0 = C_FULL + L::slots, count = empty0 + L::slots;
   uint8_t *smem;
   uint64_t *bar;
   volatile int *abort_flag;
@@ -414,73 +424,115 @@ struct ChainCtx {
   uint32_t base;
   __device__ bool wait(int idx, int parity) const { return mbar_wait(&bar[idx], parity & 1, abort_flag, status); }
   __device__ bool wait_w(int idx, int parity) const { return __all_sync(0xffffffffu, wait(idx, parity)); }
-  __device__ uint32_t slot(int n) const { return base + (uint32_t)(n % kSlots) * kSlot; }
-  __device__ bool full(int n) const { return wait_w(C_FULL + n % kSlots, n / kSlots); }
-  __device__ void release(int n) const { mma_commit_warp(&bar[C_EMPTY + n % kSlots]); }
+  __device__ uint32_t slot(int n) const { return base + (uint32_t)(n % L::slots) * kSlot; }
+  __device__ bool full(int n) const { return wait_w(C_FULL + n % L::slots, n / L::slots); }
+  __device__ void release(int n) const { mma_commit_warp(&bar[empty0 + n % L::slots]); }
+  __device__ bool gates_ready(int x) const { return wait_w(C_GFULL + x % kGateRing, x / kGateRing); }
   __device__ const float *gates(int x) const {
-    return reinterpret_cast<const float *>(smem + kChGate + (x % kGateRing) * 2048);
+    return reinterpret_cast<const float *>(smem + L::gate + (x % kGateRing) * 2048);
   }
-  // one arrival per warp, after the warp's tensor-memory accesses
+  // one arrival per warp, after the warp's accesses to tensor and shared memory
   __device__ void arrive(int idx, int lane) const {
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar[idx]);
   }
+  __device__ void setup(uint32_t *tslot, int *abort, int warp, int uop) const {
+    if (threadIdx.x == 0) {
+      *abort = 0;
+      for (int i = 0; i < count; ++i) {
+        int n = 1;
+        if (i >= C_GEMPTY && i < C_GEMPTY + kGateRing) n = L::warps + kSideWarps;
+        if (i == C_OP || i == C_SCALED || i == C_YOP) n = L::warps;
+        if (i == C_UOP) n = uop;  // the warps that make that operand
+        if (i == C_OFREE) n = kSideWarps;
+        mbar_init(&bar[i], n);
+      }
+      fence_mbar_init();
+    }
+    if (warp == 1) {
+      tmem_alloc(tslot, 512);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
 };
 
-__device__ __forceinline__ void chain_setup(const ChainCtx &k, uint32_t *tslot, int *abort_flag, int warp, int uop) {
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < C_COUNT; ++i) {
-      int n = 1;
-      if (i >= C_GEMPTY && i < C_GEMPTY + kGateRing) n = kChainWarps + kSideWarps;
-      if (i == C_OP || i == C_SCALED || i == C_YOP) n = kChainWarps;
-      if (i == C_UOP) n = uop;  // the warps that make that operand
-      if (i == C_OSC || i == C_OFREE) n = kSideWarps;
-      mbar_init(&k.bar[i], n);
+// The loading thread's side of the ring.
+template <int VS>
+struct ChainLoader {
+  const ChainCtx<VS> &k;
+  int h, b, n = 0, ng = 0;
+  bool ok = true;
+  __device__ uint64_t *slot(uint8_t *&dst, uint32_t bytes) {
+    const int s = n % Chain<VS>::slots;
+    if (n >= Chain<VS>::slots && !(ok = ok && k.wait(ChainCtx<VS>::empty0 + s, n / Chain<VS>::slots - 1))) return nullptr;
+    dst = k.smem + s * kSlot;
+    mbar_arrive_expect_tx(&k.bar[C_FULL + s], bytes);
+    ++n;
+    return &k.bar[C_FULL + s];
+  }
+  // a 64 x 128 tile of a sequence tensor, or the 64-column block of it that holds column x
+  __device__ void tile(const CUtensorMap *m, int c) {
+    uint8_t *dst;
+    uint64_t *full = ok ? slot(dst, kSlot) : nullptr;
+    if (!full) return;
+    tma_load_4d(m, full, dst, 0, kC * c, h, b, kPolicyEvictNormal);
+    tma_load_4d(m, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictNormal);
+  }
+  __device__ void block(const CUtensorMap *m, int c, int x) {
+    uint8_t *dst;
+    uint64_t *full = ok ? slot(dst, 8192) : nullptr;
+    if (full) tma_load_4d(m, full, dst, x / 64 * 64, kC * c, h, b, kPolicyEvictNormal);
+  }
+  __device__ void image(const uint8_t *src) {
+    uint8_t *dst;
+    uint64_t *full = ok ? slot(dst, kSlot) : nullptr;
+    if (full) bulk_load(full, dst, src, kSlot);
+  }
+  __device__ bool gates(const uint8_t *src) {
+    const int s = ng % kGateRing;
+    if (ng >= kGateRing && !(ok = k.wait(C_GEMPTY + s, ng / kGateRing - 1))) return false;
+    mbar_arrive_expect_tx(&k.bar[C_GFULL + s], kGateBytes);
+    bulk_load(&k.bar[C_GFULL + s], k.smem + Chain<VS>::gate + s * 2048, src, kGateBytes);
+    ++ng;
+    return true;
+  }
+  // waits for what is in flight, after the last load or an abort
+  __device__ void drain() {
+    volatile int no_abort = 0;
+    for (int s = 0; s < Chain<VS>::slots; ++s) {
+      const int uses = n > s ? (n - 1 - s) / Chain<VS>::slots + 1 : 0;
+      if (uses) mbar_wait(&k.bar[C_FULL + s], (uses - 1) & 1, &no_abort, k.status);
     }
-    fence_mbar_init();
+    for (int s = 0; s < kGateRing; ++s) {
+      const int uses = ng > s ? (ng - 1 - s) / kGateRing + 1 : 0;
+      if (uses) mbar_wait(&k.bar[C_GFULL + s], (uses - 1) & 1, &no_abort, k.status);
+    }
   }
-  if (warp == 1) {
-    tmem_alloc(tslot, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+};
+
+// 16 values of row r, columns 16 g .. + 15 of the slice, as hi and lo parts in an operand tile (`lo`: the
+// offset of the lo parts); hi returns the former, packed
+template <int VS>
+__device__ __forceinline__ void put_split(uint32_t tile, uint32_t lo, uint32_t r, uint32_t g, const float (&x)[16],
+                                          uint32_t (&hi)[8]) {
+  uint32_t l[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], l[j]);
+  // VS = 32: the lo parts are pieces 4 .. 7 of the same 128-byte row
+  const uint32_t row = tile + r * 128u, blk = VS == 32 ? row : row + lo, p = VS == 32 ? 4u : 0u;
+  st_shared_v4(row + (((2 * g) ^ (r & 7u)) << 4), hi[0], hi[1], hi[2], hi[3]);
+  st_shared_v4(row + (((2 * g + 1) ^ (r & 7u)) << 4), hi[4], hi[5], hi[6], hi[7]);
+  st_shared_v4(blk + (((p + 2 * g) ^ (r & 7u)) << 4), l[0], l[1], l[2], l[3]);
+  st_shared_v4(blk + (((p + 2 * g + 1) ^ (r & 7u)) << 4), l[4], l[5], l[6], l[7]);
 }
 
-// The loader's waits for what it has in flight, after the last load or an abort.
-__device__ __forceinline__ void chain_drain(const ChainCtx &k, int n, int ng) {
-  volatile int no_abort = 0;
-  for (int s = 0; s < kSlots; ++s) {
-    const int uses = n > s ? (n - 1 - s) / kSlots + 1 : 0;
-    if (uses) mbar_wait(&k.bar[C_FULL + s], (uses - 1) & 1, &no_abort, k.status);
-  }
-  for (int s = 0; s < kGateRing; ++s) {
-    const int uses = ng > s ? (ng - 1 - s) / kGateRing + 1 : 0;
-    if (uses) mbar_wait(&k.bar[C_GFULL + s], (uses - 1) & 1, &no_abort, k.status);
-  }
-}
-
-// 32 (16) fp32 values to words of hi and lo parts in tensor memory; hi returns the former
-__device__ __forceinline__ void store_split(const float (&x)[32], uint32_t hi_addr, uint32_t lo_addr, uint32_t (&hi)[16]) {
-  uint32_t lo[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-  tmem_st16(hi_addr, hi);
-  tmem_st16(lo_addr, lo);
-}
-__device__ __forceinline__ void store_split(const float (&x)[16], uint32_t hi_addr, uint32_t lo_addr) {
-  uint32_t hi[8], lo[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) split2(x[2 * j], x[2 * j + 1], hi[j], lo[j]);
-  tmem_st8(hi_addr, hi);
-  tmem_st8(lo_addr, lo);
-}
-// 8 packed words of row r, pieces 2 m and 2 m + 1 of a swizzled block in global memory, as one 32-byte
+// 8 packed words (16 columns) of row r, column group m of a swizzled block in global memory, as one 32-byte
 // store: the swizzle moves pairs of pieces and, in odd rows, swaps a pair.
-__device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t m, const uint32_t *w) {
+__device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t m, const uint32_t (&w)[8]) {
   const bool odd = r & 1u;
   uint8_t *dst = block + r * 128u + ((m ^ ((r & 7u) >> 1)) << 5);
   uint32_t v[8];
@@ -494,70 +546,72 @@ __device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t 
                : "memory");
 }
 
-// Tensor memory of the forward chain (columns): S^T accumulator, its hi and lo parts, Y^T, the two
-// operands made from it (hi, lo each), O^T.
-constexpr uint32_t kTS = 0, kTSop = 128, kTY = 256, kTU = 320, kTUt = 384, kTO = 448;
+// 16 columns of a state row in global memory (fp32, row and columns inside d)
+__device__ __forceinline__ void load_state16(const float *p, float (&s)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = p ? reinterpret_cast<const float4 *>(p)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+    s[4 * j] = v.x;
+    s[4 * j + 1] = v.y;
+    s[4 * j + 2] = v.z;
+    s[4 * j + 3] = v.w;
+  }
+}
+__device__ __forceinline__ void store_state16(float *p, const float (&s)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    reinterpret_cast<float4 *>(p)[j] = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+}
+__device__ __forceinline__ void tmem_ldf(uint32_t addr, float (&x)[16]) {
+  tmem_ld16(addr, *reinterpret_cast<uint32_t(*)[16]>(&x));
+}
+__device__ __forceinline__ void tmem_stf(uint32_t addr, const float (&x)[16]) {
+  tmem_st16(addr, *reinterpret_cast<const uint32_t(*)[16]>(&x));
+}
 
-__global__ void __launch_bounds__(kChainThreads, 1)
+// Tensor memory of the forward chain (columns): S; Y (both parts' products); Q S and P Y likewise.
+template <int VS>
+__global__ void __launch_bounds__(Chain<VS>::threads, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo, DeltaTcParams P) {
+                       const __grid_constant__ CUtensorMap mv, __nv_bfloat16 *o, int64_t osb, int64_t osh, int64_t ost,
+                       DeltaTcParams P) {
+  using L = Chain<VS>;
+  constexpr uint32_t kTS = 0, kTY = VS, kTQ = 3 * VS, kTP = 5 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
   uint8_t *smem = align1024(smem_raw);
-  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChBar);
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + C_COUNT);
-  const ChainCtx k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::bar);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + ChainCtx<VS>::count);
+  const ChainCtx<VS> k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int bh = blockIdx.x, b = bh / P.H, h = bh % P.H;
-  chain_setup(k, tslot, &abort_flag, warp, kChainWarps);
+  const int ns = P.d / VS, bh = blockIdx.x / ns, b = bh / P.H, h = bh % P.H;
+  const int x0 = (blockIdx.x % ns) * VS;  // the slice's first value dimension
+  k.setup(tslot, &abort_flag, warp, L::warps);
   const uint32_t tmem = *tslot;
   griddep_wait();
-  const uint8_t *rec0 = P.rec + (int64_t)bh * P.N * kRecBytes;
 
   if (warp == 0) {
     if (lane == 0) {
-      int n = 0, ng = 0, c = 0;
-      bool ok = true;
-      auto slot = [&](uint8_t *&dst, uint64_t *&full) {
-        const int s = n % kSlots;
-        if (n >= kSlots && !(ok = k.wait(C_EMPTY + s, n / kSlots - 1))) return false;
-        dst = smem + s * kSlot;
-        full = &bar[C_FULL + s];
-        mbar_arrive_expect_tx(full, kSlot);
-        ++n;
-        return true;
-      };
-      uint8_t *dst;
-      uint64_t *full;
-      auto seq = [&](const CUtensorMap *m) {
-        if (!slot(dst, full)) return;
-        tma_load_4d(m, full, dst, 0, kC * c, h, b, kPolicyEvictFirst);
-        tma_load_4d(m, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictFirst);
-      };
-      auto img = [&](const uint8_t *src) {
-        if (slot(dst, full)) bulk_load(full, dst, src, kSlot);
-      };
-      for (; c < P.N && ok; ++c) {
-        const uint8_t *rec = rec0 + c * kRecBytes;
-        if (c >= kGateRing && !(ok = k.wait(C_GEMPTY + c % kGateRing, c / kGateRing - 1))) break;
-        mbar_arrive_expect_tx(&bar[C_GFULL + c % kGateRing], kGateBytes);
-        bulk_load(&bar[C_GFULL + c % kGateRing], smem + kChGate + (c % kGateRing) * 2048, rec + kRecG, kGateBytes);
-        ++ng;
-        if (ok) seq(&mv);
-        if (ok) img(rec + kRecT);
-        if (ok) img(rec + kRecW);
-        if (ok) img(rec + kRecW + kSlot);
-        if (ok) seq(&mq);
-        if (ok) seq(&mk);
-        if (ok) img(rec + kRecP);
+      ChainLoader<VS> ld{k, h, b};
+      const uint8_t *rec = P.rec + (int64_t)bh * P.N * kRecBytes;
+      for (int c = 0; c < P.N && ld.ok; ++c, rec += kRecBytes) {
+        if (!ld.gates(rec + kRecG)) break;
+        ld.block(&mv, c, x0);
+        ld.image(rec + kRecT);
+        ld.image(rec + kRecW);
+        ld.image(rec + kRecW + kSlot);
+        ld.tile(&mq, c);
+        ld.tile(&mk, c);
+        ld.image(rec + kRecP);
       }
-      chain_drain(k, n, ng);
+      ld.drain();
     }
   } else if (warp == 1) {
     // the chain's own products, in the order of its dependences
-    const uint32_t id_vt = idesc_bf16(128, 64, true, false), id_64 = idesc_bf16(128, 64, false, false),
-                   id_k = idesc_bf16(128, 128, false, true);
-    auto vt = [&](int c) {  // Y^T = V^T T^T
+    const uint32_t id_1 = idesc_bf16(64, VS, false, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
+                   id_k = idesc_bf16(128, VS, true, true);
+    const uint32_t op = k.base + L::op, ut = k.base + L::u0;
+    auto vt = [&](int c) {  // Y = T V
       const int n = 7 * c;
       if (!k.full(n) || !k.full(n + 1)) return false;
       tc_fence_after();
@@ -565,8 +619,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       for (uint32_t p = 0; p < 2; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kTY, desc_mnmajor_h(k.slot(n), ks, 8192), desc_kmajor(k.slot(n + 1) + p * 8192, ks), id_vt,
-                      p + ks > 0);
+          mma_ss_warp(tmem + kTY, desc_kmajor(k.slot(n + 1) + p * 8192, ks),
+                      desc_mnmajor_h(k.slot(n) + (x0 & 63) * 2, ks, 8192), id_1, p + ks > 0);
       k.release(n);
       k.release(n + 1);
       return true;
@@ -574,256 +628,205 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     bool ok = vt(0);
     for (int c = 0; c < P.N && ok; ++c) {
       const int n = 7 * c;
-      // Y^T += S^T W^T: hi hi, hi lo, lo hi
+      // Y += W S: hi [hi | lo] (2 VS columns), lo hi
       if (!(ok = k.full(n + 2) && k.full(n + 3) && k.wait_w(C_OP, c))) break;
       tc_fence_after();
 #pragma unroll
-      for (uint32_t p = 0; p < 3; ++p)
+      for (uint32_t ks = 0; ks < 8; ++ks)
+        mma_ss_warp(tmem + kTY, desc_kmajor_h(k.slot(n + 2), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_2, 1);
 #pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks)
-          mma_ts_warp(tmem + kTY, tmem + kTSop + (p == 2 ? 64u : 0u) + ks * 8,
-                      desc_kmajor_h(k.slot(n + 2 + (p == 1)), ks, 8192), id_64, 1);
+      for (uint32_t ks = 0; ks < 8; ++ks)
+        mma_ss_warp(tmem + kTY, desc_kmajor_h(k.slot(n + 3), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_1, 1);
       mma_commit_warp(&bar[C_YFULL]);
       k.release(n + 2);
       k.release(n + 3);
-      // S^T += Y^T diag(phi b) K
+      // S += K^T diag(phi b) Y
       if (!(ok = k.full(n + 5) && k.wait_w(C_SCALED, c) && k.wait_w(C_YOP, c))) break;
       tc_fence_after();
 #pragma unroll
       for (uint32_t p = 0; p < 2; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ts_warp(tmem + kTS, tmem + kTUt + p * 32 + ks * 8, desc_mnmajor_h(k.slot(n + 5), ks, 8192), id_k, 1);
+          mma_ss_warp(tmem + kTS, desc_mnmajor_h(k.slot(n + 5), ks, 8192), desc_mnmajor_h(ut + p * L::row_lo, ks, 8192),
+                      id_k, 1);
       mma_commit_warp(&bar[C_ACC]);
       k.release(n + 5);
       if (c + 1 < P.N && !(ok = vt(c + 1))) break;
     }
   } else if (warp == 2) {
     // the output's products, put into the gaps that the chain leaves the tensor cores: Q S while the
-    // threads turn Y into operands, the other while they turn S into operands
-    const uint32_t id_64 = idesc_bf16(128, 64, false, false);
+    // threads turn Y into operands, P Y while they turn S into operands
+    const uint32_t id_1 = idesc_bf16(64, VS, false, true), id_2 = idesc_bf16(64, 2 * VS, false, true);
+    const uint32_t op = k.base + L::op, u = k.base + L::u1;
     bool ok = true;
     for (int c = 0; c < P.N && ok; ++c) {
       const int n = 7 * c;
-      // O^T = S^T Q^T
       if (!(ok = k.full(n + 4) && (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.wait_w(C_YFULL, c))) break;
       tc_fence_after();
 #pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks)
-          mma_ts_warp(tmem + kTO, tmem + kTSop + p * 64 + ks * 8, desc_kmajor_h(k.slot(n + 4), ks, 8192), id_64,
-                      p + ks > 0);
+      for (uint32_t ks = 0; ks < 8; ++ks)
+        mma_ss_warp(tmem + kTQ, desc_kmajor_h(k.slot(n + 4), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_2, ks > 0);
       mma_commit_warp(&bar[C_QS]);
       k.release(n + 4);
-      // O^T (scaled) += Y^T diag(b) P^T
-      if (!(ok = k.full(n + 6) && k.wait_w(C_UOP, c) && k.wait_w(C_OSC, c) && k.wait_w(C_ACC, c))) break;
+      if (!(ok = k.full(n + 6) && k.wait_w(C_UOP, c) && k.wait_w(C_ACC, c))) break;
       tc_fence_after();
 #pragma unroll
-      for (uint32_t p = 0; p < 3; ++p)
+      for (uint32_t ks = 0; ks < 4; ++ks)
+        mma_ss_warp(tmem + kTP, desc_kmajor(k.slot(n + 6), ks), desc_mnmajor_h(u, ks, L::row_lo), id_2, ks > 0);
 #pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ts_warp(tmem + kTO, tmem + kTU + (p == 2 ? 32u : 0u) + ks * 8,
-                      desc_kmajor(k.slot(n + 6) + (p == 1 ? 8192u : 0u), ks), id_64, 1);
+      for (uint32_t ks = 0; ks < 4; ++ks)
+        mma_ss_warp(tmem + kTP, desc_kmajor(k.slot(n + 6) + 8192, ks), desc_mnmajor_h(u, ks, L::row_lo), id_1, 1);
       mma_commit_warp(&bar[C_OFULL]);
       k.release(n + 6);
     }
-  } else if (warp >= 4 && warp < 4 + kChainWarps) {
-    // lane `row` of S^T, its columns (key dimensions) 32 q4 .. + 31; of Y^T, tokens 16 q4 .. + 15
-    const uint32_t q4 = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
+  } else if (warp >= 4 && warp < L::side) {
+    // S: key dimension `row`; Y: token `tok` (lanes 0..15); columns 16 cg .. + 15 of the slice
+    const uint32_t quad = warp & 3, cg = (warp - 4) >> 2, row = quad * 32 + lane, tok = quad * 16 + (lane & 15);
+    const uint32_t t = tmem + ((quad * 32) << 16) + 16 * cg;
+    const uint32_t gcol = x0 + 16 * cg;  // the columns' value dimension
+    const int64_t at = ((int64_t)bh * P.d + row) * P.d + gcol;
+    const bool in = (int)row < P.d;
+    const float zero[16] = {};
+    tmem_stf(t + kTY + VS, zero);
+    tmem_st_wait();
     bool ok = true;
     for (int c = 0; c <= P.N && ok; ++c) {
-      float s[32];
+      float s[16];
       if (c == 0) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int dk = 32 * q4 + j;
-          s[j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
-        }
+        load_state16(P.in && in ? P.in + at : nullptr, s);
       } else {
         // (Q S of the last chunk has read the operand that is rewritten here)
         if (!(ok = k.wait_w(C_QS, c - 1) && k.wait_w(C_ACC, c - 1))) break;
         tc_fence_after();
-        tmem_ld32(t + kTS + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
+        tmem_ldf(t + kTS, s);
         tmem_ld_wait();
       }
       if (c == P.N) {
-        if (P.out && (int)row < P.d)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int dk = 32 * q4 + j;
-            if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[j];
-          }
+        if (P.out && in) store_state16(P.out + at, s);
         break;
       }
-      uint32_t hi[16];
-      store_split(s, t + kTSop + 16 * q4, t + kTSop + 64 + 16 * q4, hi);
-      tmem_st_wait();
+      uint32_t hi[8];
+      put_split<VS>(k.base + L::op, L::state_lo, row, cg, s, hi);
+      fence_proxy_async_smem();
       k.arrive(C_OP, lane);
-      if (!(ok = k.wait_w(C_GFULL + c % kGateRing, c / kGateRing))) break;
+      if (!(ok = k.gates_ready(c))) break;
       const float *g = k.gates(c);
-      const float f = g[63];
+      const float f = g[63], phi = g[64 + tok], be = g[128 + tok];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s[j] *= f;
-      tmem_st32(t + kTS + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
+      for (int j = 0; j < 16; ++j) s[j] *= f;
+      tmem_stf(t + kTS, s);
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
-      if (P.simg) {
-        uint8_t *img = P.simg + ((int64_t)bh * P.N + c) * kStateImg + (q4 >> 1) * 16384;
-        store_row8(img, row, 2 * (q4 & 1), hi);
-        store_row8(img, row, 2 * (q4 & 1) + 1, hi + 8);
-      }
+      if (P.simg) store_row8(P.simg + ((int64_t)bh * P.N + c) * kStateImg + (gcol >> 6) * 16384, row, (gcol & 63) >> 4, hi);
       // The last chunk's output product is done: it has read the operand that is rewritten below, and its
       // issuer has seen that chunk's C_ACC, which the arrival at C_YOP may lead to complete again.
       if (!(ok = (c == 0 || k.wait_w(C_OFULL, c - 1)) && k.wait_w(C_YFULL, c))) break;
       tc_fence_after();
-      float y[16], u[16], v[16];
-      tmem_ld16(t + kTY + 16 * q4, *reinterpret_cast<uint32_t(*)[16]>(&y));
+      float y[16], z[16];
+      tmem_ldf(t + kTY, y);
+      tmem_ldf(t + kTY + VS, z);
       tmem_ld_wait();
-      const float4 *phi = reinterpret_cast<const float4 *>(g + 64 + 16 * q4),
-                   *be = reinterpret_cast<const float4 *>(g + 128 + 16 * q4);
+      tmem_stf(t + kTY + VS, zero);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 p = phi[j], b4 = be[j];
-        u[4 * j] = b4.x * y[4 * j];
-        u[4 * j + 1] = b4.y * y[4 * j + 1];
-        u[4 * j + 2] = b4.z * y[4 * j + 2];
-        u[4 * j + 3] = b4.w * y[4 * j + 3];
-        v[4 * j] = p.x * u[4 * j];
-        v[4 * j + 1] = p.y * u[4 * j + 1];
-        v[4 * j + 2] = p.z * u[4 * j + 2];
-        v[4 * j + 3] = p.w * u[4 * j + 3];
+      for (int j = 0; j < 16; ++j) {
+        y[j] += z[j];
+        z[j] = phi * be * y[j];
       }
-      store_split(v, t + kTUt + 8 * q4, t + kTUt + 32 + 8 * q4);
+      if (lane < 16) put_split<VS>(k.base + L::u0, L::row_lo, tok, cg, z, hi);
       tmem_st_wait();
+      fence_proxy_async_smem();
       k.arrive(C_YOP, lane);
-      store_split(u, t + kTU + 8 * q4, t + kTU + 32 + 8 * q4);
-      tmem_st_wait();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) z[j] = be * y[j];
+      if (lane < 16) put_split<VS>(k.base + L::u1, L::row_lo, tok, cg, z, hi);
+      fence_proxy_async_smem();
       k.arrive(C_UOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
-      if (P.yimg) {
-        uint32_t w[8];
+      if (P.yimg && lane < 16) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
-        store_row8(P.yimg + ((int64_t)bh * P.N + c) * kRowImg, row, q4, w);
+        for (int j = 0; j < 8; ++j) hi[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
+        store_row8(P.yimg + ((int64_t)bh * P.N + c) * kRowImg + (gcol >> 6) * 8192, tok, (gcol & 63) >> 4, hi);
       }
     }
-  } else if (warp >= 4 + kChainWarps) {
-    const uint32_t row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
-    const uint32_t stage = k.base + kChStage;
-    const bool first = threadIdx.x == 32 * (4 + kChainWarps);
+  } else if (warp >= L::side) {
+    // O = diag(e^g) Q S + P diag(b) Y, a token per lane (lanes 0..15)
+    const uint32_t quad = warp & 3, tok = quad * 16 + (lane & 15), t = tmem + ((quad * 32) << 16);
+    __nv_bfloat16 *dst = o + b * osb + h * osh + x0;
     bool ok = true;
     for (int c = 0; c < P.N && ok; ++c) {
-      // one verdict for the four warps, at the barrier below: none is left alone in it
-      ok = k.wait_w(C_GFULL + c % kGateRing, c / kGateRing) && k.wait_w(C_QS, c);
-      if (ok) {
-        tc_fence_after();
-        const float *g = k.gates(c);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float o[32];
-          tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o));
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] *= g[32 * x + j];
-          tmem_st32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o));
-        }
-        tmem_st_wait();
-        k.arrive(C_OSC, lane);
-        if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
-        ok = k.wait_w(C_OFULL, c);
-      }
-      if (first) bulk_wait_read_all();  // the previous tile has left the staging buffer
-      if (!(ok = group_all(ok, 2, 32 * kSideWarps))) break;
+      if (!(ok = k.gates_ready(c) && k.wait_w(C_QS, c) && k.wait_w(C_OFULL, c))) break;
       tc_fence_after();
+      const float eg = k.gates(c)[tok];
+      const bool in = lane < 16 && kC * c + (int)tok < P.T;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float o[32];
-        tmem_ld32(t + kTO + 32 * x, *reinterpret_cast<uint32_t(*)[32]>(&o));
+      for (int x = 0; x < VS / 16; ++x) {
+        float q[2][16], p[2][16];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          tmem_ldf(t + kTQ + y * VS + 16 * x, q[y]);
+          tmem_ldf(t + kTP + y * VS + 16 * x, p[y]);
+        }
         tmem_ld_wait();
-        if (x == 1) k.arrive(C_OFREE, lane);
+        if (x + 1 == VS / 16) k.arrive(C_OFREE, lane);
+        uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) st_shared_u16(stage + sw_el(32 * x + j, row, 8192), o[j]);
+        for (int j = 0; j < 8; ++j)
+          w[j] = pack_bf16(fmaf(eg, q[0][2 * j] + q[1][2 * j], p[0][2 * j] + p[1][2 * j]),
+                           fmaf(eg, q[0][2 * j + 1] + q[1][2 * j + 1], p[0][2 * j + 1] + p[1][2 * j + 1]));
+        if (in) {
+          uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)(kC * c + tok) * ost + 16 * x);
+          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       }
-      fence_proxy_async_smem();
-      named_bar_sync(2, 32 * kSideWarps);
-      if (first) {
-        tma_store_4d(&mo, smem + kChStage, 0, kC * c, h, b);
-        if (P.d == 128) tma_store_4d(&mo, smem + kChStage + 8192, 64, kC * c, h, b);
-        bulk_commit();
-      }
+      if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
     }
-    if (first) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Tensor memory of the reverse chain: R^T accumulator, its parts, P^T dO and K R (transposed), the
-// operand diag(b) dU (hi, lo), the operand diag(e^g) dO (hi, lo).
-constexpr uint32_t kTR = 0, kTRop = 128, kTD1 = 256, kTD2 = 320, kTD = 384, kTdO = 448;
-
-__global__ void __launch_bounds__(kChainThreads, 1)
+// Tensor memory of the reverse chain: R; P^T dO; K R (both parts' products).
+template <int VS>
+__global__ void __launch_bounds__(Chain<VS>::threads, 1)
     delta_reverse_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mdo, DeltaTcParams P) {
+  using L = Chain<VS>;
+  constexpr uint32_t kTR = 0, kT1 = VS, kT2 = 2 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
   uint8_t *smem = align1024(smem_raw);
-  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kChBar);
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + C_COUNT);
-  const ChainCtx k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
+  uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::bar);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + ChainCtx<VS>::count);
+  const ChainCtx<VS> k{smem, bar, &abort_flag, P.status, smem_u32(smem)};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int bh = blockIdx.x, b = bh / P.H, h = bh % P.H;
-  chain_setup(k, tslot, &abort_flag, warp, kSideWarps);
+  const int ns = P.d / VS, bh = blockIdx.x / ns, b = bh / P.H, h = bh % P.H, x0 = (blockIdx.x % ns) * VS;
+  k.setup(tslot, &abort_flag, warp, kSideWarps);
   const uint32_t tmem = *tslot;
   griddep_wait();
-  const uint8_t *rec0 = P.rec + (int64_t)bh * P.N * kRecBytes;
 
   // step x of the walk is chunk N - 1 - x
   if (warp == 0) {
     if (lane == 0) {
-      int n = 0, ng = 0, x = 0, c = P.N - 1;
-      bool ok = true;
-      auto slot = [&](uint8_t *&dst, uint64_t *&full) {
-        const int s = n % kSlots;
-        if (n >= kSlots && !(ok = k.wait(C_EMPTY + s, n / kSlots - 1))) return false;
-        dst = smem + s * kSlot;
-        full = &bar[C_FULL + s];
-        mbar_arrive_expect_tx(full, kSlot);
-        ++n;
-        return true;
-      };
-      uint8_t *dst;
-      uint64_t *full;
-      auto seq = [&](const CUtensorMap *m) {
-        if (!slot(dst, full)) return;
-        tma_load_4d(m, full, dst, 0, kC * c, h, b, kPolicyEvictNormal);
-        tma_load_4d(m, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictNormal);
-      };
-      auto img = [&](const uint8_t *src) {
-        if (slot(dst, full)) bulk_load(full, dst, src, kSlot);
-      };
-      for (; x < P.N && ok; ++x) {
-        c = P.N - 1 - x;
-        const uint8_t *rec = rec0 + c * kRecBytes;
-        if (x >= kGateRing && !(ok = k.wait(C_GEMPTY + x % kGateRing, x / kGateRing - 1))) break;
-        mbar_arrive_expect_tx(&bar[C_GFULL + x % kGateRing], kGateBytes);
-        bulk_load(&bar[C_GFULL + x % kGateRing], smem + kChGate + (x % kGateRing) * 2048, rec + kRecG, kGateBytes);
-        ++ng;
-        if (ok) seq(&mdo);
-        if (ok) img(rec + kRecP);
-        if (ok) seq(&mk);
-        if (ok) seq(&mq);
-        if (ok) img(rec + kRecW);
-        if (ok) img(rec + kRecW + kSlot);
+      ChainLoader<VS> ld{k, h, b};
+      for (int c = P.N - 1; c >= 0 && ld.ok; --c) {
+        const uint8_t *rec = P.rec + ((int64_t)bh * P.N + c) * kRecBytes;
+        if (!ld.gates(rec + kRecG)) break;
+        ld.block(&mdo, c, x0);
+        ld.image(rec + kRecP);
+        ld.tile(&mk, c);
+        ld.tile(&mq, c);
+        ld.image(rec + kRecW);
+        ld.image(rec + kRecW + kSlot);
       }
-      chain_drain(k, n, ng);
+      ld.drain();
     }
   } else if (warp == 1) {
-    const uint32_t id_mm = idesc_bf16(128, 64, true, true), id_64 = idesc_bf16(128, 64, false, false),
-                   id_k = idesc_bf16(128, 128, false, true);
-    auto pd = [&](int x) {  // (P^T dO)^T = dO^T P
+    const uint32_t id_p = idesc_bf16(64, VS, true, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
+                   id_k = idesc_bf16(128, VS, true, true);
+    const uint32_t op = k.base + L::op, ut = k.base + L::u0, dos = k.base + L::u1;
+    auto pd = [&](int x) {  // P^T dO
       const int n = 6 * x;
       if (!k.full(n) || !k.full(n + 1)) return false;
       tc_fence_after();
@@ -831,139 +834,127 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       for (uint32_t p = 0; p < 2; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kTD1, desc_mnmajor_h(k.slot(n), ks, 8192),
-                      desc_mnmajor_h(k.slot(n + 1) + p * 8192, ks, 8192), id_mm, p + ks > 0);
+          mma_ss_warp(tmem + kT1, desc_mnmajor_h(k.slot(n + 1) + p * 8192, ks, 8192),
+                      desc_mnmajor_h(k.slot(n) + (x0 & 63) * 2, ks, 8192), id_p, p + ks > 0);
       k.release(n + 1);
       return true;
     };
     bool ok = pd(0);
     for (int x = 0; x < P.N && ok; ++x) {
       const int n = 6 * x;
-      if (!(ok = k.wait_w(C_OP, x) && k.full(n + 2))) break;
+      if (!(ok = k.full(n + 2) && k.wait_w(C_OP, x))) break;
       tc_fence_after();
 #pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks)
-          mma_ts_warp(tmem + kTD2, tmem + kTRop + p * 64 + ks * 8, desc_kmajor_h(k.slot(n + 2), ks, 8192), id_64,
-                      p + ks > 0);
+      for (uint32_t ks = 0; ks < 8; ++ks)  // K R
+        mma_ss_warp(tmem + kT2, desc_kmajor_h(k.slot(n + 2), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_2, ks > 0);
       mma_commit_warp(&bar[C_YFULL]);
       k.release(n + 2);
-      // R^T += dO^T diag(e^g) Q
-      if (!(ok = k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x) && k.full(n + 3))) break;
+      // R += Q^T diag(e^g) dO
+      if (!(ok = k.full(n + 3) && k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x))) break;
       tc_fence_after();
 #pragma unroll
       for (uint32_t p = 0; p < 2; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ts_warp(tmem + kTR, tmem + kTdO + p * 32 + ks * 8, desc_mnmajor_h(k.slot(n + 3), ks, 8192), id_k, 1);
+          mma_ss_warp(tmem + kTR, desc_mnmajor_h(k.slot(n + 3), ks, 8192), desc_mnmajor_h(dos + p * L::row_lo, ks, 8192),
+                      id_k, 1);
       k.release(n + 3);
       k.release(n);  // the scaled dO is ready: every reader of this tile is done
-      // R^T += dU^T diag(b) W
-      if (!(ok = k.wait_w(C_YOP, x) && k.full(n + 4) && k.full(n + 5))) break;
+      // R += W^T diag(b) dU: hi hi, hi lo, lo hi
+      if (!(ok = k.full(n + 4) && k.full(n + 5) && k.wait_w(C_YOP, x))) break;
       tc_fence_after();
 #pragma unroll
       for (uint32_t p = 0; p < 3; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ts_warp(tmem + kTR, tmem + kTD + (p == 2 ? 32u : 0u) + ks * 8,
-                      desc_mnmajor_h(k.slot(n + 4 + (p == 1)), ks, 8192), id_k, 1);
+          mma_ss_warp(tmem + kTR, desc_mnmajor_h(k.slot(n + 4 + (p == 2)), ks, 8192),
+                      desc_mnmajor_h(ut + (p == 1 ? L::row_lo : 0u), ks, 8192), id_k, 1);
       mma_commit_warp(&bar[C_ACC]);
       k.release(n + 4);
       k.release(n + 5);
       if (x + 1 < P.N && !(ok = pd(x + 1))) break;
     }
-  } else if (warp >= 4 && warp < 4 + kChainWarps) {
-    const uint32_t q4 = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
+  } else if (warp >= 4 && warp < L::side) {
+    const uint32_t quad = warp & 3, cg = (warp - 4) >> 2, row = quad * 32 + lane, tok = quad * 16 + (lane & 15);
+    const uint32_t t = tmem + ((quad * 32) << 16) + 16 * cg;
+    const uint32_t gcol = x0 + 16 * cg;
+    const int64_t at = ((int64_t)bh * P.d + row) * P.d + gcol;
+    const bool in = (int)row < P.d;
     bool ok = true;
     for (int x = 0; x <= P.N && ok; ++x) {
-      const int c = P.N - 1 - x;
-      float s[32];
+      const int64_t ci = (int64_t)bh * P.N + P.N - 1 - x;
+      float s[16];
       if (x == 0) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int dk = 32 * q4 + j;
-          s[j] = P.in && dk < P.d && (int)row < P.d ? P.in[((int64_t)bh * P.d + dk) * P.d + row] : 0.f;
-        }
+        load_state16(P.in && in ? P.in + at : nullptr, s);
       } else {
         if (!(ok = k.wait_w(C_ACC, x - 1))) break;
         tc_fence_after();
-        tmem_ld32(t + kTR + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
+        tmem_ldf(t + kTR, s);
         tmem_ld_wait();
       }
       if (x == P.N) {
-        if (P.out && (int)row < P.d)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int dk = 32 * q4 + j;
-            if (dk < P.d) P.out[((int64_t)bh * P.d + dk) * P.d + row] = s[j];
-          }
+        if (P.out && in) store_state16(P.out + at, s);
         break;
       }
-      uint32_t hi[16];
-      store_split(s, t + kTRop + 16 * q4, t + kTRop + 64 + 16 * q4, hi);
-      tmem_st_wait();
+      uint32_t hi[8];
+      put_split<VS>(k.base + L::op, L::state_lo, row, cg, s, hi);
+      fence_proxy_async_smem();
       k.arrive(C_OP, lane);
-      if (!(ok = k.wait_w(C_GFULL + x % kGateRing, x / kGateRing))) break;
+      if (!(ok = k.gates_ready(x))) break;
       const float *g = k.gates(x);
-      const float f = g[63];
+      const float f = g[63], phi = g[64 + tok], be = g[128 + tok];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s[j] *= f;
-      tmem_st32(t + kTR + 32 * q4, *reinterpret_cast<uint32_t(*)[32]>(&s));
+      for (int j = 0; j < 16; ++j) s[j] *= f;
+      tmem_stf(t + kTR, s);
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
-      uint8_t *img = P.rimg + ((int64_t)bh * P.N + c) * kStateImg + (q4 >> 1) * 16384;
-      store_row8(img, row, 2 * (q4 & 1), hi);
-      store_row8(img, row, 2 * (q4 & 1) + 1, hi + 8);
-      // dU^T: tokens 16 q4 .. + 15 of this lane
+      store_row8(P.rimg + ci * kStateImg + (gcol >> 6) * 16384, row, (gcol & 63) >> 4, hi);
       if (!(ok = k.wait_w(C_YFULL, x))) break;
       tc_fence_after();
-      float u[16], v[16];
-      tmem_ld16(t + kTD1 + 16 * q4, *reinterpret_cast<uint32_t(*)[16]>(&u));
-      tmem_ld16(t + kTD2 + 16 * q4, *reinterpret_cast<uint32_t(*)[16]>(&v));
+      float u[16], v[16], w[16];
+      tmem_ldf(t + kT1, u);
+      tmem_ldf(t + kT2, v);
+      tmem_ldf(t + kT2 + VS, w);
       tmem_ld_wait();
-      const float4 *phi = reinterpret_cast<const float4 *>(g + 64 + 16 * q4),
-                   *be = reinterpret_cast<const float4 *>(g + 128 + 16 * q4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 p = phi[j], b4 = be[j];
-        u[4 * j] = fmaf(p.x, v[4 * j], u[4 * j]);
-        u[4 * j + 1] = fmaf(p.y, v[4 * j + 1], u[4 * j + 1]);
-        u[4 * j + 2] = fmaf(p.z, v[4 * j + 2], u[4 * j + 2]);
-        u[4 * j + 3] = fmaf(p.w, v[4 * j + 3], u[4 * j + 3]);
-        v[4 * j] = b4.x * u[4 * j];
-        v[4 * j + 1] = b4.y * u[4 * j + 1];
-        v[4 * j + 2] = b4.z * u[4 * j + 2];
-        v[4 * j + 3] = b4.w * u[4 * j + 3];
+      for (int j = 0; j < 16; ++j) {
+        u[j] = fmaf(phi, v[j] + w[j], u[j]);
+        v[j] = be * u[j];
       }
-      store_split(v, t + kTD + 8 * q4, t + kTD + 32 + 8 * q4);
-      tmem_st_wait();
+      if (lane < 16) put_split<VS>(k.base + L::u0, L::row_lo, tok, cg, v, hi);
+      fence_proxy_async_smem();
       k.arrive(C_YOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
-      uint32_t w[8];
+      if (lane < 16) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
-      store_row8(P.uimg + ((int64_t)bh * P.N + c) * kRowImg, row, q4, w);
+        for (int j = 0; j < 8; ++j) hi[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
+        store_row8(P.uimg + ci * kRowImg + (gcol >> 6) * 8192, tok, (gcol & 63) >> 4, hi);
+      }
     }
-  } else if (warp >= 4 + kChainWarps) {
-    // diag(e^g) dO, transposed into tensor memory
-    const uint32_t row = (warp & 3) * 32 + lane, t = tmem + (((warp & 3) * 32) << 16);
+  } else if (warp >= L::side) {
+    // diag(e^g) dO in two parts: 16 columns of a token at a time
+    const uint32_t th = threadIdx.x - 32 * L::side, tok = th & 63;
     bool ok = true;
     for (int x = 0; x < P.N && ok; ++x) {
       const int n = 6 * x;
-      if (!(ok = k.wait_w(C_GFULL + x % kGateRing, x / kGateRing) && k.full(n) && (x == 0 || k.wait_w(C_ACC, x - 1))))
-        break;
-      tc_fence_after();
-      const float *g = k.gates(x);
-      const uint32_t tile = k.slot(n);
+      if (!(ok = k.gates_ready(x) && k.full(n) && (x == 0 || k.wait_w(C_ACC, x - 1)))) break;
+      const float eg = k.gates(x)[tok];
+      const uint32_t src = k.slot(n) + tok * 128;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (uint32_t cg = th >> 6; cg < VS / 16; cg += 2) {
+        uint32_t r[8], hi[8];
+        const uint32_t p = (x0 & 63) / 8 + 2 * cg;
+        ld_shared_v4(src + ((p ^ (tok & 7u)) << 4), r[0], r[1], r[2], r[3]);
+        ld_shared_v4(src + (((p + 1) ^ (tok & 7u)) << 4), r[4], r[5], r[6], r[7]);
         float v[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = g[16 * y + j] * ld_shared_bf16(tile + sw_el(16 * y + j, row, 8192));
-        store_split(v, t + kTdO + 8 * y, t + kTdO + 32 + 8 * y);
+        for (int j = 0; j < 8; ++j) {
+          v[2 * j] = eg * bf16lo(r[j]);
+          v[2 * j + 1] = eg * bf16hi(r[j]);
+        }
+        put_split<VS>(k.base + L::u1, L::row_lo, tok, cg, v, hi);
       }
-      tmem_st_wait();
+      fence_proxy_async_smem();
       k.arrive(C_UOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
     }
@@ -981,7 +972,7 @@ constexpr int kGradThreads = 256;
 constexpr uint32_t kGrKD = 0, kGrQ = 32768, kGrS = 49152, kGrR = 81920, kGrY = 114688, kGrU = 131072, kGrT = 147456,
                    kGrZ = 163840, kGrD = 180224, kGrA = 188416, kGrV = 196608, kGrG = 212992, kGrEnd = 215040;
 constexpr size_t kGradSmem = kGrEnd + 1024;
-constexpr uint32_t kGZ = 0, kGOp = 64, kGKK = 128, kGdP = 192, kGGY = 256, kGdq = 320, kGdr = 384, kGdw = 448;
+constexpr uint32_t kGZ = 0, kGKK = 128, kGdP = 192, kGGY = 256, kGdq = 320, kGdr = 384, kGdw = 448;
 
 __global__ void __launch_bounds__(kGradThreads, 1)
     delta_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -997,7 +988,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t quad = warp & 3, hf = warp >> 2, row = quad * 32 + lane;
-  const int c = blockIdx.x, bh = blockIdx.y, b = bh / P.H, h = bh % P.H;
+  const int c = blockIdx.x % P.N, bh = blockIdx.x / P.N, b = bh / P.H, h = bh % P.H;
   const int64_t ci = (int64_t)bh * P.N + c;
   const float *g = reinterpret_cast<const float *>(smem + kGrG);
 
@@ -1033,32 +1024,33 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       tma_load_4d(&mq, &bar[1], smem + kGrQ + x * 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
   }
   const uint32_t KD = base + kGrKD, dO = KD + 8192, Y = base + kGrY, Z = base + kGrZ, S = base + kGrS, R = base + kGrR;
+  // contractions over value dimensions: d = 64 has no others (the images hold nothing there)
+  const uint32_t kd = P.d / 16;
   const uint32_t id_mm = idesc_bf16(128, 64, true, true), id_mk = idesc_bf16(128, 64, true, false),
                  id_km = idesc_bf16(128, 64, false, true), id_kk = idesc_bf16(128, 64, false, false);
   bool ok = mbar_wait(&bar[0], 0, &abort_flag, P.status);
   if (__syncthreads_and(ok)) {
-    // diag(b) dU as an operand, and the parts of dU . y over this warp's 32 value dimensions
+    // diag(b) dU as an operand (over the place of Z), and dU . y: a quarter of a token's row per thread
     {
-      float dot[32];
-      uint32_t op[16];
-      const float *be = g + 128 + 32 * hf;
+      const uint32_t tok = tid & 63, q = tid >> 6;  // columns 32 q .. + 31
+      const float be = g[128 + tok];
+      float dot = 0.f;
 #pragma unroll
       for (uint32_t p = 0; p < 4; ++p) {
         uint32_t u[4], y[4];
-        ld_shared_v4(base + kGrU + sw(row, 4 * hf + p), u[0], u[1], u[2], u[3]);
-        ld_shared_v4(Y + sw(row, 4 * hf + p), y[0], y[1], y[2], y[3]);
+        const uint32_t at = (q >> 1) * 8192 + sw(tok, 4 * (q & 1) + p);
+        ld_shared_v4(base + kGrU + at, u[0], u[1], u[2], u[3]);
+        ld_shared_v4(Y + at, y[0], y[1], y[2], y[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = 8 * p + 2 * e;
-          op[4 * p + e] = pack_bf16(be[j] * bf16lo(u[e]), be[j + 1] * bf16hi(u[e]));
-          dot[j] = bf16lo(u[e]) * bf16lo(y[e]);
-          dot[j + 1] = bf16hi(u[e]) * bf16hi(y[e]);
+          dot = fmaf(bf16lo(u[e]), bf16lo(y[e]), fmaf(bf16hi(u[e]), bf16hi(y[e]), dot));
+          u[e] = pack_bf16(be * bf16lo(u[e]), be * bf16hi(u[e]));
         }
+        st_shared_v4(Z + at, u[0], u[1], u[2], u[3]);
       }
-      tmem_st16(t + kGOp + 16 * hf, op);
-      tmem_st_wait();
-      s_dot[quad][32 * hf + lane] = warp_col_sum(dot, lane);
+      s_dot[q][tok] = 32 * (int)q < P.d ? dot : 0.f;
     }
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     if (warp == 0) {
@@ -1068,23 +1060,23 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       for (uint32_t p = 0; p < 2; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ts_warp(tmem + kGZ, tmem + kGOp + ks * 8, desc_mnmajor_h(base + kGrT + p * 8192, ks, 8192), id_km,
+          mma_ss_warp(tmem + kGZ, desc_mnmajor_h(Z, ks, 8192), desc_mnmajor_h(base + kGrT + p * 8192, ks, 8192), id_mm,
                       p + ks > 0);
       mma_commit_warp(&bar[2]);
 #pragma unroll
       for (uint32_t ks = 0; ks < 8; ++ks)
         mma_ss_warp(tmem + kGKK, desc_kmajor(KD, ks), desc_kmajor(KD, ks), id_kk, ks > 0);
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)
-        mma_ss_warp(tmem + kGdP, desc_kmajor(KD, ks), desc_mnmajor_h(Y, ks, 8192), id_km, ks > 0);
+#pragma unroll 4
+      for (uint32_t ks = 0; ks < kd; ++ks)
+        mma_ss_warp(tmem + kGdP, desc_kmajor(KD, ks), desc_kmajor_h(Y, ks, 8192), id_kk, ks > 0);
       ok = mbar_wait_w(&bar[1], 0, &abort_flag, P.status);
       if (ok) {
-#pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks)  // (dO S^T)^T
-          mma_ss_warp(tmem + kGdq, desc_mnmajor(S, ks), desc_kmajor(dO, ks), id_mk, ks > 0);
-#pragma unroll
-        for (uint32_t ks = 0; ks < 8; ++ks)  // (Y R^T)^T
-          mma_ss_warp(tmem + kGdw, desc_mnmajor(R, ks), desc_mnmajor_h(Y, ks, 8192), id_mm, ks > 0);
+#pragma unroll 4
+        for (uint32_t ks = 0; ks < kd; ++ks)  // (dO S^T)^T
+          mma_ss_warp(tmem + kGdq, desc_kmajor(S, ks), desc_kmajor(dO, ks), id_kk, ks > 0);
+#pragma unroll 4
+        for (uint32_t ks = 0; ks < kd; ++ks)  // (Y R^T)^T
+          mma_ss_warp(tmem + kGdw, desc_kmajor(R, ks), desc_kmajor_h(Y, ks, 8192), id_kk, ks > 0);
       }
     }
     ok = ok && mbar_wait(&bar[2], 0, &abort_flag, P.status);
@@ -1114,13 +1106,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     if (warp == 0) {
       __syncwarp();
       tc_fence_after();
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)  // Z Y^T (lanes 0..63)
-        mma_ss_warp(tmem + kGGY, desc_mnmajor_h(Z, ks, 16384), desc_mnmajor_h(Y, ks, 8192), id_mm, ks > 0);
+#pragma unroll 4
+      for (uint32_t ks = 0; ks < kd; ++ks)  // Z Y^T (lanes 0..63)
+        mma_ss_warp(tmem + kGGY, desc_mnmajor_h(Z, ks, 16384), desc_kmajor_h(Y, ks, 8192), id_mk, ks > 0);
       mma_commit_warp(&bar[3]);
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)  // (Z S^T)^T
-        mma_ss_warp(tmem + kGdr, desc_mnmajor(S, ks), desc_mnmajor_h(Z, ks, 8192), id_mm, ks > 0);
+#pragma unroll 4
+      for (uint32_t ks = 0; ks < kd; ++ks)  // (Z S^T)^T
+        mma_ss_warp(tmem + kGdr, desc_kmajor(S, ks), desc_mnmajor_h(Z, ks, 8192), id_km, ks > 0);
     }
     ok = mbar_wait(&bar[3], 0, &abort_flag, P.status);
   }
@@ -1140,7 +1132,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
 #pragma unroll
       for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) s_rs[warp] = dot;
+      if (lane == 0) s_rs[warp] = 64 * (int)hf < P.d ? dot : 0.f;
     }
     const int i = row & 63;
     const float hi = g[192 + i], lo = g[256 + i];
@@ -1294,6 +1286,9 @@ cudaError_t allow_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
+// Slices of 32 value dimensions while all the chains run at once with one CTA per SM, else of 64 (a chunk
+// takes longer, but not twice as long).
+bool narrow_slices(const Problem &p) { return (int64_t)p.B * p.H * (p.d / 32) <= p.num_sms; }
 int chunks(const Problem &p) { return (p.T + kC - 1) / kC; }
 size_t bhs(const Problem &p) { return (size_t)p.B * p.H; }
 size_t rec_bytes(const Problem &p) { return bhs(p) * chunks(p) * kRecBytes; }
@@ -1326,9 +1321,8 @@ size_t delta_tc_bwd_ws_bytes(const Problem &p) {
 
 cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
                          const float *init, float *fin, void *ckpt, void *ws, int *status, cudaStream_t s) {
-  CUtensorMap mq, mk, mv, mo;
-  if (!seq64_tmap(p, q, &mq) || !seq64_tmap(p, k, &mk) || !seq64_tmap(p, v, &mv) || !seq64_tmap(p, o, &mo))
-    return cudaErrorInvalidValue;
+  CUtensorMap mq, mk, mv;
+  if (!seq64_tmap(p, q, &mq) || !seq64_tmap(p, k, &mk) || !seq64_tmap(p, v, &mv)) return cudaErrorInvalidValue;
   DeltaTcParams P = params(p, g, status);
   P.rec = static_cast<uint8_t *>(ckpt ? ckpt : ws);
   if (ckpt) {
@@ -1338,16 +1332,21 @@ cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, c
   P.in = init;
   P.out = fin;
   cudaError_t e = allow_smem(delta_prep_kernel, kPrepSmem);
-  if (e == cudaSuccess) e = allow_smem(delta_chain_kernel, kChainSmem);
   if (e != cudaSuccess) return e;
   {
     TimedLaunch t(K_DELTA_PREP, s);
-    e = launch_overlapped(delta_prep_kernel, dim3(P.N, (unsigned)bhs(p)), dim3(kPrepThreads), kPrepSmem, s, mq, mk, P);
+    e = launch_overlapped(delta_prep_kernel, dim3((unsigned)(bhs(p) * P.N)), dim3(kPrepThreads), kPrepSmem, s, mq, mk, P);
     if (e != cudaSuccess) return e;
   }
-  TimedLaunch t(K_DELTA_CHAIN, s);
-  return launch_overlapped(delta_chain_kernel, dim3((unsigned)bhs(p)), dim3(kChainThreads), kChainSmem, s, mq, mk, mv,
-                           mo, P);
+  auto chain = [&](auto kernel, int slice, int threads, size_t smem) {
+    cudaError_t err = allow_smem(kernel, smem);
+    if (err != cudaSuccess) return err;
+    TimedLaunch t(K_DELTA_CHAIN, s);
+    return launch_overlapped(kernel, dim3((unsigned)(bhs(p) * (p.d / slice))), dim3(threads), smem, s, mq, mk, mv,
+                             static_cast<__nv_bfloat16 *>(o), p.sb, p.sh, p.st, P);
+  };
+  return narrow_slices(p) ? chain(delta_chain_kernel<32>, 32, Chain<32>::threads, Chain<32>::smem)
+                          : chain(delta_chain_kernel<64>, 64, Chain<64>::threads, Chain<64>::smem);
 }
 
 cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
@@ -1369,18 +1368,20 @@ cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, c
   P.dbeta = dbeta;
   P.in = d_final;
   P.out = dinit;
-  cudaError_t e = allow_smem(delta_reverse_kernel, kChainSmem);
-  if (e == cudaSuccess) e = allow_smem(delta_grad_kernel, kGradSmem);
+  cudaError_t e = allow_smem(delta_grad_kernel, kGradSmem);
+  if (e != cudaSuccess) return e;
+  auto reverse = [&](auto kernel, int slice, int threads, size_t smem) {
+    cudaError_t err = allow_smem(kernel, smem);
+    if (err != cudaSuccess) return err;
+    TimedLaunch t(K_DELTA_REVERSE, s);
+    return launch_overlapped(kernel, dim3((unsigned)(bhs(p) * (p.d / slice))), dim3(threads), smem, s, mq, mk, mdo, P);
+  };
+  e = narrow_slices(p) ? reverse(delta_reverse_kernel<32>, 32, Chain<32>::threads, Chain<32>::smem)
+                       : reverse(delta_reverse_kernel<64>, 64, Chain<64>::threads, Chain<64>::smem);
   if (e != cudaSuccess) return e;
   {
-    TimedLaunch t(K_DELTA_REVERSE, s);
-    e = launch_overlapped(delta_reverse_kernel, dim3((unsigned)bhs(p)), dim3(kChainThreads), kChainSmem, s, mq, mk, mdo,
-                          P);
-    if (e != cudaSuccess) return e;
-  }
-  {
     TimedLaunch t(K_DELTA_GRAD, s);
-    e = launch_overlapped(delta_grad_kernel, dim3(P.N, (unsigned)bhs(p)), dim3(kGradThreads), kGradSmem, s, mq, mk, mdo,
+    e = launch_overlapped(delta_grad_kernel, dim3((unsigned)(bhs(p) * P.N)), dim3(kGradThreads), kGradSmem, s, mq, mk, mdo,
                           mdq, mdk, mdv, P);
     if (e != cudaSuccess) return e;
   }
