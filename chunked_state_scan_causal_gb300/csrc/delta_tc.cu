@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(kPrepThreads)
 //
 // A chunk's path is S -> (W S) -> Y -> (K^T Y) -> S: two products and two passes of the threads, each
 // bounded by its latency (reading 64 or 128 operand rows per 16 of the contraction takes 33 to 51 cycles a
-// product whatever the width).  Warps: 0 loads, 1 issues the chain's products, 2 the output's, then
+// product whatever the width).  Every role is a long loop of its own, so their instructions have to be few:
+// with unrolled products and in-line waits two CTAs on neighbouring SMs took 3.1 us a chunk, one alone 2.0.  Warps: 0 and 3 load, 1 issues the chain's products, 2 the output's, then
 // 4 VS/16 that carry the chain (16 columns each: the threads' work is on the path, so it is spread thin) and
 // 4 for the output (forward) or the scaled dO (backward).
 constexpr int kGateRing = 4, kSideWarps = 4;
@@ -413,20 +414,52 @@ enum { C_OP = 0,    // S (R) operand parts ready
        C_QS, C_OFULL, C_OFREE,   // forward: Q S done; output complete, read
        C_GFULL, C_GEMPTY = C_GFULL + kGateRing, C_FULL = C_GEMPTY + kGateRing };
 
+// A place in the ring: slot and the parity of its use.  at(j): j loads further on.
+template <int SLOTS>
+struct RingPos {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ RingPos at(int j) const {
+    RingPos r = *this;
+    r.s += j;
+    if (r.s >= SLOTS) {
+      r.s -= SLOTS;
+      r.ph ^= 1;
+    }
+    return r;
+  }
+};
+
+// Descriptors are formed once per tile; a step of 16 along the contraction adds to the address field.
+__device__ __forceinline__ uint64_t k_tile(uint32_t tile) { return sdesc_sw128(tile, 16u, 1024u); }
+__device__ __forceinline__ uint64_t mn_tile(uint32_t tile, uint32_t block) { return sdesc_sw128(tile, block, 1024u); }
+__device__ __forceinline__ constexpr uint64_t k_step(uint32_t ks) { return (ks >> 2) * (8192u >> 4) + (ks & 3) * 2u; }
+__device__ __forceinline__ constexpr uint64_t mn_step(uint32_t ks) { return ks * 128u; }
+// D (+)= A B over KS steps; A K-major (AM = false, 64-column blocks 8 KiB apart) or MN-major, B MN-major
+template <int KS, bool AM>
+__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool fresh = false) {
+#pragma unroll
+  for (uint32_t ks = 0; ks < KS; ++ks)
+    mma_ss_warp(d, a + (AM ? mn_step(ks) : k_step(ks)), b + mn_step(ks), idesc, ks > 0 || !fresh);
+}
+
 template <int VS>
 struct ChainCtx {
   using L = Chain<VS>;
+  using Pos = RingPos<L::slots>;
   static constexpr int empty0 = C_FULL + L::slots, count = empty0 + L::slots;
   uint8_t *smem;
   uint64_t *bar;
   volatile int *abort_flag;
   int *status;
   uint32_t base;
-  __device__ bool wait(int idx, int parity) const { return mbar_wait(&bar[idx], parity & 1, abort_flag, status); }
+  __device__ bool wait(int idx, int parity) const {
+    return mbar_wait_compact(&bar[idx], parity & 1, abort_flag, status);
+  }
   __device__ bool wait_w(int idx, int parity) const { return __all_sync(0xffffffffu, wait(idx, parity)); }
-  __device__ uint32_t slot(int n) const { return base + (uint32_t)(n % L::slots) * kSlot; }
-  __device__ bool full(int n) const { return wait_w(C_FULL + n % L::slots, n / L::slots); }
-  __device__ void release(int n) const { mma_commit_warp(&bar[empty0 + n % L::slots]); }
+  __device__ uint32_t slot(Pos p) const { return base + (uint32_t)p.s * kSlot; }
+  __device__ bool full(Pos p) const { return wait_w(C_FULL + p.s, p.ph); }
+  __device__ void release(Pos p) const { mma_commit_warp(&bar[empty0 + p.s]); }
   __device__ bool gates_ready(int x) const { return wait_w(C_GFULL + x % kGateRing, x / kGateRing); }
   __device__ const float *gates(int x) const {
     return reinterpret_cast<const float *>(smem + L::gate + (x % kGateRing) * 2048);
@@ -460,57 +493,53 @@ struct ChainCtx {
   }
 };
 
-// The loading thread's side of the ring.
+// A loading thread's side of the ring; n: the index of a load in the order of use (two threads take some of
+// every chunk's each: a single one spends most of a chunk's time on its waits).
 template <int VS>
 struct ChainLoader {
+  using Pos = typename ChainCtx<VS>::Pos;
   const ChainCtx<VS> &k;
-  int h, b, n = 0, ng = 0;
+  int h, b;
   bool ok = true;
-  __device__ uint64_t *slot(uint8_t *&dst, uint32_t bytes) {
-    const int s = n % Chain<VS>::slots;
-    if (n >= Chain<VS>::slots && !(ok = ok && k.wait(ChainCtx<VS>::empty0 + s, n / Chain<VS>::slots - 1))) return nullptr;
-    dst = k.smem + s * kSlot;
-    mbar_arrive_expect_tx(&k.bar[C_FULL + s], bytes);
-    ++n;
-    return &k.bar[C_FULL + s];
+  // (a fresh barrier's wait for the parity before its first phase succeeds at once: no use precedes it)
+  __device__ uint64_t *slot(Pos p, uint8_t *&dst, uint32_t bytes) {
+    if (!ok || !(ok = k.wait(ChainCtx<VS>::empty0 + p.s, p.ph ^ 1))) return nullptr;
+    dst = k.smem + p.s * kSlot;
+    mbar_arrive_expect_tx(&k.bar[C_FULL + p.s], bytes);
+    return &k.bar[C_FULL + p.s];
   }
   // a 64 x 128 tile of a sequence tensor, or the 64-column block of it that holds column x
-  __device__ void tile(const CUtensorMap *m, int c) {
+  __device__ void tile(Pos n, const CUtensorMap *m, int c) {
     uint8_t *dst;
-    uint64_t *full = ok ? slot(dst, kSlot) : nullptr;
+    uint64_t *full = slot(n, dst, kSlot);
     if (!full) return;
     tma_load_4d(m, full, dst, 0, kC * c, h, b, kPolicyEvictNormal);
     tma_load_4d(m, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictNormal);
   }
-  __device__ void block(const CUtensorMap *m, int c, int x) {
+  __device__ void block(Pos n, const CUtensorMap *m, int c, int x) {
     uint8_t *dst;
-    uint64_t *full = ok ? slot(dst, 8192) : nullptr;
+    uint64_t *full = slot(n, dst, 8192);
     if (full) tma_load_4d(m, full, dst, x / 64 * 64, kC * c, h, b, kPolicyEvictNormal);
   }
-  __device__ void image(const uint8_t *src) {
+  __device__ void image(Pos n, const uint8_t *src) {
     uint8_t *dst;
-    uint64_t *full = ok ? slot(dst, kSlot) : nullptr;
+    uint64_t *full = slot(n, dst, kSlot);
     if (full) bulk_load(full, dst, src, kSlot);
   }
-  __device__ bool gates(const uint8_t *src) {
-    const int s = ng % kGateRing;
-    if (ng >= kGateRing && !(ok = k.wait(C_GEMPTY + s, ng / kGateRing - 1))) return false;
+  __device__ void gates(int x, const uint8_t *src) {
+    const int s = x % kGateRing;
+    if (!ok || (x >= kGateRing && !(ok = k.wait(C_GEMPTY + s, x / kGateRing - 1)))) return;
     mbar_arrive_expect_tx(&k.bar[C_GFULL + s], kGateBytes);
     bulk_load(&k.bar[C_GFULL + s], k.smem + Chain<VS>::gate + s * 2048, src, kGateBytes);
-    ++ng;
-    return true;
   }
-  // waits for what is in flight, after the last load or an abort
-  __device__ void drain() {
+  // waits for the ring's last loads (of `total`) and the last gates (of `steps`) before the block ends; after
+  // an abort each wait has its limit
+  __device__ void drain(int total, int steps) const {
     volatile int no_abort = 0;
-    for (int s = 0; s < Chain<VS>::slots; ++s) {
-      const int uses = n > s ? (n - 1 - s) / Chain<VS>::slots + 1 : 0;
-      if (uses) mbar_wait(&k.bar[C_FULL + s], (uses - 1) & 1, &no_abort, k.status);
-    }
-    for (int s = 0; s < kGateRing; ++s) {
-      const int uses = ng > s ? (ng - 1 - s) / kGateRing + 1 : 0;
-      if (uses) mbar_wait(&k.bar[C_GFULL + s], (uses - 1) & 1, &no_abort, k.status);
-    }
+    for (int n = max(0, total - Chain<VS>::slots); n < total; ++n)
+      mbar_wait(&k.bar[C_FULL + n % Chain<VS>::slots], (n / Chain<VS>::slots) & 1, ok ? &no_abort : k.abort_flag, k.status);
+    for (int x = max(0, steps - kGateRing); x < steps; ++x)
+      mbar_wait(&k.bar[C_GFULL + x % kGateRing], (x / kGateRing) & 1, ok ? &no_abort : k.abort_flag, k.status);
   }
 };
 
@@ -576,6 +605,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
                        const __grid_constant__ CUtensorMap mv, __nv_bfloat16 *o, int64_t osb, int64_t osh, int64_t ost,
                        DeltaTcParams P) {
   using L = Chain<VS>;
+  using Pos = RingPos<L::slots>;
   constexpr uint32_t kTS = 0, kTY = VS, kTQ = 3 * VS, kTP = 5 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
@@ -590,94 +620,85 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   const uint32_t tmem = *tslot;
   griddep_wait();
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     if (lane == 0) {
       ChainLoader<VS> ld{k, h, b};
       const uint8_t *rec = P.rec + (int64_t)bh * P.N * kRecBytes;
-      for (int c = 0; c < P.N && ld.ok; ++c, rec += kRecBytes) {
-        if (!ld.gates(rec + kRecG)) break;
-        ld.block(&mv, c, x0);
-        ld.image(rec + kRecT);
-        ld.image(rec + kRecW);
-        ld.image(rec + kRecW + kSlot);
-        ld.tile(&mq, c);
-        ld.tile(&mk, c);
-        ld.image(rec + kRecP);
+      Pos n;
+#pragma unroll 1
+      for (int c = 0; c < P.N && ld.ok; ++c, n = n.at(7), rec += kRecBytes) {
+        if (warp == 0) {
+          ld.block(n, &mv, c, x0);
+          ld.image(n.at(1), rec + kRecT);
+          ld.image(n.at(2), rec + kRecW);
+          ld.image(n.at(3), rec + kRecW + kSlot);
+        } else {
+          ld.gates(c, rec + kRecG);
+          ld.tile(n.at(4), &mq, c);
+          ld.tile(n.at(5), &mk, c);
+          ld.image(n.at(6), rec + kRecP);
+        }
       }
-      ld.drain();
+      ld.drain(7 * P.N, P.N);
     }
   } else if (warp == 1) {
     // the chain's own products, in the order of its dependences
     const uint32_t id_1 = idesc_bf16(64, VS, false, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
                    id_k = idesc_bf16(128, VS, true, true);
-    const uint32_t op = k.base + L::op, ut = k.base + L::u0;
-    auto vt = [&](int c) {  // Y = T V
-      const int n = 7 * c;
-      if (!k.full(n) || !k.full(n + 1)) return false;
+    const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, 8192);
+    auto vt = [&](Pos n) {  // Y = T V
+      if (!k.full(n) || !k.full(n.at(1))) return false;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kTY, desc_kmajor(k.slot(n + 1) + p * 8192, ks),
-                      desc_mnmajor_h(k.slot(n) + (x0 & 63) * 2, ks, 8192), id_1, p + ks > 0);
+      const uint64_t v = mn_tile(k.slot(n) + (x0 & 63) * 2, 8192), tt = k_tile(k.slot(n.at(1)));
+      mma_steps<4, false>(tmem + kTY, tt, v, id_1, true);
+      mma_steps<4, false>(tmem + kTY, tt + (8192 >> 4), v, id_1);
       k.release(n);
-      k.release(n + 1);
+      k.release(n.at(1));
       return true;
     };
-    bool ok = vt(0);
-    for (int c = 0; c < P.N && ok; ++c) {
-      const int n = 7 * c;
+    Pos n;
+    bool ok = vt(n);
+#pragma unroll 1
+    for (int c = 0; c < P.N && ok; ++c, n = n.at(7)) {
       // Y += W S: hi [hi | lo] (2 VS columns), lo hi
-      if (!(ok = k.full(n + 2) && k.full(n + 3) && k.wait_w(C_OP, c))) break;
+      if (!(ok = k.full(n.at(2)) && k.full(n.at(3)) && k.wait_w(C_OP, c))) break;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)
-        mma_ss_warp(tmem + kTY, desc_kmajor_h(k.slot(n + 2), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_2, 1);
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)
-        mma_ss_warp(tmem + kTY, desc_kmajor_h(k.slot(n + 3), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_1, 1);
+      mma_steps<8, false>(tmem + kTY, k_tile(k.slot(n.at(2))), op, id_2);
+      mma_steps<8, false>(tmem + kTY, k_tile(k.slot(n.at(3))), op, id_1);
       mma_commit_warp(&bar[C_YFULL]);
-      k.release(n + 2);
-      k.release(n + 3);
+      k.release(n.at(2));
+      k.release(n.at(3));
       // S += K^T diag(phi b) Y
-      if (!(ok = k.full(n + 5) && k.wait_w(C_SCALED, c) && k.wait_w(C_YOP, c))) break;
+      if (!(ok = k.full(n.at(5)) && k.wait_w(C_SCALED, c) && k.wait_w(C_YOP, c))) break;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kTS, desc_mnmajor_h(k.slot(n + 5), ks, 8192), desc_mnmajor_h(ut + p * L::row_lo, ks, 8192),
-                      id_k, 1);
+      const uint64_t kt = mn_tile(k.slot(n.at(5)), 8192);
+      mma_steps<4, true>(tmem + kTS, kt, ut, id_k);
+      mma_steps<4, true>(tmem + kTS, kt, ut + (L::row_lo >> 4), id_k);
       mma_commit_warp(&bar[C_ACC]);
-      k.release(n + 5);
-      if (c + 1 < P.N && !(ok = vt(c + 1))) break;
+      k.release(n.at(5));
+      if (c + 1 < P.N && !(ok = vt(n.at(7)))) break;
     }
   } else if (warp == 2) {
     // the output's products, put into the gaps that the chain leaves the tensor cores: Q S while the
     // threads turn Y into operands, P Y while they turn S into operands
     const uint32_t id_1 = idesc_bf16(64, VS, false, true), id_2 = idesc_bf16(64, 2 * VS, false, true);
-    const uint32_t op = k.base + L::op, u = k.base + L::u1;
+    const uint64_t op = mn_tile(k.base + L::op, L::state_lo), u = mn_tile(k.base + L::u1, L::row_lo);
+    Pos n;
     bool ok = true;
-    for (int c = 0; c < P.N && ok; ++c) {
-      const int n = 7 * c;
-      if (!(ok = k.full(n + 4) && (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.wait_w(C_YFULL, c))) break;
+#pragma unroll 1
+    for (int c = 0; c < P.N && ok; ++c, n = n.at(7)) {
+      if (!(ok = k.full(n.at(4)) && (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.wait_w(C_YFULL, c))) break;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)
-        mma_ss_warp(tmem + kTQ, desc_kmajor_h(k.slot(n + 4), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_2, ks > 0);
+      mma_steps<8, false>(tmem + kTQ, k_tile(k.slot(n.at(4))), op, id_2, true);
       mma_commit_warp(&bar[C_QS]);
-      k.release(n + 4);
-      if (!(ok = k.full(n + 6) && k.wait_w(C_UOP, c) && k.wait_w(C_ACC, c))) break;
+      k.release(n.at(4));
+      if (!(ok = k.full(n.at(6)) && k.wait_w(C_UOP, c) && k.wait_w(C_ACC, c))) break;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t ks = 0; ks < 4; ++ks)
-        mma_ss_warp(tmem + kTP, desc_kmajor(k.slot(n + 6), ks), desc_mnmajor_h(u, ks, L::row_lo), id_2, ks > 0);
-#pragma unroll
-      for (uint32_t ks = 0; ks < 4; ++ks)
-        mma_ss_warp(tmem + kTP, desc_kmajor(k.slot(n + 6) + 8192, ks), desc_mnmajor_h(u, ks, L::row_lo), id_1, 1);
+      const uint64_t pp = k_tile(k.slot(n.at(6)));
+      mma_steps<4, false>(tmem + kTP, pp, u, id_2, true);
+      mma_steps<4, false>(tmem + kTP, pp + (8192 >> 4), u, id_1);
       mma_commit_warp(&bar[C_OFULL]);
-      k.release(n + 6);
+      k.release(n.at(6));
     }
   } else if (warp >= 4 && warp < L::side) {
     // S: key dimension `row`; Y: token `tok` (lanes 0..15); columns 16 cg .. + 15 of the slice
@@ -793,6 +814,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     delta_reverse_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mdo, DeltaTcParams P) {
   using L = Chain<VS>;
+  using Pos = RingPos<L::slots>;
   constexpr uint32_t kTR = 0, kT1 = VS, kT2 = 2 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
@@ -807,72 +829,69 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   griddep_wait();
 
   // step x of the walk is chunk N - 1 - x
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     if (lane == 0) {
       ChainLoader<VS> ld{k, h, b};
-      for (int c = P.N - 1; c >= 0 && ld.ok; --c) {
+      Pos n;
+#pragma unroll 1
+      for (int x = 0; x < P.N && ld.ok; ++x, n = n.at(6)) {
+        const int c = P.N - 1 - x;
         const uint8_t *rec = P.rec + ((int64_t)bh * P.N + c) * kRecBytes;
-        if (!ld.gates(rec + kRecG)) break;
-        ld.block(&mdo, c, x0);
-        ld.image(rec + kRecP);
-        ld.tile(&mk, c);
-        ld.tile(&mq, c);
-        ld.image(rec + kRecW);
-        ld.image(rec + kRecW + kSlot);
+        if (warp == 0) {
+          ld.block(n, &mdo, c, x0);
+          ld.image(n.at(1), rec + kRecP);
+          ld.tile(n.at(2), &mk, c);
+        } else {
+          ld.gates(x, rec + kRecG);
+          ld.tile(n.at(3), &mq, c);
+          ld.image(n.at(4), rec + kRecW);
+          ld.image(n.at(5), rec + kRecW + kSlot);
+        }
       }
-      ld.drain();
+      ld.drain(6 * P.N, P.N);
     }
   } else if (warp == 1) {
     const uint32_t id_p = idesc_bf16(64, VS, true, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
                    id_k = idesc_bf16(128, VS, true, true);
-    const uint32_t op = k.base + L::op, ut = k.base + L::u0, dos = k.base + L::u1;
-    auto pd = [&](int x) {  // P^T dO
-      const int n = 6 * x;
-      if (!k.full(n) || !k.full(n + 1)) return false;
+    const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, 8192),
+                   dos = mn_tile(k.base + L::u1, 8192);
+    auto pd = [&](Pos n) {  // P^T dO
+      if (!k.full(n) || !k.full(n.at(1))) return false;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kT1, desc_mnmajor_h(k.slot(n + 1) + p * 8192, ks, 8192),
-                      desc_mnmajor_h(k.slot(n) + (x0 & 63) * 2, ks, 8192), id_p, p + ks > 0);
-      k.release(n + 1);
+      const uint64_t pp = mn_tile(k.slot(n.at(1)), 8192), d = mn_tile(k.slot(n) + (x0 & 63) * 2, 8192);
+      mma_steps<4, true>(tmem + kT1, pp, d, id_p, true);
+      mma_steps<4, true>(tmem + kT1, pp + (8192 >> 4), d, id_p);
+      k.release(n.at(1));
       return true;
     };
-    bool ok = pd(0);
-    for (int x = 0; x < P.N && ok; ++x) {
-      const int n = 6 * x;
-      if (!(ok = k.full(n + 2) && k.wait_w(C_OP, x))) break;
+    Pos n;
+    bool ok = pd(n);
+#pragma unroll 1
+    for (int x = 0; x < P.N && ok; ++x, n = n.at(6)) {
+      if (!(ok = k.full(n.at(2)) && k.wait_w(C_OP, x))) break;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)  // K R
-        mma_ss_warp(tmem + kT2, desc_kmajor_h(k.slot(n + 2), ks, 8192), desc_mnmajor_h(op, ks, L::state_lo), id_2, ks > 0);
+      mma_steps<8, false>(tmem + kT2, k_tile(k.slot(n.at(2))), op, id_2, true);  // K R
       mma_commit_warp(&bar[C_YFULL]);
-      k.release(n + 2);
+      k.release(n.at(2));
       // R += Q^T diag(e^g) dO
-      if (!(ok = k.full(n + 3) && k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x))) break;
+      if (!(ok = k.full(n.at(3)) && k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x))) break;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kTR, desc_mnmajor_h(k.slot(n + 3), ks, 8192), desc_mnmajor_h(dos + p * L::row_lo, ks, 8192),
-                      id_k, 1);
-      k.release(n + 3);
+      const uint64_t qt = mn_tile(k.slot(n.at(3)), 8192);
+      mma_steps<4, true>(tmem + kTR, qt, dos, id_k);
+      mma_steps<4, true>(tmem + kTR, qt, dos + (L::row_lo >> 4), id_k);
+      k.release(n.at(3));
       k.release(n);  // the scaled dO is ready: every reader of this tile is done
       // R += W^T diag(b) dU: hi hi, hi lo, lo hi
-      if (!(ok = k.full(n + 4) && k.full(n + 5) && k.wait_w(C_YOP, x))) break;
+      if (!(ok = k.full(n.at(4)) && k.full(n.at(5)) && k.wait_w(C_YOP, x))) break;
       tc_fence_after();
-#pragma unroll
-      for (uint32_t p = 0; p < 3; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kTR, desc_mnmajor_h(k.slot(n + 4 + (p == 2)), ks, 8192),
-                      desc_mnmajor_h(ut + (p == 1 ? L::row_lo : 0u), ks, 8192), id_k, 1);
+      const uint64_t wh = mn_tile(k.slot(n.at(4)), 8192), wl = mn_tile(k.slot(n.at(5)), 8192);
+      mma_steps<4, true>(tmem + kTR, wh, ut, id_k);
+      mma_steps<4, true>(tmem + kTR, wh, ut + (L::row_lo >> 4), id_k);
+      mma_steps<4, true>(tmem + kTR, wl, ut, id_k);
       mma_commit_warp(&bar[C_ACC]);
-      k.release(n + 4);
-      k.release(n + 5);
-      if (x + 1 < P.N && !(ok = pd(x + 1))) break;
+      k.release(n.at(4));
+      k.release(n.at(5));
+      if (x + 1 < P.N && !(ok = pd(n.at(6)))) break;
     }
   } else if (warp >= 4 && warp < L::side) {
     const uint32_t quad = warp & 3, cg = (warp - 4) >> 2, row = quad * 32 + lane, tok = quad * 16 + (lane & 15);
@@ -935,8 +954,9 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     // diag(e^g) dO in two parts: 16 columns of a token at a time
     const uint32_t th = threadIdx.x - 32 * L::side, tok = th & 63;
     bool ok = true;
-    for (int x = 0; x < P.N && ok; ++x) {
-      const int n = 6 * x;
+    Pos n;
+#pragma unroll 1
+    for (int x = 0; x < P.N && ok; ++x, n = n.at(6)) {
       if (!(ok = k.gates_ready(x) && k.full(n) && (x == 0 || k.wait_w(C_ACC, x - 1)))) break;
       const float eg = k.gates(x)[tok];
       const uint32_t src = k.slot(n) + tok * 128;

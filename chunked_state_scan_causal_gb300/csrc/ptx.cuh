@@ -113,6 +113,27 @@ __device__ __forceinline__ bool mbar_wait_w(uint64_t *bar, uint32_t parity, vola
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, detail));
 }
 
+// mbar_wait in little code: what decides whether to give up is out of line and asked every 256 tries.  For
+// kernels whose warps run long loops with many waits, where the instructions themselves have to fit the
+// caches.
+static __device__ __noinline__ bool mbar_give_up(uint64_t *t0, volatile int *abort_flag, int *status) {
+  if (*abort_flag) return true;
+  const uint64_t now = globaltimer_ns();
+  if (*t0 == 0) *t0 = now;
+  if (now - *t0 <= kWaitLimitNs) return false;
+  report_error(status, -6);
+  *abort_flag = 1;
+  return true;
+}
+__device__ __forceinline__ bool mbar_wait_compact(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0 && mbar_give_up(&t0, abort_flag, status)) return false;
+  }
+}
+
 // ----------------------------------------------------------------------------- global flags
 __device__ __forceinline__ unsigned ld_acquire_gpu(const unsigned *p) {
   unsigned v;
