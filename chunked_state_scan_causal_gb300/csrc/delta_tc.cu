@@ -389,17 +389,18 @@ __global__ void __launch_bounds__(kPrepThreads)
 // A chunk's path is S -> (W S) -> Y -> (K^T Y) -> S: two products and two passes of the threads, each
 // bounded by its latency (reading 64 or 128 operand rows per 16 of the contraction takes 33 to 51 cycles a
 // product whatever the width).  Every role is a long loop of its own, so their instructions have to be few:
-// with unrolled products and in-line waits two CTAs on neighbouring SMs took 3.1 us a chunk, one alone 2.0.  Warps: 0 and 3 load, 1 issues the chain's products, 2 the output's, then
-// 4 VS/16 that carry the chain (16 columns each: the threads' work is on the path, so it is spread thin) and
-// 4 for the output (forward) or the scaled dO (backward).
+// with unrolled products and in-line waits two CTAs on neighbouring SMs took 3.1 us a chunk, one alone 2.0.  Warps: 1 issues the chain's products, 2 the output's, 0, 3 and the last two load, 4 and on
+// (4 VS/16) carry the chain (16 columns each: the threads' work is on the path, so it is spread thin), then 4
+// make the output (forward) or the scaled dO (backward).
 constexpr int kGateRing = 4, kSideWarps = 4;
 template <int VS>
 struct Chain {
-  static constexpr int warps = VS / 4, threads = 32 * (4 + warps + kSideWarps), side = 4 + warps;  // first side warp
-  static constexpr int slots = VS == 32 ? 11 : 9;          // ring of 16 KiB tiles, in order of use
+  static constexpr int warps = VS / 4, side = 4 + warps, threads = 32 * (side + kSideWarps + 2);  // side: first such warp
+  // four rings of tiles in order of use: two of 8 KiB, then 16 KiB ones
+  static constexpr int nx = VS == 32 ? 3 : 2, ny = VS == 32 ? 4 : 3, nz = 3, slots = 2 + nx + ny + nz;
   // operand tiles: rows of hi and lo parts side by side (VS = 32: one 128-byte row; 64: two blocks)
   static constexpr uint32_t state_lo = VS == 32 ? 64 : 16384, row_lo = VS == 32 ? 64 : 8192;
-  static constexpr uint32_t op = slots * kSlot, u0 = op + 128 * VS * 4, u1 = u0 + 64 * VS * 4,
+  static constexpr uint32_t op = (slots - 1) * kSlot, u0 = op + 128 * VS * 4, u1 = u0 + 64 * VS * 4,
                             gate = u1 + 64 * VS * 4, bar = gate + kGateRing * 2048;
   static constexpr size_t smem = bar + 512 + 1024;
 };
@@ -410,22 +411,25 @@ enum { C_OP = 0,    // S (R) operand parts ready
        C_ACC,       // its accumulator complete (next chunk)
        C_YFULL,     // Y (K R) accumulator complete
        C_YOP,       // the operand made from it for the update ready
-       C_UOP,       // forward: its operand for the output ready; backward: the scaled dO
+       C_UOP,       // (C_YOP + 1)
+                    //      // forward: its operand for the output ready; backward: the scaled dO
        C_QS, C_OFULL, C_OFREE,   // forward: Q S done; output complete, read
        C_GFULL, C_GEMPTY = C_GFULL + kGateRing, C_FULL = C_GEMPTY + kGateRing };
 
-// A place in the ring: slot and the parity of its use.  at(j): j loads further on.
-template <int SLOTS>
+// A place in a ring (slots FIRST .. FIRST + CNT - 1): slot and the parity of its use.
+template <int FIRST, int CNT>
 struct RingPos {
-  int s = 0;
+  int s = FIRST;
   uint32_t ph = 0;
-  __device__ RingPos at(int j) const {
-    RingPos r = *this;
-    r.s += j;
-    if (r.s >= SLOTS) {
-      r.s -= SLOTS;
-      r.ph ^= 1;
+  __device__ void advance() {
+    if (++s == FIRST + CNT) {
+      s = FIRST;
+      ph ^= 1;
     }
+  }
+  __device__ RingPos next() const {
+    RingPos r = *this;
+    r.advance();
     return r;
   }
 };
@@ -433,20 +437,35 @@ struct RingPos {
 // Descriptors are formed once per tile; a step of 16 along the contraction adds to the address field.
 __device__ __forceinline__ uint64_t k_tile(uint32_t tile) { return sdesc_sw128(tile, 16u, 1024u); }
 __device__ __forceinline__ uint64_t mn_tile(uint32_t tile, uint32_t block) { return sdesc_sw128(tile, block, 1024u); }
-__device__ __forceinline__ constexpr uint64_t k_step(uint32_t ks) { return (ks >> 2) * (8192u >> 4) + (ks & 3) * 2u; }
+__device__ __forceinline__ constexpr uint64_t k_step(uint32_t ks) { return ks * 2u; }
 __device__ __forceinline__ constexpr uint64_t mn_step(uint32_t ks) { return ks * 128u; }
-// D (+)= A B over KS steps; A K-major (AM = false, 64-column blocks 8 KiB apart) or MN-major, B MN-major
-template <int KS, bool AM>
-__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool fresh = false) {
+// D (+)= A B over `n` times four steps, A K-major (AM = false) or MN-major, B MN-major; a_inc and b_inc lead
+// to the next four (the next 64-column block of A, the next 64 rows of B, the other part of either).
+template <bool AM>
+__device__ __forceinline__ void mma_four(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  mma_ss_warp(d, a, b, idesc, acc);
 #pragma unroll
-  for (uint32_t ks = 0; ks < KS; ++ks)
-    mma_ss_warp(d, a + (AM ? mn_step(ks) : k_step(ks)), b + mn_step(ks), idesc, ks > 0 || !fresh);
+  for (uint32_t ks = 1; ks < 4; ++ks) mma_ss_warp(d, a + (AM ? mn_step(ks) : k_step(ks)), b + mn_step(ks), idesc, 1);
 }
+// ROLL: as a loop (less code, a few cycles more): the forward, with more roles, gains from it, the backward
+// only off its path
+template <bool AM, bool ROLL, int N>
+__device__ __forceinline__ void mma_fours(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool fresh, uint32_t a_inc,
+                                          uint32_t b_inc) {
+  if (ROLL) {
+    uint32_t acc = fresh ? 0 : 1;
+#pragma unroll 1
+    for (int i = 0; i < N; ++i, a += a_inc, b += b_inc, acc = 1) mma_four<AM>(d, a, b, idesc, acc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) mma_four<AM>(d, a + i * a_inc, b + i * b_inc, idesc, i > 0 || !fresh);
+  }
+}
+constexpr uint32_t kBlock = 8192 >> 4, kRows64 = 4 * 128;  // descriptor increments: 8 KiB; 64 rows
 
 template <int VS>
 struct ChainCtx {
   using L = Chain<VS>;
-  using Pos = RingPos<L::slots>;
   static constexpr int empty0 = C_FULL + L::slots, count = empty0 + L::slots;
   uint8_t *smem;
   uint64_t *bar;
@@ -457,8 +476,12 @@ struct ChainCtx {
     return mbar_wait_compact(&bar[idx], parity & 1, abort_flag, status);
   }
   __device__ bool wait_w(int idx, int parity) const { return __all_sync(0xffffffffu, wait(idx, parity)); }
-  __device__ uint32_t slot(Pos p) const { return base + (uint32_t)p.s * kSlot; }
+  __device__ static uint32_t offset(int s) { return s < 2 ? s * 8192u : (s - 1) * kSlot; }
+  template <typename Pos>
+  __device__ uint32_t slot(Pos p) const { return base + offset(p.s); }
+  template <typename Pos>
   __device__ bool full(Pos p) const { return wait_w(C_FULL + p.s, p.ph); }
+  template <typename Pos>
   __device__ void release(Pos p) const { mma_commit_warp(&bar[empty0 + p.s]); }
   __device__ bool gates_ready(int x) const { return wait_w(C_GFULL + x % kGateRing, x / kGateRing); }
   __device__ const float *gates(int x) const {
@@ -493,55 +516,80 @@ struct ChainCtx {
   }
 };
 
-// A loading thread's side of the ring; n: the index of a load in the order of use (two threads take some of
-// every chunk's each: a single one spends most of a chunk's time on its waits).
+// A loading thread and its ring.  Four threads share every chunk's loads, since a single one spends most of a
+// chunk's time on its waits; each has a ring of its own, since a slot's waits have to be in one thread's order;
+// and all run the same code on what they are given, since code is what they have too much of.
+struct ChainLoad {
+  const CUtensorMap *map;  // a tile of a sequence tensor; or null: an image at `off` in the record
+  uint32_t off, bytes;     // (bytes 8192: only the 64-column block of the tile that starts at column `off`)
+};
 template <int VS>
 struct ChainLoader {
-  using Pos = typename ChainCtx<VS>::Pos;
   const ChainCtx<VS> &k;
-  int h, b;
-  bool ok = true;
-  // (a fresh barrier's wait for the parity before its first phase succeeds at once: no use precedes it)
-  __device__ uint64_t *slot(Pos p, uint8_t *&dst, uint32_t bytes) {
-    if (!ok || !(ok = k.wait(ChainCtx<VS>::empty0 + p.s, p.ph ^ 1))) return nullptr;
-    dst = k.smem + p.s * kSlot;
-    mbar_arrive_expect_tx(&k.bar[C_FULL + p.s], bytes);
-    return &k.bar[C_FULL + p.s];
+  int h, b, first, end;  // the ring's slots
+  int s = first;
+  uint32_t ph = 0;
+  bool ok = true, lap = false;
+  __device__ void load(const ChainLoad &l, int c, const uint8_t *rec) {
+    // (a fresh barrier's wait for the parity before its first phase succeeds at once: no use precedes it)
+    if (!ok || !(ok = k.wait(ChainCtx<VS>::empty0 + s, ph ^ 1))) return;
+    uint8_t *dst = k.smem + k.offset(s);
+    uint64_t *full = &k.bar[C_FULL + s];
+    mbar_arrive_expect_tx(full, l.bytes);
+    if (!l.map) {
+      bulk_load(full, dst, rec + l.off, l.bytes);
+    } else {
+      tma_load_4d(l.map, full, dst, l.off, kC * c, h, b, kPolicyEvictNormal);
+      if (l.bytes == kSlot) tma_load_4d(l.map, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictNormal);
+    }
+    advance(s, ph);
+    lap |= ph != 0;
   }
-  // a 64 x 128 tile of a sequence tensor, or the 64-column block of it that holds column x
-  __device__ void tile(Pos n, const CUtensorMap *m, int c) {
-    uint8_t *dst;
-    uint64_t *full = slot(n, dst, kSlot);
-    if (!full) return;
-    tma_load_4d(m, full, dst, 0, kC * c, h, b, kPolicyEvictNormal);
-    tma_load_4d(m, full, dst + 8192, 64, kC * c, h, b, kPolicyEvictNormal);
-  }
-  __device__ void block(Pos n, const CUtensorMap *m, int c, int x) {
-    uint8_t *dst;
-    uint64_t *full = slot(n, dst, 8192);
-    if (full) tma_load_4d(m, full, dst, x / 64 * 64, kC * c, h, b, kPolicyEvictNormal);
-  }
-  __device__ void image(Pos n, const uint8_t *src) {
-    uint8_t *dst;
-    uint64_t *full = slot(n, dst, kSlot);
-    if (full) bulk_load(full, dst, src, kSlot);
+  __device__ void advance(int &at, uint32_t &parity) const {
+    if (++at == end) {
+      at = first;
+      parity ^= 1;
+    }
   }
   __device__ void gates(int x, const uint8_t *src) {
-    const int s = x % kGateRing;
-    if (!ok || (x >= kGateRing && !(ok = k.wait(C_GEMPTY + s, x / kGateRing - 1)))) return;
-    mbar_arrive_expect_tx(&k.bar[C_GFULL + s], kGateBytes);
-    bulk_load(&k.bar[C_GFULL + s], k.smem + Chain<VS>::gate + s * 2048, src, kGateBytes);
+    const int g = x % kGateRing;
+    if (!ok || (x >= kGateRing && !(ok = k.wait(C_GEMPTY + g, x / kGateRing - 1)))) return;
+    mbar_arrive_expect_tx(&k.bar[C_GFULL + g], kGateBytes);
+    bulk_load(&k.bar[C_GFULL + g], k.smem + Chain<VS>::gate + g * 2048, src, kGateBytes);
   }
-  // waits for the ring's last loads (of `total`) and the last gates (of `steps`) before the block ends; after
-  // an abort each wait has its limit
-  __device__ void drain(int total, int steps) const {
+  // One chunk after the other (step: 1 or -1), loads a then l (if it has bytes) of each, and the gates.
+  __device__ void run(int n, int c, int step, const uint8_t *rec, const ChainLoad &a, const ChainLoad &l, bool with_gates) {
+#pragma unroll 1
+    for (int x = 0; x < n && ok; ++x, c += step, rec += step * (int64_t)kRecBytes) {
+#pragma unroll 1
+      for (int y = 0; y < 2; ++y)
+        if (y == 0 || l.bytes) load(y ? l : a, c, rec);
+      if (with_gates) gates(x, rec + kRecG);
+    }
+    // waits, each with its limit, for what is in flight before the block ends: the ring's last lap and the last gates
     volatile int no_abort = 0;
-    for (int n = max(0, total - Chain<VS>::slots); n < total; ++n)
-      mbar_wait(&k.bar[C_FULL + n % Chain<VS>::slots], (n / Chain<VS>::slots) & 1, ok ? &no_abort : k.abort_flag, k.status);
-    for (int x = max(0, steps - kGateRing); x < steps; ++x)
-      mbar_wait(&k.bar[C_GFULL + x % kGateRing], (x / kGateRing) & 1, ok ? &no_abort : k.abort_flag, k.status);
+    int at = lap ? s : first;
+    uint32_t parity = lap ? ph ^ 1 : 0;
+    for (int left = lap ? end - first : s - first; left > 0; --left) {
+      mbar_wait_compact(&k.bar[C_FULL + at], parity, &no_abort, k.status);
+      advance(at, parity);
+    }
+    for (int x = with_gates && ok ? max(0, n - kGateRing) : n; x < n; ++x)
+      mbar_wait_compact(&k.bar[C_GFULL + x % kGateRing], (x / kGateRing) & 1, &no_abort, k.status);
   }
 };
+// the ring of loading thread i: 0 (8 KiB slots), x, y, z
+template <int VS>
+__device__ __forceinline__ int ring_first(int i) {
+  using L = Chain<VS>;
+  return i == 0 ? 0 : i == 1 ? 2 : i == 2 ? 2 + L::nx : i == 3 ? 2 + L::nx + L::ny : L::slots;
+}
+// the loading thread that a warp is, or -1
+template <int VS>
+__device__ __forceinline__ int loader_of(int warp) {
+  const int extra = warp - Chain<VS>::side - kSideWarps;
+  return warp == 0 ? 0 : warp == 3 ? 1 : extra >= 0 ? 2 + extra : -1;
+}
 
 // 16 values of row r, columns 16 g .. + 15 of the slice, as hi and lo parts in an operand tile (`lo`: the
 // offset of the lo parts); hi returns the former, packed
@@ -605,7 +653,10 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
                        const __grid_constant__ CUtensorMap mv, __nv_bfloat16 *o, int64_t osb, int64_t osh, int64_t ost,
                        DeltaTcParams P) {
   using L = Chain<VS>;
-  using Pos = RingPos<L::slots>;
+  using RV = RingPos<0, 2>;
+  using RX = RingPos<2, L::nx>;
+  using RY = RingPos<2 + L::nx, L::ny>;
+  using RZ = RingPos<2 + L::nx + L::ny, L::nz>;
   constexpr uint32_t kTS = 0, kTY = VS, kTQ = 3 * VS, kTP = 5 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
@@ -620,87 +671,84 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   const uint32_t tmem = *tslot;
   griddep_wait();
 
-  if (warp == 0 || warp == 3) {
+  const int loader = loader_of<VS>(warp);
+  if (loader >= 0) {
+    // V, gates | T, K | W hi, W lo | Q, P
     if (lane == 0) {
-      ChainLoader<VS> ld{k, h, b};
-      const uint8_t *rec = P.rec + (int64_t)bh * P.N * kRecBytes;
-      Pos n;
-#pragma unroll 1
-      for (int c = 0; c < P.N && ld.ok; ++c, n = n.at(7), rec += kRecBytes) {
-        if (warp == 0) {
-          ld.block(n, &mv, c, x0);
-          ld.image(n.at(1), rec + kRecT);
-          ld.image(n.at(2), rec + kRecW);
-          ld.image(n.at(3), rec + kRecW + kSlot);
-        } else {
-          ld.gates(c, rec + kRecG);
-          ld.tile(n.at(4), &mq, c);
-          ld.tile(n.at(5), &mk, c);
-          ld.image(n.at(6), rec + kRecP);
-        }
-      }
-      ld.drain(7 * P.N, P.N);
+      const ChainLoad a{loader == 0 ? &mv : loader == 3 ? &mq : nullptr,
+                        loader == 0 ? x0 / 64 * 64u : loader == 1 ? kRecT : loader == 2 ? kRecW : 0u,
+                        loader == 0 ? 8192u : kSlot};
+      const ChainLoad l{loader == 1 ? &mk : nullptr, loader == 2 ? kRecW + kSlot : loader == 3 ? kRecP : 0u,
+                        loader == 0 ? 0u : kSlot};
+      ChainLoader<VS> ld{k, h, b, ring_first<VS>(loader), ring_first<VS>(loader + 1)};
+      ld.run(P.N, 0, 1, P.rec + (int64_t)bh * P.N * kRecBytes, a, l, loader == 0);
     }
   } else if (warp == 1) {
     // the chain's own products, in the order of its dependences
     const uint32_t id_1 = idesc_bf16(64, VS, false, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
                    id_k = idesc_bf16(128, VS, true, true);
     const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, 8192);
-    auto vt = [&](Pos n) {  // Y = T V
-      if (!k.full(n) || !k.full(n.at(1))) return false;
+    RV rv;  // V
+    RX rx;  // T, K
+    RY ry;  // W hi, W lo
+    auto vt = [&] {  // Y = T V
+      if (!k.full(rv) || !k.full(rx)) return false;
       tc_fence_after();
-      const uint64_t v = mn_tile(k.slot(n) + (x0 & 63) * 2, 8192), tt = k_tile(k.slot(n.at(1)));
-      mma_steps<4, false>(tmem + kTY, tt, v, id_1, true);
-      mma_steps<4, false>(tmem + kTY, tt + (8192 >> 4), v, id_1);
-      k.release(n);
-      k.release(n.at(1));
+      const uint64_t v = mn_tile(k.slot(rv) + (x0 & 63) * 2, 8192), tt = k_tile(k.slot(rx));
+      mma_fours<false, true, 2>(tmem + kTY, tt, v, id_1, true, kBlock, 0);
+      k.release(rv);
+      k.release(rx);
+      rv.advance();
+      rx.advance();
       return true;
     };
-    Pos n;
-    bool ok = vt(n);
+    bool ok = vt();
 #pragma unroll 1
-    for (int c = 0; c < P.N && ok; ++c, n = n.at(7)) {
+    for (int c = 0; c < P.N && ok; ++c) {
       // Y += W S: hi [hi | lo] (2 VS columns), lo hi
-      if (!(ok = k.full(n.at(2)) && k.full(n.at(3)) && k.wait_w(C_OP, c))) break;
+      const RY lo = ry.next();
+      if (!(ok = k.full(ry) && k.full(lo) && k.wait_w(C_OP, c))) break;
       tc_fence_after();
-      mma_steps<8, false>(tmem + kTY, k_tile(k.slot(n.at(2))), op, id_2);
-      mma_steps<8, false>(tmem + kTY, k_tile(k.slot(n.at(3))), op, id_1);
+      mma_fours<false, true, 2>(tmem + kTY, k_tile(k.slot(ry)), op, id_2, false, kBlock, kRows64);
+      mma_fours<false, true, 2>(tmem + kTY, k_tile(k.slot(lo)), op, id_1, false, kBlock, kRows64);
       mma_commit_warp(&bar[C_YFULL]);
-      k.release(n.at(2));
-      k.release(n.at(3));
+      k.release(ry);
+      k.release(lo);
+      ry = lo.next();
       // S += K^T diag(phi b) Y
-      if (!(ok = k.full(n.at(5)) && k.wait_w(C_SCALED, c) && k.wait_w(C_YOP, c))) break;
+      if (!(ok = k.full(rx) && k.wait_w(C_SCALED, c) && k.wait_w(C_YOP, c))) break;
       tc_fence_after();
-      const uint64_t kt = mn_tile(k.slot(n.at(5)), 8192);
-      mma_steps<4, true>(tmem + kTS, kt, ut, id_k);
-      mma_steps<4, true>(tmem + kTS, kt, ut + (L::row_lo >> 4), id_k);
+      mma_fours<true, true, 2>(tmem + kTS, mn_tile(k.slot(rx), 8192), ut, id_k, false, 0, L::row_lo >> 4);
       mma_commit_warp(&bar[C_ACC]);
-      k.release(n.at(5));
-      if (c + 1 < P.N && !(ok = vt(n.at(7)))) break;
+      k.release(rx);
+      rx.advance();
+      if (c + 1 < P.N && !(ok = vt())) break;
     }
   } else if (warp == 2) {
     // the output's products, put into the gaps that the chain leaves the tensor cores: Q S while the
     // threads turn Y into operands, P Y while they turn S into operands
     const uint32_t id_1 = idesc_bf16(64, VS, false, true), id_2 = idesc_bf16(64, 2 * VS, false, true);
     const uint64_t op = mn_tile(k.base + L::op, L::state_lo), u = mn_tile(k.base + L::u1, L::row_lo);
-    Pos n;
+    RZ rz;  // Q, P
     bool ok = true;
 #pragma unroll 1
-    for (int c = 0; c < P.N && ok; ++c, n = n.at(7)) {
-      if (!(ok = k.full(n.at(4)) && (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.wait_w(C_YFULL, c))) break;
+    for (int c = 0; c < P.N && ok; ++c) {
+      if (!(ok = k.full(rz) && (c == 0 || k.wait_w(C_OFREE, c - 1)) && k.wait_w(C_YFULL, c))) break;
       tc_fence_after();
-      mma_steps<8, false>(tmem + kTQ, k_tile(k.slot(n.at(4))), op, id_2, true);
+      mma_fours<false, true, 2>(tmem + kTQ, k_tile(k.slot(rz)), op, id_2, true, kBlock, kRows64);
       mma_commit_warp(&bar[C_QS]);
-      k.release(n.at(4));
-      if (!(ok = k.full(n.at(6)) && k.wait_w(C_UOP, c) && k.wait_w(C_ACC, c))) break;
+      k.release(rz);
+      rz.advance();
+      if (!(ok = k.full(rz) && k.wait_w(C_UOP, c) && k.wait_w(C_ACC, c))) break;
       tc_fence_after();
-      const uint64_t pp = k_tile(k.slot(n.at(6)));
-      mma_steps<4, false>(tmem + kTP, pp, u, id_2, true);
-      mma_steps<4, false>(tmem + kTP, pp + (8192 >> 4), u, id_1);
+      const uint64_t pp = k_tile(k.slot(rz));
+      mma_fours<false, true, 1>(tmem + kTP, pp, u, id_2, true, 0, 0);
+      mma_fours<false, true, 1>(tmem + kTP, pp + kBlock, u, id_1, false, 0, 0);
       mma_commit_warp(&bar[C_OFULL]);
-      k.release(n.at(6));
+      k.release(rz);
+      rz.advance();
     }
-  } else if (warp >= 4 && warp < L::side) {
+  } else if (warp < L::side) {
     // S: key dimension `row`; Y: token `tok` (lanes 0..15); columns 16 cg .. + 15 of the slice
     const uint32_t quad = warp & 3, cg = (warp - 4) >> 2, row = quad * 32 + lane, tok = quad * 16 + (lane & 15);
     const uint32_t t = tmem + ((quad * 32) << 16) + 16 * cg;
@@ -749,19 +797,17 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       tmem_ld_wait();
       tmem_stf(t + kTY + VS, zero);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        y[j] += z[j];
-        z[j] = phi * be * y[j];
-      }
-      if (lane < 16) put_split<VS>(k.base + L::u0, L::row_lo, tok, cg, z, hi);
+      for (int j = 0; j < 16; ++j) y[j] += z[j];
       tmem_st_wait();
-      fence_proxy_async_smem();
-      k.arrive(C_YOP, lane);
+      float w = phi * be;  // the update's factor, then the output's
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e, w = be) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) z[j] = be * y[j];
-      if (lane < 16) put_split<VS>(k.base + L::u1, L::row_lo, tok, cg, z, hi);
-      fence_proxy_async_smem();
-      k.arrive(C_UOP, lane);
+        for (int j = 0; j < 16; ++j) z[j] = w * y[j];
+        if (lane < 16) put_split<VS>(k.base + L::u0 + e * (L::u1 - L::u0), L::row_lo, tok, cg, z, hi);
+        fence_proxy_async_smem();
+        k.arrive(C_YOP + e, lane);
+      }
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
       if (P.yimg && lane < 16) {
 #pragma unroll
@@ -769,7 +815,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
         store_row8(P.yimg + ((int64_t)bh * P.N + c) * kRowImg + (gcol >> 6) * 8192, tok, (gcol & 63) >> 4, hi);
       }
     }
-  } else if (warp >= L::side) {
+  } else {
     // O = diag(e^g) Q S + P diag(b) Y, a token per lane (lanes 0..15)
     const uint32_t quad = warp & 3, tok = quad * 16 + (lane & 15), t = tmem + ((quad * 32) << 16);
     __nv_bfloat16 *dst = o + b * osb + h * osh + x0;
@@ -779,7 +825,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       tc_fence_after();
       const float eg = k.gates(c)[tok];
       const bool in = lane < 16 && kC * c + (int)tok < P.T;
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < VS / 16; ++x) {
         float q[2][16], p[2][16];
 #pragma unroll
@@ -814,7 +860,10 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     delta_reverse_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mdo, DeltaTcParams P) {
   using L = Chain<VS>;
-  using Pos = RingPos<L::slots>;
+  using RV = RingPos<0, 2>;
+  using RX = RingPos<2, L::nx>;
+  using RY = RingPos<2 + L::nx, L::ny>;
+  using RZ = RingPos<2 + L::nx + L::ny, L::nz>;
   constexpr uint32_t kTR = 0, kT1 = VS, kT2 = 2 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
@@ -829,71 +878,68 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   griddep_wait();
 
   // step x of the walk is chunk N - 1 - x
-  if (warp == 0 || warp == 3) {
+  const int loader = loader_of<VS>(warp);
+  if (loader >= 0) {
+    // dO, gates | P, K | W hi, W lo | Q
     if (lane == 0) {
-      ChainLoader<VS> ld{k, h, b};
-      Pos n;
-#pragma unroll 1
-      for (int x = 0; x < P.N && ld.ok; ++x, n = n.at(6)) {
-        const int c = P.N - 1 - x;
-        const uint8_t *rec = P.rec + ((int64_t)bh * P.N + c) * kRecBytes;
-        if (warp == 0) {
-          ld.block(n, &mdo, c, x0);
-          ld.image(n.at(1), rec + kRecP);
-          ld.tile(n.at(2), &mk, c);
-        } else {
-          ld.gates(x, rec + kRecG);
-          ld.tile(n.at(3), &mq, c);
-          ld.image(n.at(4), rec + kRecW);
-          ld.image(n.at(5), rec + kRecW + kSlot);
-        }
-      }
-      ld.drain(6 * P.N, P.N);
+      const ChainLoad a{loader == 0 ? &mdo : loader == 3 ? &mq : nullptr,
+                        loader == 0 ? x0 / 64 * 64u : loader == 1 ? kRecP : loader == 2 ? kRecW : 0u,
+                        loader == 0 ? 8192u : kSlot};
+      const ChainLoad l{loader == 1 ? &mk : nullptr, loader == 2 ? kRecW + kSlot : 0u,
+                        loader == 0 || loader == 3 ? 0u : kSlot};
+      ChainLoader<VS> ld{k, h, b, ring_first<VS>(loader), ring_first<VS>(loader + 1)};
+      ld.run(P.N, P.N - 1, -1, P.rec + ((int64_t)bh * P.N + P.N - 1) * kRecBytes, a, l, loader == 0);
     }
   } else if (warp == 1) {
     const uint32_t id_p = idesc_bf16(64, VS, true, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
                    id_k = idesc_bf16(128, VS, true, true);
     const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, 8192),
                    dos = mn_tile(k.base + L::u1, 8192);
-    auto pd = [&](Pos n) {  // P^T dO
-      if (!k.full(n) || !k.full(n.at(1))) return false;
+    RV rv;  // dO
+    RX rx;  // P, K
+    RY ry;  // W hi, W lo
+    RZ rz;  // Q
+    auto pd = [&](RV d) {  // P^T dO
+      if (!k.full(d) || !k.full(rx)) return false;
       tc_fence_after();
-      const uint64_t pp = mn_tile(k.slot(n.at(1)), 8192), d = mn_tile(k.slot(n) + (x0 & 63) * 2, 8192);
-      mma_steps<4, true>(tmem + kT1, pp, d, id_p, true);
-      mma_steps<4, true>(tmem + kT1, pp + (8192 >> 4), d, id_p);
-      k.release(n.at(1));
+      mma_fours<true, true, 2>(tmem + kT1, mn_tile(k.slot(rx), 8192), mn_tile(k.slot(d) + (x0 & 63) * 2, 8192), id_p, true,
+                               kBlock, 0);
+      k.release(rx);
+      rx.advance();
       return true;
     };
-    Pos n;
-    bool ok = pd(n);
+    bool ok = pd(rv);
 #pragma unroll 1
-    for (int x = 0; x < P.N && ok; ++x, n = n.at(6)) {
-      if (!(ok = k.full(n.at(2)) && k.wait_w(C_OP, x))) break;
+    for (int x = 0; x < P.N && ok; ++x) {
+      if (!(ok = k.full(rx) && k.wait_w(C_OP, x))) break;
       tc_fence_after();
-      mma_steps<8, false>(tmem + kT2, k_tile(k.slot(n.at(2))), op, id_2, true);  // K R
+      mma_fours<false, false, 2>(tmem + kT2, k_tile(k.slot(rx)), op, id_2, true, kBlock, kRows64);  // K R
       mma_commit_warp(&bar[C_YFULL]);
-      k.release(n.at(2));
+      k.release(rx);
+      rx.advance();
       // R += Q^T diag(e^g) dO
-      if (!(ok = k.full(n.at(3)) && k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x))) break;
+      if (!(ok = k.full(rz) && k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x))) break;
       tc_fence_after();
-      const uint64_t qt = mn_tile(k.slot(n.at(3)), 8192);
-      mma_steps<4, true>(tmem + kTR, qt, dos, id_k);
-      mma_steps<4, true>(tmem + kTR, qt, dos + (L::row_lo >> 4), id_k);
-      k.release(n.at(3));
-      k.release(n);  // the scaled dO is ready: every reader of this tile is done
+      mma_fours<true, false, 2>(tmem + kTR, mn_tile(k.slot(rz), 8192), dos, id_k, false, 0, L::row_lo >> 4);
+      k.release(rz);
+      rz.advance();
+      k.release(rv);  // the scaled dO is ready: every reader of this tile is done
+      rv.advance();
       // R += W^T diag(b) dU: hi hi, hi lo, lo hi
-      if (!(ok = k.full(n.at(4)) && k.full(n.at(5)) && k.wait_w(C_YOP, x))) break;
+      const RY lo = ry.next();
+      if (!(ok = k.full(ry) && k.full(lo) && k.wait_w(C_YOP, x))) break;
       tc_fence_after();
-      const uint64_t wh = mn_tile(k.slot(n.at(4)), 8192), wl = mn_tile(k.slot(n.at(5)), 8192);
-      mma_steps<4, true>(tmem + kTR, wh, ut, id_k);
-      mma_steps<4, true>(tmem + kTR, wh, ut + (L::row_lo >> 4), id_k);
-      mma_steps<4, true>(tmem + kTR, wl, ut, id_k);
+      mma_fours<true, false, 2>(tmem + kTR, mn_tile(k.slot(ry), 8192), ut, id_k, false, 0, L::row_lo >> 4);
+      mma_fours<true, false, 1>(tmem + kTR, mn_tile(k.slot(lo), 8192), ut, id_k, false, 0, 0);
       mma_commit_warp(&bar[C_ACC]);
-      k.release(n.at(4));
-      k.release(n.at(5));
-      if (x + 1 < P.N && !(ok = pd(n.at(6)))) break;
+      k.release(ry);
+      k.release(lo);
+      ry = lo.next();
+      if (x + 1 < P.N && !(ok = pd(rv))) break;
     }
-  } else if (warp >= 4 && warp < L::side) {
+  } else if (warp == 2) {
+    // (the forward's output products)
+  } else if (warp < L::side) {
     const uint32_t quad = warp & 3, cg = (warp - 4) >> 2, row = quad * 32 + lane, tok = quad * 16 + (lane & 15);
     const uint32_t t = tmem + ((quad * 32) << 16) + 16 * cg;
     const uint32_t gcol = x0 + 16 * cg;
@@ -950,13 +996,13 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
         store_row8(P.uimg + ci * kRowImg + (gcol >> 6) * 8192, tok, (gcol & 63) >> 4, hi);
       }
     }
-  } else if (warp >= L::side) {
+  } else {
     // diag(e^g) dO in two parts: 16 columns of a token at a time
     const uint32_t th = threadIdx.x - 32 * L::side, tok = th & 63;
     bool ok = true;
-    Pos n;
+    RV n;
 #pragma unroll 1
-    for (int x = 0; x < P.N && ok; ++x, n = n.at(6)) {
+    for (int x = 0; x < P.N && ok; ++x, n.advance()) {
       if (!(ok = k.gates_ready(x) && k.full(n) && (x == 0 || k.wait_w(C_ACC, x - 1)))) break;
       const float eg = k.gates(x)[tok];
       const uint32_t src = k.slot(n) + tok * 128;

@@ -126,6 +126,13 @@ def test_repeated_keys(dtype):
     assert rel(got[0], o) < TOL[dtype]["out"] and rel(got[1], fin) < TOL[dtype]["state"]
 
 
+@pytest.mark.parametrize("B,H,T,d", [(2, 20, 200, 128), (5, 16, 70, 64), (1, 160, 65, 128)])
+def test_many_heads(B, H, T, d):
+    """More (batch, head, slice)s than the GPU has SMs: the wider slices, and several waves of them."""
+    c = case(15, B, H, T, d, BF16)
+    check(c, run(c))
+
+
 def test_longer_bf16():
     c = case(9, 1, 3, 1000, 128, BF16, decay=0.05)
     check(c, run(c))
