@@ -38,7 +38,7 @@ constexpr uint32_t kSlot = 16384;         // a 64 x 128 (or 128 x 64) bf16 tile
 // ready for a plain bulk copy; then five fp32 rows of 64: e^g, phi, b, g and its low part (log2 units).
 constexpr uint32_t kRecW = 0, kRecT = 32768, kRecP = 49152, kRecG = 65536, kGateBytes = 5 * 64 * 4;
 constexpr size_t kRecBytes = 67584;
-constexpr size_t kStateImg = 32768, kRowImg = 16384;
+constexpr size_t kStateImg = 32768, kRowImg = 16384, kYImg = 2 * kRowImg;  // Y: hi, lo
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
   return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
@@ -76,18 +76,18 @@ __device__ __forceinline__ float ld_shared_bf16(uint32_t addr) {
 }
 __device__ __forceinline__ float2 ld_shared_f2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 
-// Column sums over a warp: on return lane l holds the sum over all lanes of x[l].
-__device__ __forceinline__ float warp_col_sum(float (&x)[32], int lane) {
+// Column sums over a warp of 16 values per lane: on return lane l holds the sum over all lanes of x[l / 2].
+__device__ __forceinline__ float warp_col_sum(float (&x)[16], int lane) {
 #pragma unroll
-  for (int n = 16; n >= 1; n /= 2) {
-    const bool up = lane & n;
+  for (int n = 8; n >= 1; n /= 2) {
+    const bool up = lane & (2 * n);
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
-      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, n);
+      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * n);
     }
   }
-  return x[0];
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
 }
 
 struct DeltaTcParams {
@@ -95,8 +95,9 @@ struct DeltaTcParams {
   int f32;                 // type of the gates
   const void *lg, *beta;
   uint8_t *rec;            // [BH][N] records
-  uint8_t *simg, *yimg;    // [BH][N] images of S entering the chunks, of Y (or null: not kept)
-  uint8_t *rimg, *uimg;    // backward: [BH][N] images of R and of dU
+  uint8_t *simg, *yimg;    // [BH][N] images of S entering the chunks, of Y in two parts (or null: not kept)
+  uint8_t *rimg, *uimg;    // backward: [BH][N] images of R and of diag(b) dU
+  float *dot;              // backward: [BH][N][64][8] parts of dU . y (16 value dimensions each)
   const float *in;         // initial state, or the final state's gradient (or null)
   float *out;              // final state, or the initial state's gradient (or null)
   float *anchor;           // backward: [BH][N] <R, S> at the chunks' ends
@@ -609,9 +610,10 @@ __device__ __forceinline__ void put_split(uint32_t tile, uint32_t lo, uint32_t r
 
 // 8 packed words (16 columns) of row r, column group m of a swizzled block in global memory, as one 32-byte
 // store: the swizzle moves pairs of pieces and, in odd rows, swaps a pair.
+__device__ __forceinline__ uint32_t row8(uint32_t r, uint32_t m) { return r * 128u + ((m ^ ((r & 7u) >> 1)) << 5); }
 __device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t m, const uint32_t (&w)[8]) {
   const bool odd = r & 1u;
-  uint8_t *dst = block + r * 128u + ((m ^ ((r & 7u) >> 1)) << 5);
+  uint8_t *dst = block + row8(r, m);
   uint32_t v[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -621,6 +623,19 @@ __device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t 
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+// the words that store_row8 wrote, from their place
+__device__ __forceinline__ void load_row8(const uint8_t *src, uint32_t r, uint32_t (&w)[8]) {
+  const uint4 a = reinterpret_cast<const uint4 *>(src)[r & 1u], b = reinterpret_cast<const uint4 *>(src)[~r & 1u];
+  w[0] = a.x;
+  w[1] = a.y;
+  w[2] = a.z;
+  w[3] = a.w;
+  w[4] = b.x;
+  w[5] = b.y;
+  w[6] = b.z;
+  w[7] = b.w;
 }
 
 // 16 columns of a state row in global memory (fp32, row and columns inside d)
@@ -810,9 +825,12 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       }
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
       if (P.yimg && lane < 16) {
+        uint32_t lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) hi[j] = pack_bf16(y[2 * j], y[2 * j + 1]);
-        store_row8(P.yimg + ((int64_t)bh * P.N + c) * kRowImg + (gcol >> 6) * 8192, tok, (gcol & 63) >> 4, hi);
+        for (int j = 0; j < 8; ++j) split2(y[2 * j], y[2 * j + 1], hi[j], lo[j]);
+        uint8_t *img = P.yimg + ((int64_t)bh * P.N + c) * kYImg + (gcol >> 6) * 8192;
+        store_row8(img, tok, (gcol & 63) >> 4, hi);
+        store_row8(img + kRowImg, tok, (gcol & 63) >> 4, lo);
       }
     }
   } else {
@@ -974,6 +992,9 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
       store_row8(P.rimg + ci * kStateImg + (gcol >> 6) * 16384, row, (gcol & 63) >> 4, hi);
+      const uint8_t *yrow = P.yimg + ci * kYImg + (gcol >> 6) * 8192 + row8(tok, (gcol & 63) >> 4);
+      prefetch_l1(yrow);
+      prefetch_l1(yrow + kRowImg);
       if (!(ok = k.wait_w(C_YFULL, x))) break;
       tc_fence_after();
       float u[16], v[16], w[16];
@@ -991,9 +1012,16 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       k.arrive(C_YOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
       if (lane < 16) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) hi[j] = pack_bf16(u[2 * j], u[2 * j + 1]);
+        // (hi: diag(b) dU)
         store_row8(P.uimg + ci * kRowImg + (gcol >> 6) * 8192, tok, (gcol & 63) >> 4, hi);
+        float dot = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          load_row8(yrow + e * kRowImg, tok, hi);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dot = fmaf(u[2 * j], bf16lo(hi[j]), fmaf(u[2 * j + 1], bf16hi(hi[j]), dot));
+        }
+        P.dot[(ci * kC + tok) * 8 + (gcol >> 4)] = dot;
       }
     }
   } else {
@@ -1031,36 +1059,45 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 }
 
 // ================================================================== gradients of a chunk
-// One CTA per chunk, 256 threads.  Products of the form [dimension x token] keep lane = dimension, as in
-// the chains; the 64 x 64 ones come from 128-row operands whose other rows are unused: [K; dO] stacked
-// gives K K^T in lanes 0..63 and dO Y^T in lanes 64..127.
-constexpr int kGradThreads = 256;
-constexpr uint32_t kGrKD = 0, kGrQ = 32768, kGrS = 49152, kGrR = 81920, kGrY = 114688, kGrU = 131072, kGrT = 147456,
-                   kGrZ = 163840, kGrD = 180224, kGrA = 188416, kGrV = 196608, kGrG = 212992, kGrEnd = 215040;
+// Chunk after chunk, independent of each other, on one CTA per SM.  Products of the form [dimension x token]
+// have lane = dimension; the 64 x 64 ones come from 128-row operands whose other rows are unused: [K; dO]
+// stacked gives K K^T in lanes 0..63 and dO Y^T in lanes 64..127.  Warps 0..15 turn products into operands and
+// results (16 columns each); warp 16 loads, issues the products and stores, so that while the threads are in
+// one chunk's last step the next one's tiles arrive and its first product runs.  Bound by the 88 products of a
+// chunk (their operand rows, about 50 cycles each) and the latencies between its five steps.
+//
+// Single bf16 operands except Y in dO Y^T and the matrix A made from it, which have two parts: with one the
+// gradients' errors come to 2.9e-3 of their size, 1.75 times the rounding of the results themselves.
+constexpr int kGradThreads = 544, kGradWarps = 16;
+constexpr uint32_t kGrKD = 0, kGrQ = 32768, kGrS = 49152, kGrR = 81920, kGrY = 114688, kGrU = 147456, kGrZ = 163840,
+                   kGrA = 180224,           // A hi, A lo, D (8 KiB each); T lives over the last two before them
+                   kGrX = 204800, kGrG = 221184, kGrEnd = kGrG + 2 * 1536;
+constexpr uint32_t kGrT = kGrA + 8192, kGrD = kGrA + 16384;
 constexpr size_t kGradSmem = kGrEnd + 1024;
-constexpr uint32_t kGZ = 0, kGKK = 128, kGdP = 192, kGGY = 256, kGdq = 320, kGdr = 384, kGdw = 448;
+static_assert(kGradSmem + 4096 <= 232448, "one CTA per SM");
+constexpr uint32_t kGZ = 0, kGKK = 64, kGdP = 128, kGGY = 192, kGdq = 256, kGdr = 320, kGdw = 384;
+enum { G_UT = 0, G_SR, G_KQ,      // loads: diag(b) dU, T, Y, gates; S, R; K, dO, Q
+       G_Z, G_64, G_ALL,          // products: Z; the 64 x 64 ones; all
+       G_ZT, G_AD, G_END,         // the threads: Z tile and dv ready; A and D; the chunk's results in place
+       G_STORED,                  // dq and dk have left shared memory
+       G_COUNT };
 
 __global__ void __launch_bounds__(kGradThreads, 1)
     delta_grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                       const __grid_constant__ CUtensorMap mdo, const __grid_constant__ CUtensorMap mdq,
                       const __grid_constant__ CUtensorMap mdk, const __grid_constant__ CUtensorMap mdv,
-                      DeltaTcParams P) {
+                      DeltaTcParams P, int items) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
-  __shared__ uint64_t bar[6];
+  __shared__ uint64_t bar[G_COUNT];
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
-  __shared__ float s_dot[4][kC], s_col[2][kC], s_x[4][kC], s_rs[8], s_kw[8];
+  __shared__ float s_col[2][kC], s_x[4][kC], s_rs[kGradWarps], s_kw[kGradWarps], s_last;
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const uint32_t quad = warp & 3, hf = warp >> 2, row = quad * 32 + lane;
-  const int c = blockIdx.x % P.N, bh = blockIdx.x / P.N, b = bh / P.H, h = bh % P.H;
-  const int64_t ci = (int64_t)bh * P.N + c;
-  const float *g = reinterpret_cast<const float *>(smem + kGrG);
-
   if (tid == 0) {
     abort_flag = 0;
-    for (int i = 0; i < 6; ++i) mbar_init(&bar[i], 1);
+    for (int i = 0; i < G_COUNT; ++i) mbar_init(&bar[i], i == G_ZT || i == G_AD || i == G_END ? kGradWarps : 1);
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -1070,270 +1107,285 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tslot, t = tmem + ((quad * 32) << 16);
+  const uint32_t tmem = tslot;
   griddep_wait();
-  if (tid == 0) {
-    const uint8_t *rec = P.rec + ci * kRecBytes;
-    mbar_arrive_expect_tx(&bar[0], 3 * 16384 + 16384 + kGateBytes + 16384);
-    bulk_load(&bar[0], smem + kGrU, P.uimg + ci * kRowImg, 16384);
-    bulk_load(&bar[0], smem + kGrG, rec + kRecG, kGateBytes);
-    bulk_load(&bar[0], smem + kGrT, rec + kRecT, 16384);
-    bulk_load(&bar[0], smem + kGrY, P.yimg + ci * kRowImg, 16384);
-    for (int x = 0; x < 2; ++x) {
-      tma_load_4d(&mk, &bar[0], smem + kGrKD + x * 16384, 64 * x, kC * c, h, b, kPolicyEvictNormal);
-      tma_load_4d(&mdo, &bar[0], smem + kGrKD + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
-    }
-    mbar_arrive_expect_tx(&bar[1], 32768 + 32768 + 16384);
-    bulk_load(&bar[1], smem + kGrS, P.simg + ((int64_t)bh * P.N + c) * kStateImg, 32768);
-    bulk_load(&bar[1], smem + kGrR, P.rimg + ci * kStateImg, 32768);
-    for (int x = 0; x < 2; ++x)
-      tma_load_4d(&mq, &bar[1], smem + kGrQ + x * 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
-  }
-  const uint32_t KD = base + kGrKD, dO = KD + 8192, Y = base + kGrY, Z = base + kGrZ, S = base + kGrS, R = base + kGrR;
-  // contractions over value dimensions: d = 64 has no others (the images hold nothing there)
-  const uint32_t kd = P.d / 16;
-  const uint32_t id_mm = idesc_bf16(128, 64, true, true), id_mk = idesc_bf16(128, 64, true, false),
-                 id_km = idesc_bf16(128, 64, false, true), id_kk = idesc_bf16(128, 64, false, false);
-  bool ok = mbar_wait(&bar[0], 0, &abort_flag, P.status);
-  if (__syncthreads_and(ok)) {
-    // diag(b) dU as an operand (over the place of Z), and dU . y: a quarter of a token's row per thread
-    {
-      const uint32_t tok = tid & 63, q = tid >> 6;  // columns 32 q .. + 31
-      const float be = g[128 + tok];
-      float dot = 0.f;
-#pragma unroll
-      for (uint32_t p = 0; p < 4; ++p) {
-        uint32_t u[4], y[4];
-        const uint32_t at = (q >> 1) * 8192 + sw(tok, 4 * (q & 1) + p);
-        ld_shared_v4(base + kGrU + at, u[0], u[1], u[2], u[3]);
-        ld_shared_v4(Y + at, y[0], y[1], y[2], y[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          dot = fmaf(bf16lo(u[e]), bf16lo(y[e]), fmaf(bf16hi(u[e]), bf16hi(y[e]), dot));
-          u[e] = pack_bf16(be * bf16lo(u[e]), be * bf16hi(u[e]));
-        }
-        st_shared_v4(Z + at, u[0], u[1], u[2], u[3]);
-      }
-      s_dot[q][tok] = 32 * (int)q < P.d ? dot : 0.f;
-    }
-    fence_proxy_async_smem();
+  auto wait = [&](int i, int parity) {
+    return __all_sync(0xffffffffu, mbar_wait_compact(&bar[i], parity & 1, &abort_flag, P.status));
+  };
+  auto arrive = [&](int i) {
     tc_fence_before();
-    __syncthreads();
-    if (warp == 0) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar[i]);
+  };
+  const uint32_t KD = base + kGrKD, dO = KD + 8192, Y = base + kGrY, Z = base + kGrZ, S = base + kGrS, R = base + kGrR;
+  bool ok = true;
+
+  if (warp == kGradWarps) {
+    // contractions over value dimensions: d = 64 has no others (the images hold nothing there)
+    const int kd = P.d / 64;
+    const uint32_t id_mm = idesc_bf16(128, 64, true, true), id_mk = idesc_bf16(128, 64, true, false),
+                   id_km = idesc_bf16(128, 64, false, true), id_kk = idesc_bf16(128, 64, false, false);
+    // D (+)= A B over n times four steps of 16; a_step and b_step within four, a_inc and b_inc to the next four
+    auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool fresh, int n, uint32_t a_step, uint32_t a_inc,
+                   uint32_t b_step, uint32_t b_inc) {
+      uint32_t acc = fresh ? 0 : 1;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i, a += a_inc, b += b_inc) {
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks, acc = 1) mma_ss_warp(tmem + d, a + ks * a_step, b + ks * b_step, id, acc);
+      }
+    };
+    constexpr uint32_t kK = 2, kM = 128, k8 = 8192 >> 4, k16 = 16384 >> 4;  // K-major and MN-major steps; blocks
+    auto load1 = [&](int item) {
+      if (lane != 0) return;
+      const int c = item % P.N, bh = item / P.N, g = (item - blockIdx.x) / gridDim.x & 1;
+      const int64_t ci = (int64_t)bh * P.N + c;
+      const uint8_t *rec = P.rec + ci * kRecBytes;
+      mbar_arrive_expect_tx(&bar[G_UT], 16384 + kGateBytes + 16384 + 32768);
+      bulk_load(&bar[G_UT], smem + kGrU, P.uimg + ci * kRowImg, 16384);
+      bulk_load(&bar[G_UT], smem + kGrT, rec + kRecT, 16384);
+      bulk_load(&bar[G_UT], smem + kGrG + g * 1536, rec + kRecG, kGateBytes);
+      bulk_load(&bar[G_UT], smem + kGrY, P.yimg + ci * kYImg, 32768);
+      mbar_arrive_expect_tx(&bar[G_SR], 65536);
+      bulk_load(&bar[G_SR], smem + kGrS, P.simg + ci * kStateImg, 32768);
+      bulk_load(&bar[G_SR], smem + kGrR, P.rimg + ci * kStateImg, 32768);
+    };
+    auto load2 = [&](int item) {
+      if (lane != 0) return;
+      const int c = item % P.N, bh = item / P.N, b = bh / P.H, h = bh % P.H;
+      mbar_arrive_expect_tx(&bar[G_KQ], 49152);
+      for (int x = 0; x < 2; ++x) {
+        tma_load_4d(&mk, &bar[G_KQ], smem + kGrKD + x * 16384, 64 * x, kC * c, h, b, kPolicyEvictFirst);
+        tma_load_4d(&mdo, &bar[G_KQ], smem + kGrKD + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictFirst);
+        tma_load_4d(&mq, &bar[G_KQ], smem + kGrQ + x * 8192, 64 * x, kC * c, h, b, kPolicyEvictFirst);
+      }
+    };
+    auto store = [&](const CUtensorMap *m, uint32_t from, int item) {
+      const int c = item % P.N, bh = item / P.N, b = bh / P.H, h = bh % P.H;
+      for (int y = 0; y < P.d / 64; ++y) tma_store_4d(m, smem + from + y * 8192, 64 * y, kC * c, h, b);
+      bulk_commit();
+    };
+    int x = 0, last = 0;  // (loads issued: x + 1 of the first kind, last + 1 of the second)
+    if ((int)blockIdx.x < items) {
+      load1(blockIdx.x);
+      load2(blockIdx.x);
+    }
+#pragma unroll 1
+    for (int item = blockIdx.x; item < items; item += gridDim.x, ++x) {
+      const uint64_t y = k_tile(Y), ylo = k_tile(Y + 16384), zm = mn_tile(Z, 16384), sk = k_tile(S), rk = k_tile(R),
+                     km = mn_tile(KD, 16384), kk = k_tile(KD), am = mn_tile(base + kGrA, 8192), ak = k_tile(base + kGrA),
+                     dm = mn_tile(base + kGrD, 8192), dk = k_tile(base + kGrD), qm = mn_tile(base + kGrQ, 8192);
+      if (!(ok = wait(G_UT, x))) break;
       tc_fence_after();
       // Z^T = (diag(b) dU)^T T
-#pragma unroll
-      for (uint32_t p = 0; p < 2; ++p)
-#pragma unroll
-        for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + kGZ, desc_mnmajor_h(Z, ks, 8192), desc_mnmajor_h(base + kGrT + p * 8192, ks, 8192), id_mm,
-                      p + ks > 0);
-      mma_commit_warp(&bar[2]);
-#pragma unroll
-      for (uint32_t ks = 0; ks < 8; ++ks)
-        mma_ss_warp(tmem + kGKK, desc_kmajor(KD, ks), desc_kmajor(KD, ks), id_kk, ks > 0);
-#pragma unroll 4
-      for (uint32_t ks = 0; ks < kd; ++ks)
-        mma_ss_warp(tmem + kGdP, desc_kmajor(KD, ks), desc_kmajor_h(Y, ks, 8192), id_kk, ks > 0);
-      ok = mbar_wait_w(&bar[1], 0, &abort_flag, P.status);
-      if (ok) {
-#pragma unroll 4
-        for (uint32_t ks = 0; ks < kd; ++ks)  // (dO S^T)^T
-          mma_ss_warp(tmem + kGdq, desc_kmajor(S, ks), desc_kmajor(dO, ks), id_kk, ks > 0);
-#pragma unroll 4
-        for (uint32_t ks = 0; ks < kd; ++ks)  // (Y R^T)^T
-          mma_ss_warp(tmem + kGdw, desc_kmajor(R, ks), desc_kmajor_h(Y, ks, 8192), id_kk, ks > 0);
+      mma(kGZ, mn_tile(base + kGrU, 8192), mn_tile(base + kGrT, 8192), id_mm, true, 2, kM, 0, kM, k8);
+      mma_commit_warp(&bar[G_Z]);
+      // the accumulators that follow were read in the last chunk's last step
+      if (x > 0) {
+        if (!(ok = wait(G_END, x - 1))) break;
+        load2(item);
+        ++last;
+        if (lane == 0) {
+          store(&mdq, kGrZ, item - gridDim.x);
+          store(&mdk, kGrX, item - gridDim.x);
+          bulk_wait_read_all();
+          mbar_arrive(&bar[G_STORED]);
+        }
+        __syncwarp();
       }
-    }
-    ok = ok && mbar_wait(&bar[2], 0, &abort_flag, P.status);
-  }
-  if (__syncthreads_and(ok)) {
-    tc_fence_after();
-    {
-      // Z: an operand tile (row = value dimension) and dv
-      float z[32];
-      tmem_ld32(t + kGZ + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&z));
-      tmem_ld_wait();
-#pragma unroll
-      for (uint32_t p = 0; p < 4; ++p)
-        st_shared_v4(Z + sw(row, 4 * hf + p), pack_bf16(z[8 * p], z[8 * p + 1]), pack_bf16(z[8 * p + 2], z[8 * p + 3]),
-                     pack_bf16(z[8 * p + 4], z[8 * p + 5]), pack_bf16(z[8 * p + 6], z[8 * p + 7]));
-#pragma unroll
-      for (int j = 0; j < 32; ++j) st_shared_u16(base + kGrV + sw_el(32 * hf + j, row, 8192), z[j]);
-    }
-    tc_fence_before();
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      tma_store_4d(&mdv, smem + kGrV, 0, kC * c, h, b);
-      if (P.d == 128) tma_store_4d(&mdv, smem + kGrV + 8192, 64, kC * c, h, b);
-      bulk_commit();
-    }
-    if (warp == 0) {
+      if (!(ok = wait(G_KQ, x))) break;
+      tc_fence_after();
+      mma(kGKK, kk, kk, id_kk, true, 2, kK, k16, kK, k16);                 // K K^T (lanes 0..63)
+      mma(kGdP, kk, y, id_kk, true, kd, kK, k16, kK, k8);                  // dO Y^T (lanes 64..127)
+      mma(kGdP, kk, ylo, id_kk, false, kd, kK, k16, kK, k8);
+      if (!(ok = wait(G_SR, x))) break;
+      tc_fence_after();
+      mma(kGdq, sk, k_tile(dO), id_kk, true, kd, kK, k16, kK, k16);        // (dO S^T)^T
+      mma(kGdw, rk, y, id_kk, true, kd, kK, k16, kK, k8);                  // (Y R^T)^T
+      if (!(ok = wait(G_ZT, x))) break;
+      tc_fence_after();
+      mma(kGGY, zm, y, id_mk, true, kd, kM, 4 * kM, kK, k8);               // Z Y^T (lanes 0..63)
+      mma_commit_warp(&bar[G_64]);
+      mma(kGdr, sk, zm, id_km, true, kd, kK, k16, kM, 4 * kM);             // (Z S^T)^T
+      if (lane == 0) store(&mdv, kGrU, item);
       __syncwarp();
+      if (!(ok = wait(G_AD, x))) break;
       tc_fence_after();
-#pragma unroll 4
-      for (uint32_t ks = 0; ks < kd; ++ks)  // Z Y^T (lanes 0..63)
-        mma_ss_warp(tmem + kGGY, desc_mnmajor_h(Z, ks, 16384), desc_kmajor_h(Y, ks, 8192), id_mk, ks > 0);
-      mma_commit_warp(&bar[3]);
-#pragma unroll 4
-      for (uint32_t ks = 0; ks < kd; ++ks)  // (Z S^T)^T
-        mma_ss_warp(tmem + kGdr, desc_kmajor(S, ks), desc_mnmajor_h(Z, ks, 8192), id_km, ks > 0);
-    }
-    ok = mbar_wait(&bar[3], 0, &abort_flag, P.status);
-  }
-  if (__syncthreads_and(ok)) {
-    tc_fence_after();
-    // <R, S> of the chunk's two states (its end's needs the tokens' writes added: below)
-    {
-      float dot = 0.f;
-#pragma unroll 4
-      for (uint32_t p = 0; p < 8; ++p) {
-        uint32_t u[4], v[4];
-        const uint32_t at = hf * 16384 + sw(row, p);
-        ld_shared_v4(S + at, u[0], u[1], u[2], u[3]);
-        ld_shared_v4(R + at, v[0], v[1], v[2], v[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) dot = fmaf(bf16lo(u[e]), bf16lo(v[e]), fmaf(bf16hi(u[e]), bf16hi(v[e]), dot));
+      mma(kGKK, km, ak, id_mk, true, 2, kM, 0, kK, k8);                    // (A K)^T
+      mma(kGdP, km, dk, id_mk, true, 1, kM, 0, kK, 0);                     // (D K)^T
+      mma(kGGY, qm, am, id_mm, true, 2, kM, 0, kM, k8);                    // (A^T Q + D^T K)^T
+      mma(kGGY, km, dm, id_mm, false, 1, kM, 0, kM, 0);
+      mma_commit_warp(&bar[G_ALL]);
+      if (item + (int)gridDim.x < items) {
+        if (!(ok = wait(G_ALL, x))) break;
+        if (lane == 0) bulk_wait_read_all();  // dv has left the place that the next chunk's dU takes
+        __syncwarp();
+        load1(item + gridDim.x);
       }
-#pragma unroll
-      for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) s_rs[warp] = 64 * (int)hf < P.d ? dot : 0.f;
     }
-    const int i = row & 63;
-    const float hi = g[192 + i], lo = g[256 + i];
-    const float *be = g + 128 + 32 * hf, *ghi = g + 192 + 32 * hf, *glo = g + 256 + 32 * hf;
-    if (quad < 2) {
-      // D_ij = -b_j Gam_ij z_i . y_j, and the parts of sum_i Gam_ij (k_i . k_j) (z_i . y_j)
-      float kk[32], zy[32];
-      tmem_ld32(t + kGKK + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&kk));
-      tmem_ld32(t + kGGY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&zy));
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float e = ex2((hi - ghi[j]) + (lo - glo[j])) * zy[j];
-        const bool in = 32 * (int)hf + j < i;
-        kk[j] = in ? e * kk[j] : 0.f;
-        zy[j] = in ? -be[j] * e : 0.f;
+    if (ok && x > 0 && (ok = wait(G_END, x - 1)) && lane == 0) {
+      const int item = blockIdx.x + (x - 1) * gridDim.x;
+      store(&mdq, kGrZ, item);
+      store(&mdk, kGrX, item);
+    }
+    if (lane == 0) {
+      bulk_wait_all();
+      if (!ok) {  // after an abort, with limits: what is in flight lands before the block ends
+        volatile int no_abort = 0;
+        mbar_wait_compact(&bar[G_UT], x & 1, &no_abort, P.status);
+        mbar_wait_compact(&bar[G_SR], x & 1, &no_abort, P.status);
+        mbar_wait_compact(&bar[G_KQ], last & 1, &no_abort, P.status);
       }
-#pragma unroll
-      for (uint32_t p = 0; p < 4; ++p)
-        st_shared_v4(base + kGrD + sw(i, 4 * hf + p), pack_bf16(zy[8 * p], zy[8 * p + 1]),
-                     pack_bf16(zy[8 * p + 2], zy[8 * p + 3]), pack_bf16(zy[8 * p + 4], zy[8 * p + 5]),
-                     pack_bf16(zy[8 * p + 6], zy[8 * p + 7]));
-      s_col[quad][32 * hf + lane] = warp_col_sum(kk, lane);
-    } else {
-      // A_ij = b_j Gam_ij dO_i . y_j
-      float a[32];
-      tmem_ld32(t + kGdP + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&a));
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        a[j] = 32 * (int)hf + j <= i ? ex2((hi - ghi[j]) + (lo - glo[j])) * be[j] * a[j] : 0.f;
-#pragma unroll
-      for (uint32_t p = 0; p < 4; ++p)
-        st_shared_v4(base + kGrA + sw(i, 4 * hf + p), pack_bf16(a[8 * p], a[8 * p + 1]),
-                     pack_bf16(a[8 * p + 2], a[8 * p + 3]), pack_bf16(a[8 * p + 4], a[8 * p + 5]),
-                     pack_bf16(a[8 * p + 6], a[8 * p + 7]));
     }
-    tc_fence_before();
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (warp == 0) {
+    __syncwarp();
+  } else {
+    const uint32_t quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16) + 16 * cg;
+    // the threads' part of the x-th chunk; false when a wait gave up
+    auto step = [&](int x) {
+      const float *g = reinterpret_cast<const float *>(smem + kGrG + (x & 1) * 1536);
+      // Z: an operand tile (row = value dimension), where dq was, and dv, where dU was
+      if (!(wait(G_Z, x) && (x == 0 || wait(G_STORED, x - 1)))) return false;
       tc_fence_after();
-      const uint32_t D = base + kGrD, A = base + kGrA, Q = base + kGrQ;
+      {
+        float z[16];
+        tmem_ldf(t + kGZ, z);
+        tmem_ld_wait();
 #pragma unroll
-      for (uint32_t ks = 0; ks < 4; ++ks)  // (A K)^T
-        mma_ss_warp(tmem + kGKK, desc_mnmajor(KD, ks), desc_kmajor(A, ks), id_mk, ks > 0);
+        for (uint32_t p = 0; p < 2; ++p)
+          st_shared_v4(Z + sw(row, 2 * cg + p), pack_bf16(z[8 * p], z[8 * p + 1]), pack_bf16(z[8 * p + 2], z[8 * p + 3]),
+                       pack_bf16(z[8 * p + 4], z[8 * p + 5]), pack_bf16(z[8 * p + 6], z[8 * p + 7]));
 #pragma unroll
-      for (uint32_t ks = 0; ks < 4; ++ks)  // (D K)^T
-        mma_ss_warp(tmem + kGdP, desc_mnmajor(KD, ks), desc_kmajor(D, ks), id_mk, ks > 0);
-#pragma unroll
-      for (uint32_t ks = 0; ks < 4; ++ks)  // (A^T Q + D^T K)^T
-        mma_ss_warp(tmem + kGGY, desc_mnmajor_h(Q, ks, 8192), desc_mnmajor_h(A, ks, 8192), id_mm, ks > 0);
-#pragma unroll
-      for (uint32_t ks = 0; ks < 4; ++ks)
-        mma_ss_warp(tmem + kGGY, desc_mnmajor(KD, ks), desc_mnmajor_h(D, ks, 8192), id_mm, 1);
-      mma_commit_warp(&bar[4]);
-    }
-    ok = mbar_wait(&bar[4], 0, &abort_flag, P.status);
-  }
-  if (__syncthreads_and(ok)) {
-    tc_fence_after();
-    // lane = key dimension, tokens 32 hf .. + 31; x gathers q . dq + k . (read - write part)
-    const float *eg = g + 32 * hf, *phi = g + 64 + 32 * hf, *be = g + 128 + 32 * hf;
-    float x[32];
-    {
-      float a[32], w[32];
-      tmem_ld32(t + kGdq + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&a));
-      tmem_ld32(t + kGKK + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&w));
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float v = fmaf(eg[j], a[j], w[j]);
-        x[j] = v * ld_shared_bf16(base + kGrQ + sw_el(32 * hf + j, row, 8192));
-        st_shared_u16(S + sw_el(32 * hf + j, row, 8192), v);
+        for (int j = 0; j < 16; ++j) st_shared_u16(base + kGrU + sw_el(16 * cg + j, row, 8192), z[j]);
       }
-    }
-    {
-      float a[32], w[32];
-      tmem_ld32(t + kGdr + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&a));
-      tmem_ld32(t + kGdP + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&w));
+      arrive(G_ZT);
+      // <R, S> of the chunk's two states (its end's needs the tokens' writes added: below)
+      if (!(wait(G_SR, x))) return false;
+      {
+        float dot = 0.f;
+        const uint32_t at = (cg >> 1) * 16384;
+#pragma unroll
+        for (uint32_t p = 0; p < 4; ++p) {
+          uint32_t u[4], v[4];
+          const uint32_t o = at + sw(row, 4 * (cg & 1) + p);
+          ld_shared_v4(S + o, u[0], u[1], u[2], u[3]);
+          ld_shared_v4(R + o, v[0], v[1], v[2], v[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot = fmaf(bf16lo(u[e]), bf16lo(v[e]), fmaf(bf16hi(u[e]), bf16hi(v[e]), dot));
+        }
+#pragma unroll
+        for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) s_rs[warp] = 32 * (int)cg < P.d ? dot : 0.f;
+      }
+      if (!(wait(G_64, x))) return false;
+      tc_fence_after();
+      {
+        const int i = row & 63;
+        const float hi = g[192 + i], lo = g[256 + i];
+        const float *be = g + 128 + 16 * cg, *ghi = g + 192 + 16 * cg, *glo = g + 256 + 16 * cg;
+        float a[16], zy[16];
+        tmem_ldf(t + (quad < 2 ? kGKK : kGdP), a);
+        tmem_ldf(t + kGGY, zy);
+        tmem_ld_wait();
+        if (quad < 2) {
+          // D_ij = -b_j Gam_ij z_i . y_j, and the parts of sum_i Gam_ij (k_i . k_j) (z_i . y_j)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float e = ex2((hi - ghi[j]) + (lo - glo[j])) * zy[j];
+            const bool in = 16 * (int)cg + j < i;
+            a[j] = in ? e * a[j] : 0.f;
+            zy[j] = in ? -be[j] * e : 0.f;
+          }
+#pragma unroll
+          for (uint32_t p = 0; p < 2; ++p)
+            st_shared_v4(base + kGrD + sw(i, 2 * cg + p), pack_bf16(zy[8 * p], zy[8 * p + 1]),
+                         pack_bf16(zy[8 * p + 2], zy[8 * p + 3]), pack_bf16(zy[8 * p + 4], zy[8 * p + 5]),
+                         pack_bf16(zy[8 * p + 6], zy[8 * p + 7]));
+          const float sum = warp_col_sum(a, lane);
+          if (!(lane & 1)) s_col[quad][16 * cg + lane / 2] = sum;
+        } else {
+          // A_ij = b_j Gam_ij dO_i . y_j
+          uint32_t ah[8], al[8];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            a[j] = 16 * (int)cg + j <= i ? ex2((hi - ghi[j]) + (lo - glo[j])) * be[j] * a[j] : 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) split2(a[2 * j], a[2 * j + 1], ah[j], al[j]);
+#pragma unroll
+          for (uint32_t p = 0; p < 2; ++p) {
+            const uint32_t at = base + kGrA + sw(i, 2 * cg + p);
+            st_shared_v4(at, ah[4 * p], ah[4 * p + 1], ah[4 * p + 2], ah[4 * p + 3]);
+            st_shared_v4(at + 8192, al[4 * p], al[4 * p + 1], al[4 * p + 2], al[4 * p + 3]);
+          }
+        }
+      }
+      arrive(G_AD);
+      if (!(wait(G_ALL, x))) return false;
+      tc_fence_after();
+      // lane = key dimension, tokens 16 cg .. + 15; w gathers q . dq + k . (read - write part)
+      const float *eg = g + 16 * cg, *phi = g + 64 + 16 * cg, *be = g + 128 + 16 * cg;
+      float w[16], a[16], e[16];
+      tmem_ldf(t + kGdq, a);
+      tmem_ldf(t + kGKK, e);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 32; ++j) a[j] = fmaf(-eg[j], a[j], w[j]);  // the read part
-      float f[32];
-      tmem_ld32(t + kGdw + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&f));
-      tmem_ld32(t + kGGY + 32 * hf, *reinterpret_cast<uint32_t(*)[32]>(&w));
+      for (int j = 0; j < 16; ++j) {
+        const float v = fmaf(eg[j], a[j], e[j]);
+        w[j] = v * ld_shared_bf16(base + kGrQ + sw_el(16 * cg + j, row, 8192));
+        st_shared_u16(Z + sw_el(16 * cg + j, row, 8192), v);
+      }
+      float f[16], u[16];
+      tmem_ldf(t + kGdr, a);
+      tmem_ldf(t + kGdP, e);
+      tmem_ldf(t + kGdw, f);
+      tmem_ldf(t + kGGY, u);
       tmem_ld_wait();
       float kw = 0.f;  // sum of phi b k^T R y: what the tokens' writes add to <R, S>
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const float kv = ld_shared_bf16(KD + sw_el(32 * hf + j, row, 16384)), r = phi[j] * be[j] * f[j];
-        const float v = r + w[j];  // the write part
+      for (int j = 0; j < 16; ++j) {
+        const float read = fmaf(-eg[j], a[j], e[j]), r = phi[j] * be[j] * f[j], write = r + u[j];
+        const float kv = ld_shared_bf16(KD + sw_el(16 * cg + j, row, 16384));
         kw = fmaf(kv, r, kw);
-        x[j] = fmaf(a[j] - v, kv, x[j]);
-        st_shared_u16(R + sw_el(32 * hf + j, row, 8192), a[j] + v);
+        w[j] = fmaf(read - write, kv, w[j]);
+        st_shared_u16(base + kGrX + sw_el(16 * cg + j, row, 8192), read + write);
       }
 #pragma unroll
       for (int o = 16; o; o /= 2) kw += __shfl_xor_sync(0xffffffffu, kw, o);
       if (lane == 0) s_kw[warp] = kw;
+      const float sum = warp_col_sum(w, lane);
+      if (!(lane & 1)) s_x[quad][16 * cg + lane / 2] = sum;
+      if (tid == kC) s_last = g[63];
+      arrive(G_END);
+      return true;
+    };
+    int x = 0;
+#pragma unroll 1
+    for (int item = blockIdx.x; item < items; item += gridDim.x, ++x) {
+      // one verdict for all warps: none is left alone in the barrier
+      if (!(ok = group_all(step(x), 1, 32 * kGradWarps))) break;
+      const int c = item % P.N, bh = item / P.N;
+      if (tid < kC) {
+        const int j = tid;
+        const int64_t ci = (int64_t)bh * P.N + c, at = (int64_t)bh * P.T + kC * c + j;
+        if (kC * c + j < P.T) {
+          P.gx[at] = (s_x[0][j] + s_x[1][j]) + (s_x[2][j] + s_x[3][j]);
+          float db = -(s_col[0][j] + s_col[1][j]);
+          const float *dot = P.dot + (ci * kC + j) * 8;
+          for (int y = 0; y < P.d / 16; ++y) db += dot[y];
+          if (P.f32)
+            static_cast<float *>(P.dbeta)[at] = db;
+          else
+            static_cast<__nv_bfloat16 *>(P.dbeta)[at] = __float2bfloat16_rn(db);
+        }
+      } else if (tid == kC) {
+        float rs = 0.f, kws = 0.f;
+        for (int y = 0; y < kGradWarps; ++y) {
+          rs += s_rs[y];
+          kws += s_kw[y];
+        }
+        P.anchor[(int64_t)bh * P.N + c] = fmaf(s_last, rs, kws);
+      }
     }
-    s_x[quad][32 * hf + lane] = warp_col_sum(x, lane);
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (tid == 0) {
-      for (int y = 0; y < (P.d == 128 ? 2 : 1); ++y) {
-        tma_store_4d(&mdq, smem + kGrS + y * 8192, 64 * y, kC * c, h, b);
-        tma_store_4d(&mdk, smem + kGrR + y * 8192, 64 * y, kC * c, h, b);
-      }
-      bulk_commit();
-    } else if (tid == 32) {
-      float rs = 0.f, kw = 0.f;
-      for (int w = 0; w < 8; ++w) {
-        rs += s_rs[w];
-        kw += s_kw[w];
-      }
-      P.anchor[ci] = fmaf(g[63], rs, kw);
-    } else if (tid >= 64 && tid < 64 + kC) {
-      const int j = tid - 64;
-      const int64_t at = (int64_t)bh * P.T + kC * c + j;
-      if (kC * c + j < P.T) {
-        P.gx[at] = (s_x[0][j] + s_x[1][j]) + (s_x[2][j] + s_x[3][j]);
-        const float db = ((s_dot[0][j] + s_dot[1][j]) + (s_dot[2][j] + s_dot[3][j])) - (s_col[0][j] + s_col[1][j]);
-        if (P.f32)
-          static_cast<float *>(P.dbeta)[at] = db;
-        else
-          static_cast<__nv_bfloat16 *>(P.dbeta)[at] = __float2bfloat16_rn(db);
-      }
-    }
-  }
-  if (tid == 0) {
-    bulk_wait_all();
-    // after an abort the loads may still be in flight (a wait with a limit; done at once otherwise)
-    volatile int no_abort = 0;
-    mbar_wait(&bar[0], 0, &no_abort, P.status);
-    mbar_wait(&bar[1], 0, &no_abort, P.status);
   }
   tc_fence_before();
   __syncthreads();
@@ -1378,11 +1430,11 @@ bool delta_tc_supported(const Problem &p) { return p.dtype == 0; }
 size_t delta_tc_fwd_ws_bytes(const Problem &p) { return align256(rec_bytes(p)); }
 size_t delta_tc_ckpt_bytes(const Problem &p) {
   if (p.T == 0) return 0;
-  return align256(rec_bytes(p) + bhs(p) * chunks(p) * (kStateImg + kRowImg));
+  return align256(rec_bytes(p) + bhs(p) * chunks(p) * (kStateImg + kYImg));
 }
 size_t delta_tc_bwd_ws_bytes(const Problem &p) {
   const size_t n = bhs(p) * chunks(p);
-  return align256(n * (kStateImg + kRowImg + sizeof(float)) + bhs(p) * p.T * sizeof(float));
+  return align256(n * (kStateImg + kRowImg + (8 * kC + 1) * sizeof(float)) + bhs(p) * p.T * sizeof(float));
 }
 
 cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
@@ -1429,7 +1481,8 @@ cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, c
   P.yimg = P.simg + bhs(p) * (size_t)P.N * kStateImg;
   P.rimg = static_cast<uint8_t *>(ws);
   P.uimg = P.rimg + n * kStateImg;
-  P.anchor = reinterpret_cast<float *>(P.uimg + n * kRowImg);
+  P.dot = reinterpret_cast<float *>(P.uimg + n * kRowImg);
+  P.anchor = P.dot + n * kC * 8;
   P.gx = P.anchor + n;
   P.dbeta = dbeta;
   P.in = d_final;
@@ -1447,8 +1500,9 @@ cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, c
   if (e != cudaSuccess) return e;
   {
     TimedLaunch t(K_DELTA_GRAD, s);
-    e = launch_overlapped(delta_grad_kernel, dim3((unsigned)(bhs(p) * P.N)), dim3(kGradThreads), kGradSmem, s, mq, mk, mdo,
-                          mdq, mdk, mdv, P);
+    const int items = (int)n, grid = items < p.num_sms ? items : p.num_sms;
+    e = launch_overlapped(delta_grad_kernel, dim3(grid), dim3(kGradThreads), kGradSmem, s, mq, mk, mdo,
+                          mdq, mdk, mdv, P, items);
     if (e != cudaSuccess) return e;
   }
   return dlg ? delta_gate_sums(p, P.gx, P.anchor, dlg, g.f32, s) : cudaSuccess;
