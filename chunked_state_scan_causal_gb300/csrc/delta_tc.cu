@@ -66,28 +66,29 @@ __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t c) { return r * 128u
 __device__ __forceinline__ uint32_t sw_el(uint32_t r, uint32_t x, uint32_t half) {
   return (x >> 6) * half + sw(r, (x & 63u) >> 3) + (x & 7u) * 2u;
 }
-__device__ __forceinline__ void st_shared_u16(uint32_t addr, float x) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))) : "memory");
+// Fragments of 16 rows x 16 columns (tmem_ld_frag): the place of lane l's address row for the four 8 x 8
+// matrices, in a tile whose rows are the fragment's rows (columns 16 g .. of a 64-column block) ...
+__device__ __forceinline__ uint32_t frag_at(uint32_t lane, uint32_t row0, uint32_t g) {
+  return sw(row0 + (lane & 15u), 2 * g + (lane >> 4));
 }
-__device__ __forceinline__ float ld_shared_bf16(uint32_t addr) {
-  unsigned short u;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(u) : "r"(addr) : "memory");
-  return __uint_as_float((uint32_t)u << 16);
+// ... and in one whose rows are the fragment's columns (row0 the first; its columns col0 .. + 15, blocks `half` apart)
+__device__ __forceinline__ uint32_t frag_at_trans(uint32_t lane, uint32_t row0, uint32_t col0, uint32_t half) {
+  const uint32_t c = (col0 >> 3) + ((lane >> 3) & 1u);
+  return (c >> 3) * half + sw(row0 + (lane & 7u) + 8 * (lane >> 4), c & 7u);
 }
-__device__ __forceinline__ float2 ld_shared_f2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
-
-// Column sums over a warp of 16 values per lane: on return lane l holds the sum over all lanes of x[l / 2].
-__device__ __forceinline__ float warp_col_sum(float (&x)[16], int lane) {
+// register i of a fragment belongs to the (i & 1) + (i & 4 ? 2 : 0)-th of the lane's four columns
+__device__ __forceinline__ constexpr int frag_col(int i) { return (i & 1) | ((i >> 1) & 2); }
+__device__ __forceinline__ uint32_t frag_token(uint32_t lane, int e) { return 2 * (lane & 3u) + (e & 1) + 8 * (e >> 1); }
+__device__ __forceinline__ void frag_pack(const float (&x)[8], uint32_t (&p)[4]) {
 #pragma unroll
-  for (int n = 8; n >= 1; n /= 2) {
-    const bool up = lane & (2 * n);
+  for (int i = 0; i < 4; ++i) p[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+}
+// sum over the fragment's rows, for each of the lane's four columns (all lanes of equal l % 4 get it)
+__device__ __forceinline__ void frag_col_sum(float (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
-      x[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * n);
-    }
-  }
-  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+  for (int o = 4; o < 32; o *= 2)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
 }
 
 struct DeltaTcParams {
@@ -114,9 +115,8 @@ __device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
 // One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
 // cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks by forward
 // substitution, one column per thread, then the off-diagonal block as two 32^3 products), and
-// W^T = K^T (T diag(e^g))^T on the tensor cores.  128 threads; three CTAs fit an SM and hide each
-// other's latencies.
-constexpr int kPrepThreads = 128;
+// W^T = K^T (T diag(e^g))^T on the tensor cores.  Three CTAs fit an SM and hide each other's latencies.
+constexpr int kPrepThreads = 256;
 constexpr int kLd = 68;  // row stride of the fp32 64 x 64 matrices: 16-byte rows, spread over the banks
 constexpr uint32_t kPrepA = 32768, kPrepT = kPrepA + 17408, kPrepEnd = kPrepT + 17408;
 constexpr size_t kPrepSmem = kPrepEnd + 1024;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       tma_load_4d(&mq, &bar[0], smem + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictNormal);
     }
   }
-  if (warp == 2) {
+  if (warp == 7) {
     // cumulative log2-gates in 64 bits (differences of far sums must keep their low bits); a gate below
     // 2^-1000 is zero either way
     const int t0 = kC * c + 2 * lane;
@@ -209,16 +209,18 @@ __global__ void __launch_bounds__(kPrepThreads)
   ok = ok && mbar_wait(&bar[1], 0, &abort_flag, P.status);
   if (__syncthreads_and(ok)) {
     tc_fence_after();
-    const int i = tid & 63;
+    // lanes 0..63: rows of K K^T, 64..127: of Q K^T; columns 32 x .. + 31
+    const uint32_t quad = warp & 3, x = warp >> 2, lb = (quad * 32) << 16;
+    const int i = (quad & 1) * 32 + lane;
     const float hi = s_hi[i], lo = s_lo[i];
-    const uint32_t lb = (uint32_t)(warp * 32) << 16;
-    if (warp < 2) {
-      // A_ij = Gam_ij (k_i . k_j) b_j, j < i
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lb + 32 * x, r);
-        tmem_ld_wait();
+    uint32_t r[32];
+    if (quad >= 2 || x <= quad) {
+      tmem_ld32(tmem + lb + 32 * x, r);
+      tmem_ld_wait();
+    }
+    if (quad < 2) {
+      // A_ij = Gam_ij (k_i . k_j) b_j, j < i (the block above the diagonal is not used)
+      if (x <= quad)
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
           float a[4];
@@ -230,97 +232,78 @@ __global__ void __launch_bounds__(kPrepThreads)
           }
           *reinterpret_cast<float4 *>(A + i * kLd + 32 * x + 4 * y) = make_float4(a[0], a[1], a[2], a[3]);
         }
-      }
-      named_bar_sync(1, 64);
-      // the diagonal block of this warp: column `lane` of its inverse
-      const float *Ab = A + (warp * 32) * kLd + warp * 32;
-      float x[32];
+      if (x == quad) {
+        // this warp's diagonal block: column `lane` of its inverse
+        __syncwarp();
+        const float *Ab = A + (quad * 32) * kLd + quad * 32;
+        float x[32];
 #pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        for (int r = 0; r < 32; ++r) {
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-        for (int m = 0; m < r; m += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(Ab + r * kLd + m);
-          s0 = fmaf(a.x, x[m], s0);
-          if (m + 1 < r) s1 = fmaf(a.y, x[m + 1], s1);
-          if (m + 2 < r) s2 = fmaf(a.z, x[m + 2], s2);
-          if (m + 3 < r) s3 = fmaf(a.w, x[m + 3], s3);
+          for (int m = 0; m < r; m += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(Ab + r * kLd + m);
+            s0 = fmaf(a.x, x[m], s0);
+            if (m + 1 < r) s1 = fmaf(a.y, x[m + 1], s1);
+            if (m + 2 < r) s2 = fmaf(a.z, x[m + 2], s2);
+            if (m + 3 < r) s3 = fmaf(a.w, x[m + 3], s3);
+          }
+          x[r] = (r == lane ? 1.f : 0.f) - ((s0 + s1) + (s2 + s3));
+          Ti[(quad * 32 + r) * kLd + quad * 32 + lane] = x[r];
         }
-        x[r] = (r == lane ? 1.f : 0.f) - ((s0 + s1) + (s2 + s3));
-        Ti[(warp * 32 + r) * kLd + warp * 32 + lane] = x[r];
       }
     } else {
       // P_ij = Gam_ij (q_i . k_j), j <= i, straight to the record
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lb + 32 * x, r);
-        tmem_ld_wait();
+      for (int y = 0; y < 4; ++y) {
+        uint32_t ph[4], pl[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t ph[4], pl[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int j = 32 * x + 8 * y + 2 * z;
-            float p0 = ex2((hi - s_hi[j]) + (lo - s_lo[j])) * __uint_as_float(r[8 * y + 2 * z]);
-            float p1 = ex2((hi - s_hi[j + 1]) + (lo - s_lo[j + 1])) * __uint_as_float(r[8 * y + 2 * z + 1]);
-            split2(j <= i ? p0 : 0.f, j + 1 <= i ? p1 : 0.f, ph[z], pl[z]);
-          }
-          const uint32_t at = sw(i, 4 * x + y);
-          *reinterpret_cast<uint4 *>(rec + kRecP + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-          *reinterpret_cast<uint4 *>(rec + kRecP + 8192 + at) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+        for (int z = 0; z < 4; ++z) {
+          const int j = 32 * x + 8 * y + 2 * z;
+          float p0 = ex2((hi - s_hi[j]) + (lo - s_lo[j])) * __uint_as_float(r[8 * y + 2 * z]);
+          float p1 = ex2((hi - s_hi[j + 1]) + (lo - s_lo[j + 1])) * __uint_as_float(r[8 * y + 2 * z + 1]);
+          split2(j <= i ? p0 : 0.f, j + 1 <= i ? p1 : 0.f, ph[z], pl[z]);
         }
+        const uint32_t at = sw(i, 4 * x + y);
+        *reinterpret_cast<uint4 *>(rec + kRecP + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+        *reinterpret_cast<uint4 *>(rec + kRecP + 8192 + at) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
       }
     }
     __syncthreads();
     {
-      // the off-diagonal block -T22 (A21 T11): X = A21 T11 parked in the (zero) upper right block
-      const int r = tid / 4, c0 = (tid % 4) * 8;
-      float acc[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      // the off-diagonal block -T22 (A21 T11): X = A21 T11 parked in the upper right block, then zeroed
+      const int r = tid / 8, c0 = (tid % 8) * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
       for (int m = 0; m < 32; ++m) {
         const float a = A[(32 + r) * kLd + m];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0);
-        const float4 v = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0 + 4);
-        acc[0] = fmaf(a, u.x, acc[0]); acc[1] = fmaf(a, u.y, acc[1]);
-        acc[2] = fmaf(a, u.z, acc[2]); acc[3] = fmaf(a, u.w, acc[3]);
-        acc[4] = fmaf(a, v.x, acc[4]); acc[5] = fmaf(a, v.y, acc[5]);
-        acc[6] = fmaf(a, v.z, acc[6]); acc[7] = fmaf(a, v.w, acc[7]);
+        acc = make_float4(fmaf(a, u.x, acc.x), fmaf(a, u.y, acc.y), fmaf(a, u.z, acc.z), fmaf(a, u.w, acc.w));
       }
       float4 *X = reinterpret_cast<float4 *>(Ti + r * kLd + 32 + c0);
-      X[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      X[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      *X = acc;
       __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
       for (int m = 0; m < 32; ++m) {
-        const float a = Ti[(32 + r) * kLd + 32 + m];
+        const float a = -Ti[(32 + r) * kLd + 32 + m];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + 32 + c0);
-        const float4 v = *reinterpret_cast<const float4 *>(Ti + m * kLd + 32 + c0 + 4);
-        acc[0] = fmaf(-a, u.x, acc[0]); acc[1] = fmaf(-a, u.y, acc[1]);
-        acc[2] = fmaf(-a, u.z, acc[2]); acc[3] = fmaf(-a, u.w, acc[3]);
-        acc[4] = fmaf(-a, v.x, acc[4]); acc[5] = fmaf(-a, v.y, acc[5]);
-        acc[6] = fmaf(-a, v.z, acc[6]); acc[7] = fmaf(-a, v.w, acc[7]);
+        acc = make_float4(fmaf(a, u.x, acc.x), fmaf(a, u.y, acc.y), fmaf(a, u.z, acc.z), fmaf(a, u.w, acc.w));
       }
       __syncthreads();
-      float4 *Y = reinterpret_cast<float4 *>(Ti + (32 + r) * kLd + c0);
-      Y[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-      Y[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-      X[0] = X[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<float4 *>(Ti + (32 + r) * kLd + c0) = acc;
+      *X = make_float4(0.f, 0.f, 0.f, 0.f);
       __syncthreads();
     }
     {
       // T to the record; T diag(e^g), the operand of W, over A
-      const int half = tid / 64;
+      const int row = tid & 63, q = tid / 64;
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < 2; ++y) {
         uint32_t th[4], tl[4], eh[4], el[4];
-        const float4 u = *reinterpret_cast<const float4 *>(Ti + i * kLd + 32 * half + 8 * y);
-        const float4 v = *reinterpret_cast<const float4 *>(Ti + i * kLd + 32 * half + 8 * y + 4);
-        const float *e = s_eg + 32 * half + 8 * y;
+        const float4 u = *reinterpret_cast<const float4 *>(Ti + row * kLd + 16 * q + 8 * y);
+        const float4 v = *reinterpret_cast<const float4 *>(Ti + row * kLd + 16 * q + 8 * y + 4);
+        const float *e = s_eg + 16 * q + 8 * y;
         split2(u.x, u.y, th[0], tl[0]);
         split2(u.z, u.w, th[1], tl[1]);
         split2(v.x, v.y, th[2], tl[2]);
@@ -329,7 +312,7 @@ __global__ void __launch_bounds__(kPrepThreads)
         split2(u.z * e[2], u.w * e[3], eh[1], el[1]);
         split2(v.x * e[4], v.y * e[5], eh[2], el[2]);
         split2(v.z * e[6], v.w * e[7], eh[3], el[3]);
-        const uint32_t at = sw(i, 4 * half + y);
+        const uint32_t at = sw(row, 2 * q + y);
         *reinterpret_cast<uint4 *>(rec + kRecT + at) = make_uint4(th[0], th[1], th[2], th[3]);
         *reinterpret_cast<uint4 *>(rec + kRecT + 8192 + at) = make_uint4(tl[0], tl[1], tl[2], tl[3]);
         st_shared_v4(base + kPrepA + at, eh[0], eh[1], eh[2], eh[3]);
@@ -352,19 +335,19 @@ __global__ void __launch_bounds__(kPrepThreads)
     ok = mbar_wait(&bar[2], 0, &abort_flag, P.status);
     if (__syncthreads_and(ok)) {
       tc_fence_after();
-      // W^T: lane = key dimension, column = token; negated, over the K and Q tiles
+      // W^T: lane = key dimension, column = token; negated, with tokens as rows over the K and Q tiles
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t r[32];
-        tmem_ld32(tmem + lb + 64 + 32 * x, r);
+      for (uint32_t y = 0; y < 4; ++y) {
+        const uint32_t row0 = quad * 32 + 16 * (y & 1), tok0 = 32 * x + 16 * (y >> 1);
+        float w[8];
+        uint32_t h[4], l[4];
+        tmem_ld_frag(tmem + (row0 << 16) + 64 + tok0, w);
         tmem_ld_wait();
 #pragma unroll
-        for (int t = 0; t < 32; ++t) {
-          const float w = -__uint_as_float(r[t]), wh = __bfloat162float(__float2bfloat16_rn(w));
-          const uint32_t at = base + sw_el(32 * x + t, tid, 8192);
-          st_shared_u16(at, w);
-          st_shared_u16(at + 16384, w - wh);
-        }
+        for (int e = 0; e < 4; ++e) split2(-w[2 * e], -w[2 * e + 1], h[e], l[e]);
+        const uint32_t at = base + frag_at_trans(lane, tok0, row0, 8192);
+        stmatrix4_trans(at, h);
+        stmatrix4_trans(at + 16384, l);
       }
       tc_fence_before();
       fence_proxy_async_smem();
@@ -1240,34 +1223,35 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     }
     __syncwarp();
   } else {
-    const uint32_t quad = warp & 3, cg = warp >> 2, row = quad * 32 + lane, t = tmem + ((quad * 32) << 16) + 16 * cg;
+    // 32 lanes (dimensions, or rows of a 64 x 64 product) and 16 columns of every product, as two fragments
+    const uint32_t quad = warp & 3, cg = warp >> 2, t = tmem + ((quad * 32) << 16) + 16 * cg;
+    auto frag = [&](uint32_t col, uint32_t hh, float (&f)[8]) { tmem_ld_frag(t + col + (hh << 20), f); };
     // the threads' part of the x-th chunk; false when a wait gave up
     auto step = [&](int x) {
       const float *g = reinterpret_cast<const float *>(smem + kGrG + (x & 1) * 1536);
       // Z: an operand tile (row = value dimension), where dq was, and dv, where dU was
       if (!(wait(G_Z, x) && (x == 0 || wait(G_STORED, x - 1)))) return false;
       tc_fence_after();
-      {
-        float z[16];
-        tmem_ldf(t + kGZ, z);
+#pragma unroll
+      for (uint32_t hh = 0; hh < 2; ++hh) {
+        float z[8];
+        uint32_t p[4];
+        frag(kGZ, hh, z);
         tmem_ld_wait();
-#pragma unroll
-        for (uint32_t p = 0; p < 2; ++p)
-          st_shared_v4(Z + sw(row, 2 * cg + p), pack_bf16(z[8 * p], z[8 * p + 1]), pack_bf16(z[8 * p + 2], z[8 * p + 3]),
-                       pack_bf16(z[8 * p + 4], z[8 * p + 5]), pack_bf16(z[8 * p + 6], z[8 * p + 7]));
-#pragma unroll
-        for (int j = 0; j < 16; ++j) st_shared_u16(base + kGrU + sw_el(16 * cg + j, row, 8192), z[j]);
+        frag_pack(z, p);
+        stmatrix4(Z + frag_at(lane, quad * 32 + 16 * hh, cg), p);
+        stmatrix4_trans(base + kGrU + frag_at_trans(lane, 16 * cg, quad * 32 + 16 * hh, 8192), p);
       }
       arrive(G_ZT);
       // <R, S> of the chunk's two states (its end's needs the tokens' writes added: below)
-      if (!(wait(G_SR, x))) return false;
+      if (!wait(G_SR, x)) return false;
       {
         float dot = 0.f;
         const uint32_t at = (cg >> 1) * 16384;
 #pragma unroll
         for (uint32_t p = 0; p < 4; ++p) {
           uint32_t u[4], v[4];
-          const uint32_t o = at + sw(row, 4 * (cg & 1) + p);
+          const uint32_t o = at + sw(quad * 32 + lane, 4 * (cg & 1) + p);
           ld_shared_v4(S + o, u[0], u[1], u[2], u[3]);
           ld_shared_v4(R + o, v[0], v[1], v[2], v[3]);
 #pragma unroll
@@ -1277,83 +1261,104 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         if (lane == 0) s_rs[warp] = 32 * (int)cg < P.d ? dot : 0.f;
       }
-      if (!(wait(G_64, x))) return false;
+      // this lane's four columns
+      float be[4], jh[4], jl[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 16 * cg + frag_token(lane, e);
+        be[e] = g[128 + j];
+        jh[e] = g[192 + j];
+        jl[e] = g[256 + j];
+      }
+      if (!wait(G_64, x)) return false;
       tc_fence_after();
-      {
-        const int i = row & 63;
-        const float hi = g[192 + i], lo = g[256 + i];
-        const float *be = g + 128 + 16 * cg, *ghi = g + 192 + 16 * cg, *glo = g + 256 + 16 * cg;
-        float a[16], zy[16];
-        tmem_ldf(t + (quad < 2 ? kGKK : kGdP), a);
-        tmem_ldf(t + kGGY, zy);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (uint32_t hh = 0; hh < 2; ++hh) {
+        const uint32_t row0 = (quad & 1) * 32 + 16 * hh;
+        float a[8], zy[8];
+        frag(quad < 2 ? kGKK : kGdP, hh, a);
+        if (quad < 2) frag(kGGY, hh, zy);
         tmem_ld_wait();
-        if (quad < 2) {
-          // D_ij = -b_j Gam_ij z_i . y_j, and the parts of sum_i Gam_ij (k_i . k_j) (z_i . y_j)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float e = ex2((hi - ghi[j]) + (lo - glo[j])) * zy[j];
-            const bool in = 16 * (int)cg + j < i;
-            a[j] = in ? e * a[j] : 0.f;
-            zy[j] = in ? -be[j] * e : 0.f;
-          }
-#pragma unroll
-          for (uint32_t p = 0; p < 2; ++p)
-            st_shared_v4(base + kGrD + sw(i, 2 * cg + p), pack_bf16(zy[8 * p], zy[8 * p + 1]),
-                         pack_bf16(zy[8 * p + 2], zy[8 * p + 3]), pack_bf16(zy[8 * p + 4], zy[8 * p + 5]),
-                         pack_bf16(zy[8 * p + 6], zy[8 * p + 7]));
-          const float sum = warp_col_sum(a, lane);
-          if (!(lane & 1)) s_col[quad][16 * cg + lane / 2] = sum;
-        } else {
-          // A_ij = b_j Gam_ij dO_i . y_j
-          uint32_t ah[8], al[8];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            a[j] = 16 * (int)cg + j <= i ? ex2((hi - ghi[j]) + (lo - glo[j])) * be[j] * a[j] : 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) split2(a[2 * j], a[2 * j + 1], ah[j], al[j]);
-#pragma unroll
-          for (uint32_t p = 0; p < 2; ++p) {
-            const uint32_t at = base + kGrA + sw(i, 2 * cg + p);
-            st_shared_v4(at, ah[4 * p], ah[4 * p + 1], ah[4 * p + 2], ah[4 * p + 3]);
-            st_shared_v4(at + 8192, al[4 * p], al[4 * p + 1], al[4 * p + 2], al[4 * p + 3]);
+        for (int i = 0; i < 8; ++i) {
+          const int e = frag_col(i), r = row0 + lane / 4 + (i & 2 ? 8 : 0), j = 16 * cg + frag_token(lane, e);
+          const float gam = ex2((g[192 + r] - jh[e]) + (g[256 + r] - jl[e]));
+          if (quad < 2) {
+            // D_ij = -b_j Gam_ij z_i . y_j, and the parts of sum_i Gam_ij (k_i . k_j) (z_i . y_j)
+            const float v = j < r ? gam * zy[i] : 0.f;
+            sum[e] += j < r ? v * a[i] : 0.f;
+            a[i] = -be[e] * v;
+          } else {
+            a[i] = j <= r ? gam * be[e] * a[i] : 0.f;  // A_ij = b_j Gam_ij dO_i . y_j
           }
         }
+        uint32_t p[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split2(a[2 * i], a[2 * i + 1], p[i], l[i]);
+        const uint32_t at = base + (quad < 2 ? kGrD : kGrA) + frag_at(lane, row0, cg);
+        stmatrix4(at, p);
+        if (quad >= 2) stmatrix4(at + 8192, l);
       }
       arrive(G_AD);
-      if (!(wait(G_ALL, x))) return false;
-      tc_fence_after();
-      // lane = key dimension, tokens 16 cg .. + 15; w gathers q . dq + k . (read - write part)
-      const float *eg = g + 16 * cg, *phi = g + 64 + 16 * cg, *be = g + 128 + 16 * cg;
-      float w[16], a[16], e[16];
-      tmem_ldf(t + kGdq, a);
-      tmem_ldf(t + kGKK, e);
-      tmem_ld_wait();
+      if (quad < 2) {
+        frag_col_sum(sum);
+        if (lane < 4)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float v = fmaf(eg[j], a[j], e[j]);
-        w[j] = v * ld_shared_bf16(base + kGrQ + sw_el(16 * cg + j, row, 8192));
-        st_shared_u16(Z + sw_el(16 * cg + j, row, 8192), v);
+          for (int e = 0; e < 4; ++e) s_col[quad][16 * cg + frag_token(lane, e)] = sum[e];
       }
-      float f[16], u[16];
-      tmem_ldf(t + kGdr, a);
-      tmem_ldf(t + kGdP, e);
-      tmem_ldf(t + kGdw, f);
-      tmem_ldf(t + kGGY, u);
-      tmem_ld_wait();
-      float kw = 0.f;  // sum of phi b k^T R y: what the tokens' writes add to <R, S>
+      float eg[4], pb[4], w[4] = {0.f, 0.f, 0.f, 0.f}, kw = 0.f;  // kw: sum of phi b k^T R y
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float read = fmaf(-eg[j], a[j], e[j]), r = phi[j] * be[j] * f[j], write = r + u[j];
-        const float kv = ld_shared_bf16(KD + sw_el(16 * cg + j, row, 16384));
-        kw = fmaf(kv, r, kw);
-        w[j] = fmaf(read - write, kv, w[j]);
-        st_shared_u16(base + kGrX + sw_el(16 * cg + j, row, 8192), read + write);
+      for (int e = 0; e < 4; ++e) {
+        const int j = 16 * cg + frag_token(lane, e);
+        eg[e] = g[j];
+        pb[e] = g[64 + j] * be[e];
+      }
+      if (!wait(G_ALL, x)) return false;
+      tc_fence_after();
+      // lane = key dimension; w gathers q . dq + k . (read - write part)
+#pragma unroll
+      for (uint32_t hh = 0; hh < 2; ++hh) {
+        const uint32_t row0 = quad * 32 + 16 * hh, at = frag_at_trans(lane, 16 * cg, row0, 8192);
+        float a[8], b[8];
+        uint32_t p[4];
+        frag(kGdq, hh, a);
+        frag(kGKK, hh, b);
+        ldmatrix4_trans(base + kGrQ + at, p);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          a[i] = fmaf(eg[frag_col(i)], a[i], b[i]);
+          w[frag_col(i)] = fmaf(a[i], i & 1 ? bf16hi(p[i / 2]) : bf16lo(p[i / 2]), w[frag_col(i)]);
+        }
+        frag_pack(a, p);
+        stmatrix4_trans(Z + at, p);
+        float f[8], u[8];
+        frag(kGdr, hh, a);
+        frag(kGdP, hh, b);
+        frag(kGdw, hh, f);
+        frag(kGGY, hh, u);
+        ldmatrix4_trans(KD + frag_at_trans(lane, 16 * cg, row0, 16384), p);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int e = frag_col(i);
+          const float kv = i & 1 ? bf16hi(p[i / 2]) : bf16lo(p[i / 2]), r = pb[e] * f[i];
+          const float read = fmaf(-eg[e], a[i], b[i]), write = r + u[i];
+          kw = fmaf(kv, r, kw);
+          w[e] = fmaf(read - write, kv, w[e]);
+          a[i] = read + write;
+        }
+        frag_pack(a, p);
+        stmatrix4_trans(base + kGrX + at, p);
       }
 #pragma unroll
       for (int o = 16; o; o /= 2) kw += __shfl_xor_sync(0xffffffffu, kw, o);
       if (lane == 0) s_kw[warp] = kw;
-      const float sum = warp_col_sum(w, lane);
-      if (!(lane & 1)) s_x[quad][16 * cg + lane / 2] = sum;
+      frag_col_sum(w);
+      if (lane < 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s_x[quad][16 * cg + frag_token(lane, e)] = w[e];
       if (tid == kC) s_last = g[63];
       arrive(G_END);
       return true;
