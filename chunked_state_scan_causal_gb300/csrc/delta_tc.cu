@@ -91,6 +91,23 @@ __device__ __forceinline__ void frag_col_sum(float (&x)[4]) {
     for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
 }
 
+// A sum of two fp32 parts, |lo| at most half a step of hi (sums by the error-free transformation of Knuth and
+// Dekker's renormalisation).
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+  const float s = __fadd_rn(a.hi, b.hi), t = __fsub_rn(s, a.hi);
+  const float e = __fadd_rn(__fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, t)), __fsub_rn(b.hi, t)), __fadd_rn(a.lo, b.lo));
+  const float hi = __fadd_rn(s, e);
+  return {hi, __fsub_rn(e, __fsub_rn(hi, s))};
+}
+__device__ __forceinline__ Two times_log2e(float x) {
+  constexpr float c = 1.44269504f, d = 1.925963033e-8f;  // log2(e) as two fp32 parts
+  const float hi = __fmul_rn(x, c);
+  return {hi, __fmaf_rn(x, d, __fmaf_rn(x, c, -hi))};
+}
+
 struct DeltaTcParams {
   int H, T, N, d;          // N chunks; d = 64 or 128 (state rows and columns; the tiles are 128 wide)
   int f32;                 // type of the gates
@@ -130,7 +147,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
   __shared__ float s_hi[kC], s_lo[kC], s_b[kC], s_eg[kC];
-  float *A = reinterpret_cast<float *>(smem + kPrepA), *Ti = reinterpret_cast<float *>(smem + kPrepT);
+  float *At = reinterpret_cast<float *>(smem + kPrepA), *Ti = reinterpret_cast<float *>(smem + kPrepT);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int c = blockIdx.x % P.N, bh = blockIdx.x / P.N, b = bh / P.H, h = bh % P.H;
@@ -158,41 +175,41 @@ __global__ void __launch_bounds__(kPrepThreads)
     }
   }
   if (warp == 7) {
-    // cumulative log2-gates in 64 bits (differences of far sums must keep their low bits); a gate below
-    // 2^-1000 is zero either way
+    // cumulative log2-gates as sums of two fp32 parts (differences of far sums must keep their low bits; in
+    // 64-bit arithmetic, slow here, the scan alone took 1.5 us); a gate below 2^-1000 is zero either way
     const int t0 = kC * c + 2 * lane;
     const int64_t gi = (int64_t)bh * P.T + t0;
-    double l[2];
+    Two l[2];
     float be[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const bool in = t0 + x < P.T;
-      double v = in && P.lg ? (double)load_gate(P.lg, gi + x, P.f32) * 1.4426950408889634 : 0.0;
-      l[x] = v < -1000.0 ? -1000.0 : v;
+      const float v = in && P.lg ? load_gate(P.lg, gi + x, P.f32) : 0.f;
+      l[x] = v < -690.f ? Two{-1000.f, 0.f} : times_log2e(v);
       be[x] = in ? load_gate(P.beta, gi + x, P.f32) : 0.f;
     }
-    double s = l[0] + l[1];
+    Two s = l[0] + l[1];
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const double y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
+      const Two y{__shfl_up_sync(0xffffffffu, s.hi, o), __shfl_up_sync(0xffffffffu, s.lo, o)};
+      if (lane >= o) s = s + y;
     }
-    const double last = __shfl_sync(0xffffffffu, s, 31);
+    const Two last{__shfl_sync(0xffffffffu, s.hi, 31), __shfl_sync(0xffffffffu, s.lo, 31)};
     float *g = reinterpret_cast<float *>(rec + kRecG);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const double gx = x ? s : s - l[1];
+      const Two gx = x ? s : s + Two{-l[1].hi, -l[1].lo};
       const int j = 2 * lane + x;
-      const float hi = (float)gx, lo = (float)(gx - (double)hi), eg = ex2(hi) * ex2(lo), phi = ex2((float)(last - gx));
-      s_hi[j] = hi;
-      s_lo[j] = lo;
+      const float eg = ex2(gx.hi) * ex2(gx.lo), phi = ex2((last.hi - gx.hi) + (last.lo - gx.lo));
+      s_hi[j] = gx.hi;
+      s_lo[j] = gx.lo;
       s_b[j] = be[x];
       s_eg[j] = eg;
       g[j] = eg;
       g[64 + j] = phi;
       g[128 + j] = be[x];
-      g[192 + j] = hi;
-      g[256 + j] = lo;
+      g[192 + j] = gx.hi;
+      g[256 + j] = gx.lo;
     }
   }
   bool ok = true;
@@ -219,38 +236,35 @@ __global__ void __launch_bounds__(kPrepThreads)
       tmem_ld_wait();
     }
     if (quad < 2) {
-      // A_ij = Gam_ij (k_i . k_j) b_j, j < i (the block above the diagonal is not used)
+      // A_ij = Gam_ij (k_i . k_j) b_j, j < i, transposed (the block above the diagonal is not used)
       if (x <= quad)
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          float a[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int j = 32 * x + 4 * y + z;
-            const float e = ex2((hi - s_hi[j]) + (lo - s_lo[j]));
-            a[z] = j < i ? e * __uint_as_float(r[4 * y + z]) * s_b[j] : 0.f;
-          }
-          *reinterpret_cast<float4 *>(A + i * kLd + 32 * x + 4 * y) = make_float4(a[0], a[1], a[2], a[3]);
+        for (int y = 0; y < 32; ++y) {
+          const int j = 32 * x + y;
+          const float e = ex2((hi - s_hi[j]) + (lo - s_lo[j]));
+          At[j * kLd + i] = j < i ? e * __uint_as_float(r[y]) * s_b[j] : 0.f;
         }
       if (x == quad) {
-        // this warp's diagonal block: column `lane` of its inverse
+        // column `lane` of the inverse of this warp's diagonal block: once an entry is final, it is taken out of
+        // all later ones, which are independent of each other
         __syncwarp();
-        const float *Ab = A + (quad * 32) * kLd + quad * 32;
-        float x[32];
+        const float *Ab = At + (quad * 32) * kLd + quad * 32;
+        float v[32];
 #pragma unroll
-        for (int r = 0; r < 32; ++r) {
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+        for (int m = 0; m < 32; ++m) v[m] = m == lane ? 1.f : 0.f;
 #pragma unroll
-          for (int m = 0; m < r; m += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(Ab + r * kLd + m);
-            s0 = fmaf(a.x, x[m], s0);
-            if (m + 1 < r) s1 = fmaf(a.y, x[m + 1], s1);
-            if (m + 2 < r) s2 = fmaf(a.z, x[m + 2], s2);
-            if (m + 3 < r) s3 = fmaf(a.w, x[m + 3], s3);
+        for (int m = 0; m < 31; ++m) {
+#pragma unroll
+          for (int n = (m + 1) / 4 * 4; n < 32; n += 4) {
+            const float4 a = *reinterpret_cast<const float4 *>(Ab + m * kLd + n);
+            if (n > m) v[n] = fmaf(-a.x, v[m], v[n]);
+            if (n + 1 > m) v[n + 1] = fmaf(-a.y, v[m], v[n + 1]);
+            if (n + 2 > m) v[n + 2] = fmaf(-a.z, v[m], v[n + 2]);
+            v[n + 3] = fmaf(-a.w, v[m], v[n + 3]);
           }
-          x[r] = (r == lane ? 1.f : 0.f) - ((s0 + s1) + (s2 + s3));
-          Ti[(quad * 32 + r) * kLd + quad * 32 + lane] = x[r];
         }
+#pragma unroll
+        for (int m = 0; m < 32; ++m) Ti[(quad * 32 + m) * kLd + quad * 32 + lane] = v[m];
       }
     } else {
       // P_ij = Gam_ij (q_i . k_j), j <= i, straight to the record
@@ -274,9 +288,9 @@ __global__ void __launch_bounds__(kPrepThreads)
       // the off-diagonal block -T22 (A21 T11): X = A21 T11 parked in the upper right block, then zeroed
       const int r = tid / 8, c0 = (tid % 8) * 4;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 16
       for (int m = 0; m < 32; ++m) {
-        const float a = A[(32 + r) * kLd + m];
+        const float a = At[m * kLd + 32 + r];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0);
         acc = make_float4(fmaf(a, u.x, acc.x), fmaf(a, u.y, acc.y), fmaf(a, u.z, acc.z), fmaf(a, u.w, acc.w));
       }
@@ -284,7 +298,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       *X = acc;
       __syncthreads();
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 16
       for (int m = 0; m < 32; ++m) {
         const float a = -Ti[(32 + r) * kLd + 32 + m];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + 32 + c0);
