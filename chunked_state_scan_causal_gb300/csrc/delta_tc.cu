@@ -131,7 +131,7 @@ __device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
 // ================================================================== prep
 // One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
 // cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks by forward
-// substitution, one column per thread, then the off-diagonal block as two 32^3 products), and
+// substitution, a column per thread, then the off-diagonal block as two 32^3 products), and
 // W^T = K^T (T diag(e^g))^T on the tensor cores.  Three CTAs fit an SM and hide each other's latencies.
 constexpr int kPrepThreads = 256;
 constexpr int kLd = 68;  // row stride of the fp32 64 x 64 matrices: 16-byte rows, spread over the banks
@@ -230,52 +230,74 @@ __global__ void __launch_bounds__(kPrepThreads)
     const uint32_t quad = warp & 3, x = warp >> 2, lb = (quad * 32) << 16;
     const int i = (quad & 1) * 32 + lane;
     const float hi = s_hi[i], lo = s_lo[i];
-    uint32_t r[32];
-    if (quad >= 2 || x <= quad) {
-      tmem_ld32(tmem + lb + 32 * x, r);
-      tmem_ld_wait();
-    }
+    // (loops stay loops here: straight-line code, run once per CTA by a few warps, is bound by fetching it)
     if (quad < 2) {
       // A_ij = Gam_ij (k_i . k_j) b_j, j < i, transposed (the block above the diagonal is not used)
       if (x <= quad)
+#pragma unroll 1
+        for (int y = 0; y < 32; y += 8) {
+          uint32_t r[8];
+          tmem_ld8(tmem + lb + 32 * x + y, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int y = 0; y < 32; ++y) {
-          const int j = 32 * x + y;
-          const float e = ex2((hi - s_hi[j]) + (lo - s_lo[j]));
-          At[j * kLd + i] = j < i ? e * __uint_as_float(r[y]) * s_b[j] : 0.f;
-        }
-      if (x == quad) {
-        // column `lane` of the inverse of this warp's diagonal block: once an entry is final, it is taken out of
-        // all later ones, which are independent of each other
-        __syncwarp();
-        const float *Ab = At + (quad * 32) * kLd + quad * 32;
-        float v[32];
-#pragma unroll
-        for (int m = 0; m < 32; ++m) v[m] = m == lane ? 1.f : 0.f;
-#pragma unroll
-        for (int m = 0; m < 31; ++m) {
-#pragma unroll
-          for (int n = (m + 1) / 4 * 4; n < 32; n += 4) {
-            const float4 a = *reinterpret_cast<const float4 *>(Ab + m * kLd + n);
-            if (n > m) v[n] = fmaf(-a.x, v[m], v[n]);
-            if (n + 1 > m) v[n + 1] = fmaf(-a.y, v[m], v[n + 1]);
-            if (n + 2 > m) v[n + 2] = fmaf(-a.z, v[m], v[n + 2]);
-            v[n + 3] = fmaf(-a.w, v[m], v[n + 3]);
+          for (int z = 0; z < 8; ++z) {
+            const int j = 32 * x + y + z;
+            const float e = ex2((hi - s_hi[j]) + (lo - s_lo[j]));
+            At[j * kLd + i] = j < i ? e * __uint_as_float(r[z]) * s_b[j] : 0.f;
           }
         }
+      if (x == quad) {
+        // column `lane` of the inverse V of this warp's diagonal block, eight rows at a time: the rows before
+        // them (in shared memory) are taken out, then the 8 x 8 triangle is solved in registers
+        __syncwarp();
+        const float *Ab = At + (quad * 32) * kLd + quad * 32;
+        float *V = Ti + (quad * 32) * kLd + quad * 32 + lane;
+#pragma unroll 1
+        for (int r = 0; r < 32; r += 8) {
+          float v[8];
 #pragma unroll
-        for (int m = 0; m < 32; ++m) Ti[(quad * 32 + m) * kLd + quad * 32 + lane] = v[m];
+          for (int e = 0; e < 8; ++e) v[e] = r + e == lane ? 1.f : 0.f;
+#pragma unroll 1
+          for (int m = 0; m < r; m += 4) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const float w = V[(m + f) * kLd];
+              const float4 a = *reinterpret_cast<const float4 *>(Ab + (m + f) * kLd + r);
+              const float4 b = *reinterpret_cast<const float4 *>(Ab + (m + f) * kLd + r + 4);
+              v[0] = fmaf(-a.x, w, v[0]);
+              v[1] = fmaf(-a.y, w, v[1]);
+              v[2] = fmaf(-a.z, w, v[2]);
+              v[3] = fmaf(-a.w, w, v[3]);
+              v[4] = fmaf(-b.x, w, v[4]);
+              v[5] = fmaf(-b.y, w, v[5]);
+              v[6] = fmaf(-b.z, w, v[6]);
+              v[7] = fmaf(-b.w, w, v[7]);
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < 7; ++f) {
+            const float4 a = *reinterpret_cast<const float4 *>(Ab + (r + f) * kLd + r);
+            const float4 b = *reinterpret_cast<const float4 *>(Ab + (r + f) * kLd + r + 4);
+            const float col[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int e = f + 1; e < 8; ++e) v[e] = fmaf(-col[e], v[f], v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) V[(r + e) * kLd] = v[e];
+        }
       }
     } else {
       // P_ij = Gam_ij (q_i . k_j), j <= i, straight to the record
-#pragma unroll
+#pragma unroll 1
       for (int y = 0; y < 4; ++y) {
-        uint32_t ph[4], pl[4];
+        uint32_t r[8], ph[4], pl[4];
+        tmem_ld8(tmem + lb + 32 * x + 8 * y, r);
+        tmem_ld_wait();
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const int j = 32 * x + 8 * y + 2 * z;
-          float p0 = ex2((hi - s_hi[j]) + (lo - s_lo[j])) * __uint_as_float(r[8 * y + 2 * z]);
-          float p1 = ex2((hi - s_hi[j + 1]) + (lo - s_lo[j + 1])) * __uint_as_float(r[8 * y + 2 * z + 1]);
+          float p0 = ex2((hi - s_hi[j]) + (lo - s_lo[j])) * __uint_as_float(r[2 * z]);
+          float p1 = ex2((hi - s_hi[j + 1]) + (lo - s_lo[j + 1])) * __uint_as_float(r[2 * z + 1]);
           split2(j <= i ? p0 : 0.f, j + 1 <= i ? p1 : 0.f, ph[z], pl[z]);
         }
         const uint32_t at = sw(i, 4 * x + y);
@@ -288,7 +310,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       // the off-diagonal block -T22 (A21 T11): X = A21 T11 parked in the upper right block, then zeroed
       const int r = tid / 8, c0 = (tid % 8) * 4;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
+#pragma unroll 4
       for (int m = 0; m < 32; ++m) {
         const float a = At[m * kLd + 32 + r];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0);
@@ -298,7 +320,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       *X = acc;
       __syncthreads();
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 16
+#pragma unroll 4
       for (int m = 0; m < 32; ++m) {
         const float a = -Ti[(32 + r) * kLd + 32 + m];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + 32 + c0);
@@ -312,7 +334,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     {
       // T to the record; T diag(e^g), the operand of W, over A
       const int row = tid & 63, q = tid / 64;
-#pragma unroll
+#pragma unroll 1
       for (int y = 0; y < 2; ++y) {
         uint32_t th[4], tl[4], eh[4], el[4];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + row * kLd + 16 * q + 8 * y);
@@ -350,7 +372,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (__syncthreads_and(ok)) {
       tc_fence_after();
       // W^T: lane = key dimension, column = token; negated, with tokens as rows over the K and Q tiles
-#pragma unroll
+#pragma unroll 1
       for (uint32_t y = 0; y < 4; ++y) {
         const uint32_t row0 = quad * 32 + 16 * (y & 1), tok0 = 32 * x + 16 * (y >> 1);
         float w[8];
@@ -1246,7 +1268,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // Z: an operand tile (row = value dimension), where dq was, and dv, where dU was
       if (!(wait(G_Z, x) && (x == 0 || wait(G_STORED, x - 1)))) return false;
       tc_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (uint32_t hh = 0; hh < 2; ++hh) {
         float z[8];
         uint32_t p[4];
@@ -1287,7 +1309,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (!wait(G_64, x)) return false;
       tc_fence_after();
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
       for (uint32_t hh = 0; hh < 2; ++hh) {
         const uint32_t row0 = (quad & 1) * 32 + 16 * hh;
         float a[8], zy[8];
@@ -1331,7 +1353,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (!wait(G_ALL, x)) return false;
       tc_fence_after();
       // lane = key dimension; w gathers q . dq + k . (read - write part)
-#pragma unroll
+#pragma unroll 1
       for (uint32_t hh = 0; hh < 2; ++hh) {
         const uint32_t row0 = quad * 32 + 16 * hh, at = frag_at_trans(lane, 16 * cg, row0, 8192);
         float a[8], b[8];
