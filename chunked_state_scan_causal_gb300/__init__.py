@@ -109,6 +109,8 @@ KERNEL_KINDS = 30
 def lib():
     """The loaded ctypes library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -312,8 +314,8 @@ def _ptr(t):
 
 def _stream(dev, stream=None):
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    return s.cuda_stream
+    # (the raw handle: building the Stream object around it costs more than some of the kernels)
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def shape_of(q, decay=None, chunk: int = 64) -> Shape:
@@ -322,20 +324,17 @@ def shape_of(q, decay=None, chunk: int = 64) -> Shape:
     if q.dim() != 4 or q.stride(-1) != 1:
         raise ValueError("sequence tensors must be [B, H, T, d] with a contiguous last dimension")
     B, H, T, d = q.shape
-    dt = {torch.bfloat16: BF16, torch.float32: F32}.get(q.dtype)
+    dt = BF16 if q.dtype == torch.bfloat16 else F32 if q.dtype == torch.float32 else None
     if dt is None:
         raise ValueError(f"unsupported dtype {q.dtype}")
-    s = Shape()
-    s.abi_version, s.B, s.H, s.T, s.dk, s.dv, s.chunk, s.dtype = ABI_VERSION, B, H, T, d, d, chunk, dt
-    s.stride_b, s.stride_h, s.stride_t = q.stride(0), q.stride(1), q.stride(2)
-    s.decay = _ptr(decay)
-    return s
+    sb, sh, st, _ = q.stride()
+    return Shape(ABI_VERSION, B, H, T, d, d, chunk, dt, sb, sh, st, _ptr(decay))
 
 
 def _same_layout(ref, *ts):
+    shape, stride, dtype, device = ref.shape, ref.stride(), ref.dtype, ref.device
     for t in ts:
-        if t is not None and (t.shape != ref.shape or t.stride() != ref.stride() or t.dtype != ref.dtype
-                              or t.device != ref.device):
+        if t is not None and (t.shape != shape or t.stride() != stride or t.dtype != dtype or t.device != device):
             raise ValueError("q, k, v (and dO, outputs) must share shape, strides, dtype and device")
 
 
@@ -657,6 +656,19 @@ def softmax_segment_bwd(q, k, v, o, dO, lse, scale: float = 0.0, outs=None, ws=N
     return dq, dk, dv
 
 
+_paged_ws = {}  # workspace bytes of paged_decode by (device, head dimension): they depend on nothing else
+
+
+def _paged_workspace(q):
+    import torch
+    n = _paged_ws.get((q.device, q.shape[-1]))
+    if n is None:
+        st, n = linattn_workspace_size(shape_of(q), OP_PAGED_DECODE)
+        _check(st, "linattn_workspace_size")
+        _paged_ws[(q.device, q.shape[-1])] = n
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
+
+
 def checkpoint_delta(q):
     """Checkpoint buffer of fwd_delta(..., ckpt=) for bwd_delta."""
     import torch
@@ -668,10 +680,10 @@ def checkpoint_delta(q):
 def _delta_gates(log_gate, beta, q):
     """The gate type of the C ABI, after checking both gates (log_gate may be None)."""
     import torch
-    dt = {torch.float32: F32, torch.bfloat16: BF16}.get(beta.dtype)
+    dt = BF16 if beta.dtype == torch.bfloat16 else F32 if beta.dtype == torch.float32 else None
+    shape, device = q.shape[:3], q.device
     for g in (beta,) if log_gate is None else (beta, log_gate):
-        if dt is None or g.dtype != beta.dtype or not g.is_contiguous() or g.shape != q.shape[:3] \
-                or g.device != q.device:
+        if dt is None or g.dtype != beta.dtype or not g.is_contiguous() or g.shape != shape or g.device != device:
             raise ValueError("log_gate and beta must be contiguous [B, H, T], both fp32 or both bf16, on q's device")
     return dt
 
@@ -680,7 +692,7 @@ def _states(q, *ts):
     import torch
     B, H, _, d = q.shape
     for t in ts:
-        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (B, H, d, d)
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.shape != (B, H, d, d)
                               or t.device != q.device):
             raise ValueError("states must be contiguous fp32 [B, H, d, d] on q's device")
 
@@ -789,7 +801,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0,
     o = out if out is not None else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if want_lse else None
     if ws is None:
-        ws = workspace(q, OP_PAGED_DECODE)
+        ws = _paged_workspace(q)
     st = linattn_paged_decode(shape_of(q), shape_of(k_cache), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
                               _ptr(lse), tab, n, stride, _ptr(seq_lens), scale, _ptr(ws), ws.numel(),
                               _stream(q.device, stream))

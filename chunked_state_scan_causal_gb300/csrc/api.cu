@@ -896,7 +896,7 @@ int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape
   if (x.T == 0) return LINATTN_OK;
   if ((st = check_ptrs({k, v, k_cache, v_cache}, {}))) return st;
   if (!start) return LINATTN_ERR_INVALID;
-  if ((int64_t)x.B * x.H * x.T > ((int64_t)1 << 36)) return LINATTN_ERR_UNSUPPORTED;  // the launch's block count
+  if ((int64_t)x.B * x.H * x.T > 0x7fffffff) return LINATTN_ERR_UNSUPPORTED;  // rows are 32-bit
   if ((st = device_ok())) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (device_status && clear_header(device_status, 4, s) != cudaSuccess) return LINATTN_ERR_CUDA;

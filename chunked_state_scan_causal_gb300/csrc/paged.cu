@@ -18,32 +18,30 @@ namespace {
 // sequence, by the launch).  Rows past new_lens, outside the table or with a page id outside the
 // cache are left unwritten; the latter two are recorded in the status word.
 __global__ void __launch_bounds__(256) paged_append_kernel(PagedProblem p, const char *k, const char *v, char *kc,
-                                                           char *vc, int T, const int *start, const int *new_lens,
-                                                           int64_t sb, int64_t sh, int64_t st, int row16,
-                                                           int64_t n, int *status) {
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  const int c = (int)(i % row16);
-  int64_t r = i / row16;
-  const int t = (int)(r % T);
-  r /= T;
-  const int h = (int)(r % p.Hkv), b = (int)(r / p.Hkv);
-  if (new_lens && t >= new_lens[b]) return;
-  const int64_t pos = (int64_t)start[b] + t;
-  const int64_t block = pos / p.page;
-  if (start[b] < 0 || block >= p.max_blocks) {
+                                                           char *vc, uint32_t T, const int *start, const int *new_lens,
+                                                           int64_t sb, int64_t sh, int64_t st, int shift,
+                                                           uint32_t rows, int *status) {
+  const uint32_t row = blockIdx.x * (256u >> shift) + (threadIdx.x >> shift), c = threadIdx.x & ((1u << shift) - 1);
+  if (row >= rows) return;
+  const uint32_t r = row / T, t = row % T, b = r / (uint32_t)p.Hkv, h = r % (uint32_t)p.Hkv;
+  if (new_lens && (int)t >= new_lens[b]) return;
+  const int first = start[b];
+  const int64_t pos = (int64_t)first + t;
+  if (first < 0 || pos >= (int64_t)p.max_blocks * p.page) {
     report_error(status, -1);
     return;
   }
+  const uint32_t block = (uint32_t)pos / (uint32_t)p.page, slot = (uint32_t)pos % (uint32_t)p.page;
   const int id = p.table[(int64_t)b * p.tstride + block];
   if (id < 0 || id >= p.pages) {
     report_error(status, -1);
     return;
   }
   const int64_t src = (b * sb + h * sh + t * st) * p.esz + 16 * c;
-  const int64_t dst = (id * p.csb + h * p.csh + (pos - block * p.page) * p.cst) * p.esz + 16 * c;
-  *reinterpret_cast<uint4 *>(kc + dst) = *reinterpret_cast<const uint4 *>(k + src);
-  *reinterpret_cast<uint4 *>(vc + dst) = *reinterpret_cast<const uint4 *>(v + src);
+  const int64_t dst = (id * p.csb + h * p.csh + slot * p.cst) * p.esz + 16 * c;
+  const uint4 x = *reinterpret_cast<const uint4 *>(k + src), y = *reinterpret_cast<const uint4 *>(v + src);
+  *reinterpret_cast<uint4 *>(kc + dst) = x;
+  *reinterpret_cast<uint4 *>(vc + dst) = y;
 }
 
 // ------------------------------------------------------------------ work split of the decode
@@ -832,11 +830,12 @@ size_t paged_decode_ws_bytes(int d, int num_sms) {
 cudaError_t paged_append(const PagedProblem &p, const void *k, const void *v, void *kc, void *vc, int T, int64_t sb,
                          int64_t sh, int64_t st, const int *start, const int *new_lens, int *status, cudaStream_t s) {
   TimedLaunch t(K_PAGED_APPEND, s);
-  const int row16 = p.d * p.esz / 16;
-  const int64_t n = (int64_t)p.B * p.Hkv * T * row16;
-  paged_append_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, (const char *)k, (const char *)v, (char *)kc,
-                                                                  (char *)vc, T, start, new_lens, sb, sh, st, row16,
-                                                                  n, status);
+  int shift = 0;  // log2 of the 16-byte pieces of a row (d = 64 or 128, 2 or 4 bytes: 8 to 32)
+  while (16 << shift < p.d * p.esz) ++shift;
+  const uint32_t rows = (uint32_t)p.B * p.Hkv * T, per = 256u >> shift;
+  paged_append_kernel<<<(rows + per - 1) / per, 256, 0, s>>>(p, (const char *)k, (const char *)v, (char *)kc, (char *)vc,
+                                                             (uint32_t)T, start, new_lens, sb, sh, st, shift, rows,
+                                                             status);
   return cudaGetLastError();
 }
 
