@@ -1081,13 +1081,14 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 // Chunk after chunk, independent of each other, on one CTA per SM.  Products of the form [dimension x token]
 // have lane = dimension; the 64 x 64 ones come from 128-row operands whose other rows are unused: [K; dO]
 // stacked gives K K^T in lanes 0..63 and dO Y^T in lanes 64..127.  Warps 0..15 turn products into operands and
-// results (16 columns each); warp 16 loads, issues the products and stores, so that while the threads are in
-// one chunk's last step the next one's tiles arrive and its first product runs.  Bound by the 88 products of a
+// results (16 columns each), warp 16 issues the products, warp 17 loads and stores: the next chunk's tiles arrive
+// and its first product runs while the threads are in this one's last step.  Bound by the 96 products of a
 // chunk (their operand rows, about 50 cycles each) and the latencies between its five steps.
 //
-// Single bf16 operands except Y in dO Y^T and the matrix A made from it, which have two parts: with one the
-// gradients' errors come to 2.9e-3 of their size, 1.75 times the rounding of the results themselves.
-constexpr int kGradThreads = 544, kGradWarps = 16;
+// Single bf16 operands except Y in dO Y^T and Y R^T and the matrix A, which have two parts: with one the
+// gradients' errors come to 2.9e-3 of their size, 1.75 times the rounding of the results themselves (now 2.0e-3
+// to 2.5e-3; Z, D and the images of S and R would cost another 40 products for 2.4e-3).
+constexpr int kGradThreads = 576, kGradWarps = 16;
 constexpr uint32_t kGrKD = 0, kGrQ = 32768, kGrS = 49152, kGrR = 81920, kGrY = 114688, kGrU = 147456, kGrZ = 163840,
                    kGrA = 180224,           // A hi, A lo, D (8 KiB each); T lives over the last two before them
                    kGrX = 204800, kGrG = 221184, kGrEnd = kGrG + 2 * 1536;
@@ -1156,40 +1157,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       }
     };
     constexpr uint32_t kK = 2, kM = 128, k8 = 8192 >> 4, k16 = 16384 >> 4;  // K-major and MN-major steps; blocks
-    auto load1 = [&](int item) {
-      if (lane != 0) return;
-      const int c = item % P.N, bh = item / P.N, g = (item - blockIdx.x) / gridDim.x & 1;
-      const int64_t ci = (int64_t)bh * P.N + c;
-      const uint8_t *rec = P.rec + ci * kRecBytes;
-      mbar_arrive_expect_tx(&bar[G_UT], 16384 + kGateBytes + 16384 + 32768);
-      bulk_load(&bar[G_UT], smem + kGrU, P.uimg + ci * kRowImg, 16384);
-      bulk_load(&bar[G_UT], smem + kGrT, rec + kRecT, 16384);
-      bulk_load(&bar[G_UT], smem + kGrG + g * 1536, rec + kRecG, kGateBytes);
-      bulk_load(&bar[G_UT], smem + kGrY, P.yimg + ci * kYImg, 32768);
-      mbar_arrive_expect_tx(&bar[G_SR], 65536);
-      bulk_load(&bar[G_SR], smem + kGrS, P.simg + ci * kStateImg, 32768);
-      bulk_load(&bar[G_SR], smem + kGrR, P.rimg + ci * kStateImg, 32768);
-    };
-    auto load2 = [&](int item) {
-      if (lane != 0) return;
-      const int c = item % P.N, bh = item / P.N, b = bh / P.H, h = bh % P.H;
-      mbar_arrive_expect_tx(&bar[G_KQ], 49152);
-      for (int x = 0; x < 2; ++x) {
-        tma_load_4d(&mk, &bar[G_KQ], smem + kGrKD + x * 16384, 64 * x, kC * c, h, b, kPolicyEvictFirst);
-        tma_load_4d(&mdo, &bar[G_KQ], smem + kGrKD + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictFirst);
-        tma_load_4d(&mq, &bar[G_KQ], smem + kGrQ + x * 8192, 64 * x, kC * c, h, b, kPolicyEvictFirst);
-      }
-    };
-    auto store = [&](const CUtensorMap *m, uint32_t from, int item) {
-      const int c = item % P.N, bh = item / P.N, b = bh / P.H, h = bh % P.H;
-      for (int y = 0; y < P.d / 64; ++y) tma_store_4d(m, smem + from + y * 8192, 64 * y, kC * c, h, b);
-      bulk_commit();
-    };
-    int x = 0, last = 0;  // (loads issued: x + 1 of the first kind, last + 1 of the second)
-    if ((int)blockIdx.x < items) {
-      load1(blockIdx.x);
-      load2(blockIdx.x);
-    }
+    int x = 0;
 #pragma unroll 1
     for (int item = blockIdx.x; item < items; item += gridDim.x, ++x) {
       const uint64_t y = k_tile(Y), ylo = k_tile(Y + 16384), zm = mn_tile(Z, 16384), sk = k_tile(S), rk = k_tile(R),
@@ -1200,35 +1168,22 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       // Z^T = (diag(b) dU)^T T
       mma(kGZ, mn_tile(base + kGrU, 8192), mn_tile(base + kGrT, 8192), id_mm, true, 2, kM, 0, kM, k8);
       mma_commit_warp(&bar[G_Z]);
-      // the accumulators that follow were read in the last chunk's last step
-      if (x > 0) {
-        if (!(ok = wait(G_END, x - 1))) break;
-        load2(item);
-        ++last;
-        if (lane == 0) {
-          store(&mdq, kGrZ, item - gridDim.x);
-          store(&mdk, kGrX, item - gridDim.x);
-          bulk_wait_read_all();
-          mbar_arrive(&bar[G_STORED]);
-        }
-        __syncwarp();
-      }
-      if (!(ok = wait(G_KQ, x))) break;
+      // (the accumulators that follow are read in the last chunk's last step)
+      if (!(ok = wait(G_KQ, x) && (x == 0 || wait(G_END, x - 1)))) break;
       tc_fence_after();
       mma(kGKK, kk, kk, id_kk, true, 2, kK, k16, kK, k16);                 // K K^T (lanes 0..63)
       mma(kGdP, kk, y, id_kk, true, kd, kK, k16, kK, k8);                  // dO Y^T (lanes 64..127)
       mma(kGdP, kk, ylo, id_kk, false, kd, kK, k16, kK, k8);
-      if (!(ok = wait(G_SR, x))) break;
-      tc_fence_after();
-      mma(kGdq, sk, k_tile(dO), id_kk, true, kd, kK, k16, kK, k16);        // (dO S^T)^T
-      mma(kGdw, rk, y, id_kk, true, kd, kK, k16, kK, k8);                  // (Y R^T)^T
       if (!(ok = wait(G_ZT, x))) break;
       tc_fence_after();
       mma(kGGY, zm, y, id_mk, true, kd, kM, 4 * kM, kK, k8);               // Z Y^T (lanes 0..63)
       mma_commit_warp(&bar[G_64]);
+      if (!(ok = wait(G_SR, x))) break;
+      tc_fence_after();
       mma(kGdr, sk, zm, id_km, true, kd, kK, k16, kM, 4 * kM);             // (Z S^T)^T
-      if (lane == 0) store(&mdv, kGrU, item);
-      __syncwarp();
+      mma(kGdq, sk, k_tile(dO), id_kk, true, kd, kK, k16, kK, k16);        // (dO S^T)^T
+      mma(kGdw, rk, y, id_kk, true, kd, kK, k16, kK, k8);                  // (Y R^T)^T
+      mma(kGdw, rk, ylo, id_kk, false, kd, kK, k16, kK, k8);
       if (!(ok = wait(G_AD, x))) break;
       tc_fence_after();
       mma(kGKK, km, ak, id_mk, true, 2, kM, 0, kK, k8);                    // (A K)^T
@@ -1236,25 +1191,55 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       mma(kGGY, qm, am, id_mm, true, 2, kM, 0, kM, k8);                    // (A^T Q + D^T K)^T
       mma(kGGY, km, dm, id_mm, false, 1, kM, 0, kM, 0);
       mma_commit_warp(&bar[G_ALL]);
-      if (item + (int)gridDim.x < items) {
-        if (!(ok = wait(G_ALL, x))) break;
-        if (lane == 0) bulk_wait_read_all();  // dv has left the place that the next chunk's dU takes
-        __syncwarp();
-        load1(item + gridDim.x);
-      }
     }
-    if (ok && x > 0 && (ok = wait(G_END, x - 1)) && lane == 0) {
-      const int item = blockIdx.x + (x - 1) * gridDim.x;
-      store(&mdq, kGrZ, item);
-      store(&mdk, kGrX, item);
-    }
+  } else if (warp > kGradWarps) {
     if (lane == 0) {
+      auto await = [&](int i, int x) { return mbar_wait_compact(&bar[i], x & 1, &abort_flag, P.status); };
+      auto load = [&](int item, int g) {
+        const int c = item % P.N, bh = item / P.N, b = bh / P.H, h = bh % P.H;
+        const uint8_t *rec = P.rec + (int64_t)item * kRecBytes;
+        mbar_arrive_expect_tx(&bar[G_UT], 16384 + kGateBytes + 16384 + 32768);
+        bulk_load(&bar[G_UT], smem + kGrU, P.uimg + (int64_t)item * kRowImg, 16384);
+        bulk_load(&bar[G_UT], smem + kGrT, rec + kRecT, 16384);
+        bulk_load(&bar[G_UT], smem + kGrG + g * 1536, rec + kRecG, kGateBytes);
+        bulk_load(&bar[G_UT], smem + kGrY, P.yimg + (int64_t)item * kYImg, 32768);
+        mbar_arrive_expect_tx(&bar[G_KQ], 49152);
+        for (int x = 0; x < 2; ++x) {
+          tma_load_4d(&mk, &bar[G_KQ], smem + kGrKD + x * 16384, 64 * x, kC * c, h, b, kPolicyEvictFirst);
+          tma_load_4d(&mdo, &bar[G_KQ], smem + kGrKD + x * 16384 + 8192, 64 * x, kC * c, h, b, kPolicyEvictFirst);
+          tma_load_4d(&mq, &bar[G_KQ], smem + kGrQ + x * 8192, 64 * x, kC * c, h, b, kPolicyEvictFirst);
+        }
+        mbar_arrive_expect_tx(&bar[G_SR], 65536);
+        bulk_load(&bar[G_SR], smem + kGrS, P.simg + (int64_t)item * kStateImg, 32768);
+        bulk_load(&bar[G_SR], smem + kGrR, P.rimg + (int64_t)item * kStateImg, 32768);
+      };
+      auto store = [&](const CUtensorMap *m, uint32_t from, int item) {
+        const int c = item % P.N, bh = item / P.N, b = bh / P.H, h = bh % P.H;
+        for (int y = 0; y < P.d / 64; ++y) tma_store_4d(m, smem + from + y * 8192, 64 * y, kC * c, h, b);
+        bulk_commit();
+      };
+      int x = 0, loaded = 0;
+      if ((int)blockIdx.x < items) load(blockIdx.x, 0);
+#pragma unroll 1
+      for (int item = blockIdx.x; item < items; item += gridDim.x, ++x) {
+        if (!(ok = await(G_ZT, x))) break;
+        store(&mdv, kGrU, item);
+        if (!(ok = await(G_ALL, x))) break;
+        bulk_wait_read_all();  // dv has left the place that the next chunk's diag(b) dU takes
+        if (item + (int)gridDim.x < items) {
+          load(item + gridDim.x, (x + 1) & 1);
+          ++loaded;
+        }
+        if (!(ok = await(G_END, x))) break;
+        store(&mdq, kGrZ, item);
+        store(&mdk, kGrX, item);
+        bulk_wait_read_all();
+        mbar_arrive(&bar[G_STORED]);
+      }
       bulk_wait_all();
       if (!ok) {  // after an abort, with limits: what is in flight lands before the block ends
         volatile int no_abort = 0;
-        mbar_wait_compact(&bar[G_UT], x & 1, &no_abort, P.status);
-        mbar_wait_compact(&bar[G_SR], x & 1, &no_abort, P.status);
-        mbar_wait_compact(&bar[G_KQ], last & 1, &no_abort, P.status);
+        for (int i = G_UT; i <= G_KQ; ++i) mbar_wait_compact(&bar[i], loaded & 1, &no_abort, P.status);
       }
     }
     __syncwarp();
@@ -1306,6 +1291,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         jh[e] = g[192 + j];
         jl[e] = g[256 + j];
       }
+      // q and k of the last step, so that their tiles are free before it
+      uint32_t qf[2][4], kf[2][4];
+      if (!wait(G_KQ, x)) return false;
+#pragma unroll
+      for (uint32_t hh = 0; hh < 2; ++hh) {
+        ldmatrix4_trans(base + kGrQ + frag_at_trans(lane, 16 * cg, quad * 32 + 16 * hh, 8192), qf[hh]);
+        ldmatrix4_trans(KD + frag_at_trans(lane, 16 * cg, quad * 32 + 16 * hh, 16384), kf[hh]);
+      }
       if (!wait(G_64, x)) return false;
       tc_fence_after();
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1353,19 +1346,18 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (!wait(G_ALL, x)) return false;
       tc_fence_after();
       // lane = key dimension; w gathers q . dq + k . (read - write part)
-#pragma unroll 1
+#pragma unroll
       for (uint32_t hh = 0; hh < 2; ++hh) {
         const uint32_t row0 = quad * 32 + 16 * hh, at = frag_at_trans(lane, 16 * cg, row0, 8192);
         float a[8], b[8];
         uint32_t p[4];
         frag(kGdq, hh, a);
         frag(kGKK, hh, b);
-        ldmatrix4_trans(base + kGrQ + at, p);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           a[i] = fmaf(eg[frag_col(i)], a[i], b[i]);
-          w[frag_col(i)] = fmaf(a[i], i & 1 ? bf16hi(p[i / 2]) : bf16lo(p[i / 2]), w[frag_col(i)]);
+          w[frag_col(i)] = fmaf(a[i], i & 1 ? bf16hi(qf[hh][i / 2]) : bf16lo(qf[hh][i / 2]), w[frag_col(i)]);
         }
         frag_pack(a, p);
         stmatrix4_trans(Z + at, p);
@@ -1374,12 +1366,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         frag(kGdP, hh, b);
         frag(kGdw, hh, f);
         frag(kGGY, hh, u);
-        ldmatrix4_trans(KD + frag_at_trans(lane, 16 * cg, row0, 16384), p);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int e = frag_col(i);
-          const float kv = i & 1 ? bf16hi(p[i / 2]) : bf16lo(p[i / 2]), r = pb[e] * f[i];
+          const float kv = i & 1 ? bf16hi(kf[hh][i / 2]) : bf16lo(kf[hh][i / 2]), r = pb[e] * f[i];
           const float read = fmaf(-eg[e], a[i], b[i]), write = r + u[i];
           kw = fmaf(kv, r, kw);
           w[e] = fmaf(read - write, kv, w[e]);
