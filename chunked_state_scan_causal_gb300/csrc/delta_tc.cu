@@ -427,7 +427,7 @@ struct Chain {
 static_assert(Chain<32>::smem <= 231000 && Chain<64>::smem <= 231000, "one CTA per SM");
 
 enum { C_OP = 0,    // S (R) operand parts ready
-       C_SCALED,    // its accumulator scaled by the chunk's decay
+       C_SCALED,    // backward: its accumulator scaled by the chunk's decay
        C_ACC,       // its accumulator complete (next chunk)
        C_YFULL,     // Y (K R) accumulator complete
        C_YOP,       // the operand made from it for the update ready
@@ -503,6 +503,19 @@ struct ChainCtx {
   __device__ bool full(Pos p) const { return wait_w(C_FULL + p.s, p.ph); }
   template <typename Pos>
   __device__ void release(Pos p) const { mma_commit_warp(&bar[empty0 + p.s]); }
+  // Several barriers at once: their tests go out back to back (one wait costs some 150 cycles even when there
+  // is nothing to wait for), and only if one is not yet there they are waited for one by one.
+  template <int N>
+  __device__ bool wait_all(const int (&idx)[N], const uint32_t (&parity)[N]) const {
+    bool ready = true;
+#pragma unroll
+    for (int i = 0; i < N; ++i) ready &= mbar_test_wait(&bar[idx[i]], parity[i] & 1);
+    if (__all_sync(0xffffffffu, ready)) return true;
+#pragma unroll 1
+    for (int i = 0; i < N; ++i)
+      if (!wait_w(idx[i], parity[i])) return false;
+    return true;
+  }
   __device__ bool gates_ready(int x) const { return wait_w(C_GFULL + x % kGateRing, x / kGateRing); }
   __device__ const float *gates(int x) const {
     return reinterpret_cast<const float *>(smem + L::gate + (x % kGateRing) * 2048);
@@ -725,8 +738,8 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     RV rv;  // V
     RX rx;  // T, K
     RY ry;  // W hi, W lo
+    auto landed = [&] { return k.full(rv) && k.full(rx) && k.full(ry) && k.full(ry.next()); };  // V, T, W
     auto vt = [&] {  // Y = T V
-      if (!k.full(rv) || !k.full(rx)) return false;
       tc_fence_after();
       const uint64_t v = mn_tile(k.slot(rv) + (x0 & 63) * 2, 8192), tt = k_tile(k.slot(rx));
       mma_fours<false, true, 2>(tmem + kTY, tt, v, id_1, true, kBlock, 0);
@@ -734,14 +747,15 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       k.release(rx);
       rv.advance();
       rx.advance();
-      return true;
     };
-    bool ok = vt();
+    // The waits for the next chunk's tiles stand in the gap before Y's operand, not on the path behind it.
+    bool ok = landed();
+    if (ok) vt();
 #pragma unroll 1
     for (int c = 0; c < P.N && ok; ++c) {
       // Y += W S: hi [hi | lo] (2 VS columns), lo hi
       const RY lo = ry.next();
-      if (!(ok = k.full(ry) && k.full(lo) && k.wait_w(C_OP, c))) break;
+      if (!(ok = k.wait_w(C_OP, c))) break;
       tc_fence_after();
       mma_fours<false, true, 2>(tmem + kTY, k_tile(k.slot(ry)), op, id_2, false, kBlock, kRows64);
       mma_fours<false, true, 2>(tmem + kTY, k_tile(k.slot(lo)), op, id_1, false, kBlock, kRows64);
@@ -750,13 +764,15 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       k.release(lo);
       ry = lo.next();
       // S += K^T diag(phi b) Y
-      if (!(ok = k.full(rx) && k.wait_w(C_SCALED, c) && k.wait_w(C_YOP, c))) break;
-      tc_fence_after();
-      mma_fours<true, true, 2>(tmem + kTS, mn_tile(k.slot(rx), 8192), ut, id_k, false, 0, L::row_lo >> 4);
-      mma_commit_warp(&bar[C_ACC]);
-      k.release(rx);
+      const RX kt = rx;
       rx.advance();
-      if (c + 1 < P.N && !(ok = vt())) break;
+      // (C_YOP: every thread has also written back its part of S, scaled)
+      if (!(ok = k.full(kt) && (c + 1 == P.N || landed()) && k.wait_w(C_YOP, c))) break;
+      tc_fence_after();
+      mma_fours<true, true, 2>(tmem + kTS, mn_tile(k.slot(kt), 8192), ut, id_k, false, 0, L::row_lo >> 4);
+      mma_commit_warp(&bar[C_ACC]);
+      if (c + 1 < P.N) vt();
+      k.release(kt);
     }
   } else if (warp == 2) {
     // the output's products, put into the gaps that the chain leaves the tensor cores: Q S while the
@@ -818,8 +834,6 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[j] *= f;
       tmem_stf(t + kTS, s);
-      tmem_st_wait();
-      k.arrive(C_SCALED, lane);
       if (P.simg) store_row8(P.simg + ((int64_t)bh * P.N + c) * kStateImg + (gcol >> 6) * 16384, row, (gcol & 63) >> 4, hi);
       // The last chunk's output product is done: it has read the operand that is rewritten below, and its
       // issuer has seen that chunk's C_ACC, which the arrival at C_YOP may lead to complete again.
@@ -937,15 +951,14 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     RY ry;  // W hi, W lo
     RZ rz;  // Q
     auto pd = [&](RV d) {  // P^T dO
-      if (!k.full(d) || !k.full(rx)) return false;
       tc_fence_after();
       mma_fours<true, true, 2>(tmem + kT1, mn_tile(k.slot(rx), 8192), mn_tile(k.slot(d) + (x0 & 63) * 2, 8192), id_p, true,
                                kBlock, 0);
       k.release(rx);
       rx.advance();
-      return true;
     };
-    bool ok = pd(rv);
+    bool ok = k.full(rv) && k.full(rx);
+    if (ok) pd(rv);
 #pragma unroll 1
     for (int x = 0; x < P.N && ok; ++x) {
       if (!(ok = k.full(rx) && k.wait_w(C_OP, x))) break;
@@ -955,24 +968,35 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       k.release(rx);
       rx.advance();
       // R += Q^T diag(e^g) dO
-      if (!(ok = k.full(rz) && k.wait_w(C_SCALED, x) && k.wait_w(C_UOP, x))) break;
+      {
+        const int idx[3] = {C_FULL + rz.s, C_SCALED, C_UOP};
+        const uint32_t parity[3] = {rz.ph, (uint32_t)x, (uint32_t)x};
+        if (!(ok = k.wait_all(idx, parity))) break;
+      }
       tc_fence_after();
       mma_fours<true, false, 2>(tmem + kTR, mn_tile(k.slot(rz), 8192), dos, id_k, false, 0, L::row_lo >> 4);
       k.release(rz);
       rz.advance();
       k.release(rv);  // the scaled dO is ready: every reader of this tile is done
       rv.advance();
-      // R += W^T diag(b) dU: hi hi, hi lo, lo hi
+      // R += W^T diag(b) dU: hi hi, hi lo, lo hi (after the waits for the next step's dO and P)
       const RY lo = ry.next();
-      if (!(ok = k.full(ry) && k.full(lo) && k.wait_w(C_YOP, x))) break;
+      if (x + 1 < P.N) {
+        const int idx[4] = {C_FULL + ry.s, C_FULL + lo.s, C_FULL + rv.s, C_FULL + rx.s};
+        const uint32_t parity[4] = {ry.ph, lo.ph, rv.ph, rx.ph};
+        ok = k.wait_all(idx, parity);
+      } else {
+        ok = k.full(ry) && k.full(lo);
+      }
+      if (!(ok = ok && k.wait_w(C_YOP, x))) break;
       tc_fence_after();
       mma_fours<true, false, 2>(tmem + kTR, mn_tile(k.slot(ry), 8192), ut, id_k, false, 0, L::row_lo >> 4);
       mma_fours<true, false, 1>(tmem + kTR, mn_tile(k.slot(lo), 8192), ut, id_k, false, 0, 0);
       mma_commit_warp(&bar[C_ACC]);
+      if (x + 1 < P.N) pd(rv);
       k.release(ry);
       k.release(lo);
       ry = lo.next();
-      if (x + 1 < P.N && !(ok = pd(rv))) break;
     }
   } else if (warp == 2) {
     // (the forward's output products)
