@@ -91,6 +91,23 @@ __device__ __forceinline__ void frag_col_sum(float (&x)[4]) {
     for (int e = 0; e < 4; ++e) x[e] += __shfl_xor_sync(0xffffffffu, x[e], o);
 }
 
+// 8 packed words (16 columns) of row r, column group m of a swizzled block in global memory, as one 32-byte
+// store: the swizzle moves pairs of pieces and, in odd rows, swaps a pair.
+__device__ __forceinline__ uint32_t row8(uint32_t r, uint32_t m) { return r * 128u + ((m ^ ((r & 7u) >> 1)) << 5); }
+__device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t m, const uint32_t (&w)[8]) {
+  const bool odd = r & 1u;
+  uint8_t *dst = block + row8(r, m);
+  uint32_t v[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = odd ? w[4 + e] : w[e];
+    v[4 + e] = odd ? w[e] : w[4 + e];
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // A sum of two fp32 parts, |lo| at most half a step of hi (sums by the error-free transformation of Knuth and
 // Dekker's renormalisation).
 struct Two {
@@ -146,7 +163,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   __shared__ uint64_t bar[3];
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
-  __shared__ float s_hi[kC], s_lo[kC], s_b[kC], s_eg[kC];
+  __shared__ float4 s_g[kC];  // g and its low part, b, e^g
   float *At = reinterpret_cast<float *>(smem + kPrepA), *Ti = reinterpret_cast<float *>(smem + kPrepT);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -201,10 +218,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       const Two gx = x ? s : s + Two{-l[1].hi, -l[1].lo};
       const int j = 2 * lane + x;
       const float eg = ex2(gx.hi) * ex2(gx.lo), phi = ex2((last.hi - gx.hi) + (last.lo - gx.lo));
-      s_hi[j] = gx.hi;
-      s_lo[j] = gx.lo;
-      s_b[j] = be[x];
-      s_eg[j] = eg;
+      s_g[j] = make_float4(gx.hi, gx.lo, be[x], eg);
       g[j] = eg;
       g[64 + j] = phi;
       g[128 + j] = be[x];
@@ -229,7 +243,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     // lanes 0..63: rows of K K^T, 64..127: of Q K^T; columns 32 x .. + 31
     const uint32_t quad = warp & 3, x = warp >> 2, lb = (quad * 32) << 16;
     const int i = (quad & 1) * 32 + lane;
-    const float hi = s_hi[i], lo = s_lo[i];
+    const float hi = s_g[i].x, lo = s_g[i].y;
     // (loops stay loops here: straight-line code, run once per CTA by a few warps, is bound by fetching it)
     if (quad < 2) {
       // A_ij = Gam_ij (k_i . k_j) b_j, j < i, transposed (the block above the diagonal is not used)
@@ -242,8 +256,9 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
           for (int z = 0; z < 8; ++z) {
             const int j = 32 * x + y + z;
-            const float e = ex2((hi - s_hi[j]) + (lo - s_lo[j]));
-            At[j * kLd + i] = j < i ? e * __uint_as_float(r[z]) * s_b[j] : 0.f;
+            const float4 gj = s_g[j];
+            const float e = ex2((hi - gj.x) + (lo - gj.y));
+            At[j * kLd + i] = j < i ? e * __uint_as_float(r[z]) * gj.z : 0.f;
           }
         }
       if (x == quad) {
@@ -289,20 +304,20 @@ __global__ void __launch_bounds__(kPrepThreads)
     } else {
       // P_ij = Gam_ij (q_i . k_j), j <= i, straight to the record
 #pragma unroll 1
-      for (int y = 0; y < 4; ++y) {
-        uint32_t r[8], ph[4], pl[4];
-        tmem_ld8(tmem + lb + 32 * x + 8 * y, r);
+      for (int y = 0; y < 2; ++y) {
+        uint32_t r[16], ph[8], pl[8];
+        tmem_ld16(tmem + lb + 32 * x + 16 * y, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const int j = 32 * x + 8 * y + 2 * z;
-          float p0 = ex2((hi - s_hi[j]) + (lo - s_lo[j])) * __uint_as_float(r[2 * z]);
-          float p1 = ex2((hi - s_hi[j + 1]) + (lo - s_lo[j + 1])) * __uint_as_float(r[2 * z + 1]);
+        for (int z = 0; z < 8; ++z) {
+          const int j = 32 * x + 16 * y + 2 * z;
+          const float4 g0 = s_g[j], g1 = s_g[j + 1];
+          const float p0 = ex2((hi - g0.x) + (lo - g0.y)) * __uint_as_float(r[2 * z]);
+          const float p1 = ex2((hi - g1.x) + (lo - g1.y)) * __uint_as_float(r[2 * z + 1]);
           split2(j <= i ? p0 : 0.f, j + 1 <= i ? p1 : 0.f, ph[z], pl[z]);
         }
-        const uint32_t at = sw(i, 4 * x + y);
-        *reinterpret_cast<uint4 *>(rec + kRecP + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-        *reinterpret_cast<uint4 *>(rec + kRecP + 8192 + at) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+        store_row8(rec + kRecP, i, 2 * x + y, ph);
+        store_row8(rec + kRecP + 8192, i, 2 * x + y, pl);
       }
     }
     __syncthreads();
@@ -334,26 +349,23 @@ __global__ void __launch_bounds__(kPrepThreads)
     {
       // T to the record; T diag(e^g), the operand of W, over A
       const int row = tid & 63, q = tid / 64;
-#pragma unroll 1
+      uint32_t th[8], tl[8];
+#pragma unroll
       for (int y = 0; y < 2; ++y) {
-        uint32_t th[4], tl[4], eh[4], el[4];
-        const float4 u = *reinterpret_cast<const float4 *>(Ti + row * kLd + 16 * q + 8 * y);
-        const float4 v = *reinterpret_cast<const float4 *>(Ti + row * kLd + 16 * q + 8 * y + 4);
-        const float *e = s_eg + 16 * q + 8 * y;
-        split2(u.x, u.y, th[0], tl[0]);
-        split2(u.z, u.w, th[1], tl[1]);
-        split2(v.x, v.y, th[2], tl[2]);
-        split2(v.z, v.w, th[3], tl[3]);
-        split2(u.x * e[0], u.y * e[1], eh[0], el[0]);
-        split2(u.z * e[2], u.w * e[3], eh[1], el[1]);
-        split2(v.x * e[4], v.y * e[5], eh[2], el[2]);
-        split2(v.z * e[6], v.w * e[7], eh[3], el[3]);
+        uint32_t eh[4], el[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const int j = 16 * q + 8 * y + 2 * z;
+          const float2 u = *reinterpret_cast<const float2 *>(Ti + row * kLd + j);
+          split2(u.x, u.y, th[4 * y + z], tl[4 * y + z]);
+          split2(u.x * s_g[j].w, u.y * s_g[j + 1].w, eh[z], el[z]);
+        }
         const uint32_t at = sw(row, 2 * q + y);
-        *reinterpret_cast<uint4 *>(rec + kRecT + at) = make_uint4(th[0], th[1], th[2], th[3]);
-        *reinterpret_cast<uint4 *>(rec + kRecT + 8192 + at) = make_uint4(tl[0], tl[1], tl[2], tl[3]);
         st_shared_v4(base + kPrepA + at, eh[0], eh[1], eh[2], eh[3]);
         st_shared_v4(base + kPrepA + 8192 + at, el[0], el[1], el[2], el[3]);
       }
+      store_row8(rec + kRecT, row, q, th);
+      store_row8(rec + kRecT + 8192, row, q, tl);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -638,23 +650,6 @@ __device__ __forceinline__ void put_split(uint32_t tile, uint32_t lo, uint32_t r
   st_shared_v4(row + (((2 * g + 1) ^ (r & 7u)) << 4), hi[4], hi[5], hi[6], hi[7]);
   st_shared_v4(blk + (((p + 2 * g) ^ (r & 7u)) << 4), l[0], l[1], l[2], l[3]);
   st_shared_v4(blk + (((p + 2 * g + 1) ^ (r & 7u)) << 4), l[4], l[5], l[6], l[7]);
-}
-
-// 8 packed words (16 columns) of row r, column group m of a swizzled block in global memory, as one 32-byte
-// store: the swizzle moves pairs of pieces and, in odd rows, swaps a pair.
-__device__ __forceinline__ uint32_t row8(uint32_t r, uint32_t m) { return r * 128u + ((m ^ ((r & 7u) >> 1)) << 5); }
-__device__ __forceinline__ void store_row8(uint8_t *block, uint32_t r, uint32_t m, const uint32_t (&w)[8]) {
-  const bool odd = r & 1u;
-  uint8_t *dst = block + row8(r, m);
-  uint32_t v[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = odd ? w[4 + e] : w[e];
-    v[4 + e] = odd ? w[e] : w[4 + e];
-  }
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 // the words that store_row8 wrote, from their place
