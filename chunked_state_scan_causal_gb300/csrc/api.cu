@@ -841,7 +841,7 @@ int32_t linattn_bwd_delta(const linattn_shape *shape, const void *q, const void 
     return cuda_status(delta_tc_bwd(p, g, q, k, dO, d_final_state, checkpoint, dq, dk, dv, d_log_gate, d_beta,
                                     d_init_state, static_cast<char *>(workspace) + kHeader,
                                     static_cast<int *>(workspace), s));
-  return cuda_status(delta_walk_bwd(p, g, q, k, dO, init_state, d_final_state, checkpoint, dq, dk, dv, d_log_gate,
+  return cuda_status(delta_walk_bwd(p, g, q, k, dO, d_final_state, checkpoint, dq, dk, dv, d_log_gate,
                                     d_beta, d_init_state, static_cast<char *>(workspace) + kHeader, s));
 }
 

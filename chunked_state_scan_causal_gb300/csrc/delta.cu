@@ -15,20 +15,23 @@
 // (Anchoring at every chunk keeps the sums short: a sum over the whole rest of the sequence would
 // gather the rounding of every later token.)
 //
-// One CTA of 512 threads walks one (batch, head); the whole d x d matrix stays in registers
-// (warp w rows w D/16 .., lane l columns l D/32 ..), so a token costs three block barriers and no
-// memory traffic besides its own rows.  Forward, then for the backward one reverse walk of R and
-// one forward walk of S: bound by the latency of those barriers, about 1 us a token, and by
-// having only B * H CTAs -- the path for fp32 checks, as the library's other fp32 walks are.
+// Four walks over the tokens, none of which waits for another warp: a warp owns four columns of S (or, once
+// y and dy are known, four rows), eight lanes each, so the sums over a column (row) are three shuffles.
+//     outputs:  forward over the columns of S     o, y, and S where every chunk begins
+//     reverse:  backward over the columns of R    dv, dy, parts of db, R and <R, S> where every chunk ends
+//     writes:   backward over the rows of R       the write part of dk, all chunks at once
+//     reads:    forward over the rows of S        dq, dk, all chunks at once
+// A CTA of four warps stages blocks of 8 tokens in shared memory while it walks the block before.  D/16
+// CTAs per (batch, head), and per chunk in the last two; bound by the latency of a token's sums.  A training
+// step of 257 tokens (B1 H2 d64) takes 167 us; with one CTA per (batch, head), the matrix in its registers
+// and three block barriers a token it took 625 us, and with the last two walks uncut 254 us.
 #include <cuda_bf16.h>
-
 #include "internal.h"
 
 namespace linattn {
 namespace {
 
-constexpr int kWalkThreads = 512;
-constexpr int kWalkWarps = kWalkThreads / 32;
+constexpr int kWalkThreads = 128, kBlockT = 8, kVecs = 16;  // tokens staged at a time; rows or columns of a CTA
 
 __device__ __forceinline__ float ld_gate(const void *p, int64_t i, int f32) {
   return f32 ? static_cast<const float *>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
@@ -44,235 +47,249 @@ __device__ __forceinline__ float ld_val(const __nv_bfloat16 *p) { return __bfloa
 __device__ __forceinline__ void st_val(float *p, float x) { *p = x; }
 __device__ __forceinline__ void st_val(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 
-// A thread's part of the matrix: D/16 rows of its warp, D/32 columns of its lane.
-template <int D>
-struct Tile {
-  static constexpr int NR = D / kWalkWarps, NC = D / 32;
-  float s[NR][NC];
-  __device__ void load(const float *m, int warp, int lane) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) s[i][c] = m ? m[(warp * NR + i) * D + lane * NC + c] : 0.f;
-  }
-  __device__ void store(float *m, int warp, int lane) const {
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) m[(warp * NR + i) * D + lane * NC + c] = s[i][c];
-  }
-  // part[warp][j] = sum over the warp's rows of s[.][j] x[row]
-  __device__ void col_sums(const float *x, float (*part)[D], int warp, int lane) const {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float a = 0.f;
-#pragma unroll
-      for (int i = 0; i < NR; ++i) a = fmaf(s[i][c], x[warp * NR + i], a);
-      part[warp][lane * NC + c] = a;
-    }
-  }
-  // out[row] = sum over all columns of s[row][.] x[.]: the warp's NR rows are halved over the
-  // lanes, then the remaining lane bits are summed
-  __device__ void row_sums(const float *x, float *out, int warp, int lane) const {
-    float a[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      a[i] = 0.f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) a[i] = fmaf(s[i][c], x[lane * NC + c], a[i]);
-    }
-    int row = 0, off = 16;
-#pragma unroll
-    for (int n = NR / 2; n >= 1; n /= 2, off /= 2) {
-      const bool up = lane & off;
-#pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const float send = up ? a[i] : a[i + n], keep = up ? a[i + n] : a[i];
-        a[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-      }
-      row += up ? n : 0;
-    }
-    for (; off >= 1; off /= 2) a[0] += __shfl_xor_sync(0xffffffffu, a[0], off);
-    if (lane % (32 / NR) == 0) out[warp * NR + row] = a[0];
-  }
-  // s = f s + x y^T
-  __device__ void update(float f, const float *x, const float *y, int warp, int lane) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) s[i][c] = fmaf(x[warp * NR + i], y[lane * NC + c], f * s[i][c]);
-  }
+enum { W_OUTPUTS = 0, W_REVERSE, W_WRITES, W_READS };
+
+// What a walk reads per token: up to three rows of D values and up to three pieces of kVecs (its own columns
+// or rows), each with its row stride; pointers already at the (batch, head).
+struct WalkRows {
+  const float *row[3], *vec[3];
+  int64_t row_st[3], vec_st[3];
+};
+struct WalkArgs {
+  const float *q, *k, *v, *dO;      // user tensors
+  float *o, *dq, *dk, *dv;          // (strides of the Problem)
+  float *y, *dy, *dkw;              // [BH][T][D]
+  float *states, *grads;            // [BH][N + 1][D][D] S, or null; [BH][N][D][D] R
+  const float *in;                  // initial state, or the final state's gradient, or null
+  float *out;                       // final state, or the initial state's gradient, or null
+  float *xpart, *dbpart, *apart;    // [BH][T][D/4], [BH][T][D/4], [BH][N][D/4]: one value per warp
 };
 
-template <int D>
-__device__ __forceinline__ float sum_parts(const float (*part)[D], int j) {
-  float a = 0.f;
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+// sum over the eight lanes of a column (row)
+__device__ __forceinline__ float sum8(float x) {
 #pragma unroll
-  for (int w = 0; w < kWalkWarps; ++w) a += part[w][j];
-  return a;
+  for (int o = 1; o < 8; o *= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// ... and over the warp's four of them
+__device__ __forceinline__ float sum4(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// Block-wide sum of one value per thread of the first D threads; valid in thread 0.
-template <int D>
-__device__ __forceinline__ float sum_rows(float x, float *buf, int tid) {
-#pragma unroll
-  for (int o = 16; o; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-  if (tid < D && tid % 32 == 0) buf[tid / 32] = x;
-  __syncthreads();
-  float r = 0.f;
-  if (tid == 0)
-    for (int i = 0; i < D / 32; ++i) r += buf[i];
-  return r;
-}
-
-// y [BH][T][D] fp32 and states [BH][N + 1][D][D] (the state entering every chunk of 64 tokens,
-// then the final one) are kept for the backward when not null.
-template <int D, typename T>
-__global__ void __launch_bounds__(kWalkThreads) delta_fwd_walk(Problem p, DeltaGates g, const T *q, const T *k,
-                                                               const T *v, T *o, const float *init, float *fin,
-                                                               float *ykeep, float *states) {
-  __shared__ float kk[D], qq[D], uu[D], part[kWalkWarps][D];
-  const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t base = (int64_t)b * p.sb + (int64_t)h * p.sh, gb = (int64_t)bh * p.T;
-  const int N = (p.T + 63) / 64;
-  Tile<D> S;
-  S.load(init ? init + (int64_t)bh * D * D : nullptr, warp, lane);
-  for (int t = 0; t < p.T; ++t) {
-    if (states && t % 64 == 0) S.store(states + ((int64_t)bh * (N + 1) + t / 64) * D * D, warp, lane);
-    const int64_t row = base + (int64_t)t * p.st;
-    const float a = g.lg ? expf(ld_gate(g.lg, gb + t, g.f32)) : 1.f, be = ld_gate(g.beta, gb + t, g.f32);
-    float vj = 0.f;
-    if (tid < D) {
-      kk[tid] = ld_val(k + row + tid);
-      qq[tid] = ld_val(q + row + tid);
-      vj = ld_val(v + row + tid);
-    }
-    __syncthreads();
-    S.col_sums(kk, part, warp, lane);
-    __syncthreads();
-    if (tid < D) {
-      const float y = fmaf(-a, sum_parts<D>(part, tid), vj);
-      uu[tid] = be * y;
-      if (ykeep) ykeep[(gb + t) * D + tid] = y;
-    }
-    __syncthreads();
-    S.update(a, kk, uu, warp, lane);
-    S.col_sums(qq, part, warp, lane);
-    __syncthreads();
-    if (tid < D) st_val(o + row + tid, sum_parts<D>(part, tid));
-    // the next token rewrites kk, qq (read before the barrier above) and, after two more
-    // barriers, part and uu
+template <int D, int MODE>
+__global__ void __launch_bounds__(kWalkThreads) delta_walk(Problem p, DeltaGates g, WalkArgs w) {
+  constexpr bool kForward = MODE == W_OUTPUTS || MODE == W_READS, kColumns = MODE == W_OUTPUTS || MODE == W_REVERSE;
+  constexpr int NV = MODE == W_OUTPUTS ? 1 : MODE == W_READS ? 3 : 2, NRW = kColumns ? 2 : 3, NE = D / 32;  // float4s
+  __shared__ float4 rows[2][NRW][kBlockT][D / 4];
+  __shared__ float4 vecs[2][NV][kBlockT][kVecs / 4];
+  __shared__ float gates[2][2][kBlockT];
+  constexpr int slices = D / kVecs;
+  const int N = (p.T + 63) / 64, seq = blockIdx.x / slices, bh = kColumns ? seq : seq / N, chunk = kColumns ? 0 : seq % N;
+  const int b = bh / p.H, h = bh % p.H, x0 = (blockIdx.x % slices) * kVecs;
+  const int begin = chunk * 64, end = kColumns ? p.T : min(p.T, begin + 64);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, x = x0 + 4 * warp + (lane >> 3), e0 = (lane & 7) * 4;
+  const int64_t user = (int64_t)b * p.sb + (int64_t)h * p.sh, own = (int64_t)bh * p.T * D, gb = (int64_t)bh * p.T;
+  const int part = x0 / 4 + warp;
+  WalkRows in;
+  auto row = [&](int i, const float *t, bool is_user) {
+    in.row[i] = t + (is_user ? user : own);
+    in.row_st[i] = is_user ? p.st : D;
+  };
+  auto vec = [&](int i, const float *t, bool is_user) {
+    in.vec[i] = t + (is_user ? user : own) + x0;
+    in.vec_st[i] = is_user ? p.st : D;
+  };
+  if (kColumns) {
+    row(0, w.k, true);
+    row(1, w.q, true);
+    vec(0, MODE == W_OUTPUTS ? w.v : w.dO, true);
+    if (MODE == W_REVERSE) vec(1, w.y, false);
+  } else {
+    row(0, w.dO, true);
+    row(1, w.dy, false);
+    row(2, w.y, false);
+    vec(0, w.q, true);
+    vec(1, w.k, true);
+    if (MODE == W_READS) vec(2, w.dkw, false);
   }
-  if (fin) S.store(fin + (int64_t)bh * D * D, warp, lane);
-  if (states) S.store(states + ((int64_t)bh * (N + 1) + N) * D * D, warp, lane);
-}
-
-// The reverse walk of R: dv, db, the write part of dk (fp32, dkw), dy (fp32) and the anchors
-// <R, S> at the chunks' ends.
-template <int D, typename T>
-__global__ void __launch_bounds__(kWalkThreads)
-    delta_rev_walk(Problem p, DeltaGates g, const T *q, const T *k, const T *dO, const float *ykeep,
-                   const float *states, const float *d_final, T *dv, void *dbeta, float *dkw, float *dyk,
-                   float *anchor, float *dinit) {
-  __shared__ float kk[D], qq[D], oo[D], uu[D], part[kWalkWarps][D], rowv[D], buf[kWalkWarps];
-  const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t base = (int64_t)b * p.sb + (int64_t)h * p.sh, gb = (int64_t)bh * p.T;
-  const int N = (p.T + 63) / 64;
-  Tile<D> R;
-  R.load(d_final ? d_final + (int64_t)bh * D * D : nullptr, warp, lane);
-  for (int t = p.T - 1; t >= 0; --t) {
-    if (t == p.T - 1 || t % 64 == 63) {
-      const float *S = states + ((int64_t)bh * (N + 1) + t / 64 + 1) * D * D;
-      float x = 0.f;
+  // block i of the walk: tokens t0 .. (in time order inside)
+  const int blocks = (end - begin + kBlockT - 1) / kBlockT;
+  auto first = [&](int i) { return begin + (kForward ? i : blocks - 1 - i) * kBlockT; };
+  auto stage = [&](int i) {
+    const int t0 = first(i), n = min(kBlockT, end - t0), s = i & 1;
 #pragma unroll
-      for (int i = 0; i < Tile<D>::NR; ++i)
+    for (int a = 0; a < NRW; ++a)
 #pragma unroll
-        for (int c = 0; c < Tile<D>::NC; ++c)
-          x = fmaf(R.s[i][c], S[(warp * Tile<D>::NR + i) * D + lane * Tile<D>::NC + c], x);
-#pragma unroll
-      for (int o = 16; o; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (lane == 0) buf[warp] = x;
-      __syncthreads();
-      if (tid == 0) {
-        float r = 0.f;
-        for (int i = 0; i < kWalkWarps; ++i) r += buf[i];
-        anchor[(int64_t)bh * N + t / 64] = r;
+      for (int e = tid; e < kBlockT * (D / 4); e += kWalkThreads) {
+        const int c = e % (D / 4), t = e / (D / 4);
+        if (t < n) cp_async16(&rows[s][a][t][c], in.row[a] + (t0 + t) * in.row_st[a] + 4 * c);
       }
-      __syncthreads();
-    }
-    const int64_t row = base + (int64_t)t * p.st;
-    const float a = g.lg ? expf(ld_gate(g.lg, gb + t, g.f32)) : 1.f, be = ld_gate(g.beta, gb + t, g.f32);
-    float y = 0.f;
-    if (tid < D) {
-      kk[tid] = ld_val(k + row + tid);
-      qq[tid] = ld_val(q + row + tid);
-      oo[tid] = ld_val(dO + row + tid);
-      y = ykeep[(gb + t) * D + tid];
-      uu[tid] = be * y;
-    }
-    __syncthreads();
-    R.update(1.f, qq, oo, warp, lane);
-    R.col_sums(kk, part, warp, lane);
-    R.row_sums(uu, rowv, warp, lane);
-    __syncthreads();
-    float db = 0.f;
-    if (tid < D) {
-      const float du = sum_parts<D>(part, tid), dy = be * du;
-      db = du * y;
-      oo[tid] = -dy;
-      st_val(dv + row + tid, dy);
-      dyk[(gb + t) * D + tid] = dy;
-      dkw[(gb + t) * D + tid] = rowv[tid];
-    }
-    db = sum_rows<D>(db, buf, tid);  // (a barrier inside: oo is complete after it)
-    if (tid == 0) st_gate(dbeta, gb + t, g.f32, db);
-    R.update(1.f, kk, oo, warp, lane);
+    static_assert(kBlockT * (kVecs / 4) == 32, "one warp stages one array's pieces");
 #pragma unroll
-    for (int i = 0; i < Tile<D>::NR; ++i)
+    for (int a = 0; a < NV; ++a)
+      if (warp == a && lane / 4 < n)
+        cp_async16(&vecs[s][a][lane / 4][lane % 4], in.vec[a] + (t0 + lane / 4) * in.vec_st[a] + 4 * (lane % 4));
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (tid < n) {
+      gates[s][0][tid] = g.lg ? expf(ld_gate(g.lg, gb + t0 + tid, g.f32)) : 1.f;
+      gates[s][1][tid] = ld_gate(g.beta, gb + t0 + tid, g.f32);
+    }
+  };
+  // element 4 m + c of this lane's part of its column (row) is entry e0 + 32 m + c
+  auto at = [&](const float *m, int i, int c) {
+    const int e = e0 + 32 * i + c;
+    return m + (kColumns ? (int64_t)e * D + x : (int64_t)x * D + e);
+  };
+  float4 s[NE];
 #pragma unroll
-      for (int c = 0; c < Tile<D>::NC; ++c) R.s[i][c] *= a;
-    __syncthreads();
+  for (int i = 0; i < NE; ++i) {
+    const float *m = MODE == W_READS    ? w.states + ((int64_t)bh * (N + 1) + chunk) * D * D
+                     : MODE == W_WRITES ? w.grads + ((int64_t)bh * N + chunk) * D * D
+                     : w.in             ? w.in + (int64_t)bh * D * D
+                                        : nullptr;
+    s[i] = m ? make_float4(*at(m, i, 0), *at(m, i, 1), *at(m, i, 2), *at(m, i, 3)) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  if (dinit) R.store(dinit + (int64_t)bh * D * D, warp, lane);
+  auto store = [&](float *m) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      *const_cast<float *>(at(m, i, 0)) = s[i].x;
+      *const_cast<float *>(at(m, i, 1)) = s[i].y;
+      *const_cast<float *>(at(m, i, 2)) = s[i].z;
+      *const_cast<float *>(at(m, i, 3)) = s[i].w;
+    }
+  };
+  auto dot = [](float4 a, float4 b, float c) { return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c)))); };
+  auto axpy = [](float f, float4 a, float4 b) {  // f a + b
+    return make_float4(fmaf(f, a.x, b.x), fmaf(f, a.y, b.y), fmaf(f, a.z, b.z), fmaf(f, a.w, b.w));
+  };
+  auto scale = [](float f, float4 a) { return make_float4(f * a.x, f * a.y, f * a.z, f * a.w); };
+  stage(0);
+#pragma unroll 1
+  for (int i = 0; i < blocks; ++i) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();  // block i is in place, and block i - 1's place is free
+    if (i + 1 < blocks) stage(i + 1);
+    const int t0 = first(i), n = min(kBlockT, end - t0), z = i & 1;
+#pragma unroll 1
+    for (int u = 0; u < n; ++u) {
+      const int tt = kForward ? u : n - 1 - u, t = t0 + tt;
+      const float a = gates[z][0][tt], be = gates[z][1][tt];
+      float4 r[NRW][NE];
+#pragma unroll
+      for (int m = 0; m < NRW; ++m)
+#pragma unroll
+        for (int e = 0; e < NE; ++e) r[m][e] = rows[z][m][tt][(lane & 7) + 8 * e];
+      float c[NV];
+#pragma unroll
+      for (int m = 0; m < NV; ++m) c[m] = reinterpret_cast<const float *>(vecs[z][m][tt])[x - x0];
+      const bool lead = (lane & 7) == 0;
+      const int64_t mine = own + (int64_t)t * D + x, theirs = user + (int64_t)t * p.st + x;
+      if (MODE == W_OUTPUTS) {
+        // rows k, q; c: v_j
+        if (w.states && t % 64 == 0) store(w.states + ((int64_t)bh * (N + 1) + t / 64) * D * D);
+        float sk = 0.f, sq = 0.f, kq = 0.f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+          sk = dot(s[e], r[0][e], sk);
+          sq = dot(s[e], r[1][e], sq);
+          kq = dot(r[0][e], r[1][e], kq);
+        }
+        sk = sum8(sk);
+        sq = sum8(sq);
+        kq = sum8(kq);
+        const float y = fmaf(-a, sk, c[0]), uj = be * y;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) s[e] = axpy(uj, r[0][e], scale(a, s[e]));
+        if (lead) {
+          w.o[theirs] = fmaf(kq, uj, a * sq);
+          if (w.y) w.y[mine] = y;
+        }
+      } else if (MODE == W_REVERSE) {
+        // rows k, q; c: dO_j, y_j
+        if (t == p.T - 1 || t % 64 == 63) {
+          const float *S = w.states + ((int64_t)bh * (N + 1) + t / 64 + 1) * D * D;
+          store(w.grads + ((int64_t)bh * N + t / 64) * D * D);
+          float d = 0.f;
+#pragma unroll
+          for (int e = 0; e < NE; ++e)
+            d = dot(s[e], make_float4(*at(S, e, 0), *at(S, e, 1), *at(S, e, 2), *at(S, e, 3)), d);
+          d = sum4(sum8(d));
+          if (lane == 0) w.apart[((int64_t)bh * N + t / 64) * (D / 4) + part] = d;
+        }
+        float du = 0.f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+          s[e] = axpy(c[0], r[1][e], s[e]);
+          du = dot(s[e], r[0][e], du);
+        }
+        du = sum8(du);
+        const float dy = be * du, db = sum4(du * c[1]);
+#pragma unroll
+        for (int e = 0; e < NE; ++e) s[e] = scale(a, axpy(-dy, r[0][e], s[e]));
+        if (lead) {
+          w.dv[theirs] = dy;
+          w.dy[mine] = dy;
+        }
+        if (lane == 0) w.dbpart[(gb + t) * (D / 4) + part] = db;
+      } else {
+        // rows dO, dy, y; c: q_i, k_i (and dkw_i)
+        float d0 = 0.f, d1 = 0.f;
+        if (MODE == W_WRITES) {
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            s[e] = axpy(c[0], r[0][e], s[e]);
+            d0 = dot(s[e], r[2][e], d0);
+            s[e] = scale(a, axpy(-c[1], r[1][e], s[e]));
+          }
+          d0 = be * sum8(d0);
+          d1 = sum4(-c[1] * d0);
+          if (lead) w.dkw[mine] = d0;
+        } else {
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            s[e] = scale(a, s[e]);
+            d0 = dot(s[e], r[1][e], d0);
+            s[e] = axpy(be * c[1], r[2][e], s[e]);
+            d1 = dot(s[e], r[0][e], d1);
+          }
+          d0 = -sum8(d0);
+          d1 = sum8(d1);
+          if (lead) {
+            w.dq[theirs] = d1;
+            w.dk[theirs] = d0 + c[NV - 1];
+          }
+          d1 = sum4(fmaf(c[0], d1, c[1] * d0));
+        }
+        if (lane == 0) w.xpart[(gb + t) * (D / 4) + part] = d1;
+      }
+    }
+  }
+  if (kColumns && w.out) store(w.out + (int64_t)bh * D * D);
+  if (MODE == W_OUTPUTS && w.states) store(w.states + ((int64_t)bh * (N + 1) + N) * D * D);
 }
 
-// The forward walk of S in the backward: dq, dk and G of every token (gx [BH][T] fp32).
-template <int D, typename T>
-__global__ void __launch_bounds__(kWalkThreads)
-    delta_grad_walk(Problem p, DeltaGates g, const T *q, const T *k, const T *dO, const float *ykeep,
-                    const float *dyk, const float *dkw, const float *init, T *dq, T *dk, float *gx) {
-  __shared__ float kk[D], oo[D], uu[D], yy[D], r1[D], r2[D], buf[kWalkWarps];
-  const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int64_t base = (int64_t)b * p.sb + (int64_t)h * p.sh, gb = (int64_t)bh * p.T;
-  Tile<D> S;
-  S.load(init ? init + (int64_t)bh * D * D : nullptr, warp, lane);
-  for (int t = 0; t < p.T; ++t) {
-    const int64_t row = base + (int64_t)t * p.st;
-    const float a = g.lg ? expf(ld_gate(g.lg, gb + t, g.f32)) : 1.f, be = ld_gate(g.beta, gb + t, g.f32);
-    float qv = 0.f, kv = 0.f, w = 0.f;
-    if (tid < D) {
-      kk[tid] = kv = ld_val(k + row + tid);
-      qv = ld_val(q + row + tid);
-      oo[tid] = ld_val(dO + row + tid);
-      uu[tid] = be * ykeep[(gb + t) * D + tid];
-      yy[tid] = dyk[(gb + t) * D + tid];
-      w = dkw[(gb + t) * D + tid];
+// The warps' parts added up, in order: G (its two walks' parts), db and the anchors.  One thread each.
+__global__ void __launch_bounds__(256) delta_walk_sums(int64_t tokens, int64_t chunks, int parts, const float *x0,
+                                                       const float *x1, const float *dbpart, const float *apart,
+                                                       float *gx, void *dbeta, int f32, float *anchor) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i < tokens) {
+    float x = 0.f, d = 0.f;
+    for (int j = 0; j < parts; ++j) {
+      x += x0[i * parts + j] + x1[i * parts + j];
+      d += dbpart[i * parts + j];
     }
-    __syncthreads();
-    S.row_sums(yy, r1, warp, lane);
-    S.update(a, kk, uu, warp, lane);
-    S.row_sums(oo, r2, warp, lane);
-    __syncthreads();
-    float x = 0.f;
-    if (tid < D) {
-      const float read = -a * r1[tid];
-      st_val(dq + row + tid, r2[tid]);
-      st_val(dk + row + tid, read + w);
-      x = fmaf(qv, r2[tid], kv * (read - w));
-    }
-    x = sum_rows<D>(x, buf, tid);
-    if (tid == 0) gx[gb + t] = x;
-    __syncthreads();
+    gx[i] = x;
+    st_gate(dbeta, i, f32, d);
+  } else if (i - tokens < chunks) {
+    float d = 0.f;
+    for (int j = 0; j < parts; ++j) d += apart[(i - tokens) * parts + j];
+    anchor[i - tokens] = d;
   }
 }
 
@@ -387,41 +404,65 @@ cudaError_t decode_launch(const Problem &p, const DeltaGates &g, const void *q, 
   return cudaGetLastError();
 }
 
-template <int D, typename T>
-cudaError_t fwd_launch(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
-                       const float *init, float *fin, void *ckpt, cudaStream_t s) {
+template <int D, int MODE>
+cudaError_t walk(const Problem &p, const DeltaGates &g, const WalkArgs &w, cudaStream_t s) {
   TimedLaunch t(K_DELTA_WALK, s);
-  float *y = static_cast<float *>(ckpt);
-  float *states = ckpt ? y + (int64_t)p.B * p.H * p.T * D : nullptr;
-  delta_fwd_walk<D, T><<<p.B * p.H, kWalkThreads, 0, s>>>(p, g, (const T *)q, (const T *)k, (const T *)v, (T *)o,
-                                                          init, fin, y, states);
+  const int64_t walks = (int64_t)p.B * p.H * (MODE == W_WRITES || MODE == W_READS ? (p.T + 63) / 64 : 1);
+  delta_walk<D, MODE><<<(unsigned)(walks * (D / kVecs)), kWalkThreads, 0, s>>>(p, g, w);
   return cudaGetLastError();
 }
 
-template <int D, typename T>
-cudaError_t bwd_launch(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
-                       const float *init, const float *d_final, const void *ckpt, void *dq, void *dk, void *dv,
-                       void *dlg, void *dbeta, float *dinit, void *ws, cudaStream_t s) {
-  const int64_t BH = (int64_t)p.B * p.H, n = BH * p.T * D;
-  const int N = (p.T + 63) / 64;
-  const float *y = static_cast<const float *>(ckpt), *states = y + n;
-  float *dyk = static_cast<float *>(ws), *dkw = dyk + n, *gx = dkw + n, *anchor = gx + BH * p.T;
+template <int D>
+cudaError_t walk_fwd(const Problem &p, const DeltaGates &g, const float *q, const float *k, const float *v, float *o,
+                     const float *init, float *fin, void *ckpt, cudaStream_t s) {
+  WalkArgs w{};
+  w.q = q;
+  w.k = k;
+  w.v = v;
+  w.o = o;
+  w.in = init;
+  w.out = fin;
+  w.y = static_cast<float *>(ckpt);
+  w.states = ckpt ? w.y + (int64_t)p.B * p.H * p.T * D : nullptr;
+  return walk<D, W_OUTPUTS>(p, g, w, s);
+}
+
+template <int D>
+cudaError_t walk_bwd(const Problem &p, const DeltaGates &g, const float *q, const float *k, const float *dO,
+                     const float *d_final, const void *ckpt, float *dq, float *dk, float *dv, void *dlg, void *dbeta,
+                     float *dinit, void *ws, cudaStream_t s) {
+  const int64_t tokens = (int64_t)p.B * p.H * p.T, chunks = (int64_t)p.B * p.H * ((p.T + 63) / 64), n = tokens * D;
+  WalkArgs w{};
+  w.q = q;
+  w.k = k;
+  w.dO = dO;
+  w.dq = dq;
+  w.dk = dk;
+  w.dv = dv;
+  w.y = static_cast<float *>(const_cast<void *>(ckpt));
+  w.states = w.y + n;
+  w.grads = static_cast<float *>(ws);
+  w.dy = w.grads + chunks * D * D;
+  w.dkw = w.dy + n;
+  float *x0 = w.dkw + n, *x1 = x0 + n / 4;
+  w.dbpart = x1 + n / 4;
+  w.apart = w.dbpart + n / 4;
+  float *gx = w.apart + chunks * (D / 4), *anchor = gx + tokens;
+  w.in = d_final;
+  w.out = dinit;
+  cudaError_t e = walk<D, W_REVERSE>(p, g, w, s);
+  w.xpart = x0;
+  if (e == cudaSuccess) e = walk<D, W_WRITES>(p, g, w, s);
+  w.xpart = x1;
+  if (e == cudaSuccess) e = walk<D, W_READS>(p, g, w, s);
+  if (e != cudaSuccess) return e;
   {
     TimedLaunch t(K_DELTA_WALK, s);
-    delta_rev_walk<D, T><<<(int)BH, kWalkThreads, 0, s>>>(p, g, (const T *)q, (const T *)k, (const T *)dO, y, states,
-                                                          d_final, (T *)dv, dbeta, dkw, dyk, anchor, dinit);
+    delta_walk_sums<<<(unsigned)((tokens + chunks + 255) / 256), 256, 0, s>>>(
+        tokens, chunks, D / 4, x0, x1, w.dbpart, w.apart, gx, dbeta, g.f32, anchor);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  {
-    TimedLaunch t(K_DELTA_WALK, s);
-    delta_grad_walk<D, T><<<(int)BH, kWalkThreads, 0, s>>>(p, g, (const T *)q, (const T *)k, (const T *)dO, y, dyk,
-                                                           dkw, init, (T *)dq, (T *)dk, gx);
-  }
-  if (dlg) {
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return delta_gate_sums(p, gx, anchor, dlg, g.f32, s);
-  }
-  return cudaGetLastError();
+  return dlg ? delta_gate_sums(p, gx, anchor, dlg, g.f32, s) : cudaSuccess;
 }
 
 }  // namespace
@@ -441,20 +482,22 @@ size_t delta_walk_ckpt_bytes(const Problem &p) {
 }
 size_t delta_walk_bwd_ws_bytes(const Problem &p) {
   const size_t BH = (size_t)p.B * p.H, N = (p.T + 63) / 64;
-  return p.T == 0 ? 0 : align256(4 * (BH * p.T * (2 * p.d + 1) + BH * N));
+  return p.T == 0 ? 0 : align256(4 * (BH * p.T * (2 * p.d + 3 * p.d / 4 + 1) + BH * N * (p.d * p.d + p.d / 4 + 1)));
 }
 
 cudaError_t delta_walk_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v,
                            void *o, const float *init, float *fin, void *ckpt, cudaStream_t s) {
-  return p.d == 64 ? fwd_launch<64, float>(p, g, q, k, v, o, init, fin, ckpt, s)
-                   : fwd_launch<128, float>(p, g, q, k, v, o, init, fin, ckpt, s);
+  auto run = p.d == 64 ? walk_fwd<64> : walk_fwd<128>;
+  return run(p, g, static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v),
+             static_cast<float *>(o), init, fin, ckpt, s);
 }
 cudaError_t delta_walk_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
-                           const float *init, const float *d_final, const void *ckpt, void *dq, void *dk, void *dv,
-                           void *dlg, void *dbeta, float *dinit, void *ws, cudaStream_t s) {
-  return p.d == 64
-             ? bwd_launch<64, float>(p, g, q, k, dO, init, d_final, ckpt, dq, dk, dv, dlg, dbeta, dinit, ws, s)
-             : bwd_launch<128, float>(p, g, q, k, dO, init, d_final, ckpt, dq, dk, dv, dlg, dbeta, dinit, ws, s);
+                           const float *d_final, const void *ckpt, void *dq, void *dk, void *dv, void *dlg,
+                           void *dbeta, float *dinit, void *ws, cudaStream_t s) {
+  auto run = p.d == 64 ? walk_bwd<64> : walk_bwd<128>;
+  return run(p, g, static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(dO),
+             d_final, ckpt, static_cast<float *>(dq), static_cast<float *>(dk), static_cast<float *>(dv), dlg, dbeta,
+             dinit, ws, s);
 }
 cudaError_t delta_decode(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v, void *o,
                          float *state, cudaStream_t s) {

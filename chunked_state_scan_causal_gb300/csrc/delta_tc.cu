@@ -62,10 +62,6 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
 }
 // offset of 16-byte piece c (0..7) of row r in a swizzled 64-column block
 __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
-// offset of element (row r, column x) of a [64 x 128] tile with blocks `half` apart
-__device__ __forceinline__ uint32_t sw_el(uint32_t r, uint32_t x, uint32_t half) {
-  return (x >> 6) * half + sw(r, (x & 63u) >> 3) + (x & 7u) * 2u;
-}
 // Fragments of 16 rows x 16 columns (tmem_ld_frag): the place of lane l's address row for the four 8 x 8
 // matrices, in a tile whose rows are the fragment's rows (columns 16 g .. of a 64-column block) ...
 __device__ __forceinline__ uint32_t frag_at(uint32_t lane, uint32_t row0, uint32_t g) {

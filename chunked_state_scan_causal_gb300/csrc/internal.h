@@ -261,15 +261,15 @@ struct DeltaGates {
   const void *lg, *beta;
   int f32;
 };
-// The CUDA-core walks (fp32): one CTA per (batch, head).  ckpt (or null) keeps y and the chunk
+// The CUDA-core walks (fp32): one warp per four columns or rows of the state.  ckpt (or null) keeps y and the chunk
 // states for the backward.
 size_t delta_walk_ckpt_bytes(const Problem &p);
 size_t delta_walk_bwd_ws_bytes(const Problem &p);
 cudaError_t delta_walk_fwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *v,
                            void *o, const float *init, float *fin, void *ckpt, cudaStream_t s);
 cudaError_t delta_walk_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
-                           const float *init, const float *d_final, const void *ckpt, void *dq, void *dk, void *dv,
-                           void *dlg, void *dbeta, float *dinit, void *ws, cudaStream_t s);
+                           const float *d_final, const void *ckpt, void *dq, void *dk, void *dv, void *dlg,
+                           void *dbeta, float *dinit, void *ws, cudaStream_t s);
 // d_log_gate from the tokens' cumulative log-gate gradients gx [BH][T] and the anchors [BH][ceil(T/64)].
 cudaError_t delta_gate_sums(const Problem &p, const float *gx, const float *anchor, void *dlg, int f32,
                             cudaStream_t s);
