@@ -554,132 +554,214 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ------------------------------------------------------------------ fp32 decode (CUDA cores)
-constexpr int kSub = 64;       // tokens staged at a time
-constexpr int kPagedThreads = 128;
+// A token's row is spread over LPT lanes, so a warp takes 32 / LPT tokens a step; every lane keeps its
+// dimensions of HN query heads and of their outputs in registers (64 + 64 values at D = 128, whatever HN:
+// more heads, more lanes per token) and copies its own pieces of K and V through a ring of its own, 16 KiB
+// per warp, so nothing in the loop waits for another lane but the sums of a score.  Those are added up while
+// the heads are halved (HN - 1 exchanges instead of HN per step), which leaves every lane one head, its
+// maximum, its sum and its weight; the weights then go round.  The warps' (and lanes') maxima, sums and
+// outputs are joined at a piece's end.  Up to 4 query heads per key head it is bound by the cache (72 us at 16
+// sequences of 8192, 4 key heads of 4 query heads, D = 128: 0.71 of copy bandwidth), with 16 by its sums (215 us).
+// Four warps on two CTAs an SM leave them 255 registers: six warps, at 168, take 83 us.
+constexpr int kSimtWarps = 4, kSimtThreads = 32 * kSimtWarps, kSimtPerSm = 2;
+template <int D, int HN>
+struct SimtLayout {
+  static constexpr int LPT = 2 * HN < D / 4 ? 2 * HN : D / 4, TPW = 32 / LPT, NP = D / 4 / LPT, depth = 16 / NP;
+  static constexpr size_t smem = (size_t)kSimtWarps * depth * 2 * NP * 32 * sizeof(float4);
+  static_assert(smem >= (size_t)kSimtWarps * HN * D * sizeof(float), "the ring holds the warps' outputs at the end");
+};
 
-template <int D>
-constexpr size_t paged_simt_smem() {
-  return (size_t)(2 * kSub * (D + 4) + kHeads * kSub + kHeads * D + 3 * kHeads) * 4;
+// 16 bytes, or zeros when !there (src is not read then)
+__device__ __forceinline__ void cp_async16_zfill(void *dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPagedThreads)
+// The sums over lanes of 2 N heads: lanes with bit X take over the upper N of them, and so on.
+template <int N, int X>
+__device__ __forceinline__ void halve_heads(float *s, int lane) {
+  if constexpr (N > 0) {
+    const bool up = lane & X;
+#pragma unroll
+    for (int h = 0; h < N; ++h)
+      s[h] = (up ? s[h + N] : s[h]) + __shfl_xor_sync(0xffffffffu, up ? s[h] : s[h + N], X);
+    halve_heads<N / 2, X / 2>(s, lane);
+  }
+}
+
+template <int D, int HN>
+__global__ void __launch_bounds__(kSimtThreads, kSimtPerSm)
     paged_decode_simt(PagedProblem p, const float *q, const float *kc, const float *vc, float *o, float *lse, float *part,
                       float *ml) {
-  constexpr int LD = D + 4;
-  constexpr int HT = kHeads * D / kPagedThreads;  // heads per thread in the value product
+  using L = SimtLayout<D, HN>;
+  constexpr int LPT = L::LPT, NP = L::NP, S = L::depth, kStep = kSimtWarps * L::TPW;
   extern __shared__ float4 smem4[];
   __shared__ int64_t buf[34];
-  float *sk = reinterpret_cast<float *>(smem4), *sv = sk + kSub * LD, *sp = sv + kSub * LD, *sq = sp + kHeads * kSub;
-  float *sm = sq + kHeads * D, *sl = sm + kHeads, *sc = sl + kHeads;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = blockIdx.x;
+  __shared__ float sm[kSimtWarps][HN], sl[kSimtWarps][HN];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, sub = lane / LPT, g = blockIdx.x;
   griddep_wait();
   griddep_launch_dependents();
   PagedWalk w;
-  if (!walk_start<kPagedThreads>(p, buf, w)) return;
+  if (!walk_start<kSimtThreads>(p, buf, w)) return;
   const float c = p.scale * 1.4426950408889634f;
-  const int dim = tid % D, hbase = (tid / D) * HT;
+  const int mine = lane % LPT / (LPT / HN), home = lane & ~(LPT - 1);
+  float4 *ring = smem4 + warp * (S * 2 * NP * 32) + lane;  // [slot][k, v][piece], a lane's own column
   int slot = 0;
   while (w.next(p)) {
     const PagedItem it = w.it;
-    const int b = w.b, t0 = w.t0, t1 = w.t1, len = w.len;
-    for (int e = tid; e < kHeads * D; e += kPagedThreads) {
-      const int h = e / D;
-      sq[e] = h < it.nh ? q[b * p.qsb + (it.h0 + h) * p.qsh + e % D] * c : 0.f;
+    const int b = w.b, end = min(w.t1 * kTile, w.len), first = w.t0 * kTile + warp * L::TPW + sub;
+    const int steps = (end - w.t0 * kTile + kStep - 1) / kStep;
+    const int *table = p.table + (int64_t)b * p.tstride;
+    float4 qr[HN][NP], acc[HN][NP];
+    float m = -INFINITY, l = 0.f;  // of head `mine`
+#pragma unroll
+    for (int h = 0; h < HN; ++h) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        acc[h][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        qr[h][j] = acc[h][j];
+        if (h < it.nh) {
+          const float4 x = *reinterpret_cast<const float4 *>(q + b * p.qsb + (it.h0 + h) * p.qsh +
+                                                             4 * (j * LPT + lane % LPT));
+          qr[h][j] = make_float4(x.x * c, x.y * c, x.z * c, x.w * c);
+        }
+      }
     }
-    if (tid < kHeads) {
-      sm[tid] = -INFINITY;
-      sl[tid] = 0.f;
+    // acc[h] times the factor that head h's lane holds
+    auto rescale = [&](float f) {
+#pragma unroll
+      for (int h = 0; h < HN; ++h) {
+        const float fh = __shfl_sync(0xffffffffu, f, home + h * (LPT / HN));
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+          acc[h][j] = make_float4(acc[h][j].x * fh, acc[h][j].y * fh, acc[h][j].z * fh, acc[h][j].w * fh);
+      }
+    };
+    // step i: this lane's token is first + i kStep; its page's id is read a step before the copies that use it
+    uint32_t ok = 0;  // bit per slot: the token is there
+    auto page_of = [&](int i) {
+      const int n = first + i * kStep;
+      return i < steps && n < end ? table[n / p.page] : 0;
+    };
+    auto copy = [&](int i, int id) {
+      const int n = first + i * kStep, z = i % S;
+      if (i < steps) {
+        bool there = n < end;
+        if (there && (id < 0 || id >= p.pages)) {
+          if (lane % LPT == 0) report_error(p.status, -1);
+          there = false;
+        }
+        const int64_t at = there ? id * p.csb + it.hk * p.csh + (int64_t)(n % p.page) * p.cst + 4 * (lane % LPT) : 0;
+        ok = there ? ok | (1u << z) : ok & ~(1u << z);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          cp_async16_zfill(ring + ((z * 2) * NP + j) * 32, kc + at + 4 * LPT * j, there);
+          cp_async16_zfill(ring + ((z * 2 + 1) * NP + j) * 32, vc + at + 4 * LPT * j, there);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int id = page_of(0);
+    for (int i = 0; i < S - 1; ++i) {
+      const int now = id;
+      id = page_of(i + 1);
+      copy(i, now);
     }
-    float acc[HT];
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+      const int now = id;
+      id = page_of(i + S);
+      copy(i + S - 1, now);
+      asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+      const float4 *kv = ring + (i % S) * 2 * NP * 32;
+      float s[HN];
 #pragma unroll
-    for (int h = 0; h < HT; ++h) acc[h] = 0.f;
-    for (int n0 = t0 * kTile; n0 < min(t1 * kTile, len); n0 += kSub) {
-      __syncthreads();
-      for (int r = warp; r < kSub; r += kPagedThreads / 32) {
-        const int n = n0 + r;
-        int id = -1;
-        if (n < len) {
-          id = p.table[(int64_t)b * p.tstride + n / p.page];
-          if (id < 0 || id >= p.pages) {
-            if (lane == 0) report_error(p.status, -1);
-            id = -1;
-          }
-        }
-        const int64_t off = id * p.csb + it.hk * p.csh + (n % p.page) * p.cst;
-        for (int e = lane; e < D; e += 32) {
-          sk[r * LD + e] = id >= 0 ? kc[off + e] : 0.f;
-          sv[r * LD + e] = id >= 0 ? vc[off + e] : 0.f;
-        }
-        if (lane < kHeads) sp[lane * kSub + r] = id >= 0 ? 0.f : -INFINITY;
+      for (int h = 0; h < HN; ++h) s[h] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float4 x = kv[j * 32];
+#pragma unroll
+        for (int h = 0; h < HN; ++h)
+          s[h] = fmaf(x.x, qr[h][j].x, fmaf(x.y, qr[h][j].y, fmaf(x.z, qr[h][j].z, fmaf(x.w, qr[h][j].w, s[h]))));
       }
-      __syncthreads();
-      {
-        const int n = tid % kSub;
-        const float4 *kr = reinterpret_cast<const float4 *>(sk + n * LD);
-        for (int h = tid / kSub; h < it.nh; h += kPagedThreads / kSub) {
-          const float4 *qr = reinterpret_cast<const float4 *>(sq + h * D);
-          float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll 8
-          for (int e = 0; e < D / 4; ++e) {
-            const float4 u = kr[e], w = qr[e];
-            a0 = fmaf(u.x, w.x, a0);
-            a1 = fmaf(u.y, w.y, a1);
-            a2 = fmaf(u.z, w.z, a2);
-            a3 = fmaf(u.w, w.w, a3);
-          }
-          if (sp[h * kSub + n] == 0.f) sp[h * kSub + n] = (a0 + a1) + (a2 + a3);
-        }
+      halve_heads<HN / 2, LPT / 2>(s, lane);
+#pragma unroll
+      for (int x = LPT / HN / 2; x; x /= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], x);
+      const float score = (ok >> (i % S)) & 1 ? s[0] : -INFINITY;
+      if (__any_sync(0xffffffffu, score > m)) {  // rare once the first steps have passed
+        const float mn = fmaxf(m, score), f = exp2f(m - (mn == -INFINITY ? 0.f : mn));
+        m = mn;
+        l *= f;
+        rescale(f);
       }
-      __syncthreads();
-      for (int h = warp; h < it.nh; h += kPagedThreads / 32) {
-        const float s0 = sp[h * kSub + lane], s1 = sp[h * kSub + lane + 32];
-        float m = fmaxf(s0, s1);
+      const float weight = exp2f(score - (m == -INFINITY ? 0.f : m));
+      l += weight;
 #pragma unroll
-        for (int w = 16; w; w /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-        const float old = sm[h], mn = fmaxf(old, m), use = mn == -INFINITY ? 0.f : mn;
-        const float p0 = exp2f(s0 - use), p1 = exp2f(s1 - use);
-        float l = p0 + p1;
+      for (int h = 0; h < HN; ++h) s[h] = __shfl_sync(0xffffffffu, weight, home + h * (LPT / HN));
 #pragma unroll
-        for (int w = 16; w; w /= 2) l += __shfl_xor_sync(0xffffffffu, l, w);
-        sp[h * kSub + lane] = p0;
-        sp[h * kSub + lane + 32] = p1;
-        __syncwarp();
-        if (lane == 0) {
-          const float f = exp2f(old - use);
-          sc[h] = f;
-          sl[h] = sl[h] * f + l;
-          sm[h] = mn;
-        }
+      for (int j = 0; j < NP; ++j) {
+        const float4 x = kv[(NP + j) * 32];
+#pragma unroll
+        for (int h = 0; h < HN; ++h)
+          acc[h][j] = make_float4(fmaf(s[h], x.x, acc[h][j].x), fmaf(s[h], x.y, acc[h][j].y),
+                                  fmaf(s[h], x.z, acc[h][j].z), fmaf(s[h], x.w, acc[h][j].w));
       }
-      __syncthreads();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // the lanes of different tokens joined, then the warps
+    float mn = m;
 #pragma unroll
-      for (int h = 0; h < HT; ++h)
-        if (hbase + h < it.nh) {
-          float a = acc[h] * sc[hbase + h];
-          const float *pr = sp + (hbase + h) * kSub;
-#pragma unroll 8
-          for (int r = 0; r < kSub; ++r) a = fmaf(pr[r], sv[r * LD + dim], a);
-          acc[h] = a;
+    for (int x = LPT; x < 32; x *= 2) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+    const float f = exp2f(m - (mn == -INFINITY ? 0.f : mn));
+    m = mn;
+    l *= f;
+    rescale(f);
+#pragma unroll
+    for (int x = LPT; x < 32; x *= 2) {
+      l += __shfl_xor_sync(0xffffffffu, l, x);
+#pragma unroll
+      for (int h = 0; h < HN; ++h)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          acc[h][j].x += __shfl_xor_sync(0xffffffffu, acc[h][j].x, x);
+          acc[h][j].y += __shfl_xor_sync(0xffffffffu, acc[h][j].y, x);
+          acc[h][j].z += __shfl_xor_sync(0xffffffffu, acc[h][j].z, x);
+          acc[h][j].w += __shfl_xor_sync(0xffffffffu, acc[h][j].w, x);
         }
+    }
+    __syncthreads();  // every warp has left its ring
+    if (sub == 0) {
+#pragma unroll
+      for (int h = 0; h < HN; ++h)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) smem4[(warp * HN + h) * (D / 4) + j * LPT + lane] = acc[h][j];
+      sm[warp][mine] = m;
+      sl[warp][mine] = l;
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == w.nt;
+    const bool whole = w.t0 == 0 && w.t1 == w.nt;
+    for (int e = tid; e < it.nh * D; e += kSimtThreads) {
+      const int h = e / D, dim = e % D;
+      float mx = -INFINITY, a = 0.f, sum = 0.f;
 #pragma unroll
-    for (int h = 0; h < HT; ++h)
-      if (hbase + h < it.nh) {
-        const int hh = hbase + h;
-        if (whole)
-          o[b * p.qsb + (it.h0 + hh) * p.qsh + dim] = sl[hh] > 0.f ? acc[h] / sl[hh] : 0.f;
-        else
-          part[((int64_t)(2 * g + slot) * kHeads + hh) * D + dim] = acc[h];
+      for (int x = 0; x < kSimtWarps; ++x) mx = fmaxf(mx, sm[x][h]);
+#pragma unroll
+      for (int x = 0; x < kSimtWarps; ++x) {
+        const float f = exp2f(sm[x][h] - (mx == -INFINITY ? 0.f : mx));
+        a = fmaf(f, reinterpret_cast<const float *>(smem4)[(x * HN + h) * D + dim], a);
+        sum = fmaf(f, sl[x][h], sum);
       }
-    if (tid < it.nh) {
+      const int64_t piece = (int64_t)(2 * g + slot) * kHeads + h;
       if (whole) {
-        if (lse) lse[(int64_t)b * p.Hq + it.h0 + tid] = (sm[tid] + log2f(sl[tid])) * 0.6931471805599453f;
+        o[b * p.qsb + (it.h0 + h) * p.qsh + dim] = sum > 0.f ? a / sum : 0.f;
+        if (lse && dim == 0) lse[(int64_t)b * p.Hq + it.h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
       } else {
-        ml[((int64_t)(2 * g + slot) * kHeads + tid) * 2] = sm[tid];
-        ml[((int64_t)(2 * g + slot) * kHeads + tid) * 2 + 1] = sl[tid];
+        part[piece * D + dim] = a;
+        if (dim == 0) {
+          ml[piece * 2] = mx;
+          ml[piece * 2 + 1] = sum;
+        }
       }
     }
     slot = 1;
@@ -785,16 +867,19 @@ cudaError_t run_decode(Launch launch, int per, const PagedProblem &p, void *o, f
 template <int D>
 cudaError_t run_dim(const PagedProblem &p, const void *q, const void *kc, const void *vc, void *o, float *lse, void *ws,
                     cudaStream_t s) {
+  const int group = p.Hq / p.Hkv;
   if (p.esz == 4) {
-    constexpr size_t smem = paged_simt_smem<D>();
-    cudaError_t e = cudaFuncSetAttribute(paged_decode_simt<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto kernel = group <= 4 ? paged_decode_simt<D, 4> : group <= 8 ? paged_decode_simt<D, 8> : paged_decode_simt<D, 16>;
+    constexpr size_t smem = SimtLayout<D, 4>::smem;
+    static_assert(smem == SimtLayout<D, 8>::smem && smem == SimtLayout<D, 16>::smem, "16 KiB per warp");
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return run_decode<D, float>(
         [&](int G, float *part, float *ml) {
-          return launch_overlapped(paged_decode_simt<D>, dim3(G), dim3(kPagedThreads), smem, s, p, (const float *)q,
-                                   (const float *)kc, (const float *)vc, (float *)o, lse, part, ml);
+          return launch_overlapped(kernel, dim3(G), dim3(kSimtThreads), smem, s, p, (const float *)q, (const float *)kc,
+                                   (const float *)vc, (float *)o, lse, part, ml);
         },
-        2, p, o, lse, ws, s);
+        kSimtPerSm, p, o, lse, ws, s);
   }
   using bf16 = __nv_bfloat16;
   // the rows of one copy: the largest power of two up to 128 that divides a page (a copy stays inside a page
@@ -808,7 +893,6 @@ cudaError_t run_dim(const PagedProblem &p, const void *q, const void *kc, const 
     if (!make_tmap_bf16(&mk, kc, dims, strides, box) || !make_tmap_bf16(&mv, vc, dims, strides, box))
       return cudaErrorInvalidValue;
   }
-  const int group = p.Hq / p.Hkv;
   auto kernel = group <= 4 ? paged_decode_tc<D, 4> : group <= 8 ? paged_decode_tc<D, 8> : paged_decode_tc<D, 16>;
   constexpr size_t smem = TcLayout<D>::smem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
