@@ -34,10 +34,14 @@ namespace {
 
 constexpr int kC = 64;                    // tokens of a chunk
 constexpr uint32_t kSlot = 16384;         // a 64 x 128 (or 128 x 64) bf16 tile
-// A chunk's record: W hi, W lo (64 x 128), T hi, lo (64 x 64), P hi, lo (64 x 64), all as swizzled tiles
+// A chunk's record: W (64 x 128), T (64 x 64), P (64 x 64), each in two bf16 parts, as swizzled tiles
 // ready for a plain bulk copy; then five fp32 rows of 64: e^g, phi, b, g and its low part (log2 units).
 constexpr uint32_t kRecW = 0, kRecT = 32768, kRecP = 49152, kRecG = 65536, kGateBytes = 5 * 64 * 4;
 constexpr size_t kRecBytes = 67584;
+// P's parts are two tiles.  W and T are tiles of 128 rows: of every 16 tokens the hi rows, then the lo rows, so
+// that one product of 128 rows takes both and their sums meet in one warp's lanes.
+__device__ __forceinline__ uint32_t part_row(uint32_t token) { return 2 * (token & ~15u) + (token & 15u); }
+constexpr uint32_t kPartLo = 16 * 128;  // from a hi row to its lo row
 constexpr size_t kStateImg = 32768, kRowImg = 16384, kYImg = 2 * kRowImg;  // Y: hi, lo
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -360,8 +364,8 @@ __global__ void __launch_bounds__(kPrepThreads)
         st_shared_v4(base + kPrepA + at, eh[0], eh[1], eh[2], eh[3]);
         st_shared_v4(base + kPrepA + 8192 + at, el[0], el[1], el[2], el[3]);
       }
-      store_row8(rec + kRecT, row, q, th);
-      store_row8(rec + kRecT + 8192, row, q, tl);
+      store_row8(rec + kRecT, part_row(row), q, th);
+      store_row8(rec + kRecT + kPartLo, part_row(row), q, tl);
     }
     fence_proxy_async_smem();
     tc_fence_before();
@@ -389,9 +393,9 @@ __global__ void __launch_bounds__(kPrepThreads)
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 4; ++e) split2(-w[2 * e], -w[2 * e + 1], h[e], l[e]);
-        const uint32_t at = base + frag_at_trans(lane, tok0, row0, 8192);
+        const uint32_t at = base + frag_at_trans(lane, part_row(tok0), row0, 16384);
         stmatrix4_trans(at, h);
-        stmatrix4_trans(at + 16384, l);
+        stmatrix4_trans(at + kPartLo, l);
       }
       tc_fence_before();
       fence_proxy_async_smem();
@@ -425,7 +429,7 @@ template <int VS>
 struct Chain {
   static constexpr int warps = VS / 4, side = 4 + warps, threads = 32 * (side + kSideWarps + 2);  // side: first such warp
   // four rings of tiles in order of use: two of 8 KiB, then 16 KiB ones
-  static constexpr int nx = VS == 32 ? 3 : 2, ny = VS == 32 ? 4 : 3, nz = 3, slots = 2 + nx + ny + nz;
+  static constexpr int nx = VS == 32 ? 3 : 2, ny = 4, nz = VS == 32 ? 3 : 2, slots = 2 + nx + ny + nz;
   // operand tiles: rows of hi and lo parts side by side (VS = 32: one 128-byte row; 64: two blocks)
   static constexpr uint32_t state_lo = VS == 32 ? 64 : 16384, row_lo = VS == 32 ? 64 : 8192;
   static constexpr uint32_t op = (slots - 1) * kSlot, u0 = op + 128 * VS * 4, u1 = u0 + 64 * VS * 4,
@@ -469,24 +473,26 @@ __device__ __forceinline__ constexpr uint64_t k_step(uint32_t ks) { return ks * 
 __device__ __forceinline__ constexpr uint64_t mn_step(uint32_t ks) { return ks * 128u; }
 // D (+)= A B over `n` times four steps, A K-major (AM = false) or MN-major, B MN-major; a_inc and b_inc lead
 // to the next four (the next 64-column block of A, the next 64 rows of B, the other part of either).
-template <bool AM>
+// (A_ROWS: MN-major, the rows from one step of A to the next in units of 16)
+template <bool AM, int A_ROWS = 1>
 __device__ __forceinline__ void mma_four(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   mma_ss_warp(d, a, b, idesc, acc);
 #pragma unroll
-  for (uint32_t ks = 1; ks < 4; ++ks) mma_ss_warp(d, a + (AM ? mn_step(ks) : k_step(ks)), b + mn_step(ks), idesc, 1);
+  for (uint32_t ks = 1; ks < 4; ++ks)
+    mma_ss_warp(d, a + (AM ? mn_step(A_ROWS * ks) : k_step(ks)), b + mn_step(ks), idesc, 1);
 }
 // ROLL: as a loop (less code, a few cycles more): the forward, with more roles, gains from it, the backward
 // only off its path
-template <bool AM, bool ROLL, int N>
+template <bool AM, bool ROLL, int N, int A_ROWS = 1>
 __device__ __forceinline__ void mma_fours(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool fresh, uint32_t a_inc,
                                           uint32_t b_inc) {
   if (ROLL) {
     uint32_t acc = fresh ? 0 : 1;
 #pragma unroll 1
-    for (int i = 0; i < N; ++i, a += a_inc, b += b_inc, acc = 1) mma_four<AM>(d, a, b, idesc, acc);
+    for (int i = 0; i < N; ++i, a += a_inc, b += b_inc, acc = 1) mma_four<AM, A_ROWS>(d, a, b, idesc, acc);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) mma_four<AM>(d, a + i * a_inc, b + i * b_inc, idesc, i > 0 || !fresh);
+    for (int i = 0; i < N; ++i) mma_four<AM, A_ROWS>(d, a + i * a_inc, b + i * b_inc, idesc, i > 0 || !fresh);
   }
 }
 constexpr uint32_t kBlock = 8192 >> 4, kRows64 = 4 * 128;  // descriptor increments: 8 KiB; 64 rows
@@ -711,7 +717,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 
   const int loader = loader_of<VS>(warp);
   if (loader >= 0) {
-    // V, gates | T, K | W hi, W lo | Q, P
+    // V, gates | T, K | W | Q, P
     if (lane == 0) {
       const ChainLoad a{loader == 0 ? &mv : loader == 3 ? &mq : nullptr,
                         loader == 0 ? x0 / 64 * 64u : loader == 1 ? kRecT : loader == 2 ? kRecW : 0u,
@@ -723,17 +729,17 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     }
   } else if (warp == 1) {
     // the chain's own products, in the order of its dependences
-    const uint32_t id_1 = idesc_bf16(64, VS, false, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
+    const uint32_t id_1 = idesc_bf16(128, VS, false, true), id_2 = idesc_bf16(128, 2 * VS, false, true),
                    id_k = idesc_bf16(128, VS, true, true);
     const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, 8192);
     RV rv;  // V
     RX rx;  // T, K
-    RY ry;  // W hi, W lo
+    RY ry;  // W, in two blocks of 64 key dimensions
     auto landed = [&] { return k.full(rv) && k.full(rx) && k.full(ry) && k.full(ry.next()); };  // V, T, W
     auto vt = [&] {  // Y = T V
       tc_fence_after();
       const uint64_t v = mn_tile(k.slot(rv) + (x0 & 63) * 2, 8192), tt = k_tile(k.slot(rx));
-      mma_fours<false, true, 2>(tmem + kTY, tt, v, id_1, true, kBlock, 0);
+      mma_fours<false, true, 1>(tmem + kTY, tt, v, id_1, true, 0, 0);
       k.release(rv);
       k.release(rx);
       rv.advance();
@@ -744,16 +750,16 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     if (ok) vt();
 #pragma unroll 1
     for (int c = 0; c < P.N && ok; ++c) {
-      // Y += W S: hi [hi | lo] (2 VS columns), lo hi
-      const RY lo = ry.next();
+      // Y += W [S hi | S lo] (2 VS columns)
+      const RY second = ry.next();
       if (!(ok = k.wait_w(C_OP, c))) break;
       tc_fence_after();
-      mma_fours<false, true, 2>(tmem + kTY, k_tile(k.slot(ry)), op, id_2, false, kBlock, kRows64);
-      mma_fours<false, true, 2>(tmem + kTY, k_tile(k.slot(lo)), op, id_1, false, kBlock, kRows64);
+      mma_fours<false, true, 1>(tmem + kTY, k_tile(k.slot(ry)), op, id_2, false, 0, 0);
+      mma_fours<false, true, 1>(tmem + kTY, k_tile(k.slot(second)), op + kRows64, id_2, false, 0, 0);
       mma_commit_warp(&bar[C_YFULL]);
       k.release(ry);
-      k.release(lo);
-      ry = lo.next();
+      k.release(second);
+      ry = second.next();
       // S += K^T diag(phi b) Y
       const RX kt = rx;
       rx.advance();
@@ -790,7 +796,8 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       rz.advance();
     }
   } else if (warp < L::side) {
-    // S: key dimension `row`; Y: token `tok` (lanes 0..15); columns 16 cg .. + 15 of the slice
+    // S: key dimension `row`, columns 16 cg .. + 15 of the slice; Y: token `tok`, the sums' parts from the hi
+    // rows of T and W in lanes 0..15 and from the lo rows in 16..31, put together as 8 columns per lane
     const uint32_t quad = warp & 3, cg = (warp - 4) >> 2, row = quad * 32 + lane, tok = quad * 16 + (lane & 15);
     const uint32_t t = tmem + ((quad * 32) << 16) + 16 * cg;
     const uint32_t gcol = x0 + 16 * cg;  // the columns' value dimension
@@ -837,24 +844,31 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       tmem_stf(t + kTY + VS, zero);
 #pragma unroll
       for (int j = 0; j < 16; ++j) y[j] += z[j];
+      const bool up = lane & 16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        y[j] = (up ? y[j + 8] : y[j]) + __shfl_xor_sync(0xffffffffu, up ? y[j] : y[j + 8], 16);
       tmem_st_wait();
+      const uint32_t piece = 2 * cg + (lane >> 4);
       float w = phi * be;  // the update's factor, then the output's
 #pragma unroll 1
       for (int e = 0; e < 2; ++e, w = be) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] = w * y[j];
-        if (lane < 16) put_split<VS>(k.base + L::u0 + e * (L::u1 - L::u0), L::row_lo, tok, cg, z, hi);
+        for (int j = 0; j < 4; ++j) split2(w * y[2 * j], w * y[2 * j + 1], hi[j], hi[4 + j]);
+        const uint32_t at = k.base + L::u0 + e * (L::u1 - L::u0) + tok * 128u, ao = VS == 32 ? at : at + L::row_lo;
+        st_shared_v4(at + ((piece ^ (tok & 7u)) << 4), hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(ao + (((piece + (VS == 32 ? 4u : 0u)) ^ (tok & 7u)) << 4), hi[4], hi[5], hi[6], hi[7]);
         fence_proxy_async_smem();
         k.arrive(C_YOP + e, lane);
       }
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + c % kGateRing]);
-      if (P.yimg && lane < 16) {
-        uint32_t lo[8];
+      if (P.yimg) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split2(y[2 * j], y[2 * j + 1], hi[j], lo[j]);
-        uint8_t *img = P.yimg + ((int64_t)bh * P.N + c) * kYImg + (gcol >> 6) * 8192;
-        store_row8(img, tok, (gcol & 63) >> 4, hi);
-        store_row8(img + kRowImg, tok, (gcol & 63) >> 4, lo);
+        for (int j = 0; j < 4; ++j) split2(y[2 * j], y[2 * j + 1], hi[j], hi[4 + j]);
+        uint8_t *img = P.yimg + ((int64_t)bh * P.N + c) * kYImg + (gcol >> 6) * 8192 +
+                       sw(tok, ((gcol & 63) >> 3) + (lane >> 4));
+        *reinterpret_cast<uint4 *>(img) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(img + kRowImg) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
       }
     }
   } else {
@@ -922,7 +936,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   // step x of the walk is chunk N - 1 - x
   const int loader = loader_of<VS>(warp);
   if (loader >= 0) {
-    // dO, gates | P, K | W hi, W lo | Q
+    // dO, gates | P, K | W | Q
     if (lane == 0) {
       const ChainLoad a{loader == 0 ? &mdo : loader == 3 ? &mq : nullptr,
                         loader == 0 ? x0 / 64 * 64u : loader == 1 ? kRecP : loader == 2 ? kRecW : 0u,
@@ -939,7 +953,8 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
                    dos = mn_tile(k.base + L::u1, 8192);
     RV rv;  // dO
     RX rx;  // P, K
-    RY ry;  // W hi, W lo
+    RY ry;  // W, in two blocks of 64 key dimensions (neighbours in a ring of an even number)
+    static_assert(L::ny % 2 == 0, "");
     RZ rz;  // Q
     auto pd = [&](RV d) {  // P^T dO
       tc_fence_after();
@@ -971,23 +986,24 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       k.release(rv);  // the scaled dO is ready: every reader of this tile is done
       rv.advance();
       // R += W^T diag(b) dU: hi hi, hi lo, lo hi (after the waits for the next step's dO and P)
-      const RY lo = ry.next();
+      const RY second = ry.next();
       if (x + 1 < P.N) {
-        const int idx[4] = {C_FULL + ry.s, C_FULL + lo.s, C_FULL + rv.s, C_FULL + rx.s};
-        const uint32_t parity[4] = {ry.ph, lo.ph, rv.ph, rx.ph};
+        const int idx[4] = {C_FULL + ry.s, C_FULL + second.s, C_FULL + rv.s, C_FULL + rx.s};
+        const uint32_t parity[4] = {ry.ph, second.ph, rv.ph, rx.ph};
         ok = k.wait_all(idx, parity);
       } else {
-        ok = k.full(ry) && k.full(lo);
+        ok = k.full(ry) && k.full(second);
       }
       if (!(ok = ok && k.wait_w(C_YOP, x))) break;
       tc_fence_after();
-      mma_fours<true, false, 2>(tmem + kTR, mn_tile(k.slot(ry), 8192), ut, id_k, false, 0, L::row_lo >> 4);
-      mma_fours<true, false, 1>(tmem + kTR, mn_tile(k.slot(lo), 8192), ut, id_k, false, 0, 0);
+      const uint64_t wt = mn_tile(k.slot(ry), kSlot);
+      mma_fours<true, false, 2, 2>(tmem + kTR, wt, ut, id_k, false, 0, L::row_lo >> 4);
+      mma_fours<true, false, 1, 2>(tmem + kTR, wt + (kPartLo >> 4), ut, id_k, false, 0, 0);
       mma_commit_warp(&bar[C_ACC]);
       if (x + 1 < P.N) pd(rv);
       k.release(ry);
-      k.release(lo);
-      ry = lo.next();
+      k.release(second);
+      ry = second.next();
     }
   } else if (warp == 2) {
     // (the forward's output products)
@@ -1181,7 +1197,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       if (!(ok = wait(G_UT, x))) break;
       tc_fence_after();
       // Z^T = (diag(b) dU)^T T
-      mma(kGZ, mn_tile(base + kGrU, 8192), mn_tile(base + kGrT, 8192), id_mm, true, 2, kM, 0, kM, k8);
+      mma(kGZ, mn_tile(base + kGrU, 8192), mn_tile(base + kGrT, 8192), id_mm, true, 2, kM, 0, 2 * kM, kM);
       mma_commit_warp(&bar[G_Z]);
       // (the accumulators that follow are read in the last chunk's last step)
       if (!(ok = wait(G_KQ, x) && (x == 0 || wait(G_END, x - 1)))) break;
