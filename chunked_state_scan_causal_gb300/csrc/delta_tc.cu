@@ -654,17 +654,12 @@ __device__ __forceinline__ void put_split(uint32_t tile, uint32_t lo, uint32_t r
   st_shared_v4(blk + (((p + 2 * g + 1) ^ (r & 7u)) << 4), l[4], l[5], l[6], l[7]);
 }
 
-// the words that store_row8 wrote, from their place
-__device__ __forceinline__ void load_row8(const uint8_t *src, uint32_t r, uint32_t (&w)[8]) {
-  const uint4 a = reinterpret_cast<const uint4 *>(src)[r & 1u], b = reinterpret_cast<const uint4 *>(src)[~r & 1u];
-  w[0] = a.x;
-  w[1] = a.y;
-  w[2] = a.z;
-  w[3] = a.w;
-  w[4] = b.x;
-  w[5] = b.y;
-  w[6] = b.z;
-  w[7] = b.w;
+// 8 values of row r, piece p of the slice, already split: words 0..3 are the hi parts, 4..7 the lo parts
+template <int VS>
+__device__ __forceinline__ void put_piece(uint32_t tile, uint32_t lo, uint32_t r, uint32_t p, const uint32_t (&w)[8]) {
+  const uint32_t row = tile + r * 128u, blk = VS == 32 ? row : row + lo, pl = VS == 32 ? p + 4u : p;
+  st_shared_v4(row + ((p ^ (r & 7u)) << 4), w[0], w[1], w[2], w[3]);
+  st_shared_v4(blk + ((pl ^ (r & 7u)) << 4), w[4], w[5], w[6], w[7]);
 }
 
 // 16 columns of a state row in global memory (fp32, row and columns inside d)
@@ -855,9 +850,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       for (int e = 0; e < 2; ++e, w = be) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) split2(w * y[2 * j], w * y[2 * j + 1], hi[j], hi[4 + j]);
-        const uint32_t at = k.base + L::u0 + e * (L::u1 - L::u0) + tok * 128u, ao = VS == 32 ? at : at + L::row_lo;
-        st_shared_v4(at + ((piece ^ (tok & 7u)) << 4), hi[0], hi[1], hi[2], hi[3]);
-        st_shared_v4(ao + (((piece + (VS == 32 ? 4u : 0u)) ^ (tok & 7u)) << 4), hi[4], hi[5], hi[6], hi[7]);
+        put_piece<VS>(k.base + L::u0 + e * (L::u1 - L::u0), L::row_lo, tok, piece, hi);
         fence_proxy_async_smem();
         k.arrive(C_YOP + e, lane);
       }
@@ -1042,9 +1035,9 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
       store_row8(P.rimg + ci * kStateImg + (gcol >> 6) * 16384, row, (gcol & 63) >> 4, hi);
-      const uint8_t *yrow = P.yimg + ci * kYImg + (gcol >> 6) * 8192 + row8(tok, (gcol & 63) >> 4);
-      prefetch_l1(yrow);
-      prefetch_l1(yrow + kRowImg);
+      const int64_t img = ci * kYImg + (gcol >> 6) * 8192 + sw(tok, ((gcol & 63) >> 3) + (lane >> 4));
+      prefetch_l1(P.yimg + img);
+      prefetch_l1(P.yimg + img + kRowImg);
       if (!(ok = k.wait_w(C_YFULL, x))) break;
       tc_fence_after();
       float u[16], v[16], w[16];
@@ -1053,26 +1046,31 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       tmem_ldf(t + kT2 + VS, w);
       tmem_ld_wait();
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        u[j] = fmaf(phi, v[j] + w[j], u[j]);
-        v[j] = be * u[j];
+      for (int j = 0; j < 16; ++j) u[j] = fmaf(phi, v[j] + w[j], u[j]);
+      // lanes 16..31 take over the last 8 columns of lanes 0..15
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = __shfl_sync(0xffffffffu, u[j + 8], lane & 15);
+        if (lane & 16) u[j] = y;
       }
-      if (lane < 16) put_split<VS>(k.base + L::u0, L::row_lo, tok, cg, v, hi);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split2(be * u[2 * j], be * u[2 * j + 1], hi[j], hi[4 + j]);
+      put_piece<VS>(k.base + L::u0, L::row_lo, tok, 2 * cg + (lane >> 4), hi);
       fence_proxy_async_smem();
       k.arrive(C_YOP, lane);
       if (lane == 0) mbar_arrive(&bar[C_GEMPTY + x % kGateRing]);
-      if (lane < 16) {
-        // (hi: diag(b) dU)
-        store_row8(P.uimg + ci * kRowImg + (gcol >> 6) * 8192, tok, (gcol & 63) >> 4, hi);
-        float dot = 0.f;
+      // (hi: diag(b) dU)
+      *reinterpret_cast<uint4 *>(P.uimg + img - ci * kRowImg) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      float dot = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          load_row8(yrow + e * kRowImg, tok, hi);
+      for (int e = 0; e < 2; ++e) {
+        const uint4 y = *reinterpret_cast<const uint4 *>(P.yimg + img + e * kRowImg);
+        const uint32_t t[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dot = fmaf(u[2 * j], bf16lo(hi[j]), fmaf(u[2 * j + 1], bf16hi(hi[j]), dot));
-        }
-        P.dot[(ci * kC + tok) * 8 + (gcol >> 4)] = dot;
+        for (int j = 0; j < 4; ++j) dot = fmaf(u[2 * j], bf16lo(t[j]), fmaf(u[2 * j + 1], bf16hi(t[j]), dot));
       }
+      dot += __shfl_xor_sync(0xffffffffu, dot, 16);
+      if (lane < 16) P.dot[(ci * kC + tok) * 8 + (gcol >> 4)] = dot;
     }
   } else {
     // diag(e^g) dO in two parts: 16 columns of a token at a time
