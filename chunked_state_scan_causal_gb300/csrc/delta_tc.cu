@@ -685,7 +685,7 @@ __device__ __forceinline__ void tmem_stf(uint32_t addr, const float (&x)[16]) {
   tmem_st16(addr, *reinterpret_cast<const uint32_t(*)[16]>(&x));
 }
 
-// Tensor memory of the forward chain (columns): S; Y (both parts' products); Q S and P Y likewise.
+// Tensor memory of the forward chain (columns): S, Y, Q S and P Y, each as the products of both parts.
 template <int VS>
 __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -696,7 +696,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   using RX = RingPos<2, L::nx>;
   using RY = RingPos<2 + L::nx, L::ny>;
   using RZ = RingPos<2 + L::nx + L::ny, L::nz>;
-  constexpr uint32_t kTS = 0, kTY = VS, kTQ = 3 * VS, kTP = 5 * VS;
+  constexpr uint32_t kTS = 0, kTY = 2 * VS, kTQ = 4 * VS, kTP = 6 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
   uint8_t *smem = align1024(smem_raw);
@@ -725,8 +725,8 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   } else if (warp == 1) {
     // the chain's own products, in the order of its dependences
     const uint32_t id_1 = idesc_bf16(128, VS, false, true), id_2 = idesc_bf16(128, 2 * VS, false, true),
-                   id_k = idesc_bf16(128, VS, true, true);
-    const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, 8192);
+                   id_k = idesc_bf16(128, 2 * VS, true, true);
+    const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, L::row_lo);
     RV rv;  // V
     RX rx;  // T, K
     RY ry;  // W, in two blocks of 64 key dimensions
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       // (C_YOP: every thread has also written back its part of S, scaled)
       if (!(ok = k.full(kt) && (c + 1 == P.N || landed()) && k.wait_w(C_YOP, c))) break;
       tc_fence_after();
-      mma_fours<true, true, 2>(tmem + kTS, mn_tile(k.slot(kt), 8192), ut, id_k, false, 0, L::row_lo >> 4);
+      mma_fours<true, true, 1>(tmem + kTS, mn_tile(k.slot(kt), 8192), ut, id_k, false, 0, 0);
       mma_commit_warp(&bar[C_ACC]);
       if (c + 1 < P.N) vt();
       k.release(kt);
@@ -810,8 +810,12 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
         // (Q S of the last chunk has read the operand that is rewritten here)
         if (!(ok = k.wait_w(C_QS, c - 1) && k.wait_w(C_ACC, c - 1))) break;
         tc_fence_after();
+        float s2[16];
         tmem_ldf(t + kTS, s);
+        tmem_ldf(t + kTS + VS, s2);
         tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[j] += s2[j];
       }
       if (c == P.N) {
         if (P.out && in) store_state16(P.out + at, s);
@@ -827,6 +831,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[j] *= f;
       tmem_stf(t + kTS, s);
+      tmem_stf(t + kTS + VS, zero);
       if (P.simg) store_row8(P.simg + ((int64_t)bh * P.N + c) * kStateImg + (gcol >> 6) * 16384, row, (gcol & 63) >> 4, hi);
       // The last chunk's output product is done: it has read the operand that is rewritten below, and its
       // issuer has seen that chunk's C_ACC, which the arrival at C_YOP may lead to complete again.
@@ -903,7 +908,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Tensor memory of the reverse chain: R; P^T dO; K R (both parts' products).
+// Tensor memory of the reverse chain: R (both parts' products); P^T dO; K R (both).
 template <int VS>
 __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     delta_reverse_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -913,7 +918,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
   using RX = RingPos<2, L::nx>;
   using RY = RingPos<2 + L::nx, L::ny>;
   using RZ = RingPos<2 + L::nx + L::ny, L::nz>;
-  constexpr uint32_t kTR = 0, kT1 = VS, kT2 = 2 * VS;
+  constexpr uint32_t kTR = 0, kT1 = 2 * VS, kT2 = 3 * VS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int abort_flag;
   uint8_t *smem = align1024(smem_raw);
@@ -941,9 +946,9 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     }
   } else if (warp == 1) {
     const uint32_t id_p = idesc_bf16(64, VS, true, true), id_2 = idesc_bf16(64, 2 * VS, false, true),
-                   id_k = idesc_bf16(128, VS, true, true);
-    const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, 8192),
-                   dos = mn_tile(k.base + L::u1, 8192);
+                   id_k = idesc_bf16(128, VS, true, true), id_k2 = idesc_bf16(128, 2 * VS, true, true);
+    const uint64_t op = mn_tile(k.base + L::op, L::state_lo), ut = mn_tile(k.base + L::u0, L::row_lo),
+                   dos = mn_tile(k.base + L::u1, L::row_lo);
     RV rv;  // dO
     RX rx;  // P, K
     RY ry;  // W, in two blocks of 64 key dimensions (neighbours in a ring of an even number)
@@ -973,7 +978,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
         if (!(ok = k.wait_all(idx, parity))) break;
       }
       tc_fence_after();
-      mma_fours<true, false, 2>(tmem + kTR, mn_tile(k.slot(rz), 8192), dos, id_k, false, 0, L::row_lo >> 4);
+      mma_fours<true, false, 1>(tmem + kTR, mn_tile(k.slot(rz), 8192), dos, id_k2, false, 0, 0);
       k.release(rz);
       rz.advance();
       k.release(rv);  // the scaled dO is ready: every reader of this tile is done
@@ -990,7 +995,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       if (!(ok = ok && k.wait_w(C_YOP, x))) break;
       tc_fence_after();
       const uint64_t wt = mn_tile(k.slot(ry), kSlot);
-      mma_fours<true, false, 2, 2>(tmem + kTR, wt, ut, id_k, false, 0, L::row_lo >> 4);
+      mma_fours<true, false, 1, 2>(tmem + kTR, wt, ut, id_k2, false, 0, 0);
       mma_fours<true, false, 1, 2>(tmem + kTR, wt + (kPartLo >> 4), ut, id_k, false, 0, 0);
       mma_commit_warp(&bar[C_ACC]);
       if (x + 1 < P.N) pd(rv);
@@ -1006,6 +1011,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
     const uint32_t gcol = x0 + 16 * cg;
     const int64_t at = ((int64_t)bh * P.d + row) * P.d + gcol;
     const bool in = (int)row < P.d;
+    const float zero[16] = {};
     bool ok = true;
     for (int x = 0; x <= P.N && ok; ++x) {
       const int64_t ci = (int64_t)bh * P.N + P.N - 1 - x;
@@ -1015,8 +1021,12 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
       } else {
         if (!(ok = k.wait_w(C_ACC, x - 1))) break;
         tc_fence_after();
+        float s2[16];
         tmem_ldf(t + kTR, s);
+        tmem_ldf(t + kTR + VS, s2);
         tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[j] += s2[j];
       }
       if (x == P.N) {
         if (P.out && in) store_state16(P.out + at, s);
@@ -1032,6 +1042,7 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[j] *= f;
       tmem_stf(t + kTR, s);
+      tmem_stf(t + kTR + VS, zero);
       tmem_st_wait();
       k.arrive(C_SCALED, lane);
       store_row8(P.rimg + ci * kStateImg + (gcol >> 6) * 16384, row, (gcol & 63) >> 4, hi);
