@@ -149,14 +149,16 @@ __device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
 // One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
 // cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks by forward
 // substitution, a column per thread, then the off-diagonal block as two 32^3 products), and
-// W^T = K^T (T diag(e^g))^T on the tensor cores.  Three CTAs fit an SM and hide each other's latencies.
+// W^T = K^T (T diag(e^g))^T on the tensor cores.  Four CTAs fit an SM and hide each other's latencies.
 constexpr int kPrepThreads = 256;
-constexpr int kLd = 68;  // row stride of the fp32 64 x 64 matrices: 16-byte rows, spread over the banks
-constexpr uint32_t kPrepA = 32768, kPrepT = kPrepA + 17408, kPrepEnd = kPrepT + 17408;
+constexpr int kLd = 68;  // row stride of the fp32 matrix T: 16-byte rows, spread over the banks
+// The stacked tile [K; Q] (two blocks of 64 columns), then T.  A^T, later the parts of T diag(e^g), take the
+// place of Q: rows 0..31 (the hi part) in the first block, the others in the second.
+constexpr uint32_t kPrepA = 8192, kPrepT = 32768, kPrepEnd = kPrepT + kLd * 64 * 4;
 constexpr size_t kPrepSmem = kPrepEnd + 1024;
-static_assert(kPrepT % 1024 == 0 && kLd * 64 * 4 == 17408, "tiles stay 1 KiB aligned");
+static_assert(4 * (kPrepSmem + 2048) <= 232448, "four CTAs per SM (as the tensor memory has it)");
 
-__global__ void __launch_bounds__(kPrepThreads)
+__global__ void __launch_bounds__(kPrepThreads, 4)
     delta_prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, DeltaTcParams P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
@@ -164,7 +166,8 @@ __global__ void __launch_bounds__(kPrepThreads)
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
   __shared__ float4 s_g[kC];  // g and its low part, b, e^g
-  float *At = reinterpret_cast<float *>(smem + kPrepA), *Ti = reinterpret_cast<float *>(smem + kPrepT);
+  float *Ti = reinterpret_cast<float *>(smem + kPrepT);
+  auto At = [&](int j) { return reinterpret_cast<float *>(smem + kPrepA + (j >> 5) * 16384) + (j & 31) * 64; };
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int c = blockIdx.x % P.N, bh = blockIdx.x / P.N, b = bh / P.H, h = bh % P.H;
@@ -258,14 +261,14 @@ __global__ void __launch_bounds__(kPrepThreads)
             const int j = 32 * x + y + z;
             const float4 gj = s_g[j];
             const float e = ex2((hi - gj.x) + (lo - gj.y));
-            At[j * kLd + i] = j < i ? e * __uint_as_float(r[z]) * gj.z : 0.f;
+            At(j)[i] = j < i ? e * __uint_as_float(r[z]) * gj.z : 0.f;
           }
         }
       if (x == quad) {
         // column `lane` of the inverse V of this warp's diagonal block, eight rows at a time: the rows before
         // them (in shared memory) are taken out, then the 8 x 8 triangle is solved in registers
         __syncwarp();
-        const float *Ab = At + (quad * 32) * kLd + quad * 32;
+        const float *Ab = At(quad * 32) + quad * 32;
         float *V = Ti + (quad * 32) * kLd + quad * 32 + lane;
 #pragma unroll 1
         for (int r = 0; r < 32; r += 8) {
@@ -277,8 +280,8 @@ __global__ void __launch_bounds__(kPrepThreads)
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
               const float w = V[(m + f) * kLd];
-              const float4 a = *reinterpret_cast<const float4 *>(Ab + (m + f) * kLd + r);
-              const float4 b = *reinterpret_cast<const float4 *>(Ab + (m + f) * kLd + r + 4);
+              const float4 a = *reinterpret_cast<const float4 *>(Ab + (m + f) * 64 + r);
+              const float4 b = *reinterpret_cast<const float4 *>(Ab + (m + f) * 64 + r + 4);
               v[0] = fmaf(-a.x, w, v[0]);
               v[1] = fmaf(-a.y, w, v[1]);
               v[2] = fmaf(-a.z, w, v[2]);
@@ -291,8 +294,8 @@ __global__ void __launch_bounds__(kPrepThreads)
           }
 #pragma unroll
           for (int f = 0; f < 7; ++f) {
-            const float4 a = *reinterpret_cast<const float4 *>(Ab + (r + f) * kLd + r);
-            const float4 b = *reinterpret_cast<const float4 *>(Ab + (r + f) * kLd + r + 4);
+            const float4 a = *reinterpret_cast<const float4 *>(Ab + (r + f) * 64 + r);
+            const float4 b = *reinterpret_cast<const float4 *>(Ab + (r + f) * 64 + r + 4);
             const float col[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int e = f + 1; e < 8; ++e) v[e] = fmaf(-col[e], v[f], v[e]);
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int m = 0; m < 32; ++m) {
-        const float a = At[m * kLd + 32 + r];
+        const float a = At(m)[32 + r];
         const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0);
         acc = make_float4(fmaf(a, u.x, acc.x), fmaf(a, u.y, acc.y), fmaf(a, u.z, acc.z), fmaf(a, u.w, acc.w));
       }
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kPrepThreads)
         }
         const uint32_t at = sw(row, 2 * q + y);
         st_shared_v4(base + kPrepA + at, eh[0], eh[1], eh[2], eh[3]);
-        st_shared_v4(base + kPrepA + 8192 + at, el[0], el[1], el[2], el[3]);
+        st_shared_v4(base + kPrepA + 16384 + at, el[0], el[1], el[2], el[3]);
       }
       store_row8(rec + kRecT, part_row(row), q, th);
       store_row8(rec + kRecT + kPartLo, part_row(row), q, tl);
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       for (uint32_t p = 0; p < 2; ++p)
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)
-          mma_ss_warp(tmem + 64, desc_mnmajor(base, ks), desc_kmajor(base + kPrepA + p * 8192, ks),
+          mma_ss_warp(tmem + 64, desc_mnmajor(base, ks), desc_kmajor(base + kPrepA + p * 16384, ks),
                       idesc_bf16(128, 64, true, false), p + ks > 0);
       mma_commit_warp(&bar[2]);
     }
