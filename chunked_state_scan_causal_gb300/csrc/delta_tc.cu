@@ -148,7 +148,8 @@ __device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
 // ================================================================== prep
 // One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
 // cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks by forward
-// substitution, a column per thread, then the off-diagonal block as two 32^3 products), and
+// substitution, a column per thread, then the off-diagonal block as two 32^3 products in 4 x 4 tiles, since
+// what bounds the kernel is what it reads from shared memory), and
 // W^T = K^T (T diag(e^g))^T on the tensor cores.  Four CTAs fit an SM and hide each other's latencies.
 constexpr int kPrepThreads = 256;
 constexpr int kLd = 68;  // row stride of the fp32 matrix T: 16-byte rows, spread over the banks
@@ -158,6 +159,31 @@ constexpr uint32_t kPrepA = 8192, kPrepT = 32768, kPrepEnd = kPrepT + kLd * 64 *
 constexpr size_t kPrepSmem = kPrepEnd + 1024;
 static_assert(4 * (kPrepSmem + 2048) <= 232448, "four CTAs per SM (as the tensor memory has it)");
 
+// A 4 x 4 tile of a product: one step of the contraction (a: four rows, u: four columns).
+__device__ __forceinline__ void tile_fma(float4 (&acc)[4], const float4 &a, const float4 &u) {
+  const float f[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    acc[e] = make_float4(fmaf(f[e], u.x, acc[e].x), fmaf(f[e], u.y, acc[e].y), fmaf(f[e], u.z, acc[e].z),
+                         fmaf(f[e], u.w, acc[e].w));
+}
+// The sums of four lanes' tiles (lanes l, l ^ 8, l ^ 16, l ^ 24), a row to each: left in acc[0], the row returned.
+__device__ __forceinline__ int tile_sum(float4 (&acc)[4], int lane) {
+#pragma unroll
+  for (int n = 2; n; n /= 2) {
+    const bool up = lane & (8 * n);
+#pragma unroll
+    for (int e = 0; e < n; ++e) {
+      const float4 keep = up ? acc[e + n] : acc[e], send = up ? acc[e] : acc[e + n];
+      acc[e] = make_float4(keep.x + __shfl_xor_sync(0xffffffffu, send.x, 8 * n),
+                           keep.y + __shfl_xor_sync(0xffffffffu, send.y, 8 * n),
+                           keep.z + __shfl_xor_sync(0xffffffffu, send.z, 8 * n),
+                           keep.w + __shfl_xor_sync(0xffffffffu, send.w, 8 * n));
+    }
+  }
+  return lane >> 3;
+}
+
 __global__ void __launch_bounds__(kPrepThreads, 4)
     delta_prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, DeltaTcParams P) {
   extern __shared__ uint8_t smem_raw[];
@@ -165,7 +191,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
   __shared__ uint64_t bar[3];
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
-  __shared__ float4 s_g[kC];  // g and its low part, b, e^g
+  __shared__ float2 s_g[kC];  // g and its low part
+  __shared__ float s_b[kC], s_eg[kC];
   float *Ti = reinterpret_cast<float *>(smem + kPrepT);
   auto At = [&](int j) { return reinterpret_cast<float *>(smem + kPrepA + (j >> 5) * 16384) + (j & 31) * 64; };
   const uint32_t base = smem_u32(smem);
@@ -221,7 +248,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       const Two gx = x ? s : s + Two{-l[1].hi, -l[1].lo};
       const int j = 2 * lane + x;
       const float eg = ex2(gx.hi) * ex2(gx.lo), phi = ex2((last.hi - gx.hi) + (last.lo - gx.lo));
-      s_g[j] = make_float4(gx.hi, gx.lo, be[x], eg);
+      s_g[j] = make_float2(gx.hi, gx.lo);
+      s_b[j] = be[x];
+      s_eg[j] = eg;
       g[j] = eg;
       g[64 + j] = phi;
       g[128 + j] = be[x];
@@ -259,9 +288,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 #pragma unroll
           for (int z = 0; z < 8; ++z) {
             const int j = 32 * x + y + z;
-            const float4 gj = s_g[j];
+            const float2 gj = s_g[j];
             const float e = ex2((hi - gj.x) + (lo - gj.y));
-            At(j)[i] = j < i ? e * __uint_as_float(r[z]) * gj.z : 0.f;
+            At(j)[i] = j < i ? e * __uint_as_float(r[z]) * s_b[j] : 0.f;
           }
         }
       if (x == quad) {
@@ -314,7 +343,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 #pragma unroll
         for (int z = 0; z < 8; ++z) {
           const int j = 32 * x + 16 * y + 2 * z;
-          const float4 g0 = s_g[j], g1 = s_g[j + 1];
+          const float2 g0 = s_g[j], g1 = s_g[j + 1];
           const float p0 = ex2((hi - g0.x) + (lo - g0.y)) * __uint_as_float(r[2 * z]);
           const float p1 = ex2((hi - g1.x) + (lo - g1.y)) * __uint_as_float(r[2 * z + 1]);
           split2(j <= i ? p0 : 0.f, j + 1 <= i ? p1 : 0.f, ph[z], pl[z]);
@@ -326,26 +355,38 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
     __syncthreads();
     {
       // the off-diagonal block -T22 (A21 T11): X = A21 T11 parked in the upper right block, then zeroed
-      const int r = tid / 8, c0 = (tid % 8) * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int m = 0; m < 32; ++m) {
-        const float a = At(m)[32 + r];
-        const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + c0);
-        acc = make_float4(fmaf(a, u.x, acc.x), fmaf(a, u.y, acc.y), fmaf(a, u.z, acc.z), fmaf(a, u.w, acc.w));
+      const int r0 = 4 * warp, c0 = (lane & 7) * 4, m0 = (lane >> 3) * 8;
+      float4 acc[4] = {};
+#pragma unroll 1
+      for (int m = m0; m < m0 + 8; m += 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 a = *reinterpret_cast<const float4 *>(At(m + e) + 32 + r0);
+          const float4 u = *reinterpret_cast<const float4 *>(Ti + (m + e) * kLd + c0);
+          tile_fma(acc, a, u);
+        }
       }
-      float4 *X = reinterpret_cast<float4 *>(Ti + r * kLd + 32 + c0);
-      *X = acc;
+      const int row = tile_sum(acc, lane);
+      float4 *X = reinterpret_cast<float4 *>(Ti + (r0 + row) * kLd + 32 + c0);
+      *X = acc[0];
       __syncthreads();
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int m = 0; m < 32; ++m) {
-        const float a = -Ti[(32 + r) * kLd + 32 + m];
-        const float4 u = *reinterpret_cast<const float4 *>(Ti + m * kLd + 32 + c0);
-        acc = make_float4(fmaf(a, u.x, acc.x), fmaf(a, u.y, acc.y), fmaf(a, u.z, acc.z), fmaf(a, u.w, acc.w));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int m = m0; m < m0 + 8; m += 4) {
+        float4 t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = *reinterpret_cast<const float4 *>(Ti + (32 + r0 + e) * kLd + 32 + m);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 u = *reinterpret_cast<const float4 *>(Ti + (m + e) * kLd + 32 + c0);
+          auto at = [&](const float4 &x) { return e == 0 ? -x.x : e == 1 ? -x.y : e == 2 ? -x.z : -x.w; };
+          tile_fma(acc, make_float4(at(t[0]), at(t[1]), at(t[2]), at(t[3])), u);
+        }
       }
+      tile_sum(acc, lane);
       __syncthreads();
-      *reinterpret_cast<float4 *>(Ti + (32 + r) * kLd + c0) = acc;
+      *reinterpret_cast<float4 *>(Ti + (32 + r0 + row) * kLd + c0) = acc[0];
       *X = make_float4(0.f, 0.f, 0.f, 0.f);
       __syncthreads();
     }
@@ -361,7 +402,7 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
           const int j = 16 * q + 8 * y + 2 * z;
           const float2 u = *reinterpret_cast<const float2 *>(Ti + row * kLd + j);
           split2(u.x, u.y, th[4 * y + z], tl[4 * y + z]);
-          split2(u.x * s_g[j].w, u.y * s_g[j + 1].w, eh[z], el[z]);
+          split2(u.x * s_eg[j], u.y * s_eg[j + 1], eh[z], el[z]);
         }
         const uint32_t at = sw(row, 2 * q + y);
         st_shared_v4(base + kPrepA + at, eh[0], eh[1], eh[2], eh[3]);
