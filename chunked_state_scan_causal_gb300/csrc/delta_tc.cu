@@ -147,9 +147,8 @@ __device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
 
 // ================================================================== prep
 // One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
-// cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks by forward
-// substitution, a column per thread, then the off-diagonal block as two 32^3 products in 4 x 4 tiles, since
-// what bounds the kernel is what it reads from shared memory), and
+// cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks, then the block
+// below them; products in 4 x 4 tiles, since what bounds the kernel is what it reads from shared memory), and
 // W^T = K^T (T diag(e^g))^T on the tensor cores.  Four CTAs fit an SM and hide each other's latencies.
 constexpr int kPrepThreads = 256;
 constexpr int kLd = 68;  // row stride of the fp32 matrix T: 16-byte rows, spread over the banks
@@ -167,21 +166,106 @@ __device__ __forceinline__ void tile_fma(float4 (&acc)[4], const float4 &a, cons
     acc[e] = make_float4(fmaf(f[e], u.x, acc[e].x), fmaf(f[e], u.y, acc[e].y), fmaf(f[e], u.z, acc[e].z),
                          fmaf(f[e], u.w, acc[e].w));
 }
-// The sums of four lanes' tiles (lanes l, l ^ 8, l ^ 16, l ^ 24), a row to each: left in acc[0], the row returned.
-__device__ __forceinline__ int tile_sum(float4 (&acc)[4], int lane) {
+// One halving step of a sum over lanes: lanes l and l ^ X keep N rows each of the sum of their 2 N rows.
+template <int N, int X>
+__device__ __forceinline__ void tile_halve(float4 (&acc)[4], int lane) {
+  const bool up = lane & X;
 #pragma unroll
-  for (int n = 2; n; n /= 2) {
-    const bool up = lane & (8 * n);
+  for (int e = 0; e < N; ++e) {
+    const float4 keep = up ? acc[e + N] : acc[e], send = up ? acc[e] : acc[e + N];
+    acc[e] = make_float4(keep.x + __shfl_xor_sync(0xffffffffu, send.x, X), keep.y + __shfl_xor_sync(0xffffffffu, send.y, X),
+                         keep.z + __shfl_xor_sync(0xffffffffu, send.z, X), keep.w + __shfl_xor_sync(0xffffffffu, send.w, X));
+  }
+}
+// acc += A U and acc -= T U over 8 steps from m0: rows r0 .. + 3 of A (transposed, row stride 64) or T and
+// columns c0 .. + 3 of U (both with row stride kLd).
+__device__ __forceinline__ void tile_at(float4 (&acc)[4], const float *at, const float *u) {
+#pragma unroll 1
+  for (int m = 0; m < 8; m += 4, at += 4 * 64, u += 4 * kLd)
 #pragma unroll
-    for (int e = 0; e < n; ++e) {
-      const float4 keep = up ? acc[e + n] : acc[e], send = up ? acc[e] : acc[e + n];
-      acc[e] = make_float4(keep.x + __shfl_xor_sync(0xffffffffu, send.x, 8 * n),
-                           keep.y + __shfl_xor_sync(0xffffffffu, send.y, 8 * n),
-                           keep.z + __shfl_xor_sync(0xffffffffu, send.z, 8 * n),
-                           keep.w + __shfl_xor_sync(0xffffffffu, send.w, 8 * n));
+    for (int e = 0; e < 4; ++e)
+      tile_fma(acc, *reinterpret_cast<const float4 *>(at + e * 64), *reinterpret_cast<const float4 *>(u + e * kLd));
+}
+__device__ __forceinline__ void tile_minus(float4 (&acc)[4], const float *t, const float *u) {
+#pragma unroll 1
+  for (int m = 0; m < 8; m += 4, t += 4, u += 4 * kLd) {
+    float4 r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = *reinterpret_cast<const float4 *>(t + e * kLd);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      auto at = [&](const float4 &x) { return e == 0 ? -x.x : e == 1 ? -x.y : e == 2 ? -x.z : -x.w; };
+      tile_fma(acc, make_float4(at(r[0]), at(r[1]), at(r[2]), at(r[3])), *reinterpret_cast<const float4 *>(u + e * kLd));
     }
   }
-  return lane >> 3;
+}
+// V (row stride kLd) = (I + A)^-1 for the strictly lower triangular 32 x 32 A, given transposed (row stride 64),
+// by one warp: four 8 x 8 blocks by substitution, a column per lane, then twice the block below the diagonal,
+// -T22 (A21 T11), with X = A21 T11 parked above the diagonal in between and zeroed after.
+__device__ __forceinline__ void invert32(const float *A, float *V, int lane) {
+  {
+    const int o = lane & ~7, col = lane & 7;
+    const float *a = A + o * 64 + o;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e == col ? 1.f : 0.f;
+#pragma unroll
+    for (int f = 0; f < 7; ++f) {
+      const float4 x = *reinterpret_cast<const float4 *>(a + f * 64), y = *reinterpret_cast<const float4 *>(a + f * 64 + 4);
+      const float c[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = f + 1; e < 8; ++e) v[e] = fmaf(-c[e], v[f], v[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) V[(o + e) * kLd + o + col] = v[e];
+  }
+  __syncwarp();
+  {
+    // 8 -> 16, both blocks at once: four outputs of a row per lane
+    const int o = lane & 16, r = (lane & 15) >> 1, c0 = (lane & 1) * 4;
+    float4 *X = reinterpret_cast<float4 *>(V + (o + r) * kLd + o + 8 + c0);
+    const float *a = A + o * 64 + o + 8 + r, *u = V + o * kLd + o + c0, *t = V + (o + 8 + r) * kLd + o + 8;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const float f = a[m * 64];
+      const float4 y = *reinterpret_cast<const float4 *>(u + m * kLd);
+      x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+    }
+    *X = x;
+    __syncwarp();
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const float f = -t[m];
+      const float4 y = *reinterpret_cast<const float4 *>(u + m * kLd + 8);
+      x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+    }
+    __syncwarp();
+    *reinterpret_cast<float4 *>(V + (o + 8 + r) * kLd + o + c0) = x;
+    *X = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __syncwarp();
+  {
+    // 16 -> 32: a 4 x 4 tile and half of the contraction per lane
+    const int r0 = lane & 12, c0 = (lane & 3) * 4, m0 = (lane >> 4) * 8, row = r0 + 2 * (lane >> 4);
+    float4 acc[4] = {};
+    tile_at(acc, A + m0 * 64 + 16 + r0, V + m0 * kLd + c0);
+    tile_halve<2, 16>(acc, lane);
+    float4 *X = reinterpret_cast<float4 *>(V + row * kLd + 16 + c0);
+    X[0] = acc[0];
+    X[kLd / 4] = acc[1];
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    tile_minus(acc, V + (16 + r0) * kLd + 16 + m0, V + m0 * kLd + 16 + c0);
+    tile_halve<2, 16>(acc, lane);
+    __syncwarp();
+    float4 *Y = reinterpret_cast<float4 *>(V + (16 + row) * kLd + c0);
+    Y[0] = acc[0];
+    Y[kLd / 4] = acc[1];
+    X[0] = X[kLd / 4] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
 }
 
 __global__ void __launch_bounds__(kPrepThreads, 4)
@@ -294,44 +378,8 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
           }
         }
       if (x == quad) {
-        // column `lane` of the inverse V of this warp's diagonal block, eight rows at a time: the rows before
-        // them (in shared memory) are taken out, then the 8 x 8 triangle is solved in registers
         __syncwarp();
-        const float *Ab = At(quad * 32) + quad * 32;
-        float *V = Ti + (quad * 32) * kLd + quad * 32 + lane;
-#pragma unroll 1
-        for (int r = 0; r < 32; r += 8) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = r + e == lane ? 1.f : 0.f;
-#pragma unroll 1
-          for (int m = 0; m < r; m += 4) {
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-              const float w = V[(m + f) * kLd];
-              const float4 a = *reinterpret_cast<const float4 *>(Ab + (m + f) * 64 + r);
-              const float4 b = *reinterpret_cast<const float4 *>(Ab + (m + f) * 64 + r + 4);
-              v[0] = fmaf(-a.x, w, v[0]);
-              v[1] = fmaf(-a.y, w, v[1]);
-              v[2] = fmaf(-a.z, w, v[2]);
-              v[3] = fmaf(-a.w, w, v[3]);
-              v[4] = fmaf(-b.x, w, v[4]);
-              v[5] = fmaf(-b.y, w, v[5]);
-              v[6] = fmaf(-b.z, w, v[6]);
-              v[7] = fmaf(-b.w, w, v[7]);
-            }
-          }
-#pragma unroll
-          for (int f = 0; f < 7; ++f) {
-            const float4 a = *reinterpret_cast<const float4 *>(Ab + (r + f) * 64 + r);
-            const float4 b = *reinterpret_cast<const float4 *>(Ab + (r + f) * 64 + r + 4);
-            const float col[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int e = f + 1; e < 8; ++e) v[e] = fmaf(-col[e], v[f], v[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) V[(r + e) * kLd] = v[e];
-        }
+        invert32(At(quad * 32) + quad * 32, Ti + (quad * 32) * kLd + quad * 32, lane);
       }
     } else {
       // P_ij = Gam_ij (q_i . k_j), j <= i, straight to the record
@@ -357,36 +405,20 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
       // the off-diagonal block -T22 (A21 T11): X = A21 T11 parked in the upper right block, then zeroed
       const int r0 = 4 * warp, c0 = (lane & 7) * 4, m0 = (lane >> 3) * 8;
       float4 acc[4] = {};
-#pragma unroll 1
-      for (int m = m0; m < m0 + 8; m += 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 a = *reinterpret_cast<const float4 *>(At(m + e) + 32 + r0);
-          const float4 u = *reinterpret_cast<const float4 *>(Ti + (m + e) * kLd + c0);
-          tile_fma(acc, a, u);
-        }
-      }
-      const int row = tile_sum(acc, lane);
-      float4 *X = reinterpret_cast<float4 *>(Ti + (r0 + row) * kLd + 32 + c0);
+      tile_at(acc, At(m0) + 32 + r0, Ti + m0 * kLd + c0);
+      tile_halve<2, 16>(acc, lane);
+      tile_halve<1, 8>(acc, lane);
+      const int row = r0 + (lane >> 3);
+      float4 *X = reinterpret_cast<float4 *>(Ti + row * kLd + 32 + c0);
       *X = acc[0];
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-      for (int m = m0; m < m0 + 8; m += 4) {
-        float4 t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = *reinterpret_cast<const float4 *>(Ti + (32 + r0 + e) * kLd + 32 + m);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float4 u = *reinterpret_cast<const float4 *>(Ti + (m + e) * kLd + 32 + c0);
-          auto at = [&](const float4 &x) { return e == 0 ? -x.x : e == 1 ? -x.y : e == 2 ? -x.z : -x.w; };
-          tile_fma(acc, make_float4(at(t[0]), at(t[1]), at(t[2]), at(t[3])), u);
-        }
-      }
-      tile_sum(acc, lane);
+      tile_minus(acc, Ti + (32 + r0) * kLd + 32 + m0, Ti + m0 * kLd + 32 + c0);
+      tile_halve<2, 16>(acc, lane);
+      tile_halve<1, 8>(acc, lane);
       __syncthreads();
-      *reinterpret_cast<float4 *>(Ti + (32 + r0 + row) * kLd + c0) = acc[0];
+      *reinterpret_cast<float4 *>(Ti + (32 + row) * kLd + c0) = acc[0];
       *X = make_float4(0.f, 0.f, 0.f, 0.f);
       __syncthreads();
     }
