@@ -149,7 +149,8 @@ __device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
 // One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
 // cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks, then the block
 // below them; products in 4 x 4 tiles, since what bounds the kernel is what it reads from shared memory), and
-// W^T = K^T (T diag(e^g))^T on the tensor cores.  Four CTAs fit an SM and hide each other's latencies.
+// W^T = K^T (T diag(e^g))^T on the tensor cores.  Four CTAs fit an SM and hide each other's latencies: 197 us at
+// B2 H16 T16384, 4.1 TB/s of what it reads and writes.
 constexpr int kPrepThreads = 256;
 constexpr int kLd = 68;  // row stride of the fp32 matrix T: 16-byte rows, spread over the banks
 // The stacked tile [K; Q] (two blocks of 64 columns), then T.  A^T, later the parts of T diag(e^g), take the
@@ -489,17 +490,20 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 
 // ================================================================== chains
 // One CTA per (batch, head, slice of VS value dimensions): the columns of S are independent given W, K and
-// T, so slices spread a chain over several SMs.  Lanes are key dimensions (S: 128 rows) or tokens (Y, O, dU:
-// 64 rows, lanes 16 q .. 16 q + 15 of every quarter), columns the slice.  What the threads make for the next
-// product (S, Y, R, dU in two bf16 parts, side by side) goes to shared memory as its B operand; both parts
-// of S (R) meet the same A tile in one product of 2 VS columns.
+// T, so slices spread a chain over several SMs.  Lanes are key dimensions (S: 128 rows) or tokens (O, dU: 64
+// rows, lanes 16 q .. 16 q + 15 of every quarter; Y: the same for T's and W's hi parts and the other lanes for
+// the lo parts), columns the slice.  What the threads make for the next product (S, Y, R, dU in two bf16 parts,
+// side by side) goes to shared memory as its B operand, and both parts meet the same A tile in one product of
+// 2 VS columns: a product costs what reading its operand rows costs (33 to 35 cycles per 16 of the contraction
+// for 64 rows, 42 to 51 for 128, whatever the width up to 64), so few wide ones beat many narrow ones.
 //
-// A chunk's path is S -> (W S) -> Y -> (K^T Y) -> S: two products and two passes of the threads, each
-// bounded by its latency (reading 64 or 128 operand rows per 16 of the contraction takes 33 to 51 cycles a
-// product whatever the width).  Every role is a long loop of its own, so their instructions have to be few:
-// with unrolled products and in-line waits two CTAs on neighbouring SMs took 3.1 us a chunk, one alone 2.0.  Warps: 1 issues the chain's products, 2 the output's, 0, 3 and the last two load, 4 and on
-// (4 VS/16) carry the chain (16 columns each: the threads' work is on the path, so it is spread thin), then 4
-// make the output (forward) or the scaled dO (backward).
+// A chunk's path is S -> (W S) -> Y -> (K^T Y) -> S: two products and two passes of the threads, each bounded
+// by its latency: 1.71 us a chunk forward and 1.76 backward with slices of 32 (0.44 and 0.45 ms at B2 H16
+// T16384, on 128 SMs; the other tensor work fits into the gaps).  Every role is a long loop of its own, so their
+// instructions have to be few: with unrolled products and in-line waits two CTAs on neighbouring SMs took 1.5
+// times as long as one alone.  Warps: 1 issues the chain's products, 2 the output's, 0, 3 and the last two load,
+// 4 and on (4 VS/16) carry the chain (16 columns each: the threads' work is on the path, so it is spread thin),
+// then 4 make the output (forward) or the scaled dO (backward).
 constexpr int kGateRing = 4, kSideWarps = 4;
 template <int VS>
 struct Chain {
@@ -515,12 +519,11 @@ struct Chain {
 static_assert(Chain<32>::smem <= 231000 && Chain<64>::smem <= 231000, "one CTA per SM");
 
 enum { C_OP = 0,    // S (R) operand parts ready
-       C_SCALED,    // backward: its accumulator scaled by the chunk's decay
+       C_SCALED,    // backward: R's accumulator scaled by the chunk's decay
        C_ACC,       // its accumulator complete (next chunk)
        C_YFULL,     // Y (K R) accumulator complete
        C_YOP,       // the operand made from it for the update ready
-       C_UOP,       // (C_YOP + 1)
-                    //      // forward: its operand for the output ready; backward: the scaled dO
+       C_UOP,       // (C_YOP + 1) forward: its operand for the output ready; backward: the scaled dO
        C_QS, C_OFULL, C_OFREE,   // forward: Q S done; output complete, read
        C_GFULL, C_GEMPTY = C_GFULL + kGateRing, C_FULL = C_GEMPTY + kGateRing };
 
@@ -762,12 +765,16 @@ __device__ __forceinline__ void tmem_stf(uint32_t addr, const float (&x)[16]) {
 }
 
 // Tensor memory of the forward chain (columns): S, Y, Q S and P Y, each as the products of both parts.
-template <int VS>
-__global__ void __launch_bounds__(Chain<VS>::threads, 1)
+// Forward slices are always of 32: with 64, a chunk takes 2.2 times as long (B2 H32 T4096, two turns of slices of
+// 32: 230 us; one turn of slices of 64: 247).
+constexpr int kSlice = 32;
+using kChain = Chain<kSlice>;
+__global__ void __launch_bounds__(kChain::threads, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, __nv_bfloat16 *o, int64_t osb, int64_t osh, int64_t ost,
                        DeltaTcParams P) {
-  using L = Chain<VS>;
+  constexpr int VS = kSlice;
+  using L = kChain;
   using RV = RingPos<0, 2>;
   using RX = RingPos<2, L::nx>;
   using RY = RingPos<2 + L::nx, L::ny>;
@@ -1198,8 +1205,9 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 // have lane = dimension; the 64 x 64 ones come from 128-row operands whose other rows are unused: [K; dO]
 // stacked gives K K^T in lanes 0..63 and dO Y^T in lanes 64..127.  Warps 0..15 turn products into operands and
 // results (16 columns each), warp 16 issues the products, warp 17 loads and stores: the next chunk's tiles arrive
-// and its first product runs while the threads are in this one's last step.  Bound by the 96 products of a
-// chunk (their operand rows, about 50 cycles each) and the latencies between its five steps.
+// and its first product runs while the threads are in this one's last step.  Bound by its 224 KB a chunk (0.365 ms
+// at B2 H16 T16384: 5.0 TB/s, 0.74 of copy bandwidth) and the latencies between the five steps: the tiles of one
+// chunk fill shared memory, so the loads overlap only the last step.
 //
 // Single bf16 operands except Y in dO Y^T and Y R^T and the matrix A, which have two parts: with one the
 // gradients' errors come to 2.9e-3 of their size, 1.75 times the rounding of the results themselves (now 2.0e-3
@@ -1552,8 +1560,8 @@ cudaError_t allow_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-// Slices of 32 value dimensions while all the chains run at once with one CTA per SM, else of 64 (a chunk
-// takes longer, but not twice as long).
+// The reverse chain's slices: of 32 value dimensions while all the chains run at once with one CTA per SM, else
+// of 64 (a chunk takes 1.6 times as long: 182 us at B2 H32 T4096, where slices of 32 would take two turns of 120).
 bool narrow_slices(const Problem &p) { return (int64_t)p.B * p.H * (p.d / 32) <= p.num_sms; }
 int chunks(const Problem &p) { return (p.T + kC - 1) / kC; }
 size_t bhs(const Problem &p) { return (size_t)p.B * p.H; }
@@ -1604,15 +1612,10 @@ cudaError_t delta_tc_fwd(const Problem &p, const DeltaGates &g, const void *q, c
     e = launch_overlapped(delta_prep_kernel, dim3((unsigned)(bhs(p) * P.N)), dim3(kPrepThreads), kPrepSmem, s, mq, mk, P);
     if (e != cudaSuccess) return e;
   }
-  auto chain = [&](auto kernel, int slice, int threads, size_t smem) {
-    cudaError_t err = allow_smem(kernel, smem);
-    if (err != cudaSuccess) return err;
-    TimedLaunch t(K_DELTA_CHAIN, s);
-    return launch_overlapped(kernel, dim3((unsigned)(bhs(p) * (p.d / slice))), dim3(threads), smem, s, mq, mk, mv,
-                             static_cast<__nv_bfloat16 *>(o), p.sb, p.sh, p.st, P);
-  };
-  return narrow_slices(p) ? chain(delta_chain_kernel<32>, 32, Chain<32>::threads, Chain<32>::smem)
-                          : chain(delta_chain_kernel<64>, 64, Chain<64>::threads, Chain<64>::smem);
+  if ((e = allow_smem(delta_chain_kernel, kChain::smem)) != cudaSuccess) return e;
+  TimedLaunch t(K_DELTA_CHAIN, s);
+  return launch_overlapped(delta_chain_kernel, dim3((unsigned)(bhs(p) * (p.d / kSlice))), dim3(kChain::threads),
+                           kChain::smem, s, mq, mk, mv, static_cast<__nv_bfloat16 *>(o), p.sb, p.sh, p.st, P);
 }
 
 cudaError_t delta_tc_bwd(const Problem &p, const DeltaGates &g, const void *q, const void *k, const void *dO,
