@@ -235,3 +235,36 @@ def test_graph_and_streams(dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, e) for a, e in zip(w, r))
+
+
+def test_offsets_past_32_bits():
+    """Records of more than 2^32 bytes: the same bits as the sequence in two pieces (cut between two chunks)."""
+    B, H, T, d = 4, 32, 32832, 128
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("not enough free memory")
+    g = torch.Generator(device="cuda").manual_seed(31)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    k = rn(B, H, T, d)
+    k = (k / k.norm(dim=-1, keepdim=True)).bfloat16()
+    q, v, dO = ((rn(B, H, T, d) * s).bfloat16() for s in (d ** -0.5, 1.0, 1.0))
+    beta, lg = torch.rand(B, H, T, generator=g, device="cuda"), -0.1 * torch.rand(B, H, T, generator=g, device="cuda")
+    ck = la.checkpoint_delta(q)
+    assert ck.numel() > 1 << 32
+    o, fin = la.fwd_delta(q, k, v, lg, beta, want_final=True, ckpt=ck)
+    grads = la.bwd_delta(q, k, v, dO, lg, beta, ck, want_dinit=True)
+    cut, state, pieces = T // 128 * 64, None, []
+    for part in (slice(0, cut), slice(cut, T)):
+        x = [t[:, :, part] for t in (q, k, v)] + [t[:, :, part].contiguous() for t in (lg, beta)]
+        ckp = la.checkpoint_delta(x[0])
+        op, nxt = la.fwd_delta(*x, init_state=state, want_final=True, ckpt=ckp)
+        assert torch.equal(op, o[:, :, part])
+        pieces.append((x, ckp, state, dO[:, :, part], part))
+        state = nxt
+    assert torch.equal(state, fin)
+    D = None
+    for x, ckp, init, up, part in reversed(pieces):
+        got = la.bwd_delta(*x[:3], up, *x[3:], ckp, init_state=init, d_final=D, want_dinit=True)
+        for a, b in zip(got[:5], grads[:5]):
+            assert torch.equal(a, b[:, :, part])
+        D = got[5]
+    assert torch.equal(D, grads[5])

@@ -225,3 +225,22 @@ def test_repeatable_and_concurrent(dtype):
     torch.cuda.synchronize()
     for r in got:
         assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_offsets_past_32_bits(dtype):
+    """A cache of more than 2^31 elements, its last pages in use."""
+    pages, Hq, Hkv, page, d = 66000, 8, 4, 64, 128
+    free = torch.cuda.mem_get_info()[0]
+    if free < 3 * pages * Hkv * page * d * torch.finfo(dtype).bits // 8:
+        pytest.skip("not enough free memory")
+    kc, vc = (torch.empty(pages, Hkv, page, d, dtype=dtype, device="cuda") for _ in range(2))
+    assert kc.numel() > 1 << 31
+    q, sk, sv, small, lens = case(12, [250, 130], Hq, Hkv, d, page, dtype, poison=False)
+    far = (pages - 1 - small.long() * 7).to(torch.int32)
+    K, V = (torch.stack([c[small[b].long()].transpose(0, 1).reshape(Hkv, -1, d) for b in range(2)]) for c in (sk, sv))
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    la.paged_append(K.cuda(), V.cuda(), kc, vc, far.cuda(), zero, new_lens=lens.cuda())
+    o, lse = la.paged_decode(q.cuda(), kc, vc, far.cuda(), lens.cuda(), want_lse=True)
+    ro, rl = paged_attention(q, sk, sv, small, lens)
+    assert rel(o, ro) < TOL[dtype] and float((lse.cpu().double() - rl).abs().max()) < 6.3e-5
