@@ -509,7 +509,7 @@ template <int VS>
 struct Chain {
   static constexpr int warps = VS / 4, side = 4 + warps, threads = 32 * (side + kSideWarps + 2);  // side: first such warp
   // four rings of tiles in order of use: two of 8 KiB, then 16 KiB ones
-  static constexpr int nx = VS == 32 ? 3 : 2, ny = 4, nz = VS == 32 ? 3 : 2, slots = 2 + nx + ny + nz;
+  static constexpr int nx = VS == 32 ? 4 : 2, ny = 4, nz = 2, slots = 2 + nx + ny + nz;
   // operand tiles: rows of hi and lo parts side by side (VS = 32: one 128-byte row; 64: two blocks)
   static constexpr uint32_t state_lo = VS == 32 ? 64 : 16384, row_lo = VS == 32 ? 64 : 8192;
   static constexpr uint32_t op = (slots - 1) * kSlot, u0 = op + 128 * VS * 4, u1 = u0 + 64 * VS * 4,
