@@ -604,7 +604,7 @@ struct ChainCtx {
 #pragma unroll
     for (int i = 0; i < N; ++i) ready &= mbar_test_wait(&bar[idx[i]], parity[i] & 1);
     if (__all_sync(0xffffffffu, ready)) return true;
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < N; ++i)
       if (!wait_w(idx[i], parity[i])) return false;
     return true;

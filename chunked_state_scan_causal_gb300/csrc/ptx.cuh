@@ -113,25 +113,26 @@ __device__ __forceinline__ bool mbar_wait_w(uint64_t *bar, uint32_t parity, vola
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, detail));
 }
 
-// mbar_wait in little code: what decides whether to give up is out of line and asked every 256 tries.  For
-// kernels whose warps run long loops with many waits, where the instructions themselves have to fit the
-// caches.
-static __device__ __noinline__ bool mbar_give_up(uint64_t *t0, volatile int *abort_flag, int *status) {
-  if (*abort_flag) return true;
-  const uint64_t now = globaltimer_ns();
-  if (*t0 == 0) *t0 = now;
-  if (now - *t0 <= kWaitLimitNs) return false;
+// mbar_wait in little code: the clock is asked every 256 tries, in 32 bits, and the report is out of line, behind
+// the loop (a call inside it makes the compiler keep what is live around every wait in memory).  For kernels
+// whose warps run long loops with many waits, where the instructions themselves have to fit the caches.
+static __device__ __noinline__ void mbar_gave_up(volatile int *abort_flag, int *status) {
   report_error(status, -6);
   *abort_flag = 1;
-  return true;
 }
 __device__ __forceinline__ bool mbar_wait_compact(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *status) {
-  uint64_t t0 = 0;
+  static_assert(kWaitLimitNs < (1ull << 32), "the difference of two 32-bit clocks");
+  uint32_t t0 = 0;
 #pragma unroll 1
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0 && mbar_give_up(&t0, abort_flag, status)) return false;
+    if (i & 255u) continue;
+    const uint32_t now = (uint32_t)globaltimer_ns() | 1u;
+    if (t0 == 0) t0 = now;
+    if (*abort_flag || now - t0 > (uint32_t)kWaitLimitNs) break;
   }
+  mbar_gave_up(abort_flag, status);
+  return false;
 }
 
 // ----------------------------------------------------------------------------- global flags
