@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ int abort_flag;
   __shared__ __align__(16) float s_red[2][HN][4];
   __shared__ float s_m[HN], s_l[HN];
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
   const uint32_t base = smem_u32(smem);
   if (tid == 0) {
     abort_flag = 0;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tslot;  // S of the even and odd tiles: columns 0, 16; their O^T: 32, 64
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tslot, 0);  // S of the even and odd tiles: columns 0, 16; their O^T: 32, 64
   griddep_wait();
   griddep_launch_dependents();
   PagedWalk w;
