@@ -12,6 +12,7 @@ take torch tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -669,12 +670,29 @@ def _paged_workspace(q):
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
+@functools.lru_cache(maxsize=1024)
+def _delta_bytes(op, B, H, T, d, dtype, device):
+    st, n = linattn_workspace_size(Shape(ABI_VERSION, B, H, T, d, d, 64, dtype, H * T * d, T * d, d, None), op)
+    _check(st, "linattn_workspace_size")
+    return max(n, 256)
+
+
+def _delta_buffer(op, sh, device):
+    """A workspace or checkpoint: its size depends on the shape (and the device) alone, and is asked for once."""
+    import torch
+    return torch.empty(_delta_bytes(op, sh.B, sh.H, sh.T, sh.dk, sh.dtype, device), dtype=torch.uint8, device=device)
+
+
+def _like(q):
+    """An output with q's layout."""
+    import torch
+    return torch.empty_like(q) if q.is_contiguous() else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype,
+                                                                            device=q.device)
+
+
 def checkpoint_delta(q):
     """Checkpoint buffer of fwd_delta(..., ckpt=) for bwd_delta."""
-    import torch
-    st, n = linattn_workspace_size(shape_of(q), OP_CHECKPOINT_DELTA)
-    _check(st, "linattn_workspace_size")
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    return _delta_buffer(OP_CHECKPOINT_DELTA, shape_of(q), q.device)
 
 
 def _delta_gates(log_gate, beta, q):
@@ -705,12 +723,13 @@ def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=No
     _same_layout(q, k, v, out)
     gdt = _delta_gates(log_gate, beta, q)
     _states(q, init_state)
-    o = out if out is not None else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    o = out if out is not None else _like(q)
     B, H, T, d = q.shape
     fin = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if want_final else None
+    sh = shape_of(q)
     if ws is None:
-        ws = workspace(q, OP_FWD_DELTA)
-    st = linattn_fwd_delta(shape_of(q), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
+        ws = _delta_buffer(OP_FWD_DELTA, sh, q.device)
+    st = linattn_fwd_delta(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
                            _ptr(init_state), _ptr(fin), _ptr(ckpt), 0 if ckpt is None else ckpt.numel(), _ptr(ws),
                            ws.numel(), _stream(q.device, stream))
     _check(st, "linattn_fwd_delta")
@@ -727,15 +746,17 @@ def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, 
     _states(q, init_state, d_final)
     B, H, T, d = q.shape
     if outs is None:
-        outs = [torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device) for _ in range(3)]
-    dq, dk, dv = outs
-    _same_layout(q, dq, dk, dv)
+        dq, dk, dv = _like(q), _like(q), _like(q)
+    else:
+        dq, dk, dv = outs
+        _same_layout(q, dq, dk, dv)
     dlg = None if log_gate is None else torch.empty_like(log_gate)
     db = torch.empty_like(beta)
     dinit = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if want_dinit else None
+    sh = shape_of(q)
     if ws is None:
-        ws = workspace(q, OP_BWD_DELTA)
-    st = linattn_bwd_delta(shape_of(q), _ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(log_gate), _ptr(beta), gdt,
+        ws = _delta_buffer(OP_BWD_DELTA, sh, q.device)
+    st = linattn_bwd_delta(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(log_gate), _ptr(beta), gdt,
                            _ptr(init_state), _ptr(d_final), _ptr(ckpt), ckpt.numel(), _ptr(dq), _ptr(dk), _ptr(dv),
                            _ptr(dlg), _ptr(db), _ptr(dinit), _ptr(ws), ws.numel(), _stream(q.device, stream))
     _check(st, "linattn_bwd_delta")
@@ -744,11 +765,10 @@ def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, 
 
 def decode_delta(q, k, v, log_gate, beta, state, out=None, stream=None):
     """o of the gated delta rule for T new tokens [B, H, T, d]; `state` [B, H, d, d] fp32 is updated in place."""
-    import torch
     _same_layout(q, k, v, out)
     gdt = _delta_gates(log_gate, beta, q)
     _states(q, state)
-    o = out if out is not None else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    o = out if out is not None else _like(q)
     st = linattn_decode_delta(shape_of(q), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
                               _ptr(state), _stream(q.device, stream))
     _check(st, "linattn_decode_delta")
@@ -798,7 +818,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0,
         raise ValueError("q and the cache must be on one device")
     _int_rows(q, q.shape[0], seq_lens)
     tab, n, stride = _table(q, block_table)
-    o = out if out is not None else torch.empty_strided(q.shape, q.stride(), dtype=q.dtype, device=q.device)
+    o = out if out is not None else _like(q)
     lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if want_lse else None
     if ws is None:
         ws = _paged_workspace(q)
