@@ -152,8 +152,8 @@ __device__ __forceinline__ float load_gate(const void *p, int64_t i, int f32) {
 // One CTA per chunk: the stacked product [K; Q] K^T (lanes 0..63: K K^T, 64..127: Q K^T) on the tensor
 // cores, the unit lower triangular inverse in fp32 on the CUDA cores (two 32 x 32 blocks, then the block
 // below them; products in 4 x 4 tiles, since what bounds the kernel is what it reads from shared memory), and
-// W^T = K^T (T diag(e^g))^T on the tensor cores.  Four CTAs fit an SM and hide each other's latencies: 197 us at
-// B2 H16 T16384, 4.1 TB/s of what it reads and writes.
+// W^T = K^T (T diag(e^g))^T on the tensor cores.  Four CTAs fit an SM and hide each other's latencies: 192 us at
+// B2 H16 T16384, 4.3 TB/s of what it reads and writes.
 constexpr int kPrepThreads = 256;
 constexpr int kLd = 68;  // row stride of the fp32 matrix T: 16-byte rows, spread over the banks
 // The stacked tile [K; Q] (two blocks of 64 columns), then T.  A^T, later the parts of T diag(e^g), take the
@@ -501,10 +501,11 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // for 64 rows, 42 to 51 for 128, whatever the width up to 64), so few wide ones beat many narrow ones.
 //
 // A chunk's path is S -> (W S) -> Y -> (K^T Y) -> S: two products and two passes of the threads, each bounded
-// by its latency: 1.71 us a chunk forward and 1.76 backward with slices of 32 (0.44 and 0.45 ms at B2 H16
-// T16384, on 128 SMs; the other tensor work fits into the gaps).  Every role is a long loop of its own, so their
-// instructions have to be few: with unrolled products and in-line waits two CTAs on neighbouring SMs took 1.5
-// times as long as one alone.  Warps: 1 issues the chain's products, 2 the output's, 0, 3 and the last two load,
+// by its latency: 1.52 us a chunk forward and 1.50 backward with slices of 32 (0.388 and 0.384 ms at B2 H16
+// T16384, on 128 SMs; the other tensor work fits into the gaps).  Next comes what an SM takes in: 104 KB a chunk
+// forward, 9 TB/s over all of them; with a slot less for W the rings run dry (0.49 ms).  Every role is a long
+// loop of its own, so their instructions have to be few: with unrolled products and in-line waits two CTAs on
+// neighbouring SMs took 1.5 times as long as one alone.  Warps: 1 issues the chain's products, 2 the output's, 0, 3 and the last two load,
 // 4 and on (4 VS/16) carry the chain (16 columns each: the threads' work is on the path, so it is spread thin),
 // then 4 make the output (forward) or the scaled dO (backward).
 constexpr int kGateRing = 4, kSideWarps = 4;
@@ -768,8 +769,8 @@ __device__ __forceinline__ void tmem_stf(uint32_t addr, const float (&x)[16]) {
 }
 
 // Tensor memory of the forward chain (columns): S, Y, Q S and P Y, each as the products of both parts.
-// Forward slices are always of 32: with 64, a chunk takes 2.2 times as long (B2 H32 T4096, two turns of slices of
-// 32: 230 us; one turn of slices of 64: 247).
+// Forward slices are always of 32: with 64, a chunk took 2.2 times as long (B2 H32 T4096, one turn of slices of 64
+// against two of slices of 32: 247 us against 230, which are 203 now).
 constexpr int kSlice = 32;
 using kChain = Chain<kSlice>;
 __global__ void __launch_bounds__(kChain::threads, 1)
@@ -1208,8 +1209,8 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 // have lane = dimension; the 64 x 64 ones come from 128-row operands whose other rows are unused: [K; dO]
 // stacked gives K K^T in lanes 0..63 and dO Y^T in lanes 64..127.  Warps 0..15 turn products into operands and
 // results (16 columns each), warp 16 issues the products, warp 17 loads and stores: the next chunk's tiles arrive
-// and its first product runs while the threads are in this one's last step.  Bound by its 224 KB a chunk (0.365 ms
-// at B2 H16 T16384: 5.0 TB/s, 0.74 of copy bandwidth) and the latencies between the five steps: the tiles of one
+// and its first product runs while the threads are in this one's last step.  Bound by its 224 KB a chunk (0.338 ms
+// at B2 H16 T16384: 5.4 TB/s, 0.80 of copy bandwidth) and the latencies between the five steps: the tiles of one
 // chunk fill shared memory, so the loads overlap only the last step.
 //
 // Single bf16 operands except Y in dO Y^T and Y R^T and the matrix A, which have two parts: with one the
@@ -1564,7 +1565,7 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 }
 
 // The reverse chain's slices: of 32 value dimensions while all the chains run at once with one CTA per SM, else
-// of 64 (a chunk takes 1.6 times as long: 182 us at B2 H32 T4096, where slices of 32 would take two turns of 120).
+// of 64 (a chunk takes 1.5 times as long: 153 us at B2 H32 T4096, where slices of 32 would take two turns of 102).
 bool narrow_slices(const Problem &p) { return (int64_t)p.B * p.H * (p.d / 32) <= p.num_sms; }
 int chunks(const Problem &p) { return (p.T + kC - 1) / kC; }
 size_t bhs(const Problem &p) { return (size_t)p.B * p.H; }
