@@ -505,9 +505,9 @@ __global__ void __launch_bounds__(kPrepThreads, 4)
 // T16384, on 128 SMs; the other tensor work fits into the gaps).  Next comes what an SM takes in: 104 KB a chunk
 // forward, 9 TB/s over all of them; with a slot less for W the rings run dry (0.49 ms).  Every role is a long
 // loop of its own, so their instructions have to be few: with unrolled products and in-line waits two CTAs on
-// neighbouring SMs took 1.5 times as long as one alone.  Warps: 1 issues the chain's products, 2 the output's, 0, 3 and the last two load,
-// 4 and on (4 VS/16) carry the chain (16 columns each: the threads' work is on the path, so it is spread thin),
-// then 4 make the output (forward) or the scaled dO (backward).
+// neighbouring SMs took 1.5 times as long as one alone.  Warps: 1 issues the chain's products, 2 the output's, 0, 3
+// and the last two load, 4 and on (4 VS/16) carry the chain (16 columns each: the threads' work is on the path, so
+// it is spread thin), then 4 make the output (forward) or the scaled dO (backward).
 constexpr int kGateRing = 4, kSideWarps = 4;
 template <int VS>
 struct Chain {

@@ -165,7 +165,7 @@ __device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
 // Warps: 0..3 and 4..7 softmax and output of the even and odd tiles, 8 issues the products, 9..12 load.
 // Pages of a multiple of 8 tokens are loaded by tensor-map copies of up to 128 rows (one lane per copy);
 // other pages by 16-byte asynchronous copies of all four warps, which are slower (a warp moves 512 bytes an
-// instruction: 1.07 ms instead of 0.36 at 64 sequences of 16K).  Either way the softmax threads clear the
+// instruction: 1.1 ms instead of 0.37 at 64 sequences of 16K).  Either way the softmax threads clear the
 // value rows of absent tokens: a slot past the length may hold NaN, and 0 x NaN is NaN.
 constexpr int kTcThreads = 416, kLoadWarps = 4;
 template <int D>
