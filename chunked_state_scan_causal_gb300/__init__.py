@@ -667,7 +667,7 @@ def _paged_workspace(q):
         st, n = linattn_workspace_size(shape_of(q), OP_PAGED_DECODE)
         _check(st, "linattn_workspace_size")
         _paged_ws[(q.device, q.shape[-1])] = n
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return q.new_empty(n, dtype=torch.uint8)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -677,10 +677,10 @@ def _delta_bytes(op, B, H, T, d, dtype, device):
     return max(n, 256)
 
 
-def _delta_buffer(op, sh, device):
+def _delta_buffer(op, sh, q):
     """A workspace or checkpoint: its size depends on the shape (and the device) alone, and is asked for once."""
     import torch
-    return torch.empty(_delta_bytes(op, sh.B, sh.H, sh.T, sh.dk, sh.dtype, device), dtype=torch.uint8, device=device)
+    return q.new_empty(_delta_bytes(op, sh.B, sh.H, sh.T, sh.dk, sh.dtype, q.device), dtype=torch.uint8)
 
 
 def _like(q):
@@ -692,7 +692,7 @@ def _like(q):
 
 def checkpoint_delta(q):
     """Checkpoint buffer of fwd_delta(..., ckpt=) for bwd_delta."""
-    return _delta_buffer(OP_CHECKPOINT_DELTA, shape_of(q), q.device)
+    return _delta_buffer(OP_CHECKPOINT_DELTA, shape_of(q), q)
 
 
 def _delta_gates(log_gate, beta, q):
@@ -725,10 +725,10 @@ def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=No
     _states(q, init_state)
     o = out if out is not None else _like(q)
     B, H, T, d = q.shape
-    fin = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if want_final else None
+    fin = q.new_empty((B, H, d, d), dtype=torch.float32) if want_final else None
     sh = shape_of(q)
     if ws is None:
-        ws = _delta_buffer(OP_FWD_DELTA, sh, q.device)
+        ws = _delta_buffer(OP_FWD_DELTA, sh, q)
     st = linattn_fwd_delta(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
                            _ptr(init_state), _ptr(fin), _ptr(ckpt), 0 if ckpt is None else ckpt.numel(), _ptr(ws),
                            ws.numel(), _stream(q.device, stream))
@@ -752,10 +752,10 @@ def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, 
         _same_layout(q, dq, dk, dv)
     dlg = None if log_gate is None else torch.empty_like(log_gate)
     db = torch.empty_like(beta)
-    dinit = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device) if want_dinit else None
+    dinit = q.new_empty((B, H, d, d), dtype=torch.float32) if want_dinit else None
     sh = shape_of(q)
     if ws is None:
-        ws = _delta_buffer(OP_BWD_DELTA, sh, q.device)
+        ws = _delta_buffer(OP_BWD_DELTA, sh, q)
     st = linattn_bwd_delta(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(log_gate), _ptr(beta), gdt,
                            _ptr(init_state), _ptr(d_final), _ptr(ckpt), ckpt.numel(), _ptr(dq), _ptr(dk), _ptr(dv),
                            _ptr(dlg), _ptr(db), _ptr(dinit), _ptr(ws), ws.numel(), _stream(q.device, stream))
@@ -819,7 +819,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0,
     _int_rows(q, q.shape[0], seq_lens)
     tab, n, stride = _table(q, block_table)
     o = out if out is not None else _like(q)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if want_lse else None
+    lse = q.new_empty(q.shape[:3], dtype=torch.float32) if want_lse else None
     if ws is None:
         ws = _paged_workspace(q)
     st = linattn_paged_decode(shape_of(q), shape_of(k_cache), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),

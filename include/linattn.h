@@ -313,7 +313,8 @@ int32_t linattn_decode_delta(const linattn_shape *shape, const void *q, const vo
  * all T; larger values are taken as T, negative ones as 0).  Positions outside the table
  * and page ids outside the cache are not written; device_status (int32 device, 16-byte
  * aligned, or NULL) is zeroed and then receives LINATTN_ERR_INVALID if there were any.
- * Two tokens of one call with the same slot leave one of them.  Returns a status. */
+ * Two tokens of one call with the same slot leave any mixture of their rows there.
+ * Returns a status. */
 int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape *cache_shape, const void *k,
                              const void *v, void *k_cache, void *v_cache, const int32_t *block_table,
                              int32_t max_blocks, int64_t table_stride, const int32_t *start,
