@@ -683,6 +683,14 @@ def _delta_buffer(op, sh, q):
     return q.new_empty(_delta_bytes(op, sh.B, sh.H, sh.T, sh.dk, sh.dtype, q.device), dtype=torch.uint8)
 
 
+def _under(stream, f, *args):
+    """f with `stream` the current one, so that what it allocates belongs to that stream too (memory of another
+    stream could be handed out again while the call still runs)."""
+    import torch
+    with torch.cuda.stream(stream):
+        return f(*args)
+
+
 def _like(q):
     """An output with q's layout."""
     import torch
@@ -719,6 +727,8 @@ def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=No
     """(o, final_state or None) of the gated delta rule: S_t = S' + beta_t k_t (v_t - S'^T k_t)^T with
     S' = exp(log_gate_t) S_{t-1}, o_t = S_t^T q_t (log_gate None: no decay; log_gate and beta [B, H, T],
     both fp32 or both bf16).  With ``ckpt`` (from checkpoint_delta) what bwd_delta needs is kept."""
+    if stream is not None:
+        return _under(stream, fwd_delta, q, k, v, log_gate, beta, init_state, want_final, out, ws, None, ckpt)
     import torch
     _same_layout(q, k, v, out)
     gdt = _delta_gates(log_gate, beta, q)
@@ -731,7 +741,7 @@ def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=No
         ws = _delta_buffer(OP_FWD_DELTA, sh, q)
     st = linattn_fwd_delta(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
                            _ptr(init_state), _ptr(fin), _ptr(ckpt), 0 if ckpt is None else ckpt.numel(), _ptr(ws),
-                           ws.numel(), _stream(q.device, stream))
+                           ws.numel(), _stream(q.device))
     _check(st, "linattn_fwd_delta")
     return o, fin
 
@@ -740,6 +750,8 @@ def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, 
               stream=None):
     """(dq, dk, dv, d_log_gate or None, d_beta, d_init or None) of fwd_delta for the upstream gradient dO
     (the gates' gradients in the gates' type)."""
+    if stream is not None:
+        return _under(stream, bwd_delta, q, k, v, dO, log_gate, beta, ckpt, init_state, d_final, want_dinit, outs, ws)
     import torch
     _same_layout(q, k, v, dO)
     gdt = _delta_gates(log_gate, beta, q)
@@ -758,19 +770,21 @@ def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, 
         ws = _delta_buffer(OP_BWD_DELTA, sh, q)
     st = linattn_bwd_delta(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(dO), _ptr(log_gate), _ptr(beta), gdt,
                            _ptr(init_state), _ptr(d_final), _ptr(ckpt), ckpt.numel(), _ptr(dq), _ptr(dk), _ptr(dv),
-                           _ptr(dlg), _ptr(db), _ptr(dinit), _ptr(ws), ws.numel(), _stream(q.device, stream))
+                           _ptr(dlg), _ptr(db), _ptr(dinit), _ptr(ws), ws.numel(), _stream(q.device))
     _check(st, "linattn_bwd_delta")
     return dq, dk, dv, dlg, db, dinit
 
 
 def decode_delta(q, k, v, log_gate, beta, state, out=None, stream=None):
     """o of the gated delta rule for T new tokens [B, H, T, d]; `state` [B, H, d, d] fp32 is updated in place."""
+    if stream is not None:
+        return _under(stream, decode_delta, q, k, v, log_gate, beta, state, out)
     _same_layout(q, k, v, out)
     gdt = _delta_gates(log_gate, beta, q)
     _states(q, state)
     o = out if out is not None else _like(q)
     st = linattn_decode_delta(shape_of(q), _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
-                              _ptr(state), _stream(q.device, stream))
+                              _ptr(state), _stream(q.device))
     _check(st, "linattn_decode_delta")
     return o
 
@@ -796,6 +810,8 @@ def paged_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, devi
     """Writes new tokens k, v [B, Hkv, T, d] into a paged cache [pages, Hkv, page, d] (any strides): token t of
     sequence b at position start[b] + t, in page block_table[b, position // page].  new_lens [B]: only the first
     new_lens[b] tokens of a padded batch.  device_status: int32 tensor for LINATTN_ERR_INVALID (bad pages)."""
+    if stream is not None:
+        return _under(stream, paged_append, k, v, k_cache, v_cache, block_table, start, new_lens, device_status)
     _same_layout(k, v)
     _same_layout(k_cache, v_cache)
     if k_cache.device != k.device:
@@ -803,7 +819,7 @@ def paged_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, devi
     _int_rows(k, k.shape[0], start, new_lens)
     tab, n, stride = _table(k, block_table)
     st = linattn_paged_append(shape_of(k), shape_of(k_cache), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), tab, n,
-                              stride, _ptr(start), _ptr(new_lens), _ptr(device_status), _stream(k.device, stream))
+                              stride, _ptr(start), _ptr(new_lens), _ptr(device_status), _stream(k.device))
     _check(st, "linattn_paged_append")
 
 
@@ -811,6 +827,8 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0,
                  ws=None, stream=None):
     """(o, lse or None): softmax attention of one new token per sequence, q [B, Hq, 1, d], over the first
     seq_lens[b] tokens of its pages (scale 0 means 1/sqrt(d); lse [B, Hq, 1] fp32)."""
+    if stream is not None:
+        return _under(stream, paged_decode, q, k_cache, v_cache, block_table, seq_lens, scale, want_lse, out, ws)
     import torch
     _same_layout(q, out)
     _same_layout(k_cache, v_cache)
@@ -824,7 +842,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0,
         ws = _paged_workspace(q)
     st = linattn_paged_decode(shape_of(q), shape_of(k_cache), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(o),
                               _ptr(lse), tab, n, stride, _ptr(seq_lens), scale, _ptr(ws), ws.numel(),
-                              _stream(q.device, stream))
+                              _stream(q.device))
     _check(st, "linattn_paged_decode")
     return o, lse
 

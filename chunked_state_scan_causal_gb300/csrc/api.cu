@@ -795,7 +795,7 @@ int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void 
   if (p.T == 0) {
     if ((st = device_ok())) return st;
     if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
-    if (!final_state) return LINATTN_OK;
+    if (!final_state || final_state == init_state) return LINATTN_OK;
     const size_t bytes = (size_t)p.B * p.H * p.d * p.d * sizeof(float);
     return cuda_status(init_state ? cudaMemcpyAsync(final_state, init_state, bytes, cudaMemcpyDeviceToDevice, s)
                                   : cudaMemsetAsync(final_state, 0, bytes, s));
@@ -824,7 +824,7 @@ int32_t linattn_bwd_delta(const linattn_shape *shape, const void *q, const void 
   if (p.T == 0) {
     if ((st = device_ok())) return st;
     if (clear_header(workspace, kHeader, s) != cudaSuccess) return LINATTN_ERR_CUDA;
-    if (!d_init_state) return LINATTN_OK;
+    if (!d_init_state || d_init_state == d_final_state) return LINATTN_OK;
     const size_t bytes = (size_t)p.B * p.H * p.d * p.d * sizeof(float);
     return cuda_status(d_final_state
                            ? cudaMemcpyAsync(d_init_state, d_final_state, bytes, cudaMemcpyDeviceToDevice, s)

@@ -271,8 +271,9 @@ int32_t linattn_decode(const linattn_shape *shape, const void *q, const void *k,
  *   checkpoint  LINATTN_OP_CHECKPOINT_DELTA bytes, 256-byte aligned, filled for
  *               linattn_bwd_delta; or NULL (inference)
  *   workspace   LINATTN_OP_FWD_DELTA bytes
- * T == 0: final_state is init_state (or zeros).  Returns a status
- * (LINATTN_ERR_INVALID for a misaligned or short checkpoint). */
+ * Outputs overlap no input, but final_state may be init_state itself.  T == 0:
+ * final_state is init_state (or zeros).  Returns a status (LINATTN_ERR_INVALID for a
+ * misaligned or short checkpoint). */
 int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void *k, const void *v,
                           const void *log_gate, const void *beta, int32_t gate_dtype, void *o,
                           const float *init_state, float *final_state, void *checkpoint, size_t checkpoint_bytes,
@@ -287,6 +288,7 @@ int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void 
  *   R_{t-1} = exp(log_gate_t) (R_t - k_t dy_t^T) + q_{t-1} dO_{t-1}^T,
  * d_init_state ([B,H,dk,dv] fp32, or NULL) the gradient at the initial state.
  * d_log_gate (NULL exactly when log_gate is) and d_beta [B,H,T] have gate_dtype.
+ * Outputs overlap no input, but d_init_state may be d_final_state itself.
  * Workspace: LINATTN_OP_BWD_DELTA bytes.  Returns a status. */
 int32_t linattn_bwd_delta(const linattn_shape *shape, const void *q, const void *k, const void *v, const void *dO,
                           const void *log_gate, const void *beta, int32_t gate_dtype, const float *init_state,

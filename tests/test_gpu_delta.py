@@ -268,3 +268,66 @@ def test_offsets_past_32_bits():
             assert torch.equal(a, b[:, :, part])
         D = got[5]
     assert torch.equal(D, grads[5])
+
+
+def test_two_graphs_one_workspace():
+    """Two captured steps of different shapes that share one workspace and checkpoint, replayed in turn."""
+    steps = []
+    for B, H, T in ((1, 3, 200), (2, 2, 129)):
+        g = torch.Generator(device="cuda").manual_seed(T)
+        rn = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        k = torch.nn.functional.normalize(rn(B, H, T, 128), dim=-1).bfloat16()
+        q, v, dO = ((rn(B, H, T, 128) * s).bfloat16() for s in (0.1, 1.0, 1.0))
+        beta, lg = torch.rand(B, H, T, generator=g, device="cuda"), -torch.rand(B, H, T, generator=g, device="cuda")
+        steps.append((q, k, v, dO, lg, beta))
+    sizes = [max(f(s[0]).numel() for s in steps) for f in (
+        la.checkpoint_delta, lambda q: la.workspace(q, la.OP_FWD_DELTA), lambda q: la.workspace(q, la.OP_BWD_DELTA))]
+    ck, w1, w2 = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes)
+
+    def step(s):
+        o, fin = la.fwd_delta(*s[:3], *s[4:], want_final=True, ckpt=ck, ws=w1)
+        return (o, fin, *la.bwd_delta(*s, ck, ws=w2, want_dinit=True))
+
+    want = [[t.clone() for t in step(s)] for s in steps]
+    graphs, got = [], []
+    for s in steps:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(step(s))
+    for i in (0, 1, 1, 0, 1):
+        for t in got[i]:
+            t.fill_(7)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got[i], want[i]):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_named_stream(dtype):
+    """stream=: workspaces and outputs that a call allocates are not handed out again while it still runs."""
+    c = {n: x.cuda() for n, x in case(41, 2, 4, 300, 128, dtype).items()}
+    seq, gates = (c["q"], c["k"], c["v"]), (c["lg"], c["beta"])
+    state = c["init"].clone()
+
+    def steps(**kw):
+        ck = la.checkpoint_delta(c["q"])
+        o, fin = la.fwd_delta(*seq, *gates, init_state=c["init"], want_final=True, ckpt=ck, **kw)
+        grads = la.bwd_delta(*seq, c["dO"], *gates, ck, init_state=c["init"], d_final=c["D"], want_dinit=True, **kw)
+        one = [x[:, :, :1] for x in seq] + [x[:, :, :1].contiguous() for x in gates]
+        return (o, fin, *grads, la.decode_delta(*one, state, **kw)), ck, one
+
+    want, _, _ = steps()
+    state.copy_(c["init"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200000)
+    got, *keep = steps(stream=side)
+    sizes = {la.workspace(c["q"], op).numel() for op in (la.OP_FWD_DELTA, la.OP_BWD_DELTA)}
+    for _ in range(200):
+        for n in sizes:
+            torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)

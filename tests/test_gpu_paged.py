@@ -244,3 +244,35 @@ def test_offsets_past_32_bits(dtype):
     o, lse = la.paged_decode(q.cuda(), kc, vc, far.cuda(), lens.cuda(), want_lse=True)
     ro, rl = paged_attention(q, sk, sv, small, lens)
     assert rel(o, ro) < TOL[dtype] and float((lse.cpu().double() - rl).abs().max()) < 6.3e-5
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_shared_pages(dtype):
+    """Sequences with a common prefix of pages, and a page twice in one sequence."""
+    q, kc, vc, table, lens = case(13, [300, 290, 64, 7], 8, 2, 128, 32, dtype, poison=False)
+    table[1, :6], table[2, 1], table[3] = table[0, :6], table[2, 0], table[0]
+    check((q, kc, vc, table, lens))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_named_stream(dtype):
+    """stream=: the workspace that a call allocates is not handed out again while it still runs."""
+    c = [t.cuda() for t in case(14, [5000, 300], 8, 2, 128, 64, dtype, poison=False)]
+    k = c[1][0, :, :1][None].expand(2, -1, -1, -1).contiguous()
+    side = torch.cuda.Stream()
+
+    def step(**kw):
+        la.paged_append(k, k, c[1], c[2], c[3], c[4] - 1, **kw)
+        return la.paged_decode(*c, want_lse=True, **kw)
+
+    want, last = step(), c[4] - 1
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200000)
+    la.paged_append(k, k, c[1], c[2], c[3], last, stream=side)
+    got = la.paged_decode(*c, want_lse=True, stream=side)
+    n = la.workspace(c[0], la.OP_PAGED_DECODE).numel()
+    for _ in range(200):
+        torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
