@@ -293,8 +293,8 @@ __global__ void __launch_bounds__(256) delta_walk_sums(int64_t tokens, int64_t c
   }
 }
 
-// d_log_gate: the sums of G from every token to its chunk's end, plus the chunk's anchor.
-// One warp per chunk of 64 tokens.
+// d_log_gate: the sums of G from every token to its chunk's end, plus the chunk's anchor.  One warp per chunk
+// of 64 tokens; bound by its launch (4 us at B2 H16 T4096).
 __global__ void delta_gate_grad(int64_t BH, int T, int N, const float *gx, const float *anchor, void *dlg, int f32) {
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
   const int lane = threadIdx.x % 32;
@@ -317,14 +317,16 @@ __global__ void delta_gate_grad(int64_t BH, int T, int N, const float *gx, const
 // As the library's linear decode: CS CTAs of 8 warps per sequence, each owning D/CS columns of the
 // state in registers.  Both column reductions run on the state before the update,
 //     y = v - a S^T k,   u = b y,   o = a S^T q + (q . k) u,   S <- a S + k u^T,
-// so a token takes one reduction across the warps.  Bound by the state's read and write
-// (2 x 64 KiB per head at d = 128).
+// so a token takes one reduction across the warps.  Bound by the state's read and write (2 x 64 KiB per head at
+// d = 128): 157 us at B512 H16, 1.01 of copy bandwidth, with 8-byte accesses marked as passing through (168 us with
+// single floats, 163 without the marks).
 constexpr int kDecThreads = 256;
 
 template <int D, int CS, typename T>
 __global__ void __launch_bounds__(kDecThreads) delta_decode_kernel(Problem p, DeltaGates g, const T *q, const T *k,
                                                                    const T *v, T *o, float *state) {
   constexpr int W = D / CS, NC = W / 32, NR = D / 8;
+  static_assert(NC == 2, "a lane's columns are one float2");
   __shared__ float kk[D], qq[D], pk[8][W], pq[8][W], uu[W], dots[8];
   const int bh = blockIdx.x, b = bh / p.H, h = bh % p.H, c0 = blockIdx.y * W;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -332,9 +334,11 @@ __global__ void __launch_bounds__(kDecThreads) delta_decode_kernel(Problem p, De
   float *base = state + (int64_t)bh * D * D + c0 + NC * lane;
   float s[NR][NC];
 #pragma unroll
-  for (int i = 0; i < NR; ++i)
-#pragma unroll
-    for (int c = 0; c < NC; ++c) s[i][c] = base[(warp + 8 * i) * D + c];
+  for (int i = 0; i < NR; ++i) {
+    const float2 x = __ldcs(reinterpret_cast<const float2 *>(base + (warp + 8 * i) * D));
+    s[i][0] = x.x;
+    s[i][1] = x.y;
+  }
   for (int t = 0; t < p.T; ++t) {
     const int64_t row = off + (int64_t)t * p.st;
     const float a = g.lg ? expf(ld_gate(g.lg, gb + t, g.f32)) : 1.f, be = ld_gate(g.beta, gb + t, g.f32);
@@ -390,8 +394,7 @@ __global__ void __launch_bounds__(kDecThreads) delta_decode_kernel(Problem p, De
   }
 #pragma unroll
   for (int i = 0; i < NR; ++i)
-#pragma unroll
-    for (int c = 0; c < NC; ++c) base[(warp + 8 * i) * D + c] = s[i][c];
+    __stcs(reinterpret_cast<float2 *>(base + (warp + 8 * i) * D), make_float2(s[i][0], s[i][1]));
 }
 
 template <int D, typename T>
