@@ -51,6 +51,11 @@ __global__ void __launch_bounds__(256) paged_append_kernel(PagedProblem p, const
 // holds a whole item writes its output; the pieces of the other items go to the workspace, at most
 // two per CTA (its first and its last item), and paged_join_kernel joins them.
 constexpr int kTile = 128;
+// What is not a number in the cache or in q reaches the rows that read it, as in the formula.  Maxima are taken with
+// fmaxf, which drops NaN, over scores of at least kLowest where a token is there and -inf where none is: so a maximum
+// of -inf says that no token is there (o = 0), and from any other one a NaN score gets a NaN weight and a score of
+// -inf a weight of zero (0 / 0, NaN, if every weight is).
+constexpr float kLowest = -3.402823466e+38f;
 
 __device__ __forceinline__ int seq_len(const PagedProblem &p, int b) {
   const int64_t cap = (int64_t)p.max_blocks * p.page;
@@ -444,7 +449,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_before();
         float x[HN], y[HN];
 #pragma unroll
-        for (int h = 0; h < HN; ++h) y[h] = x[h] = valid ? __uint_as_float(r[h]) * c : -INFINITY;
+        for (int h = 0; h < HN; ++h) {
+          x[h] = valid ? __uint_as_float(r[h]) * c : -INFINITY;
+          y[h] = valid ? fmaxf(x[h], kLowest) : -INFINITY;
+        }
         reduce(y, [](float u, float v) { return fmaxf(u, v); });
         named_bar_sync(1 + gr, 128);
         bool move = false;
@@ -454,7 +462,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float4 v = *reinterpret_cast<const float4 *>(s_red[gr][h]);
           const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
           f[h] = 1.f;
-          if (mx > m[h] + 8.f) {  // (also the first finite score: m is -inf)
+          if (mx > m[h] + 8.f) {  // (also the first token: m is -inf)
             f[h] = ex2(m[h] - mx);
             m[h] = mx;
             move = true;
@@ -546,7 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float acc = (last >= 0 ? f0 * __uint_as_float(a[h]) : 0.f) + ((int)lt < D ? f1 * X[h * D + lt] : 0.f);
           if (whole) {
             if ((int)lt < D)
-              o[w.b * p.qsb + (w.it.h0 + h) * p.qsh + lt] = __float2bfloat16_rn(sum > 0.f ? acc / sum : 0.f);
+              o[w.b * p.qsb + (w.it.h0 + h) * p.qsh + lt] = __float2bfloat16_rn(mx == -INFINITY ? 0.f : acc / sum);
             if (lse && lt == 0) lse[(int64_t)w.b * p.Hq + w.it.h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
           } else {
             if ((int)lt < D) part[(at + h) * D + lt] = acc;
@@ -701,9 +709,10 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm)
       halve_heads<HN / 2, LPT / 2>(s, lane);
 #pragma unroll
       for (int x = LPT / HN / 2; x; x /= 2) s[0] += __shfl_xor_sync(0xffffffffu, s[0], x);
-      const float score = (ok >> (i % S)) & 1 ? s[0] : -INFINITY;
-      if (__any_sync(0xffffffffu, score > m)) {  // rare once the first steps have passed
-        const float mn = fmaxf(m, score), f = exp2f(m - (mn == -INFINITY ? 0.f : mn));
+      const bool there = (ok >> (i % S)) & 1;
+      const float score = there ? s[0] : -INFINITY, top = there ? fmaxf(score, kLowest) : -INFINITY;
+      if (__any_sync(0xffffffffu, top > m)) {  // rare once the first steps have passed
+        const float mn = fmaxf(m, top), f = exp2f(m - (mn == -INFINITY ? 0.f : mn));
         m = mn;
         l *= f;
         rescale(f);
@@ -767,7 +776,7 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm)
       }
       const int64_t piece = (int64_t)(2 * g + slot) * kHeads + h;
       if (whole) {
-        o[b * p.qsb + (it.h0 + h) * p.qsh + dim] = sum > 0.f ? a / sum : 0.f;
+        o[b * p.qsb + (it.h0 + h) * p.qsh + dim] = mx == -INFINITY ? 0.f : a / sum;
         if (lse && dim == 0) lse[(int64_t)b * p.Hq + it.h0 + h] = (mx + log2f(sum)) * 0.6931471805599453f;
       } else {
         part[piece * D + dim] = a;
@@ -851,7 +860,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(PagedProblem p, int grid,
     a = fmaf(f, part[at(g) * D + tid], a);
     l = fmaf(f, s_f[2 * (g - g0) + 1], l);
   }
-  o[orow] = (T)(l > 0.f ? a / l : 0.f);
+  o[orow] = (T)(m == -INFINITY ? 0.f : a / l);
   if (lse && tid == 0) lse[(int64_t)b * p.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
