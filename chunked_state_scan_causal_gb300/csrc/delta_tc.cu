@@ -1240,7 +1240,9 @@ __global__ void __launch_bounds__(kGradThreads, 1)
   __shared__ uint64_t bar[G_COUNT];
   __shared__ uint32_t tslot;
   __shared__ int abort_flag;
-  __shared__ float s_col[2][kC], s_x[4][kC], s_rs[kGradWarps], s_kw[kGradWarps], s_last;
+  // (s_rs twice, by the chunk's parity: the next chunk's sums may be written while one thread still adds these up.
+  // The others are written behind products that wait for every warp's arrival in the next chunk.)
+  __shared__ float s_col[2][kC], s_x[4][kC], s_rs[2][kGradWarps], s_kw[kGradWarps], s_last;
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
   if (tid == 0) {
@@ -1408,7 +1410,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
         }
 #pragma unroll
         for (int o = 16; o; o /= 2) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) s_rs[warp] = 32 * (int)cg < P.d ? dot : 0.f;
+        if (lane == 0) s_rs[x & 1][warp] = 32 * (int)cg < P.d ? dot : 0.f;
       }
       // this lane's four columns
       float be[4], jh[4], jl[4];
@@ -1540,7 +1542,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
       } else if (tid == kC) {
         float rs = 0.f, kws = 0.f;
         for (int y = 0; y < kGradWarps; ++y) {
-          rs += s_rs[y];
+          rs += s_rs[x & 1][y];
           kws += s_kw[y];
         }
         P.anchor[(int64_t)bh * P.N + c] = fmaf(s_last, rs, kws);
