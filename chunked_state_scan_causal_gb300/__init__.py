@@ -803,7 +803,10 @@ def _table(q, block_table):
             or block_table.stride(1) != 1 or block_table.device != q.device:
         raise ValueError("block_table must be int32 [B, max_blocks] with contiguous rows on the cache's device")
     n = block_table.shape[1]
-    return _ptr(block_table), n, max(n, block_table.stride(0)) if block_table.shape[0] > 1 else n
+    stride = block_table.stride(0) if block_table.shape[0] > 1 else n
+    if stride < n:  # (one row expanded over the batch, say: its storage does not hold B rows)
+        raise ValueError("block_table's rows must not overlap")
+    return _ptr(block_table), n, stride
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, device_status=None, stream=None):

@@ -185,3 +185,18 @@ def test_paged_reference_skips_bad_pages():
     K = torch.cat((kc[2, 0], kc[0, 0, :2])).double()
     x = (q[0, :, 0].double() @ K.T) * 8 ** -0.5
     assert torch.allclose(o[0, :, 0], torch.softmax(x, -1) @ K) and torch.allclose(lse[0, :, 0], torch.logsumexp(x, -1))
+
+
+def test_overlapping_table_rows():
+    """A row expanded over the batch (stride 0) or rows that overlap are refused, not read as if they were apart; one
+    sequence may have any row stride, and rows may be further apart than they are long."""
+    q, kc = torch.zeros(2, 2, 1, 64), torch.zeros(4, 2, 16, 64)
+    n, flat = torch.zeros(2, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    for tab in (flat[:3].expand(2, 3), flat.as_strided((2, 3), (2, 1)), flat[:1].expand(2, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            la.paged_decode(q, kc, kc, tab, n)
+        with pytest.raises(ValueError, match="overlap"):
+            la.paged_append(q, q, kc, kc, tab, n)
+    assert la._table(q, flat.as_strided((2, 3), (5, 1)))[1:] == (3, 5)
+    assert la._table(q, flat.view(2, 4))[1:] == (4, 4)
+    assert la._table(q[:1], flat.as_strided((1, 3), (0, 1)))[1:] == (3, 3)
