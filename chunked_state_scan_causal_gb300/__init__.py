@@ -815,11 +815,15 @@ def paged_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, devi
     new_lens[b] tokens of a padded batch.  device_status: int32 tensor for LINATTN_ERR_INVALID (bad pages)."""
     if stream is not None:
         return _under(stream, paged_append, k, v, k_cache, v_cache, block_table, start, new_lens, device_status)
+    import torch
     _same_layout(k, v)
     _same_layout(k_cache, v_cache)
     if k_cache.device != k.device:
         raise ValueError("the new tokens and the cache must be on one device")
     _int_rows(k, k.shape[0], start, new_lens)
+    if device_status is not None and (device_status.dtype != torch.int32 or device_status.numel() < 1
+                                      or device_status.device != k.device):
+        raise ValueError("device_status must be an int32 tensor on the cache's device")
     tab, n, stride = _table(k, block_table)
     st = linattn_paged_append(shape_of(k), shape_of(k_cache), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), tab, n,
                               stride, _ptr(start), _ptr(new_lens), _ptr(device_status), _stream(k.device))

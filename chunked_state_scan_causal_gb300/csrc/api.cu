@@ -140,6 +140,13 @@ static int check_ptrs(std::initializer_list<const void *> required, std::initial
   return LINATTN_OK;
 }
 
+// 32-bit values (lengths, positions, page ids, lse, a status word); null is for the caller to judge
+static int check_ptrs32(std::initializer_list<const void *> xs) {
+  for (const void *x : xs)
+    if (reinterpret_cast<uintptr_t>(x) & 3u) return LINATTN_ERR_ALIGN;
+  return LINATTN_OK;
+}
+
 static int cuda_status(cudaError_t e) { return e == cudaSuccess ? LINATTN_OK : LINATTN_ERR_CUDA; }
 
 // ------------------------------------------------------------------ workspace layout
@@ -896,6 +903,7 @@ int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape
   if (x.T == 0) return LINATTN_OK;
   if ((st = check_ptrs({k, v, k_cache, v_cache}, {}))) return st;
   if (!start) return LINATTN_ERR_INVALID;
+  if ((st = check_ptrs32({block_table, start, new_lens, device_status}))) return st;
   if ((int64_t)x.B * x.H * x.T > 0x7fffffff) return LINATTN_ERR_UNSUPPORTED;  // rows are 32-bit
   if ((st = device_ok())) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -916,6 +924,7 @@ int32_t linattn_paged_decode(const linattn_shape *q_shape, const linattn_shape *
   if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale)) return LINATTN_ERR_INVALID;
   if ((st = check_ptrs({q, k_cache, v_cache, o}, {}))) return st;
   if (!seq_lens) return LINATTN_ERR_INVALID;
+  if ((st = check_ptrs32({block_table, seq_lens, lse}))) return st;
   if ((st = check_ws(workspace, workspace_bytes, kHeader + paged_decode_ws_bytes(x.d, x.num_sms)))) return st;
   if ((st = device_ok())) return st;
   p.Hq = x.H;

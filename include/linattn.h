@@ -308,13 +308,14 @@ int32_t linattn_decode_delta(const linattn_shape *shape, const void *q, const vo
  * element strides of k_cache and v_cache (so [pages, H, page, d] and [pages, page, H,
  * d] orders both fit).  Token n of sequence b sits in page block_table[b][n / page],
  * slot n % page; block_table is int32 device memory, rows table_stride >= max_blocks
- * apart.  max_blocks * page must stay below 2^31 - 256.
+ * apart.  max_blocks * page must stay below 2^31 - 256.  32-bit arrays (tables, lengths,
+ * positions, lse, status words) are 4-byte aligned (LINATTN_ERR_ALIGN otherwise).
  *
  * linattn_paged_append copies new tokens k, v ([B, H, T, d] of new_shape, the cache's
  * type) to positions start[b] .. start[b] + new_lens[b] - 1 (int32 device; new_lens NULL:
  * all T; larger values are taken as T, negative ones as 0).  Positions outside the table
- * and page ids outside the cache are not written; device_status (int32 device, 16-byte
- * aligned, or NULL) is zeroed and then receives LINATTN_ERR_INVALID if there were any.
+ * and page ids outside the cache are not written; device_status (int32 device or NULL)
+ * is zeroed and then receives LINATTN_ERR_INVALID if there were any.
  * Two tokens of one call with the same slot leave any mixture of their rows there.
  * Returns a status. */
 int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape *cache_shape, const void *k,

@@ -200,3 +200,26 @@ def test_overlapping_table_rows():
     assert la._table(q, flat.as_strided((2, 3), (5, 1)))[1:] == (3, 5)
     assert la._table(q, flat.view(2, 4))[1:] == (4, 4)
     assert la._table(q[:1], flat.as_strided((1, 3), (0, 1)))[1:] == (3, 3)
+
+
+def test_words_of_32_bits():
+    """A status word, lengths, positions, page ids and lse off a 4-byte boundary are refused (a kernel would read or
+    write them whole); so is a status tensor that is not int32 or is empty."""
+    new = _shape(T=3, stride_b=2 * 3 * 128, stride_h=3 * 128)
+    q = _shape(H=8, T=1, stride_b=8 * 128, stride_h=128)
+    _, need = la.linattn_workspace_size(q, la.OP_PAGED_DECODE)
+    for off in (1, 2, 3):
+        for i in range(4):
+            tab, start, lens, status = (FAKE + (off if i == j else 0) for j in range(4))
+            assert la.linattn_paged_append(new, _cache(), FAKE, FAKE, FAKE, FAKE, tab, 4, 4, start, lens, status,
+                                           None) == la.ERR_ALIGN
+        for i in range(3):
+            tab, lens, lse = (FAKE + (off if i == j else 0) for j in range(3))
+            assert la.linattn_paged_decode(q, _cache(), FAKE, FAKE, FAKE, FAKE, lse, tab, 4, 4, lens, 0.0, FAKE, need,
+                                           None) == la.ERR_ALIGN
+    x, kc = torch.zeros(1, 2, 1, 64), torch.zeros(4, 2, 16, 64)
+    tab, n = torch.zeros(1, 3, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for status in (torch.zeros(1, dtype=torch.int8), torch.zeros(1), torch.zeros(0, dtype=torch.int32),
+                   torch.zeros(1, dtype=torch.int32, device="meta")):
+        with pytest.raises(ValueError, match="device_status"):
+            la.paged_append(x, x, kc, kc, tab, n, device_status=status)
