@@ -900,13 +900,18 @@ int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape
   int st = paged_checks(new_shape, cache_shape, block_table, max_blocks, table_stride, &x, &p);
   if (st) return st;
   if (x.H != p.Hkv) return LINATTN_ERR_INVALID;
-  if (x.T == 0) return LINATTN_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (x.T == 0) {
+    if (!device_status) return LINATTN_OK;
+    if ((st = check_ptrs32({device_status}))) return st;
+    if ((st = device_ok())) return st;
+    return cuda_status(clear_header(device_status, 4, s));
+  }
   if ((st = check_ptrs({k, v, k_cache, v_cache}, {}))) return st;
   if (!start) return LINATTN_ERR_INVALID;
   if ((st = check_ptrs32({block_table, start, new_lens, device_status}))) return st;
   if ((int64_t)x.B * x.H * x.T > 0x7fffffff) return LINATTN_ERR_UNSUPPORTED;  // rows are 32-bit
   if ((st = device_ok())) return st;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (device_status && clear_header(device_status, 4, s) != cudaSuccess) return LINATTN_ERR_CUDA;
   return cuda_status(paged_append(p, k, v, k_cache, v_cache, x.T, x.sb, x.sh, x.st, start, new_lens, device_status, s));
 }

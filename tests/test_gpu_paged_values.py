@@ -227,3 +227,17 @@ def test_two_layers_agree():
                             torch.tensor([T], dtype=torch.int32, device="cuda"))
     assert torch.equal(o1.isnan(), o2.isnan()) and o2[0, 1].isnan().all() and not o2[0, 0].isnan().any()
     assert math.isfinite(float(o2[0, 0].float().norm()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_append_status_is_this_call_s(dtype):
+    """The status word tells of this call alone, also when the call has no tokens."""
+    kc, vc = (torch.zeros(3, 2, 16, 64, dtype=dtype, device="cuda") for _ in range(2))
+    k = torch.ones(1, 2, 4, 64, dtype=dtype, device="cuda")
+    bad, good = (torch.tensor([[i]], dtype=torch.int32, device="cuda") for i in (9, 1))
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    status = torch.full((3,), 5, dtype=torch.int32, device="cuda")[1:2]   # a word of its own, 4-byte aligned
+    for table, T, want in ((bad, 4, la.ERR_INVALID), (bad, 0, la.OK), (bad, 1, la.ERR_INVALID), (good, 1, la.OK)):
+        la.paged_append(k[:, :, :T], k[:, :, :T], kc, vc, table, zero, device_status=status)
+        assert int(status) == want, (T, int(status))
+    assert (kc[1, :, 0] == 1).all() and int((kc != 0).sum()) == 2 * 64
