@@ -738,7 +738,8 @@ def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=No
     fin = q.new_empty((B, H, d, d), dtype=torch.float32) if want_final else None
     sh = shape_of(q)
     if ws is None:
-        ws = _delta_buffer(OP_FWD_DELTA, sh, q)
+        # (with a checkpoint only its status word is used)
+        ws = _delta_buffer(OP_FWD_DELTA, sh, q) if ckpt is None else q.new_empty(256, dtype=torch.uint8)
     st = linattn_fwd_delta(sh, _ptr(q), _ptr(k), _ptr(v), _ptr(log_gate), _ptr(beta), gdt, _ptr(o),
                            _ptr(init_state), _ptr(fin), _ptr(ckpt), 0 if ckpt is None else ckpt.numel(), _ptr(ws),
                            ws.numel(), _stream(q.device))

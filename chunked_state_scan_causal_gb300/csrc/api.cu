@@ -795,7 +795,8 @@ int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void 
   int st = delta_checks(shape, &p, gate_dtype);
   if (st) return st;
   if ((st = check_ptrs({}, {init_state, final_state}))) return st;
-  if ((st = check_ws(workspace, workspace_bytes, delta_fwd_ws_bytes(p)))) return st;
+  // the chunks' records go to the checkpoint when there is one
+  if ((st = check_ws(workspace, workspace_bytes, checkpoint ? kHeader : delta_fwd_ws_bytes(p)))) return st;
   if (checkpoint && ((reinterpret_cast<uintptr_t>(checkpoint) & 255u) || checkpoint_bytes < delta_ckpt_bytes(p)))
     return LINATTN_ERR_INVALID;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

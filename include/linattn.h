@@ -270,7 +270,8 @@ int32_t linattn_decode(const linattn_shape *shape, const void *q, const void *k,
  *   init_state  [B,H,dk,dv] fp32 or NULL (zeros); final_state the same or NULL
  *   checkpoint  LINATTN_OP_CHECKPOINT_DELTA bytes, 256-byte aligned, filled for
  *               linattn_bwd_delta; or NULL (inference)
- *   workspace   LINATTN_OP_FWD_DELTA bytes
+ *   workspace   LINATTN_OP_FWD_DELTA bytes; with a checkpoint, which then holds the
+ *               intermediate values, 256 are enough
  * Outputs overlap no input, but final_state may be init_state itself.  T == 0:
  * final_state is init_state (or zeros).  Returns a status (LINATTN_ERR_INVALID for a
  * misaligned or short checkpoint). */

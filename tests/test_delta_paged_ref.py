@@ -223,3 +223,14 @@ def test_words_of_32_bits():
                    torch.zeros(1, dtype=torch.int32, device="meta")):
         with pytest.raises(ValueError, match="device_status"):
             la.paged_append(x, x, kc, kc, tab, n, device_status=status)
+
+
+def test_forward_workspace_with_a_checkpoint():
+    """With a checkpoint the forward's workspace is its status word's 256 bytes; without one, what the size query says."""
+    for s in (_shape(), _shape(dtype=la.F32), _shape(dk=64, dv=64)):
+        _, nck = la.linattn_workspace_size(s, la.OP_CHECKPOINT_DELTA)
+        _, nws = la.linattn_workspace_size(s, la.OP_FWD_DELTA)
+        assert fwd(s, ck=FAKE, nck=nck, nws=255) == la.ERR_WORKSPACE
+        # (the next refusal after the workspace's: it was long enough)
+        assert fwd(s, q=None, ck=FAKE, nck=nck, nws=256) == la.ERR_INVALID
+        assert fwd(s, nws=nws - 1) == la.ERR_WORKSPACE

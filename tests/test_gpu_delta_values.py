@@ -34,3 +34,20 @@ def test_gradients_repeat_over_many_chunks(d):
     for _ in range(10):
         for a, b in zip(la.bwd_delta(q, k, v, dO, lg, beta, ck)[:5], want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d,dtype", [(128, BF16), (64, BF16), (64, torch.float32)])
+def test_checkpointed_forward_needs_no_workspace(d, dtype):
+    """A training forward allocates its output and 256 bytes, and gives the bits of the one without a checkpoint."""
+    q, k, v, dO, lg, beta = inputs(2, 1, 3, 300, d, dtype, torch.float32, 0.1, "cuda")
+    want, fin = la.fwd_delta(q, k, v, lg, beta, want_final=True)
+    ck = la.checkpoint_delta(q)
+    torch.cuda.synchronize()
+    held = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    o, _ = la.fwd_delta(q, k, v, lg, beta, ckpt=ck)
+    assert torch.cuda.max_memory_allocated() - held <= o.numel() * o.element_size() + 1024
+    assert torch.equal(o, want)
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    o, f = la.fwd_delta(q, k, v, lg, beta, want_final=True, ckpt=ck, ws=ws)
+    assert torch.equal(o, want) and torch.equal(f, fin) and la.device_status(ws) == la.OK
