@@ -27,6 +27,7 @@
 // and three block barriers a token it took 625 us, and with the last two walks uncut 254 us.
 #include <cuda_bf16.h>
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace linattn {
 namespace {
@@ -65,10 +66,6 @@ struct WalkArgs {
   float *xpart, *dbpart, *apart;    // [BH][T][D/4], [BH][T][D/4], [BH][N][D/4]: one value per warp
 };
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
-               : "memory");
-}
 // sum over the eight lanes of a column (row)
 __device__ __forceinline__ float sum8(float x) {
 #pragma unroll
@@ -127,13 +124,14 @@ __global__ void __launch_bounds__(kWalkThreads) delta_walk(Problem p, DeltaGates
 #pragma unroll
       for (int e = tid; e < kBlockT * (D / 4); e += kWalkThreads) {
         const int c = e % (D / 4), t = e / (D / 4);
-        if (t < n) cp_async16(&rows[s][a][t][c], in.row[a] + (t0 + t) * in.row_st[a] + 4 * c);
+        if (t < n) cp_async16(smem_u32(&rows[s][a][t][c]), in.row[a] + (t0 + t) * in.row_st[a] + 4 * c);
       }
     static_assert(kBlockT * (kVecs / 4) == 32, "one warp stages one array's pieces");
 #pragma unroll
     for (int a = 0; a < NV; ++a)
       if (warp == a && lane / 4 < n)
-        cp_async16(&vecs[s][a][lane / 4][lane % 4], in.vec[a] + (t0 + lane / 4) * in.vec_st[a] + 4 * (lane % 4));
+        cp_async16(smem_u32(&vecs[s][a][lane / 4][lane % 4]),
+                   in.vec[a] + (t0 + lane / 4) * in.vec_st[a] + 4 * (lane % 4));
     asm volatile("cp.async.commit_group;" ::: "memory");
     if (tid < n) {
       gates[s][0][tid] = g.lg ? expf(ld_gate(g.lg, gb + t0 + tid, g.f32)) : 1.f;

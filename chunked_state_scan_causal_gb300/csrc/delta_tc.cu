@@ -50,11 +50,6 @@ constexpr size_t kStateImg = 32768, kRowImg = 16384, kYImg = 2 * kRowImg;  // Y:
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
   return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // a and b as packed bf16 and what is left of them as packed bf16 (the difference of a pair in one
 // packed instruction)
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {

@@ -187,14 +187,6 @@ struct TcLayout {
 // The ring's full and empty barriers follow.
 enum { T_Q = 0, T_OFREE, T_S, T_P = T_S + 2, T_O = T_P + 2, T_FULL = T_O + 2 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void st_shared_h(uint32_t addr, float x) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))) : "memory");
 }

@@ -160,6 +160,11 @@ __device__ __forceinline__ void prefetch_l1(const void *p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 
+// Asynchronous copy of 16 bytes (both addresses 16-byte aligned) to shared memory.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // ----------------------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
@@ -403,11 +408,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -439,13 +439,10 @@ __device__ __forceinline__ uint64_t desc_mnmajor(uint32_t tile, uint32_t kstep) 
   return sdesc_sw128(tile + kstep * 2048u, kTileHalfBytes, 1024u);
 }
 
-// The same views of a tile whose 64-column blocks are `half` bytes apart (any number of rows: one
+// The first view of a tile whose 64-column blocks are `half` bytes apart (any number of rows: one
 // block of 64 rows is 8 KiB).
 __device__ __forceinline__ uint64_t desc_kmajor_h(uint32_t tile, uint32_t kstep, uint32_t half) {
   return sdesc_sw128(tile + (kstep >> 2) * half + (kstep & 3) * 32u, 16u, 1024u);
-}
-__device__ __forceinline__ uint64_t desc_mnmajor_h(uint32_t tile, uint32_t kstep, uint32_t half) {
-  return sdesc_sw128(tile + kstep * 2048u, half, 1024u);
 }
 
 // Byte offset of (row, 16-byte chunk c in [0,16)) inside an SW128 tile.
@@ -454,6 +451,12 @@ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t chunk) {
 }
 
 // ----------------------------------------------------------------------------- conversions
+// 2^x with the PTX ex2.approx instruction (flush-to-zero; 2^-inf = 0)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));

@@ -72,13 +72,6 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
   return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// 2^x with the PTX ex2.approx instruction (flush-to-zero; 2^-inf = 0)
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // pairs of fp32 values in one 64-bit register: the packed FMA and add of sm_100 and later
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
   uint64_t r;
