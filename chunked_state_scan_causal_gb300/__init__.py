@@ -315,8 +315,12 @@ def _ptr(t):
 
 def _stream(dev, stream=None):
     import torch
+    if stream is not None:
+        return stream.cuda_stream
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be on a CUDA device, not on {dev}")
     # (the raw handle: building the Stream object around it costs more than some of the kernels)
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def shape_of(q, decay=None, chunk: int = 64) -> Shape:

@@ -234,3 +234,17 @@ def test_forward_workspace_with_a_checkpoint():
         # (the next refusal after the workspace's: it was long enough)
         assert fwd(s, q=None, ck=FAKE, nck=nck, nws=256) == la.ERR_INVALID
         assert fwd(s, nws=nws - 1) == la.ERR_WORKSPACE
+
+
+def test_tensors_of_the_host_are_refused():
+    """Every kind of call says so (ValueError) before the library gets a pointer."""
+    q, kc = torch.zeros(1, 2, 8, 64), torch.zeros(4, 2, 16, 64)
+    g, S = torch.zeros(1, 2, 8), torch.zeros(1, 2, 64, 64)
+    tab, n = torch.zeros(1, 3, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    ck, one = torch.zeros(1 << 20, dtype=torch.uint8), q[:, :, :1]
+    for call in (lambda: la.fwd(q, q, q), lambda: la.decode(q, q, q, S), lambda: la.fwd_delta(q, q, q, g, g),
+                 lambda: la.bwd_delta(q, q, q, q, g, g, ck), lambda: la.decode_delta(q, q, q, g, g, S),
+                 lambda: la.paged_append(one, one, kc, kc, tab, n), lambda: la.paged_decode(one, kc, kc, tab, n),
+                 lambda: la.device_status(ck)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
