@@ -695,6 +695,13 @@ def _under(stream, f, *args):
         return f(*args)
 
 
+def _buffers(q, *ts):
+    """Workspaces and checkpoints that the caller brought: kernels write them."""
+    for t in ts:
+        if t is not None and (t.device != q.device or not t.is_contiguous()):
+            raise ValueError("workspaces and checkpoints must be contiguous, on the inputs' device")
+
+
 def _like(q):
     """An output with q's layout."""
     import torch
@@ -737,6 +744,7 @@ def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=No
     _same_layout(q, k, v, out)
     gdt = _delta_gates(log_gate, beta, q)
     _states(q, init_state)
+    _buffers(q, ws, ckpt)
     o = out if out is not None else _like(q)
     B, H, T, d = q.shape
     fin = q.new_empty((B, H, d, d), dtype=torch.float32) if want_final else None
@@ -761,6 +769,7 @@ def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, 
     _same_layout(q, k, v, dO)
     gdt = _delta_gates(log_gate, beta, q)
     _states(q, init_state, d_final)
+    _buffers(q, ws, ckpt)
     B, H, T, d = q.shape
     if outs is None:
         dq, dk, dv = _like(q), _like(q), _like(q)
@@ -847,6 +856,7 @@ def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0,
     if k_cache.device != q.device:
         raise ValueError("q and the cache must be on one device")
     _int_rows(q, q.shape[0], seq_lens)
+    _buffers(q, ws)
     tab, n, stride = _table(q, block_table)
     o = out if out is not None else _like(q)
     lse = q.new_empty(q.shape[:3], dtype=torch.float32) if want_lse else None

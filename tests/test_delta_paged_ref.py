@@ -248,3 +248,16 @@ def test_tensors_of_the_host_are_refused():
                  lambda: la.device_status(ck)):
         with pytest.raises(ValueError, match="CUDA device"):
             call()
+
+
+def test_buffers_of_another_device_are_refused():
+    """A workspace or checkpoint elsewhere, or one whose bytes are not its own (expanded), never reaches a kernel."""
+    q, g = torch.zeros(1, 2, 8, 64), torch.zeros(1, 2, 8)
+    kc, n = torch.zeros(4, 2, 16, 64), torch.zeros(1, dtype=torch.int32)
+    tab, ck = torch.zeros(1, 3, dtype=torch.int32), torch.zeros(1 << 20, dtype=torch.uint8)
+    for bad in (torch.zeros(1 << 20, dtype=torch.uint8, device="meta"), torch.zeros(1, dtype=torch.uint8).expand(1 << 20)):
+        for call in (lambda: la.fwd_delta(q, q, q, g, g, ws=bad), lambda: la.fwd_delta(q, q, q, g, g, ckpt=bad),
+                     lambda: la.bwd_delta(q, q, q, q, g, g, bad), lambda: la.bwd_delta(q, q, q, q, g, g, ck, ws=bad),
+                     lambda: la.paged_decode(q[:, :, :1], kc, kc, tab, n, ws=bad)):
+            with pytest.raises(ValueError, match="workspaces and checkpoints"):
+                call()
