@@ -762,7 +762,8 @@ def fwd_delta(q, k, v, log_gate, beta, init_state=None, want_final=False, out=No
 def bwd_delta(q, k, v, dO, log_gate, beta, ckpt, init_state=None, d_final=None, want_dinit=False, outs=None, ws=None,
               stream=None):
     """(dq, dk, dv, d_log_gate or None, d_beta, d_init or None) of fwd_delta for the upstream gradient dO
-    (the gates' gradients in the gates' type)."""
+    (the gates' gradients in the gates' type).  v and init_state are the forward's: what they add is in the checkpoint,
+    and they are only checked."""
     if stream is not None:
         return _under(stream, bwd_delta, q, k, v, dO, log_gate, beta, ckpt, init_state, d_final, want_dinit, outs, ws)
     import torch
@@ -847,7 +848,8 @@ def paged_append(k, v, k_cache, v_cache, block_table, start, new_lens=None, devi
 def paged_decode(q, k_cache, v_cache, block_table, seq_lens, scale: float = 0.0, want_lse: bool = False, out=None,
                  ws=None, stream=None):
     """(o, lse or None): softmax attention of one new token per sequence, q [B, Hq, 1, d], over the first
-    seq_lens[b] tokens of its pages (scale 0 means 1/sqrt(d); lse [B, Hq, 1] fp32)."""
+    seq_lens[b] tokens of its pages (scale 0 means 1/sqrt(d); lse [B, Hq, 1] fp32).  Page ids outside the cache count
+    as absent tokens: pass ws= (workspace(q, OP_PAGED_DECODE)) to read of them with device_status(ws)."""
     if stream is not None:
         return _under(stream, paged_decode, q, k_cache, v_cache, block_table, seq_lens, scale, want_lse, out, ws)
     import torch

@@ -19,11 +19,13 @@
 //     db_j = dU_j . y_j - sum_{i > j} Gam_ij (k_i . k_j) (z_i . y_j),
 //     d(cumulative log-gate)_i = q_i . dq_i + k_i . [read part] - k_i . [write part].
 //
-// Precision: the state and every accumulator are fp32.  Operands of the chain that are not bf16 inputs
-// (S, Y, W, T, P, R, dU) enter its products as two bf16 parts, hi + lo (16 significant bits), three
-// products for two such operands: what the chain carries from chunk to chunk stays within about 2^-16
-// per step instead of 2^-8, so a final state is good for a decode that goes on for long.  The
-// gradient kernel's operands are single bf16 (its results are rounded to bf16 anyway).
+// Precision: the state and every accumulator are fp32.  Operands of the chains that are not bf16 inputs
+// (S, Y, W, T, P, R, dU) enter their products as two bf16 parts, hi + lo (16 significant bits): what a chain
+// carries from chunk to chunk stays within about 2^-16 per step instead of 2^-8, so a final state is good for
+// a decode that goes on for long (2.4e-6 to 4.4e-6 of exact at 777 to 8192 tokens, d_init_state alike; products
+// of fp32 operands would leave 1.5e-7).  The gradient kernel's operands are single bf16 but for Y in dO Y^T and
+// Y R^T and for A, which have two parts: its results are rounded to bf16 anyway, and gates' gradients that are
+// returned in fp32 come from the same operands (0.3e-3 to 2.4e-3).
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -1209,8 +1211,8 @@ __global__ void __launch_bounds__(Chain<VS>::threads, 1)
 // chunk fill shared memory, so the loads overlap only the last step.
 //
 // Single bf16 operands except Y in dO Y^T and Y R^T and the matrix A, which have two parts: with one the
-// gradients' errors come to 2.9e-3 of their size, 1.75 times the rounding of the results themselves (now 2.0e-3
-// to 2.5e-3; Z, D and the images of S and R would cost another 40 products for 2.4e-3).
+// gradients' errors come to 2.9e-3 of their size, 1.75 times the rounding of the results themselves, 1.65e-3 (now
+// 1.7e-3 to 2.7e-3; Z, D and the images of S and R would cost another 40 products for at most 0.5e-3).
 constexpr int kGradThreads = 576, kGradWarps = 16;
 constexpr uint32_t kGrKD = 0, kGrQ = 32768, kGrS = 49152, kGrR = 81920, kGrY = 114688, kGrU = 147456, kGrZ = 163840,
                    kGrA = 180224,           // A hi, A lo, D (8 KiB each); T lives over the last two before them

@@ -162,14 +162,16 @@ __device__ bool walk_start(const PagedProblem &p, int64_t *buf, PagedWalk &w) {
 //     S = K Q^T,   p = 2^(c S - m),   O^T += V^T p^T   (lane = value dimension, column = query head):
 // K and V are the 128-row A operands straight from shared memory, and the (at most 16) query heads the
 // narrow side, so a tile costs 16 small products whatever the number of heads (each bound by reading its
-// 128-row operand), and the kernel is bound by reading the cache once.  p enters as two bf16 parts side by
+// 128-row operand), and the kernel is bound by reading the cache once.  The softmax threads' work does grow with the
+// heads: 64 sequences of up to 16384 tokens run at 1.04 of copy bandwidth with 1 or 4 query heads a key head (8 key
+// heads), 1.01 with 8, 0.88 with 16 (4 key heads); more than 16 read the cache once per 16.  p enters as two bf16 parts side by
 // side (columns 0..15 and 16..31 of O), so the weights keep 16 bits at no extra product.  The reference maximum m
 // moves only when a tile exceeds it by more than 8 (in log2): p stays below 2^8 and O is rescaled rarely.
 // Even and odd tiles are two streams with an m, a sum and an O of their own, joined at the piece's end, so
 // the softmax of one tile overlaps the products of the next.
 // With many short sequences a piece's latencies count (about 4.5 us a piece of three tiles): the next piece's Q is
 // loaded and its first scores are made while this one's output goes out (256 sequences of 125 to 500 tokens, 8 key
-// heads: 101 -> 93 us, 0.50 of copy bandwidth; long sequences run at it).
+// heads: 101 -> 93 us, 93 to 95 by the card, 0.50 of copy bandwidth; long sequences run at it).
 // Warps: 0..3 and 4..7 softmax and output of the even and odd tiles, 8 issues the products, 9..12 load.
 // Pages of a multiple of 8 tokens are loaded by tensor-map copies of up to 128 rows (one lane per copy);
 // other pages by 16-byte asynchronous copies of all four warps, which are slower (a warp moves 512 bytes an
@@ -574,7 +576,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // the heads are halved (HN - 1 exchanges instead of HN per step), which leaves every lane one head, its
 // maximum, its sum and its weight; the weights then go round.  The warps' (and lanes') maxima, sums and
 // outputs are joined at a piece's end.  Up to 4 query heads per key head it is bound by the cache (72 us at 16
-// sequences of 8192, 4 key heads of 4 query heads, D = 128: 0.71 of copy bandwidth), with 16 by its sums (215 us).
+// sequences of 8192, 4 key heads of 4 query heads, D = 128: 0.71 of copy bandwidth), with 16 by its sums (216 us).
 // Four warps on two CTAs an SM leave them 255 registers: six warps, at 168, take 83 us.
 constexpr int kSimtWarps = 4, kSimtThreads = 32 * kSimtWarps, kSimtPerSm = 2;
 template <int D, int HN>

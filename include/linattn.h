@@ -264,7 +264,8 @@ int32_t linattn_decode(const linattn_shape *shape, const void *q, const void *k,
  *   S_t  = S'_t + beta_t k_t y_t^T,   o_t = S_t^T q_t.
  * log_gate [B,H,T] (values <= 0; NULL: no decay) and beta [B,H,T] (write strengths,
  * usually in [0, 1]) are contiguous, 16-byte aligned and both of type gate_dtype
- * (LINATTN_F32 or LINATTN_BF16, with either type of shape).  The recurrence is
+ * (LINATTN_F32 or LINATTN_BF16, with either type of shape; in fp32 beside bf16
+ * tensors the gates' gradients are as exact as the others, about 2e-3).  The recurrence is
  * stable for beta_t |k_t|^2 in [0, 2]; callers normalise k.  q is used as given
  * (no scale).  The shape's decay must be NULL.
  *   init_state  [B,H,dk,dv] fp32 or NULL (zeros); final_state the same or NULL
@@ -281,7 +282,8 @@ int32_t linattn_fwd_delta(const linattn_shape *shape, const void *q, const void 
                           void *workspace, size_t workspace_bytes, void *stream);
 
 /* Backward of linattn_fwd_delta (same shape, q, k, v, gates, init_state and its
- * checkpoint), for an upstream gradient dO and the gradient d_final_state arriving at
+ * checkpoint; v and init_state are in the checkpoint already and are not read again:
+ * others than the forward's go unnoticed), for an upstream gradient dO and the gradient d_final_state arriving at
  * the final state (or NULL).  With R_t the gradient at S_t (R_{T-1} starts from
  * d_final_state), u_t = beta_t y_t and dy_t = beta_t R_t^T k_t:
  *   dq_t = S_t dO_t,   dv_t = dy_t,   dk_t = R_t u_t - S'_t dy_t,
@@ -315,7 +317,8 @@ int32_t linattn_decode_delta(const linattn_shape *shape, const void *q, const vo
  * linattn_paged_append copies new tokens k, v ([B, H, T, d] of new_shape, the cache's
  * type) to positions start[b] .. start[b] + new_lens[b] - 1 (int32 device; new_lens NULL:
  * all T; larger values are taken as T, negative ones as 0).  Positions outside the table
- * and page ids outside the cache are not written; device_status (int32 device or NULL)
+ * and page ids outside the cache are not written, nor is any token of a sequence whose
+ * start is negative; device_status (int32 device or NULL)
  * is zeroed and then receives LINATTN_ERR_INVALID if there were any.
  * Two tokens of one call with the same slot leave any mixture of their rows there.
  * Returns a status. */
