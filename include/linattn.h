@@ -334,8 +334,9 @@ int32_t linattn_paged_append(const linattn_shape *new_shape, const linattn_shape
  * the cache's heads, T = 1, the strides of q and o).  Slots past seq_lens[b] are never
  * used, whatever they hold.  A row with no token (an empty sequence, or bad pages only)
  * gives o = 0, lse = -inf.  Inside a length NaN counts: a NaN query or key, or a score
- * of +inf, makes the row's o and lse NaN, and a NaN value its dimension of o; a score
- * of -inf is a weight of zero (o is NaN if there is no other).  The length is
+ * of +inf, makes the row's o and lse NaN, a NaN value its dimension of o, and an
+ * infinite value its dimension infinite or NaN; a score of -inf is a weight of zero (o is
+ * NaN if there is no other).  The length is
  * split over the whole GPU and the pieces are joined.  Bad page ids count as absent
  * tokens and set the workspace's status word to LINATTN_ERR_INVALID; lengths are
  * clamped to [0, max_blocks * page].
