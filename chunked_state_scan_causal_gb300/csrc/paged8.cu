@@ -27,6 +27,12 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t f16x2) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(f16x2));
   return r;
 }
+// two f16 as e5m2 codes, to nearest
+__device__ __forceinline__ uint32_t e5m2x2(uint32_t f16x2) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(f16x2));
+  return r;
+}
 
 // The exponent e of the scale of a block whose largest finite magnitude has these fp32 bits: with amax = m 2^E
 // (1 <= m < 2) it is E - 8, or E - 7 where m > 1.75 (448 = 1.75 2^8).  Between -126 and 120.
@@ -221,17 +227,19 @@ __global__ void __launch_bounds__(256, 5)
 // ------------------------------------------------------------------ bf16 decode (tensor cores)
 // As in the bf16 cache's kernel (paged.cu), a tile is 128 tokens, the rows are the narrow side of the products, and
 //     S = K Q^T  (lane = token, column = row),   O^T += V^T P^T  (lane = value dimension, column = row),
-// here with the codes as the 128-row operands of e4m3 products, straight from shared memory: nothing of the cache is
-// converted.  What is not in the cache is cut into e4m3 parts, 4 significant bits each, a column of the product per part:
-//   q / qs = q1 + q2 / 16 with qs a power of two: exact (a bf16 value has 8 bits) down to 2^-14 of the row's largest
-//     value, within 2^-21 of that value below;
-//   the weight w = p1 + p2 / 16 + p3 / 256: 11 bits (what an f16 holds).
-// A key's scale goes into its score, a value's into its weight, relative to a bound on the value scales so far (vref):
-//   x = c ks qs (S1 + S2 / 16),   w = 2^(x - m) vs / vref <= 2^8,   o = vref (O1 + O2 / 16 + O3 / 256) / sum 2^(x - m).
+// here with the codes as the 128-row operands of 8-bit products, straight from shared memory: nothing of the cache is
+// converted.  What is not in the cache is cut into 8-bit parts, a column of the product per part:
+//   q / qs = q1 + q2 / 16 with qs a power of two, in e4m3 (4 significant bits): exact (a bf16 value has 8 bits) down to
+//     2^-14 of the row's largest value, within 2^-21 of that value below;
+//   the weight, an f16, w = p1 + p2 / 16 + p3 / 256 in e5m2: exact for every f16 up to 2^15, since a part (3 bits, rounded to
+//     nearest) leaves at most 2^-3 of its power of two, 16 times which loses no bits above the smallest f16, 2^-24.
+// (e4m3 parts, whose smallest step is 2^-9, would hold a weight to 2^-17 only, whatever its size, and many small
+// weights beside a large one are what a softmax often consists of.)
+// A key's scale goes into its score, a value's into its weight, relative to a bound on the value scales so far (128 vref):
+//   x = c ks qs (S1 + S2 / 16),   w = 2^(x - m) vs / vref <= 2^15,   o = vref (O1 + O2 / 16 + O3 / 256) / sum 2^(x - m).
 // The reference m moves only when a score exceeds it by more than 8 (to 4 below that score) and vref only when a value
-// scale exceeds it (to four times that scale, which leaves the smallest weights 2^-20 of the largest to be held to);
-// both are asked for by one vote of the threads per tile, so that the reductions over the
-// tile's tokens and the rescaling of O happen in the first tile and rarely after.
+// scale exceeds 128 times it (to 1 / 32 of that scale); both are asked for by one vote of the threads per tile, so that the
+// reductions over the tile's tokens and the rescaling of O happen in the first tile and rarely after.
 //
 // Warps: four for the softmax (lane = token) and the output (lane = value dimension), eight with more than 8 rows, each
 // four for half of them; then one that issues the products, one that walks the CTA's pieces, publishes them and
@@ -272,9 +280,9 @@ struct Piece8 {
   int b, hk, h0, nh, t0, t1, nt, len;
 };
 
-// Instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D (the fields of idesc_bf16).
-__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// Instruction descriptor, kind::f8f6f4: e4m3 A, B of type b (0 e4m3, 1 e5m2), fp32 D (the fields of idesc_bf16).
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t b, uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (b << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 // Shared-memory descriptor with the layout field: 0 no swizzle, 2 128 bytes, 4 64 bytes.
 __device__ __forceinline__ uint64_t sdesc(uint32_t start, uint32_t lbo, uint32_t sbo, uint64_t layout) {
@@ -282,7 +290,7 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t start, uint32_t lbo, uint32_t
          layout << 61;
 }
 // D[tmem] (+)= A[smem] B[smem], issued by one elected lane of the warp.
-__device__ __forceinline__ void mma_e4m3_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void mma_codes_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred e, p;\n\t"
@@ -327,6 +335,13 @@ __device__ __forceinline__ uint32_t left16(uint32_t h, uint32_t part) {
   const uint32_t a = f16x2_of_e4m3x2(part);
   const __half2 m = __float2half2_rn(-16.f), n = __float2half2_rn(16.f);
   const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), m, __hmul2(*reinterpret_cast<__half2 *>(&h), n));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+// The same after their e5m2 part, which is an f16's upper byte (up to 2^15: 16 h itself would not fit).
+__device__ __forceinline__ uint32_t left16_e5m2(uint32_t h, uint32_t part) {
+  const uint32_t a = __byte_perm(part, 0, 0x1404);
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&a)),
+                            __float2half2_rn(16.f));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
@@ -577,7 +592,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
     empty_rows<D>(p, o, lse, lane);
   } else if (warp == 4 * G) {
     // ------------------------------------------------------------ products
-    const uint32_t id_qk = idesc_e4m3(128, L::NS, false, false), id_pv = idesc_e4m3(128, L::NO, true, true);
+    const uint32_t id_qk = idesc_e4m3(0, 128, L::NS, false, false), id_pv = idesc_e4m3(1, 128, L::NO, true, true);
     // Scores run a tile ahead of the weighted sums, across pieces too.  i: the tile of the scores, of piece k, t behind
     // the tiles that are issued; first: whether it is a piece's first, and the tile's before
     bool more = true, first = false, before;
@@ -600,7 +615,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
         tc_fence_after();
 #pragma unroll
         for (uint32_t ks = 0; ks < D / 32; ++ks)
-          mma_e4m3_warp(tmem + (i & 1) * L::NS, desc_rows<D>(base + s * L::tile, ks),
+          mma_codes_warp(tmem + (i & 1) * L::NS, desc_rows<D>(base + s * L::tile, ks),
                         desc_rows<D>(base + L::q + (L::scol ? 0 : (k & 1) * L::qbuf), ks), id_qk, ks > 0);
         mma_commit_warp(&bar[B_S + (i & 1)]);
         mma_commit_warp(&bar[B_EMPTY + s]);
@@ -612,7 +627,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
         tc_fence_after();
 #pragma unroll
         for (uint32_t ks = 0; ks < 4; ++ks)  // P: 16 columns (bytes) of a token side by side, 128 tokens; then the next 16
-          mma_e4m3_warp(tmem + 2 * L::NS, desc_cols<D>(base + s * L::tile, ks), sdesc(base + L::p + ks * 512, 128, 2048, 0),
+          mma_codes_warp(tmem + 2 * L::NS, desc_cols<D>(base + s * L::tile, ks), sdesc(base + L::p + ks * 512, 128, 2048, 0),
                         id_pv, !before || ks > 0);
         mma_commit_warp(&bar[B_O]);
         mma_commit_warp(&bar[B_EMPTY + s]);
@@ -636,7 +651,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
       if (!dead && w.nh) await(B_SQ + k % kPieces, k / kPieces);
       if (!group_all(!dead, 3, 128 * G) || !w.nh) break;  // one verdict
       float mu[HG], l[HG], my_mu = kNone;  // m (kNone before the first token; in lane h row h's), this thread's sum
-      float vref = 1.17549435e-38f, rv = 1.f / vref;
+      float vref = 1.17549435e-38f, rv = 1.f / vref;  // 2^-126, 2^126
 #pragma unroll
       for (int h = 0; h < HG; ++h) {
         mu[h] = kNone;
@@ -684,7 +699,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
         // d: the score behind its reference
         float d[HG];
         // (the first tile decides for all: there NaN has to move the reference too)
-        bool up = t == w.t0 || (valid && vs > vref);
+        bool up = t == w.t0 || (valid && vs > 128.f * vref);
 #pragma unroll
         for (int h = 0; h < HG; ++h) {
           if (!valid) x[h] = -INFINITY;
@@ -705,10 +720,10 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
           const float4 v = *reinterpret_cast<const float4 *>(s_red[gr][min(lane, HG)]);
           const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), vmax = __shfl_sync(0xffffffffu, mx, HG);
           float fv = 1.f, f = 1.f;
-          if (vmax > vref) {
-            rv = __fdividef(0.25f, vmax);
+          if (vmax > 128.f * vref) {
+            rv = __fdividef(32.f, vmax);
             fv = vref * rv;
-            vref = 4.f * vmax;
+            vref = 0.03125f * vmax;
           }
           if (mx > my_mu + 8.f) {
             const float m = fmaxf(mx - 4.f, kFloor);
@@ -765,11 +780,11 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
             l[h + z] += e[z];
           }
           const uint32_t a = f16x2(e[0] * vr, e[1] * vr), b = f16x2(e[2] * vr, e[3] * vr);
-          const uint32_t a1 = e4m3x2(a), b1 = e4m3x2(b), ra = left16(a, a1), rb = left16(b, b1);
-          const uint32_t a2 = e4m3x2(ra), b2 = e4m3x2(rb);
+          const uint32_t a1 = e5m2x2(a), b1 = e5m2x2(b), ra = left16_e5m2(a, a1), rb = left16_e5m2(b, b1);
+          const uint32_t a2 = e5m2x2(ra), b2 = e5m2x2(rb);
           pt[0][h / 4] = a1 | b1 << 16;
           pt[1][h / 4] = a2 | b2 << 16;
-          pt[2][h / 4] = e4m3x2(left16(ra, a2)) | e4m3x2(left16(rb, b2)) << 16;
+          pt[2][h / 4] = e5m2x2(left16_e5m2(ra, a2)) | e5m2x2(left16_e5m2(rb, b2)) << 16;
         }
         if (i >= 1) await(B_O, i - 1);  // P of the tile before has been read
         const uint32_t P = base + L::p + lt * 16;
