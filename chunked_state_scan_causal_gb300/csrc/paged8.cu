@@ -235,11 +235,13 @@ __global__ void __launch_bounds__(256, 5)
 //     nearest) leaves at most 2^-3 of its power of two, 16 times which loses no bits above the smallest f16, 2^-24.
 // (e4m3 parts, whose smallest step is 2^-9, would hold a weight to 2^-17 only, whatever its size, and many small
 // weights beside a large one are what a softmax often consists of.)
-// A key's scale goes into its score, a value's into its weight, relative to a bound on the value scales so far (128 vref):
-//   x = c ks qs (S1 + S2 / 16),   w = 2^(x - m) vs / vref <= 2^15,   o = vref (O1 + O2 / 16 + O3 / 256) / sum 2^(x - m).
-// The reference m moves only when a score exceeds it by more than 8 (to 4 below that score) and vref only when a value
-// scale exceeds 128 times it (to 1 / 32 of that scale); both are asked for by one vote of the threads per tile, so that the
-// reductions over the tile's tokens and the rescaling of O happen in the first tile and rarely after.
+// A key's scale goes into its score, a value's into its weight:
+//   x = c ks qs (S1 + S2 / 16),   w = 2^(x - m) vs r <= 2^15,   o = (O1 + O2 / 16 + O3 / 256) / (r sum 2^(x - m)).
+// Both references are a row's own and made of the tokens that it sees: r places the largest weight times value scale, so that
+// large values at tokens of no weight leave the weights that count where they are.  m moves only when a score exceeds
+// it by more than 8 (to that score), r only when a w exceeds 2^15 (that w to 2^11, where an f16 holds its 11 bits down to 2^-25 of
+// it); both are asked for by one vote of the threads per tile, so that the reductions over the tile's tokens and the
+// rescaling of O happen in the first tile and rarely after.
 //
 // Warps: four for the softmax (lane = token) and the output (lane = value dimension), eight with more than 8 rows, each
 // four for half of them; then one that issues the products, one that walks the CTA's pieces, publishes them and
@@ -263,7 +265,7 @@ struct Layout8 {
   static constexpr uint32_t qbuf = HN == 4 ? 8 * D : NS * D, scol = HN == 4 ? 8 : 0;
   static constexpr uint32_t tile = 128 * D, q = ring * tile, p = q + 2 * qbuf, sc = p + 128 * NO,
                             sq = sc + nsc * 64, desc = sq + pieces * HN * 4, red = desc + pieces * 32,
-                            sum = red + G * (HG + 1) * 16, nan = sum + HN * 16, bars = nan + D * 4;
+                            ref = red + G * HG * 32, sum = ref + G * HG * 8, nan = sum + HN * 16, bars = nan + D * 4;
   static constexpr int nbars = 2 * pieces + 2 * 2 + 2 + 2 + nsc + 2 * ring;
   static constexpr uint32_t end = bars + nbars * 8 + 16;  // (the tensor memory's address, two flags)
   // (at D = 64 the second half of a value tile's 128 lanes is whatever follows the tile)
@@ -325,6 +327,12 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
+// The larger ones (NaN left out).
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -379,10 +387,11 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
   uint64_t *bar = reinterpret_cast<uint64_t *>(smem + L::bars);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bar + L::nbars);
   int *abort_flag = reinterpret_cast<int *>(tslot + 1), *status = abort_flag + 1;
-  float(*s_red)[HG + 1][4] = reinterpret_cast<float(*)[HG + 1][4]>(smem + L::red);
+  float2(*s_red)[HG][4] = reinterpret_cast<float2(*)[HG][4]>(smem + L::red);
   float(*s_q)[HN] = reinterpret_cast<float(*)[HN]>(smem + L::sq);
   float2(*s_sc)[8] = reinterpret_cast<float2(*)[8]>(smem + L::sc);
   Piece8 *s_piece = reinterpret_cast<Piece8 *>(smem + L::desc);
+  float(*s_ref)[2][HG] = reinterpret_cast<float(*)[2][HG]>(smem + L::ref);
   float(*s_sum)[4] = reinterpret_cast<float(*)[4]>(smem + L::sum);
   int *s_nan = reinterpret_cast<int *>(smem + L::nan);  // see the tail tiles
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid / 32, 0), lane = tid % 32;
@@ -650,13 +659,11 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
       if (!dead) w = s_piece[k % kPieces];
       if (!dead && w.nh) await(B_SQ + k % kPieces, k / kPieces);
       if (!group_all(!dead, 3, 128 * G) || !w.nh) break;  // one verdict
-      float mu[HG], l[HG], my_mu = kNone;  // m (kNone before the first token; in lane h row h's), this thread's sum
-      float vref = 1.17549435e-38f, rv = 1.f / vref;  // 2^-126, 2^126
+      // in lane h row h's m (kNone before the first token) and log2 r; all rows' m and r; this thread's sums
+      float l[HG], my_mu = kNone, my_lr = 0.f;
+      const float *refs = s_ref[gr][0];
 #pragma unroll
-      for (int h = 0; h < HG; ++h) {
-        mu[h] = kNone;
-        l[h] = 0.f;
-      }
+      for (int h = 0; h < HG; ++h) l[h] = 0.f;
       const int partly = w.len - p.T + 1;  // the first token that not every row sees
       const int hr = row_head(p, w.h0 + h0), tr = w.h0 + h0 - hr * p.T;  // head and new token of the first row
       int tok = w.t0 * kTile + lt;
@@ -667,23 +674,23 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
         tc_fence_after();
         const float2 sc = s_sc[i % L::nsc][lt / kScaleTokens];
         const bool valid = tok < w.len && !(sc.y < 0.f);
-        const float ks = sc.x, vs = sc.y;
+        const float ks = sc.x, vs = valid ? sc.y : 0.f;
         float x[HG];
         {
           constexpr int kPart = HG;
-          uint32_t r[2 * kPart];
+          uint32_t s[2 * kPart];
           if constexpr (HG == 4) {
-            tmem_ld8(t4 + (i & 1) * L::NS + (k & 1) * L::scol, r);
+            tmem_ld8(t4 + (i & 1) * L::NS + (k & 1) * L::scol, s);
           } else if constexpr (G == 1) {
-            tmem_ld16(t4 + (i & 1) * L::NS, r);
+            tmem_ld16(t4 + (i & 1) * L::NS, s);
           } else {
-            tmem_ld8(t4 + (i & 1) * L::NS + h0, reinterpret_cast<uint32_t(&)[8]>(r));
-            tmem_ld8(t4 + (i & 1) * L::NS + HN + h0, reinterpret_cast<uint32_t(&)[8]>(r[8]));
+            tmem_ld8(t4 + (i & 1) * L::NS + h0, reinterpret_cast<uint32_t(&)[8]>(s));
+            tmem_ld8(t4 + (i & 1) * L::NS + HN + h0, reinterpret_cast<uint32_t(&)[8]>(s[8]));
           }
           tmem_ld_wait();
 #pragma unroll
           for (int h = 0; h < HG; ++h)
-            x[h] = max_nan(fmaf(__uint_as_float(r[kPart + h]), 0.0625f, __uint_as_float(r[h])) * ks * s_q[k % kPieces][h0 + h],
+            x[h] = max_nan(fmaf(__uint_as_float(s[kPart + h]), 0.0625f, __uint_as_float(s[h])) * ks * s_q[k % kPieces][h0 + h],
                            kFirst);
         }
         // from here on a score of -inf says that the row does not see the token
@@ -696,90 +703,104 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
             y = y + 1 == p.T ? 0 : y + 1;
           }
         }
-        // d: the score behind its reference
-        float d[HG];
-        // (the first tile decides for all: there NaN has to move the reference too)
-        bool up = t == w.t0 || (valid && vs > 128.f * vref);
 #pragma unroll
-        for (int h = 0; h < HG; ++h) {
+        for (int h = 0; h < HG; ++h)
           if (!valid) x[h] = -INFINITY;
-          d[h] = x[h] - mu[h];
-          up |= d[h] > 8.f;
-        }
-        if (group_any(up, 1 + gr, 128)) {
-          float y[HG];
+        // the exponentials and the weights, two rows a word; where they leave their range, and in the first tile, the references
+        // move before
+        float e[HG];
+        uint32_t wt[HG / 2];
+#pragma unroll 1
+        for (bool move = t == w.t0;; move = true) {
+          if (move) {
+            const float lv = __log2f(vs);
 #pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            y[h] = warp_max(x[h] == -INFINITY ? -INFINITY : fmaxf(x[h], kFirst));
-            if (lane == 0) s_red[gr][h][warp & 3] = y[h];
-          }
-          const float tv = warp_max(valid ? vs : 0.f);
-          if (lane == 0) s_red[gr][HG][warp & 3] = tv;
-          named_bar_sync(1 + gr, 128);
-          // lane h: row h; lane HG: the value scales
-          const float4 v = *reinterpret_cast<const float4 *>(s_red[gr][min(lane, HG)]);
-          const float mx = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)), vmax = __shfl_sync(0xffffffffu, mx, HG);
-          float fv = 1.f, f = 1.f;
-          if (vmax > 128.f * vref) {
-            rv = __fdividef(32.f, vmax);
-            fv = vref * rv;
-            vref = 0.03125f * vmax;
-          }
-          if (mx > my_mu + 8.f) {
-            const float m = fmaxf(mx - 4.f, kFloor);
-            f = ex2(my_mu - m);  // (0 from kNone)
-            my_mu = m;
-          }
-#pragma unroll
-          for (int h = 0; h < HG; ++h) {
-            mu[h] = __shfl_sync(0xffffffffu, my_mu, h);
-            y[h] = __shfl_sync(0xffffffffu, f, h);
-            l[h] *= y[h];
-            d[h] = x[h] - mu[h];
-            y[h] *= fv;
-          }
-          if (t > w.t0) {  // O (lane = value dimension) to the new references
-            await(B_O, i - 1);
-            tc_fence_after();
-#pragma unroll
-            for (int z = 0; z < 3; ++z) {
-              if constexpr (HG == 4) {
-                uint32_t a[4];
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
-                             : "r"(O + 4 * z));
-                tmem_ld_wait();
-#pragma unroll
-                for (int h = 0; h < 4; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * y[h]);
-                asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(O + 4 * z), "r"(a[0]),
-                             "r"(a[1]), "r"(a[2]), "r"(a[3])
-                             : "memory");
-              } else {
-                uint32_t a[8];
-                tmem_ld8(O + 8 * z, a);
-                tmem_ld_wait();
-#pragma unroll
-                for (int h = 0; h < 8; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * y[h]);
-                asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(O + 8 * z),
-                             "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])
-                             : "memory");
-              }
+            for (int h = 0; h < HG; ++h) {
+              // the warp's largest score, and the largest of score + log2 scale behind that score
+              const float z = x[h] == -INFINITY ? -INFINITY : fmaxf(x[h], kFirst), xw = warp_max(z);
+              const float jw = warp_max(z == -INFINITY ? -INFINITY : (z - xw) + lv);
+              if (lane == 0) s_red[gr][h][warp & 3] = make_float2(xw, jw);
             }
-            tmem_st_wait();
+            named_bar_sync(1 + gr, 128);
+            // lane h: row h
+            const float4 v0 = *reinterpret_cast<const float4 *>(s_red[gr][lane % HG]),
+                         v1 = *reinterpret_cast<const float4 *>(s_red[gr][lane % HG] + 2);
+            const float xm = fmaxf(fmaxf(v0.x, v0.z), fmaxf(v1.x, v1.z));
+            const float m = xm > my_mu + 8.f ? fmaxf(xm, kFloor) : my_mu;
+            // (what is not there is -inf or NaN, which the maxima leave out)
+            const float j = fmaxf(fmaxf(v0.y + (v0.x - m), v0.w + (v0.z - m)), fmaxf(v1.y + (v1.x - m), v1.w + (v1.z - m)));
+            float lr = my_lr + (m - my_mu);  // (O as it is)
+            if (j + lr > 15.f) lr = 11.f - j;
+            lr = fminf(fmaxf(lr, -120.f), 120.f);
+            const float f = ex2(my_mu - m), g = ex2((my_mu - m) + (lr - my_lr)), now = ex2(lr);  // (f 0 from kNone)
+            my_mu = m;
+            my_lr = lr;
+            if (lane < HG) {  // (every warp the same values, which the others have read their last of before the barrier)
+              s_ref[gr][0][lane] = m;
+              s_ref[gr][1][lane] = now;
+            }
+            __syncwarp();
+            if (t > w.t0) {  // O (lane = value dimension) to the new references
+              await(B_O, i - 1);
+              tc_fence_after();
+              float y[HG];
+#pragma unroll
+              for (int h = 0; h < HG; ++h) {
+                l[h] *= __shfl_sync(0xffffffffu, f, h);
+                y[h] = __shfl_sync(0xffffffffu, g, h);
+              }
+#pragma unroll
+              for (int z = 0; z < 3; ++z) {
+                if constexpr (HG == 4) {
+                  uint32_t a[4];
+                  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                               : "r"(O + 4 * z));
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int h = 0; h < 4; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * y[h]);
+                  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(O + 4 * z), "r"(a[0]),
+                               "r"(a[1]), "r"(a[2]), "r"(a[3])
+                               : "memory");
+                } else {
+                  uint32_t a[8];
+                  tmem_ld8(O + 8 * z, a);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int h = 0; h < 8; ++h) a[h] = __float_as_uint(__uint_as_float(a[h]) * y[h]);
+                  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(O + 8 * z),
+                               "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])
+                               : "memory");
+                }
+              }
+              tmem_st_wait();
+            }
           }
+          bool up = false;
+          uint32_t top = 0;
+#pragma unroll
+          for (int h = 0; h < HG; h += 4) {
+            const float4 m = *reinterpret_cast<const float4 *>(refs + h), r = *reinterpret_cast<const float4 *>(refs + HG + h);
+            e[h] = ex2(x[h] - m.x);
+            e[h + 1] = ex2(x[h + 1] - m.y);
+            e[h + 2] = ex2(x[h + 2] - m.z);
+            e[h + 3] = ex2(x[h + 3] - m.w);
+            wt[h / 2] = f16x2(e[h] * vs * r.x, e[h + 1] * vs * r.y);
+            wt[h / 2 + 1] = f16x2(e[h + 2] * vs * r.z, e[h + 3] * vs * r.w);
+            top = max_f16x2(top, max_f16x2(wt[h / 2], wt[h / 2 + 1]));
+#pragma unroll
+            for (int z = 0; z < 4; ++z) up |= e[h + z] > 256.f;
+          }
+          // (the upper and the lower half against 2^15 = 0x7800: they are not negative)
+          if (move || !group_any(up || top >= 0x78010000u || (top & 0xffffu) > 0x7800u, 1 + gr, 128)) break;
         }
-        // the weights and their parts: a word per part and four rows
-        const float vr = valid ? vs * rv : 0.f;
+        // their parts: a word per part and four rows
         uint32_t pt[3][HG / 4];
 #pragma unroll
-        for (int h = 0; h < HG; h += 4) {
-          float e[4];
+        for (int h = 0; h < HG; ++h) l[h] += e[h];
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            e[z] = ex2(d[h + z]);
-            l[h + z] += e[z];
-          }
-          const uint32_t a = f16x2(e[0] * vr, e[1] * vr), b = f16x2(e[2] * vr, e[3] * vr);
+        for (int h = 0; h < HG; h += 4) {
+          const uint32_t a = wt[h / 2], b = wt[h / 2 + 1];
           const uint32_t a1 = e5m2x2(a), b1 = e5m2x2(b), ra = left16_e5m2(a, a1), rb = left16_e5m2(b, b1);
           const uint32_t a2 = e5m2x2(ra), b2 = e5m2x2(rb);
           pt[0][h / 4] = a1 | b1 << 16;
@@ -839,13 +860,13 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
       await(B_O, i - 1);
       named_bar_sync(3, 128 * G);
       tc_fence_after();
-      uint32_t r[24];
+      uint32_t a[24];
       if constexpr (HG == 4) {
-        tmem_ld16(O, reinterpret_cast<uint32_t(&)[16]>(r));
+        tmem_ld16(O, reinterpret_cast<uint32_t(&)[16]>(a));
       } else {
-        tmem_ld8(O, reinterpret_cast<uint32_t(&)[8]>(r));
-        tmem_ld8(O + 8, reinterpret_cast<uint32_t(&)[8]>(r[8]));
-        tmem_ld8(O + 16, reinterpret_cast<uint32_t(&)[8]>(r[16]));
+        tmem_ld8(O, reinterpret_cast<uint32_t(&)[8]>(a));
+        tmem_ld8(O + 8, reinterpret_cast<uint32_t(&)[8]>(a[8]));
+        tmem_ld8(O + 16, reinterpret_cast<uint32_t(&)[8]>(a[16]));
       }
       tmem_ld_wait();
       tc_fence_before();
@@ -856,7 +877,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
       const float4 sums = *reinterpret_cast<const float4 *>(s_sum[h0 + row]);
       const float sum = (sums.x + sums.y) + (sums.z + sums.w), m = my_mu;
       const bool none = m == kNone && sum == 0.f;
-      const float factor = whole ? __fdividef(1.f, sum) : 1.f;
+      const float over_r = ex2(-my_lr), factor = whole ? __fdividef(over_r, sum) : over_r;
       const uint32_t nothing = __ballot_sync(0xffffffffu, none);
       if ((int)lt < HG && h0 + (int)lt < w.nh) {
         if (!whole) *reinterpret_cast<float2 *>(ml + (at + lt) * 2) = make_float2(none ? -INFINITY : m, sum);
@@ -870,9 +891,9 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
       int y = tr;
 #pragma unroll
       for (int h = 0; h < HG; ++h) {
-        float acc = fmaf(fmaf(__uint_as_float(r[2 * HG + h]), 0.0625f, __uint_as_float(r[HG + h])), 0.0625f,
-                         __uint_as_float(r[h])) *
-                    vref * __shfl_sync(0xffffffffu, factor, h);
+        float acc = fmaf(fmaf(__uint_as_float(a[2 * HG + h]), 0.0625f, __uint_as_float(a[HG + h])), 0.0625f,
+                         __uint_as_float(a[h])) *
+                    __shfl_sync(0xffffffffu, factor, h);
         if (bad_from < y) acc = __uint_as_float(0x7fc00000u);
         if (nothing >> h & 1) acc = 0.f;
         if ((int)lt < D && h0 + h < w.nh) {

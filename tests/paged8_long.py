@@ -57,14 +57,14 @@ def tolerance(dtype, d, n, bound):
     Scores: sums of d exact products in fp32, (d + 4) roundings (truncations in the tensor cores: 2^-23 each) of at most X in
     all; a weight's relative error is twice that (its own and the sum's), plus 2^-20 for the exponential, and the sums take a rounding
     per 32 tokens (a product of the tensor cores) and 16 at a piece's end.
-    bf16: a weight times its value scale is an f16: within 2^-11 of itself, or 2^-25 where it is below 2^-14, while the row's largest is
-    at least 2^9 (of a sequence whose value scales are alike): 2^-34 M, times a code; and the output is rounded (2^-8)."""
+    bf16: a weight times its value scale is an f16: within 2^-11 of itself, or 2^-25 where it is below 2^-14, while the largest of the
+    tokens that the row sees is at least 2^11 (to 2^-20): 2^-36 M, times a code; and the output is rounded (2^-8)."""
     A, X, M, C = bound
     ds = (d + 4) * 2.0 ** -23 * X
     sums = 2.0 ** -20 + (n / 32 + 16) * 2.0 ** -23
     w = (2 * ds + 2 * sums)[..., None]
     if dtype == torch.bfloat16:
-        return lambda o: 2.0 ** -8 * o.abs() + (w + 2.0 ** -11) * A + 2.0 ** -34 * M[..., None] * C, ds + sums
+        return lambda o: 2.0 ** -8 * o.abs() + (w + 2.0 ** -11) * A + 2.0 ** -36 * M[..., None] * C, ds + sums
     return lambda o: 2.0 ** -24 * o.abs() + w * A, ds + sums
 
 

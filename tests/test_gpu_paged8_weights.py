@@ -64,3 +64,29 @@ def test_sinks(dtype, d, rows, sink, value, spread):
     tokens, items = 9000, 2 * 2 * sms()
     assert max(map(max, ref.pieces([tokens] * (items // 2), 2 * rows, 2, 1, dtype, sms()))) >= 64
     check(sink_case(rows + sink, dtype, d, rows, tokens, items, sink, value, spread))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d,rows", [(64, 4), (128, 4), (64, 8), (128, 8), (64, 16), (128, 16)])
+@pytest.mark.parametrize("larger", [4, 8, 14, 20, 40])
+@pytest.mark.parametrize("sink,block", [(0, 0), (11, 3), (11, 70), (0, 561)])
+def test_large_values_without_weight(dtype, d, rows, larger, sink, block):
+    """A block of values 2^larger times the others' at tokens of a weight of e^-30 (the first block of a piece, one of its first
+    tile, one further on, the last one) costs the other tokens nothing."""
+    c = sink_case(rows + larger, dtype, d, rows, 9000, 2 * 2 * sms(), sink, 0.02, 1.0)
+    page, slot = c[4][0, block // 4].long(), block % 4
+    c[1][page, :, slot * 16:slot * 16 + 16, 0] = torch.tensor(-30.0).to(E4M3)
+    c[3][page, :, slot, 1] *= 2.0 ** larger
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,T", [(2, 2), (2, 4), (2, 8), (4, 8)])
+@pytest.mark.parametrize("larger", [10, 30])
+def test_large_values_not_seen(dtype, d, Hq, T, larger):
+    """The last token's value, alone in its block and 2^larger times the others', reaches the last row and no other."""
+    q, kc, vc, sc, table, lens = sink_case(T, dtype, d, 1, 2001, 80, 8, 0.02, 1.0)
+    q = torch.randn(len(lens), Hq, T, d, generator=torch.Generator().manual_seed(T)).cuda().to(dtype)
+    sc[table[0, 2000 // 64].long(), :, 2000 % 64 // 16, 1] *= 2.0 ** larger
+    check((q, kc, vc, sc, table, lens), scale=d ** -0.5)
