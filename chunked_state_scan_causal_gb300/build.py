@@ -1,5 +1,5 @@
-"""Builds liblinattn.so in-tree with nvcc for sm_103a (translation units compiled in parallel), and with the C++
-compiler the module that takes ordinary calls from torch tensors to it (csrc/bind.cpp, for the installed torch).
+"""Builds liblinattn.so in-tree with nvcc for sm_103a (translation units compiled in parallel), and where torch is
+installed, with the C++ compiler, the module that takes ordinary calls from its tensors to the library (csrc/bind.cpp).
 
 Usage: ``python -m chunked_state_scan_causal_gb300.build [--verbose]``.
 """
@@ -48,50 +48,68 @@ def _bind_flags():
             *(f"-I{d}" for d in include)]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(bind_path()):
+def _stale(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(bind_path()))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "linattn.h"))
-    deps.append(os.path.abspath(__file__))
+    t = os.path.getmtime(target)
+    deps = [*(os.path.join(CSRC, f) for f in deps), os.path.join(HERE, "..", "include", "linattn.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
+def _run(cmd, what: str, verbose: bool = False) -> None:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        sys.stderr.write(f"--- {what}\n{r.stdout}{r.stderr}")
+
+
+def _link(out: str, cmd) -> None:
+    tmp = out + f".tmp{os.getpid()}"
+    _run([*cmd, "-shared", "-o", tmp], "link")
+    os.replace(tmp, out)
+
+
+def _object(src: str) -> str:
+    return os.path.join(OUT_DIR, "obj", os.path.splitext(src)[0] + ".o")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA translation unit and link liblinattn.so; returns its path."""
-    if not force and not _stale():
-        return LIB
-    nvcc, cxx = _nvcc(), shutil.which("g++") or "c++"
-    obj_dir = os.path.join(OUT_DIR, "obj")
-    os.makedirs(obj_dir, exist_ok=True)
+    """Compile every CUDA translation unit and link liblinattn.so; returns its path.  The module of the compiled marshalling
+    comes with it where torch, its headers and a C++ compiler are; without it calls take the Python way."""
+    why = None  # the module is left out
+    try:
+        module = bind_path()
+    except ImportError as e:
+        module, why = None, e
+    need_lib = force or _stale(LIB, [f for f in os.listdir(CSRC) if f != BIND])
+    need_module = module and (force or _stale(module, [BIND]))
+    os.makedirs(os.path.join(OUT_DIR, "obj"), exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose else []
+    cxx = shutil.which("g++") or "c++"
 
-    def compile_one(src: str) -> str:
-        obj = os.path.join(obj_dir, os.path.splitext(src)[0] + ".o")
-        cmd = [cxx, *_bind_flags()] if src == BIND else [nvcc, *ARCH, *FLAGS, *extra]
-        r = subprocess.run([*cmd, "-c", os.path.join(CSRC, src), "-o", obj], capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cmd[0]} failed for {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            sys.stderr.write(f"--- {src}\n{r.stdout}{r.stderr}")
-        return obj
+    def compile_one(src: str) -> None:
+        _run([_nvcc(), *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", _object(src)], src, verbose)
 
-    import torch
+    def compile_module() -> None:
+        _run([cxx, *_bind_flags(), "-c", os.path.join(CSRC, BIND), "-o", _object(BIND)], BIND, verbose)
+
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        objs = list(ex.map(compile_one, [BIND, *SOURCES]))
-    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-
-    def link(out, cmd):
-        tmp = out + f".tmp{os.getpid()}"
-        r = subprocess.run([*cmd, "-shared", "-o", tmp], capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, out)
-
-    link(LIB, [nvcc, *ARCH, *objs[1:]])
-    link(bind_path(), [cxx, objs[0], f"-L{OUT_DIR}", "-llinattn", f"-L{torch_lib}", "-ltorch_python", "-ltorch_cpu",
-                       "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+        waiting = ex.submit(compile_module) if need_module else None
+        if need_lib:
+            list(ex.map(compile_one, SOURCES))
+            _link(LIB, [_nvcc(), *ARCH, *map(_object, SOURCES)])
+        if waiting:
+            import torch
+            torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+            try:
+                waiting.result()
+                _link(module, [cxx, _object(BIND), f"-L{OUT_DIR}", "-llinattn", f"-L{torch_lib}", "-ltorch_python",
+                               "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
+            except (RuntimeError, OSError) as e:
+                why = e
+    if why:
+        sys.stderr.write(f"the compiled marshalling is left out (calls take the Python way): {why}\n")
     return LIB
 
 
