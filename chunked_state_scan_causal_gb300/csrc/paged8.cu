@@ -273,9 +273,9 @@ struct Layout8 {
   static_assert(per_sm * (smem + 1024) <= 233472, "what an SM holds");
   static constexpr uint32_t cols = HN > 8 ? 128 : 64;           // of tensor memory: S of even and odd tiles, O
 };
-// The reference of a row that no token has reached yet; above it what a token's score counts as at least, -inf and
-// (when the reference moves) NaN too, so that o is 0 only where no token is; and above that the least that a reference
-// moves to, so that a score of -inf has a weight of zero even among its like (0 / 0).
+// The reference of a row that no token has reached yet (NaN scores move none: their sum says that there are some); above it
+// what a token's score counts as at least, -inf too, so that o is 0 only where no token is; and above that the least that
+// a reference moves to, so that a score of -inf has a weight of zero even among its like (0 / 0).
 constexpr float kNone = kLowest, kFirst = -3.2e38f, kFloor = -3e38f;
 // A published piece.
 struct Piece8 {
@@ -327,10 +327,36 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
 }
+// The largest of three (NaN left out).
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+// Two products, and two sums, an instruction.
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(r))
+      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(r))
+      : "l"(reinterpret_cast<uint64_t &>(x)), "l"(reinterpret_cast<uint64_t &>(y)));
+  return r;
+}
 // The larger ones (NaN left out).
 __device__ __forceinline__ uint32_t max_f16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {  // (to 2^-22 or so: it only places a reference)
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -659,7 +685,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
       if (!dead) w = s_piece[k % kPieces];
       if (!dead && w.nh) await(B_SQ + k % kPieces, k / kPieces);
       if (!group_all(!dead, 3, 128 * G) || !w.nh) break;  // one verdict
-      // in lane h row h's m (kNone before the first token) and log2 r; all rows' m and r; this thread's sums
+      // in lane h row h's m (kNone before the first token) and log2 r; all rows' -m and r; this thread's sums
       float l[HG], my_mu = kNone, my_lr = 0.f;
       const float *refs = s_ref[gr][0];
 #pragma unroll
@@ -713,12 +739,11 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
 #pragma unroll 1
         for (bool move = t == w.t0;; move = true) {
           if (move) {
-            const float lv = __log2f(vs);
+            // the warp's largest score, and the largest of score + log2 scale behind that score
+            const float lv = lg2(vs);
 #pragma unroll
             for (int h = 0; h < HG; ++h) {
-              // the warp's largest score, and the largest of score + log2 scale behind that score
-              const float z = x[h] == -INFINITY ? -INFINITY : fmaxf(x[h], kFirst), xw = warp_max(z);
-              const float jw = warp_max(z == -INFINITY ? -INFINITY : (z - xw) + lv);
+              const float xw = warp_max(x[h]), jw = warp_max((x[h] - xw) + lv);
               if (lane == 0) s_red[gr][h][warp & 3] = make_float2(xw, jw);
             }
             named_bar_sync(1 + gr, 128);
@@ -735,8 +760,8 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
             const float f = ex2(my_mu - m), g = ex2((my_mu - m) + (lr - my_lr)), now = ex2(lr);  // (f 0 from kNone)
             my_mu = m;
             my_lr = lr;
-            if (lane < HG) {  // (every warp the same values, which the others have read their last of before the barrier)
-              s_ref[gr][0][lane] = m;
+            if (lane < HG) {  // (every warp the same values; the last reads of the ones before were before the barrier)
+              s_ref[gr][0][lane] = -m;
               s_ref[gr][1][lane] = now;
             }
             __syncwarp();
@@ -749,7 +774,7 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
                 l[h] *= __shfl_sync(0xffffffffu, f, h);
                 y[h] = __shfl_sync(0xffffffffu, g, h);
               }
-#pragma unroll
+#pragma unroll 1
               for (int z = 0; z < 3; ++z) {
                 if constexpr (HG == 4) {
                   uint32_t a[4];
@@ -776,23 +801,23 @@ __global__ void __launch_bounds__(Layout8<D, HN>::threads, Layout8<D, HN>::per_s
               tmem_st_wait();
             }
           }
-          bool up = false;
+          float most = 0.f;
           uint32_t top = 0;
 #pragma unroll
           for (int h = 0; h < HG; h += 4) {
             const float4 m = *reinterpret_cast<const float4 *>(refs + h), r = *reinterpret_cast<const float4 *>(refs + HG + h);
-            e[h] = ex2(x[h] - m.x);
-            e[h + 1] = ex2(x[h + 1] - m.y);
-            e[h + 2] = ex2(x[h + 2] - m.z);
-            e[h + 3] = ex2(x[h + 3] - m.w);
-            wt[h / 2] = f16x2(e[h] * vs * r.x, e[h + 1] * vs * r.y);
-            wt[h / 2 + 1] = f16x2(e[h + 2] * vs * r.z, e[h + 3] * vs * r.w);
+            const float2 d0 = add2(make_float2(x[h], x[h + 1]), make_float2(m.x, m.y)),
+                         d1 = add2(make_float2(x[h + 2], x[h + 3]), make_float2(m.z, m.w));
+            e[h] = ex2(d0.x), e[h + 1] = ex2(d0.y), e[h + 2] = ex2(d1.x), e[h + 3] = ex2(d1.y);
+            const float2 v = make_float2(vs, vs), w0 = mul2(mul2(make_float2(e[h], e[h + 1]), v), make_float2(r.x, r.y)),
+                         w1 = mul2(mul2(make_float2(e[h + 2], e[h + 3]), v), make_float2(r.z, r.w));
+            wt[h / 2] = f16x2(w0.x, w0.y);
+            wt[h / 2 + 1] = f16x2(w1.x, w1.y);
             top = max_f16x2(top, max_f16x2(wt[h / 2], wt[h / 2 + 1]));
-#pragma unroll
-            for (int z = 0; z < 4; ++z) up |= e[h + z] > 256.f;
+            most = max3(max3(most, e[h], e[h + 1]), e[h + 2], e[h + 3]);
           }
           // (the upper and the lower half against 2^15 = 0x7800: they are not negative)
-          if (move || !group_any(up || top >= 0x78010000u || (top & 0xffffu) > 0x7800u, 1 + gr, 128)) break;
+          if (move || !group_any(most > 256.f || top >= 0x78010000u || (top & 0xffffu) > 0x7800u, 1 + gr, 128)) break;
         }
         // their parts: a word per part and four rows
         uint32_t pt[3][HG / 4];

@@ -101,3 +101,71 @@ def test_ragged(dtype, Hq, Hkv, T):
     """Documents from nothing to 70 tiles in one batch, several key heads."""
     lens = [8960, 0, 5, 3000, 129, 8000, 1, 640, 128, 4097]
     check(batch(3, lens, 200, Hq, 128, T, dtype, 80, 1, 1, Hkv))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Hq,T", [(4, 1), (8, 1), (4, 4)])
+def test_not_a_number_in_long_pieces(dtype, Hq, T):
+    """NaN scores of a whole first tile, of a token further on, and a NaN value: the rows (or the dimension) that see them are NaN, and
+    nothing else is."""
+    count = ranges(Hq * T, dtype)
+    c = batch(5, [2000, 2000, 2000, 2000], count, Hq, 64, T, dtype, 128, 0, 0)
+    q, kc, vc, sc, table, lens = c
+    raw = lambda x, doc, n: x.view(torch.uint8)[table[doc, n // 128].long(), 0, n % 128]  # noqa: E731
+    for n in range(128):
+        raw(kc, 0, n)[5] = 0x7f
+    raw(kc, 1, 1500)[0] = 0xff
+    raw(vc, 2, 900)[7] = 0x7f
+    o, lse = la.paged_decode_q8(*c, want_lse=True)
+    bad = torch.zeros_like(o, dtype=torch.bool)
+    doc = torch.arange(count, device="cuda") % 4
+    bad[(doc == 0) | (doc == 1)] = True
+    bad[..., 7] |= (doc == 2)[:, None, None]
+    assert torch.equal(o.isnan(), bad) and o[~bad].isfinite().all()
+    assert torch.equal(lse.isnan(), ((doc == 0) | (doc == 1))[:, None, None].expand_as(lse))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Hq,T", [(4, 1), (8, 1), (16, 1), (2, 2)])
+@pytest.mark.parametrize("power", [-126, -90, 60, 105])
+def test_value_scales_of_any_size(dtype, Hq, T, power):
+    """Values of the smallest and of very large scales; and a first tile whose values are all zero (their scale is the smallest)
+    before ordinary ones."""
+    lens = [700, 90, 333]
+    c = batch(6, lens, 60, Hq, 128, T, dtype, 64, 0, 0)
+    c[3][..., 1] = 2.0 ** power
+    # r is at most 2^120: a row's largest weight is 2^-6 at a scale of 2^-126, and its smallest step 2^-19 of that
+    ro, rl, (A, X, M, C) = ref.attention(c[0], c[1].float().nan_to_num(0.0), c[2].float().nan_to_num(0.0), c[3].nan_to_num(1.0), *c[4:])
+    to, _ = ref.tolerance(dtype, 128, 700, (A, X, M * 2.0 ** 17, C))
+    o, _ = la.paged_decode_q8(*c)
+    assert bool(((o.double() - ro).abs() <= to(ro)).all())
+    c = batch(7, lens, 60, Hq, 128, T, dtype, 64, 0, 0)
+    for j in range(3):
+        at = c[4][j, :2].long()
+        c[2].view(torch.uint8)[at] = 0
+        c[3][at, ..., 1] = 2.0 ** -126
+    check(c)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Hq,T", [(4, 1), (8, 1), (16, 1)])
+@pytest.mark.parametrize("size", [20, 30, 60])
+@pytest.mark.parametrize("power", [-60, 0, 60])
+def test_one_token_takes_all(dtype, Hq, T, size, power):
+    """Scores so far apart that one token has all the weight: o is its value, whatever its scale is beside the others'."""
+    g = torch.Generator().manual_seed(size)
+    n, page, d = 1000, 128, 64
+    kc = torch.ones(8, 1, page, d)
+    kc[..., 0] = torch.tensor([1.0, 2.0, 4.0, 8.0])[torch.randint(0, 4, (8, 1, page), generator=g)]
+    kc[5, 0, 77, 0] = 64.0
+    vc = (torch.randn(8, 1, page, d, generator=g) * 60).clamp(-448, 448).to(E4M3)
+    sc = torch.ones(8, 1, page // 16, 2)
+    sc[5, 0, 77 // 16, 1] = 2.0 ** power
+    q = torch.zeros(3, Hq, T, d, dtype=dtype)
+    q[..., 0] = 2.0 ** size
+    table = torch.arange(8, dtype=torch.int32).expand(3, 8).contiguous()
+    o, lse = la.paged_decode_q8(q.cuda(), kc.to(E4M3).cuda(), vc.cuda(), sc.cuda(), table.cuda(),
+                                torch.full((3,), n, dtype=torch.int32, device="cuda"), scale=1.0, want_lse=True)
+    want = (vc[5, 0, 77].double() * 2.0 ** power).cuda()
+    assert bool(((o.double() - want).abs() <= torch.finfo(dtype).eps * want.abs()).all())
+    assert bool(((lse.double() / (64 * 2.0 ** size) - 1).abs() <= 2.0 ** -21).all())
