@@ -65,9 +65,13 @@ struct PagedItem {
 };
 // rows of a key head
 __device__ __forceinline__ int group_rows(const PagedProblem &p) { return p.Hq / p.Hkv * p.T; }
-// where row r of sequence b lies in q and o
+// The head of row r < 2^28: the quotient by T <= 16 as a product with p.over_t = ceil(2^32 / T).
+__device__ __forceinline__ int row_head(const PagedProblem &p, int r) { return p.T == 1 ? r : (int)__umulhi(r, p.over_t); }
+// Where row r of sequence b lies in q and o.  (Without a division, whose branches would keep the loads of a piece's rows
+// from overlapping: 200 fp32 sequences of up to 300 tokens 35.3 us, with one 37.9.)
 __device__ __forceinline__ int64_t row_at(const PagedProblem &p, int b, int r) {
-  return b * p.qsb + (p.T == 1 ? r * p.qsh : r / p.T * p.qsh + r % p.T * p.qst);
+  const int head = row_head(p, r);
+  return b * p.qsb + head * p.qsh + (r - head * p.T) * p.qst;
 }
 __device__ __forceinline__ PagedItem item_of(const PagedProblem &p, int slices, int b, int i) {
   PagedItem it;
@@ -272,9 +276,6 @@ __device__ __forceinline__ int block_of(const PagedProblem &p, int token) {
   return p.page_mul ? (int)(__umulhi(token, p.page_mul) >> p.page_shift) : token;
 }
 
-// The head of row r < 2^28: the quotient by T <= 16 as a product with p.over_t = ceil(2^32 / T).
-__device__ __forceinline__ int row_head(const PagedProblem &p, int r) { return p.T == 1 ? r : (int)__umulhi(r, p.over_t); }
-
 // Zero rows (and records of nothing to join) for the sequences without tokens, by one warp of every CTA.
 template <int D, typename T>
 __device__ __noinline__ void empty_rows(const PagedProblem &p, T *o, float *lse, int lane) {
@@ -301,9 +302,9 @@ __device__ __noinline__ void empty_rows(const PagedProblem &p, T *o, float *lse,
 // per warp, so nothing in the loop waits for another lane but the sums of a score.  Those are added up while
 // the heads are halved (HN - 1 exchanges instead of HN per step), which leaves every lane one head, its
 // maximum, its sum and its weight; the weights then go round.  The warps' (and lanes') maxima, sums and
-// outputs are joined at a piece's end.  Up to 4 query heads per key head it is bound by the cache (107 us at 16
-// sequences of 8192, 4 key heads of 4 query heads, D = 128: 0.74 of copy bandwidth), with 16 by its sums (258 us); on
-// codes by its sums, shuffles and latencies (up to 8192 of them: 49 us, a quarter of copy bandwidth).
+// outputs are joined at a piece's end.  Up to 4 query heads per key head it is bound by the cache (105 us at 16
+// sequences of 8192, 4 key heads of 4 query heads, D = 128: 0.75 of copy bandwidth), with 16 by its sums (257 us); on
+// codes by its sums, shuffles and latencies (up to 8192 of them: 47 us, 0.27 of copy bandwidth).
 // Four warps on two CTAs an SM leave them 255 registers: six warps, at 168, take 1.15 times as long.
 constexpr int kSimtWarps = 4, kSimtThreads = 32 * kSimtWarps, kSimtPerSm = 2;
 template <int D, int HN, bool Q8>
@@ -506,18 +507,18 @@ __global__ void __launch_bounds__(kSimtThreads, kSimtPerSm)
       }
     };
     // Copies are committed by groups of U steps (a commit is 140 cycles), 4 or more groups to the ring; when there are no
-    // more to issue all are waited for.
+    // more to issue all are waited for (with groups of one step: the step's own, by empty groups behind it).
     auto copies = [&](int i0) {
 #pragma unroll 1
       for (int i = i0; i < i0 + U; ++i) copy(i);
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
-    for (int i = 0; i < S - U && i < steps; i += U) copies(i);
+    for (int i = 0; i < S - U && (U == 1 || i < steps); i += U) copies(i);
 #pragma unroll 1
     for (int i = 0; i < steps; i += P) {
       if (i % U == 0) {
-        if (i + S - U < steps) {
+        if (U == 1 || i + S - U < steps) {
           copies(i + S - U);
           asm volatile("cp.async.wait_group %0;" ::"n"(S / U - 1) : "memory");
         } else {
@@ -655,14 +656,14 @@ template <int D, typename T>
 __global__ void __launch_bounds__(D) paged_join_kernel(PagedProblem p, int grid, T *o, float *lse, const float *part,
                                                        const float *ml) {
   __shared__ int64_t buf[2 * D / 32 + 2];
-  const int all_rows = p.Hq * p.T, b = blockIdx.x / all_rows, h = blockIdx.x % all_rows, tid = threadIdx.x;
+  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, tid = threadIdx.x;  // (T = 1)
   griddep_wait();
-  const int group = group_rows(p), slices = (group + kHeads - 1) / kHeads, items = p.Hkv * slices;
-  const int64_t orow = row_at(p, b, h) + tid;
+  const int group = p.Hq / p.Hkv, slices = (group + kHeads - 1) / kHeads, items = p.Hkv * slices;
+  const int64_t orow = b * p.qsb + h * p.qsh + tid;
   const int nt = seq_tiles(p, b);
   if (nt == 0) {
     o[orow] = (T)0.f;
-    if (lse && tid == 0) lse[(int64_t)b * all_rows + h] = -INFINITY;
+    if (lse && tid == 0) lse[(int64_t)b * p.Hq + h] = -INFINITY;
     return;
   }
   int64_t before = 0, all = 0;
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(D) paged_join_kernel(PagedProblem p, int grid,
     l = fmaf(f, s_f[2 * (g - g0) + 1], l);
   }
   o[orow] = (T)(m == -INFINITY ? 0.f : a / l);
-  if (lse && tid == 0) lse[(int64_t)b * all_rows + h] = (m + log2f(l)) * 0.6931471805599453f;
+  if (lse && tid == 0) lse[(int64_t)b * p.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
 // CTAs: `per` on each SM, fewer when even the longest possible sequences have fewer tiles.
@@ -737,7 +738,7 @@ cudaError_t run_decode(Launch launch, int per, const PagedProblem &p, void *o, f
     if (e != cudaSuccess) return e;
   }
   TimedLaunch t(K_PAGED_JOIN, s);
-  return launch_overlapped(paged_join_kernel<D, T>, dim3(p.B * p.Hq * p.T), dim3(D), 0, s, p, G, (T *)o, lse,
+  return launch_overlapped(paged_join_kernel<D, T>, dim3(p.B * p.Hq), dim3(D), 0, s, p, G, (T *)o, lse,
                            (const float *)part, (const float *)ml);
 }
 
