@@ -108,6 +108,7 @@ _SIGS = {
     "linattn_device_status": ([_vp, _vp], _i32),
     "linattn_state_scan_noalloc": ([_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32),
     "linattn_diag_mma": ([_i32, _vp, _vp, _vp, _vp], _i32),
+    "linattn_diag_wait": ([_vp, _vp], _i32),
     "linattn_segment_decay": ([_vp, _i32, _i32, _i32, _vp, _vp], _i32),
     "linattn_softmax_segment_fwd": ([ctypes.POINTER(Shape), ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp,
                                      ctypes.c_float, _vp, _sz, _vp], _i32),
@@ -374,6 +375,10 @@ def linattn_diag_scan_withhold(G, BH, dk, dv, local, out, withhold_tile, wait_li
 
 def linattn_diag_mma(mode, A, B, D, stream) -> int:
     return lib().linattn_diag_mma(mode, A, B, D, stream)
+
+
+def linattn_diag_wait(out, stream) -> int:
+    return lib().linattn_diag_wait(out, stream)
 
 
 def linattn_timing_enable(on: bool) -> int:

@@ -1375,4 +1375,11 @@ int32_t linattn_diag_mma(int32_t mode, const void *A, const void *B, float *D, v
   return cuda_status(diag_mma(mode, A, B, D, static_cast<cudaStream_t>(stream)));
 }
 
+int32_t linattn_diag_wait(int32_t *out, void *stream) {
+  if (!out) return LINATTN_ERR_INVALID;
+  int st = check_ptrs32({out});
+  if (st || (st = device_ok())) return st;
+  return cuda_status(diag_wait(out, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

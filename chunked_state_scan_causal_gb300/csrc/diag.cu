@@ -105,7 +105,42 @@ __global__ void __launch_bounds__(128) diag_mma_kernel(const __grid_constant__ C
   if (warp == 0) tmem_dealloc(tmem, 256);
 }
 
+// The 8-bit decode's bounded wait by one warp, on a barrier that no one arrives at before the third wait.
+__global__ void __launch_bounds__(32) diag_wait_kernel(int *out) {
+  __shared__ uint64_t bar;
+  __shared__ int flags[2];
+  const int lane = threadIdx.x;
+  if (lane == 0) {
+    mbar_init(&bar, 1);
+    fence_mbar_init();
+    flags[0] = flags[1] = 0;
+  }
+  __syncwarp();
+  auto wait = [&](int i) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_short<1u << 14>(&bar, 0, flags));
+    if (lane == 0) {
+      out[3 * i] = ok;
+      out[3 * i + 1] = flags[0];
+      out[3 * i + 2] = flags[1];
+    }
+    __syncwarp();
+  };
+  wait(0);
+  if (lane == 0) flags[1] = 7;  // a wait that the flag ends leaves the status
+  __syncwarp();
+  wait(1);
+  if (lane == 0) mbar_arrive(&bar);
+  __syncwarp();
+  wait(2);
+}
+
 }  // namespace
+
+cudaError_t diag_wait(int *out, cudaStream_t s) {
+  TimedLaunch t(K_DIAG, s);
+  diag_wait_kernel<<<1, 32, 0, s>>>(out);
+  return cudaGetLastError();
+}
 
 cudaError_t diag_mma(int mode, const void *A, const void *B, float *D, cudaStream_t s) {
   alignas(64) CUtensorMap mA, mB;

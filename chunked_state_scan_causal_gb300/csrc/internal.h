@@ -247,11 +247,11 @@ cudaError_t softmax_segment_bwd(const SoftmaxProblem &p, const void *q, const vo
 // ---------------------------------------------------------------- TMA descriptors (api.cu)
 // 4-D bf16 tiled tensor map, dims innermost first, strides in bytes for dims 1..3,
 // box {64, box_rows, 1, 1} with the 128-byte swizzle (128 rows: the SW128 tile half).
-// the same for bytes: boxes of box_cols (64 or 128: the swizzle's width) by box_rows
-bool make_tmap_u8(void *map, const void *base, const uint64_t dims[4], const uint64_t strides[3], uint32_t box_cols,
-                  uint32_t box_rows);
 bool make_tmap_bf16(void *map, const void *base, const uint64_t dims[4], const uint64_t strides[3],
                     uint32_t box_rows = 128);
+// The same for bytes: boxes of box_cols (64 or 128: the swizzle's width) by box_rows.
+bool make_tmap_u8(void *map, const void *base, const uint64_t dims[4], const uint64_t strides[3], uint32_t box_cols,
+                  uint32_t box_rows);
 
 // ---------------------------------------------------------------- recurrent decode (decode.cu)
 // For t = 0..T-1: S <- lambda S + k_t v_t^T, o_t = S^T q_t; state [BH][d][d] in/out.
@@ -345,5 +345,6 @@ cudaError_t rope(const RopeProblem &p, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- diagnostics (diag.cu)
 cudaError_t diag_mma(int mode, const void *A, const void *B, float *D, cudaStream_t s);
+cudaError_t diag_wait(int *out, cudaStream_t s);
 
 }  // namespace linattn

@@ -1029,8 +1029,9 @@ cudaError_t run_and_join(PagedProblem p, int per_sm, T *o, float *lse, void *ws,
     if (e != cudaSuccess) return e;
   }
   TimedLaunch t(K_PAGED_JOIN, s);
-  // four rows a CTA, or where an item has many pieces (a row's are read by one CTA) one
-  const bool single = G >= 16 * items;
+  // Four rows a CTA, or where an item has many pieces, all of which a row's CTA reads, one: with 32 pieces an item 8.0 us instead of
+  // 8.4 (B1 H16/4, 4000 tokens), with 304 17.2 instead of 25.0 (B1 H16/1, 100000), with 16 8.1 instead of 7.6 (B4 H16/4 2000).
+  const bool single = G >= 32 * items;
   auto join = [&](auto k, int rows) {
     return launch_overlapped(k, dim3((p.by_item ? items : G) + 1, HN / rows), dim3(512), 0, s, p, o, lse, (const float *)part,
                              (const float *)ml, G);

@@ -136,7 +136,8 @@ __device__ __forceinline__ bool mbar_wait_compact(uint64_t *bar, uint32_t parity
 }
 
 // The same in less code still, without a call: `flags` are two words of shared memory, whether the block gives up and its
-// status.  Gives up after 2^31 of the SM's cycles (about a second).
+// status.  Gives up after LIMIT of the SM's cycles (about a second).
+template <uint32_t LIMIT = 0x80000000u>
 __device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, int *flags) {
   uint32_t ok;
   asm volatile(
@@ -152,14 +153,14 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity, 
       "@q bra DONE;\n\t"
       "mov.u32 u, %%clock;\n\t"
       "sub.u32 u, u, t;\n\t"
-      "setp.lt.u32 q, u, 0x80000000;\n\t"
+      "setp.lt.u32 q, u, %4;\n\t"
       "@q bra LOOP;\n\t"
       "st.volatile.shared.u32 [%3], 1;\n\t"
       "st.volatile.shared.u32 [%3+4], -6;\n\t"
       "DONE:\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(flags))
+      : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(flags)), "n"(LIMIT)
       : "memory");
   return ok != 0;
 }

@@ -606,6 +606,12 @@ int32_t linattn_diag_scan_withhold(int32_t G, int32_t BH, int32_t dk, int32_t dv
  * Returns a status (LINATTN_ERR_DEVICE off sm_103). */
 int32_t linattn_diag_mma(int32_t mode, const void *A, const void *B, float *D, void *stream);
 
+/* Diagnostic: the bounded wait of the 8-bit decode, on a barrier of one warp's own, with a limit of 2^14 cycles.
+ * out (9 int32, device): for each of three waits its result (1: done), the flag "give up" and the status that it left:
+ * nothing arrives (0, 1, LINATTN_ERR_DEVICE_TIMEOUT); the same with the flag set before, which ends it at once; the barrier
+ * has been arrived at (1, the flag and the status as they were). */
+int32_t linattn_diag_wait(int32_t *out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
