@@ -1009,8 +1009,8 @@ def paged_append_q8(k, v, k_cache, v_cache, scales, block_table, start, new_lens
     """paged_append into a cache in 8 bits: k_cache, v_cache [pages, Hkv, page, d] float8_e4m3fn (any strides, pages a
     multiple of 16 tokens) and scales [pages, Hkv, page / 16, 2] fp32 for every 16 tokens' keys and values.
     The scale is the smallest power of two that holds the block; a block that is already begun keeps its scale or, where the
-    new tokens need a larger one, has its codes rounded again.  Values that are not finite become NaN.  Tokens behind the
-    last new one of a block do not outlast the call."""
+    new tokens need a larger one, has its codes rounded again (not at once: order the call with readers of that block on other
+    streams).  Values that are not finite become NaN.  Tokens behind the last new one of a block do not outlast the call."""
     if stream is None and device_status is None and (_fast or _bind()).paged_append_q8(
             k, v, k_cache, v_cache, scales, block_table, start, new_lens):
         return
@@ -1170,7 +1170,8 @@ def rope_fwd(q, k, freqs, positions, layout: str = "half", factor: float = 1.0, 
     """(q', k' or None): rotary positions on q [B, Hq, T, d] and k [B, Hkv, T, d] (or None): the pairs of the first
     2 len(freqs) dimensions, (i, i + rot / 2) ("half") or (2 i, 2 i + 1) ("interleaved"), are turned by position x
     freqs[i] (rope_frequencies) and multiplied by `factor`; the rest is copied.  positions int32: [B], the first
-    token's (the others follow), or [B, T].  outs may be (q, k) themselves."""
+    token's (the others follow), or [B, T].  Outputs have their inputs' strides, so that those of slices of one
+    projection span as much as it does; outs may be (q, k) themselves, which takes no memory (rope_bwd needs neither)."""
     return _rope("linattn_rope_fwd", q, k, freqs, positions, layout, factor, outs, stream)
 
 

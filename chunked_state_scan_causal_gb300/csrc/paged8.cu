@@ -248,9 +248,9 @@ __global__ void __launch_bounds__(256, 5)
 // loads tiles (tensor-map copies) and scales, one that cuts the queries of the next piece into parts.  A tile's chain
 // (scores, softmax, product) takes longer than its loads, and a piece's ends add to it, so an SM holds as many
 // CTAs as fit rather than deep rings: four up to 4 rows, three up to 8, two above.
-// Bound by memory where sequences are long (64 of up to 16384 tokens, 8 key heads: 200 us, 0.98 of copy bandwidth, with
-// up to 4 rows, 0.96 with 8, 0.87 with 16; d = 64, where a tile has half the bytes, 0.85); with 256 sequences of 125 to 500
-// tokens by the pieces' ends (38 us with 4 rows, 48 with 8; the bytes alone 24).  The seven or eleven warps of a
+// Bound by memory where sequences are long (64 of up to 16384 tokens, 8 key heads: 198 us, 0.99 of copy bandwidth, with
+// up to 4 rows, 0.96 with 8, 0.88 with 16; d = 64, where a tile has half the bytes, 0.85); with 256 sequences of 125 to 500
+// tokens by the pieces' ends (38 us with 4 rows, 47 with 8; the bytes alone 24).  The seven or eleven warps of a
 // CTA run five different programs, so their instructions have to fit the caches: loops are not unrolled but over rows,
 // waits are short, and a tile has one path.
 template <int D, int HN>

@@ -371,6 +371,10 @@ int32_t linattn_paged_decode(const linattn_shape *q_shape, const linattn_shape *
  * from appending at once by that).  Slots without a new token keep their bytes, but their block's scale may be
  * another: tokens behind the last new one of its block (of an append that goes back) are no longer what they were.
  * Two tokens of one call in one block by way of two table entries leave any mixture of their codes and scales there.
+ * The older codes of a begun block and its scale are not rewritten at once: unlike linattn_paged_append, an append has to be
+ * ordered with readers of earlier tokens of the same block (a decode over the shorter length on another stream, say).
+ * Tokens that are taken back (drafted ones, by a shorter length) leave the scale that they asked for, and the older codes
+ * rounded to it.
  * device_status as in linattn_paged_append.  Returns a status. */
 int32_t linattn_paged_append_q8(const linattn_shape *new_shape, const linattn_shape *cache_shape, const void *k,
                                 const void *v, void *k_cache, void *v_cache, float *scales, int64_t scale_stride_p,
@@ -397,6 +401,10 @@ int32_t linattn_paged_gather_q8(const linattn_shape *out_shape, const linattn_sh
  * seen does (an infinite query makes its row NaN; codes are finite or NaN).  Scales of blocks inside a length are positive
  * and at most 2^120, and need not be powers of two.  Scores, and sums of up to 2^8 x value over the tokens, are fp32:
  * what leaves its range counts as infinite (a score of +inf makes its row NaN, one of -inf is a weight of zero).
+ * With bf16 queries a token's weight times its value scale is an f16 beside the row's largest such product M among the
+ * tokens that it sees: to 11 bits down to 2^-25 M, and within 2^-36 M below (scales under 2^-109 with fewer bits: within
+ * 2^-145 of the row's largest weight); a query is exact but for values under 2^-14 of its row's largest, which are held to 2^-21
+ * of that.  fp32 computes both in fp32.
  * LINATTN_ERR_UNSUPPORTED: Hq * T above 2^28; 2^30 or more tiles of 128 tokens, were every sequence as long as the table
  * (B * ceil(max_blocks * page / 128), times the cache's heads, times the rows of one, Hq T / H, in 16s).
  *   workspace: LINATTN_OP_PAGED_DECODE bytes for q_shape.  Returns a status. */
